@@ -61,6 +61,10 @@ extern "C" {
 #define TF_MAX_PROMPT_ROWS 65536  /* rows of one prompt call (tf_prompt_build) */
 #define TF_PROMPT_WINDOW_ROWS 32  /* a prompt call's attention window (tf_prompt_build) */
 #define TF_MAX_STREAMS 65536
+#define TF_MIN_PAGE_KEYS 16       /* cache rows of a page (paged tables): a power of two */
+#define TF_MAX_PAGE_KEYS 256
+#define TF_MAX_PAGES (1 << 24)    /* pages of a pool */
+#define TF_MAX_PAGE_IDS (1 << 28) /* entries of a paged table's lists together */
 #define TF_MK       256         /* width of the drafter's Markov head rows (W1, W2) */
 
 typedef enum {
@@ -369,6 +373,62 @@ int tf_prompt_build(int32_t rows, int32_t keys, int32_t kv_capacity,
                     const void* const* conv_state, const void* const* k_cache,
                     const void* const* v_cache, int n_conv, int n_attn,
                     tf_cuda_stream stream, tf_segments** out);
+
+/* ---- paged caches -----------------------------------------------------------
+ * A paged table's streams keep their keys and values in pages of a pool that
+ * all streams share, one pool of K and one of V a layer, instead of one
+ * contiguous cache each: a stream grows by a page at a time, a forked stream
+ * lists its parent's pages, and streams with a common prompt list its pages
+ * once written. Key t of a stream is slot t % page_keys of the page that the
+ * stream's list names at t / page_keys, the same page in every layer.
+ *   pool    bf16 [n_pages][TF_NKV][page_keys][TF_D] (head-major in a page)
+ *
+ * tf_paged_build is tf_segments_build for pages:
+ *   streams     as there; kv_capacity is a multiple of page_keys
+ *   pages       host array of page ids, stream after stream, kv_capacity /
+ *               page_keys entries each, every entry in [0, n_pages) (the
+ *               entries past a stream's keys are checked and not used)
+ *   page_keys   a power of two, TF_MIN_PAGE_KEYS..TF_MAX_PAGE_KEYS
+ *   k_pool, v_pool  host arrays [n_attn] of device pointers
+ * A page may stand in several lists, or several times in one, for reading; a
+ * page that holds rows of a stream's window (they are appended there) must
+ * stand in the lists exactly once: copy a shared last page first
+ * (tf_pages_copy). Refuses what tf_segments_build refuses, pools that overlap,
+ * a bad page size, an id out of range and a shared page with window rows
+ * (TF_EINVAL); n_pages > TF_MAX_PAGES or more than TF_MAX_PAGE_IDS entries
+ * (TF_ERANGE).
+ *
+ * tf_paged_prompt_build is tf_prompt_build for pages: one list of kv_capacity /
+ * page_keys entries.
+ *
+ * Either table serves every call that a dense table of its kind serves, except
+ * that its attention is tf_attn_paged: tf_attn, tf_attn_block, their partials
+ * forms, tf_attn_merge and tf_attn_static refuse it (TF_EINVAL). */
+int tf_paged_build(const tf_stream* streams, int n_streams, const void* const* conv_state,
+                   const void* const* conv_hist, const int32_t* pages, int32_t page_keys,
+                   int32_t n_pages, const void* const* k_pool, const void* const* v_pool,
+                   int n_conv, int n_attn, tf_cuda_stream stream, tf_segments** out);
+int tf_paged_prompt_build(int32_t rows, int32_t keys, int32_t kv_capacity,
+                          const void* const* conv_state, const int32_t* pages,
+                          int32_t page_keys, int32_t n_pages, const void* const* k_pool,
+                          const void* const* v_pool, int n_conv, int n_attn,
+                          tf_cuda_stream stream, tf_segments** out);
+
+/* The attention of one layer over a paged table in one call: tf_attn (full ==
+ * 0) or tf_attn_block (full != 0) with the keys and values in pages. Same
+ * masks, kernels, chunks, partial scratch (tf_partials_bytes), failure report
+ * and rule on overlapping calls as there; a stream's result does not depend on
+ * which pages hold its keys. What a page holds past its stream's keys is never
+ * used.
+ *   q    bf16 [R][TF_NQ][TF_D]
+ *   out  bf16 [R][TF_NQ][TF_D]: the fp32 result rounded once to nearest even
+ *        (what the output projection reads; the probabilities are fp16, which
+ *        leaves the fp32 result about 2e-4 of its size, a tenth of that
+ *        rounding)
+ * Errors: TF_EINVAL (a table that is not paged, attn_layer out of range, null
+ * or misaligned pointers). */
+int tf_attn_paged(const tf_segments* seg, int attn_layer, const void* q, void* partials,
+                  void* out, int full, tf_cuda_stream stream);
 
 /* ---- failures on the device ------------------------------------------------
  * The tensor-core attention kernel (tf_attn*, streams of 9 rows or more and

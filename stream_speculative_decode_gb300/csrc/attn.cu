@@ -29,6 +29,12 @@
 // block seeing the keys [0, len + 1)): with `full` set every window row sees
 // all of the stream's keys instead of its causal count; nothing else changes,
 // and the merge is shared (it reads only the records).
+//
+// Paged tables (tf_attn_paged) run the same kernels with kPaged set: the
+// chunk's page ids are read into shared memory before the dependency wait (the
+// table is immutable), every 16-byte copy finds its page there, and the output
+// is bf16. A page holds at least 16 keys, so each 2 KB of a head's K or V is
+// still contiguous and the copies stay whole 128-byte lines.
 #include "attn_item.cuh"
 
 namespace tf {
@@ -43,16 +49,34 @@ using item::ex2;
 // windows run as several items of at most two m-tiles: a third m-tile needs
 // 230 registers (two CTAs per SM), squeezed to three CTAs it spills, and
 // either way the whole launch ran slower.
-template <int MT>
+template <int MT, bool kPaged>
 __global__ void __launch_bounds__(kThreads, 3)
 attn_partials_kernel(SegTable t, int layer, const uint16_t* __restrict__ q,
-                     float* __restrict__ part_o, float2* __restrict__ part_ml, float* __restrict__ out,
+                     float* __restrict__ part_o, float2* __restrict__ part_ml, OutT<kPaged>* __restrict__ out,
                      int full) {
     extern __shared__ __align__(128) unsigned char smem[];
     const int g = blockIdx.x % TF_NKV;
     const AttnItem it = t.items[blockIdx.x / TF_NKV];
     const SegStream st = t.streams[it.stream];
-    if constexpr (MT == 1) {
+    int32_t* page_ids = nullptr;
+    if constexpr (kPaged) {
+        page_ids = reinterpret_cast<int32_t*>(smem + smem_bytes(MT));
+        const int c0 = it.chunk * st.chunk_keys;
+        item::load_page_ids(t, it.stream, c0, min(st.chunk_keys, st.keys - c0), page_ids, threadIdx.x, kThreads);
+        __syncthreads();
+    }
+    if constexpr (MT == 1 && kPaged) {   // the same prefetch, a page a thread (at most 12 pages)
+        const int nkeys = min(st.chunk_keys, st.keys - it.chunk * st.chunk_keys);
+        const int k0 = int(threadIdx.x) << t.page_shift;
+        const int n = min(min(nkeys, (item::kStages - 1) * item::kKT) - k0, 1 << t.page_shift);
+        if (n > 0) {
+            const size_t slot = size_t(layer) * t.S + it.stream;
+            const size_t off = ((size_t(page_ids[threadIdx.x]) * TF_NKV + g) << t.page_shift) * TF_D;
+            l2_prefetch_bulk(static_cast<const uint16_t*>(t.k_cache[slot]) + off, uint32_t(n) * item::kRowB);
+            l2_prefetch_bulk(static_cast<const uint16_t*>(t.v_cache[slot]) + off, uint32_t(n) * item::kRowB);
+        }
+    }
+    if constexpr (MT == 1 && !kPaged) {
         // narrow windows (one m-tile: short launches, one wave): the first
         // stages' keys and values into L2 while the previous kernel finishes
         // (measured 17.0 -> 16.0 us a layer for 16 one-row streams; the
@@ -69,7 +93,8 @@ attn_partials_kernel(SegTable t, int layer, const uint16_t* __restrict__ q,
     }
     pdl_wait();   // the table above; queries and caches below
     const int mode = out ? st.merge_mode : kMergeKernel;   // records only in the two-call form
-    item::attn_item<MT, true, 0>(t, layer, it, st, g, q, part_o, part_ml, out, mode, full, smem, threadIdx.x, true);
+    item::attn_item<MT, true, 0, kPaged>(t, layer, it, st, g, q, part_o, part_ml, out, mode, full, smem, threadIdx.x,
+                                         true, page_ids);
     if (mode == kMergeLastCta) {
         __shared__ int last_flag;
         finish_last_cta<MT == 1 ? 8 : 16>(t, layer, it.stream, st, g, part_o, part_ml, out, &last_flag);
@@ -91,9 +116,10 @@ constexpr int kMergeBatch = 2 * kMergeLoads;         // records per warp batch (
 // (earlier batches rescaled when it grows). The warps' (M, L, o) are combined
 // through shared memory at the end. 3 CTAs per SM: the long-context
 // workload's 24 rows x 16 head pairs fit one wave.
+template <typename O>
 __global__ void __launch_bounds__(kMergeThreads, 3)
 attn_merge_kernel(SegTable t, const float* __restrict__ part_o, const float2* __restrict__ part_ml,
-                  float* __restrict__ out, int kernel_mode_only) {
+                  O* __restrict__ out, int kernel_mode_only) {
     const int row = blockIdx.x / kMergeCtasPerRow;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int hl = warp / kMergeSplit, split = warp % kMergeSplit;
@@ -191,30 +217,48 @@ attn_merge_kernel(SegTable t, const float* __restrict__ part_o, const float2* __
             o4.w += f * w4.w;
         }
         const float inv = 1.f / L;
-        *reinterpret_cast<float4*>(out + (size_t(row) * TF_NQ + h) * TF_D + d4) =
-            make_float4(o4.x * inv, o4.y * inv, o4.z * inv, o4.w * inv);
+        store_out4(out + (size_t(row) * TF_NQ + h) * TF_D + d4,
+                   make_float4(o4.x * inv, o4.y * inv, o4.z * inv, o4.w * inv));
     }
 }
 
-template <int MT>
+template <int MT, bool kPaged>
+constexpr int partials_smem() { return smem_bytes(MT) + (kPaged ? item::kPageIdsB : 0); }
+
+template <int MT, bool kPaged>
 int prepare_one() {
-    cudaError_t e = cudaFuncSetAttribute(attn_partials_kernel<MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         smem_bytes(MT));
+    cudaError_t e = cudaFuncSetAttribute(attn_partials_kernel<MT, kPaged>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         partials_smem<MT, kPaged>());
     return e == cudaSuccess ? TF_OK : cuda_fail(e);
+}
+
+// The mma.sync launch of one attention layer.
+template <bool kPaged>
+int launch_mma(const SegTable& t, int layer, const uint16_t* q, float* po, float2* pml, cudaStream_t stream,
+               OutT<kPaged>* out, int full) {
+    const dim3 grid(t.n_items_mma * TF_NKV);
+    if (t.mma_mt == 1)
+        return launch_pdl(attn_partials_kernel<1, kPaged>, grid, dim3(kThreads), partials_smem<1, kPaged>(), stream, t,
+                          layer, q, po, pml, out, full);
+    return launch_pdl(attn_partials_kernel<2, kPaged>, grid, dim3(kThreads), partials_smem<2, kPaged>(), stream, t,
+                      layer, q, po, pml, out, full);
 }
 
 }  // namespace
 
 int attn_prepare() {
     int rc;
-    if ((rc = prepare_one<1>()) != TF_OK) return rc;
-    return prepare_one<2>();
+    if ((rc = prepare_one<1, false>()) != TF_OK) return rc;
+    if ((rc = prepare_one<2, false>()) != TF_OK) return rc;
+    if ((rc = prepare_one<1, true>()) != TF_OK) return rc;
+    return prepare_one<2, true>();
 }
 
 // Launchers for other translation units: the partials and the merge of one
 // attention layer with the partial records at `po` (o) and `pml` (m, l).
+template <bool kPaged>
 int launch_attn_partials(const SegTable& t, int layer, const uint16_t* q, float* po, float2* pml,
-                         cudaStream_t stream, float* out, int full) {
+                         cudaStream_t stream, OutT<kPaged>* out, int full) {
     if (t.n_items_mma > 0 && t.n_items_mma < t.n_items && t.side) {
         // both kinds of windows: the two launches run side by side (they write
         // disjoint streams' records and outputs). The persistent tensor-core
@@ -226,47 +270,40 @@ int launch_attn_partials(const SegTable& t, int layer, const uint16_t* q, float*
         cudaError_t e = cudaEventRecord(t.ev_fork, stream);
         if (e == cudaSuccess) e = cudaStreamWaitEvent(t.side, t.ev_fork, 0);
         if (e != cudaSuccess) return cuda_fail(e);
-        int rc = launch_attn_partials_tc(t, layer, q, po, pml, stream, out, full, t.tc_grid_mixed);
+        int rc = launch_attn_partials_tc<kPaged>(t, layer, q, po, pml, stream, out, full, t.tc_grid_mixed);
         if (rc != TF_OK) return rc;
-        const dim3 grid(t.n_items_mma * TF_NKV);
-        if (t.mma_mt == 1)
-            rc = launch_pdl(attn_partials_kernel<1>, grid, dim3(kThreads), smem_bytes(1), t.side, t, layer, q, po, pml,
-                            out, full);
-        else
-            rc = launch_pdl(attn_partials_kernel<2>, grid, dim3(kThreads), smem_bytes(2), t.side, t, layer, q, po, pml,
-                            out, full);
+        rc = launch_mma<kPaged>(t, layer, q, po, pml, t.side, out, full);
         if (rc != TF_OK) return rc;
         e = cudaEventRecord(t.ev_join, t.side);
         if (e == cudaSuccess) e = cudaStreamWaitEvent(stream, t.ev_join, 0);
         return e == cudaSuccess ? TF_OK : cuda_fail(e);
     }
     if (t.n_items_mma > 0) {
-        const dim3 grid(t.n_items_mma * TF_NKV);
-        int rc;
-        if (t.mma_mt == 1)
-            rc = launch_pdl(attn_partials_kernel<1>, grid, dim3(kThreads), smem_bytes(1), stream, t, layer, q, po, pml,
-                            out, full);
-        else
-            rc = launch_pdl(attn_partials_kernel<2>, grid, dim3(kThreads), smem_bytes(2), stream, t, layer, q, po, pml,
-                            out, full);
+        const int rc = launch_mma<kPaged>(t, layer, q, po, pml, stream, out, full);
         if (rc != TF_OK) return rc;
     }
-    if (t.n_items_mma < t.n_items) return launch_attn_partials_tc(t, layer, q, po, pml, stream, out, full);
+    if (t.n_items_mma < t.n_items) return launch_attn_partials_tc<kPaged>(t, layer, q, po, pml, stream, out, full);
     return TF_OK;
 }
 
-int launch_attn_merge(const SegTable& t, const float* po, const float2* pml, float* out, cudaStream_t stream,
+template <bool kPaged>
+int launch_attn_merge(const SegTable& t, const float* po, const float2* pml, OutT<kPaged>* out, cudaStream_t stream,
                       bool kernel_mode_only) {
-    return launch_pdl(attn_merge_kernel, dim3(t.R * kMergeCtasPerRow), dim3(kMergeThreads), 0, stream, t, po, pml,
+    return launch_pdl(attn_merge_kernel<OutT<kPaged>>, dim3(t.R * kMergeCtasPerRow), dim3(kMergeThreads), 0, stream, t, po, pml,
                       out, kernel_mode_only ? 1 : 0);
 }
+
+// attn_static.cu's
+template int launch_attn_partials<false>(const SegTable&, int, const uint16_t*, float*, float2*, cudaStream_t, float*,
+                                         int);
+template int launch_attn_merge<false>(const SegTable&, const float*, const float2*, float*, cudaStream_t, bool);
 
 }  // namespace tf
 
 extern "C" int tf_attn_partials(const tf_segments* seg, int attn_layer, const void* q, void* partials,
                                 tf_cuda_stream stream) {
     using namespace tf;
-    if (!seg) return TF_EINVAL;
+    if (!seg || seg->paged) return TF_EINVAL;   // pages: tf_attn_paged
     const SegTable& t = seg->dev;
     if (attn_layer < 0 || attn_layer >= t.n_attn) return TF_EINVAL;
     if (t.R == 0) return TF_OK;
@@ -279,7 +316,7 @@ extern "C" int tf_attn_partials(const tf_segments* seg, int attn_layer, const vo
 extern "C" int tf_attn(const tf_segments* seg, int attn_layer, const void* q, void* partials, float* out,
                        tf_cuda_stream stream) {
     using namespace tf;
-    if (!seg) return TF_EINVAL;
+    if (!seg || seg->paged) return TF_EINVAL;   // pages: tf_attn_paged
     const SegTable& t = seg->dev;
     if (attn_layer < 0 || attn_layer >= t.n_attn) return TF_EINVAL;
     if (t.R == 0) return TF_OK;
@@ -294,7 +331,7 @@ extern "C" int tf_attn(const tf_segments* seg, int attn_layer, const void* q, vo
 extern "C" int tf_attn_block_partials(const tf_segments* seg, int attn_layer, const void* q, void* partials,
                                       tf_cuda_stream stream) {
     using namespace tf;
-    if (!seg) return TF_EINVAL;
+    if (!seg || seg->paged) return TF_EINVAL;   // pages: tf_attn_paged
     const SegTable& t = seg->dev;
     if (attn_layer < 0 || attn_layer >= t.n_attn) return TF_EINVAL;
     if (t.R == 0) return TF_OK;
@@ -307,7 +344,7 @@ extern "C" int tf_attn_block_partials(const tf_segments* seg, int attn_layer, co
 extern "C" int tf_attn_block(const tf_segments* seg, int attn_layer, const void* q, void* partials, float* out,
                              tf_cuda_stream stream) {
     using namespace tf;
-    if (!seg) return TF_EINVAL;
+    if (!seg || seg->paged) return TF_EINVAL;   // pages: tf_attn_paged
     const SegTable& t = seg->dev;
     if (attn_layer < 0 || attn_layer >= t.n_attn) return TF_EINVAL;
     if (t.R == 0) return TF_OK;
@@ -319,9 +356,26 @@ extern "C" int tf_attn_block(const tf_segments* seg, int attn_layer, const void*
     return launch_attn_merge(t, po, pml, out, stream, true);
 }
 
+extern "C" int tf_attn_paged(const tf_segments* seg, int attn_layer, const void* q, void* partials, void* out, int full,
+                             tf_cuda_stream stream) {
+    using namespace tf;
+    if (!seg || !seg->paged) return TF_EINVAL;
+    const SegTable& t = seg->dev;
+    if (attn_layer < 0 || attn_layer >= t.n_attn) return TF_EINVAL;
+    if (t.R == 0) return TF_OK;
+    if (!q || !partials || !out || !aligned16(q) || !aligned16(partials) || !aligned16(out)) return TF_EINVAL;
+    float* po = static_cast<float*>(partials);
+    float2* pml = reinterpret_cast<float2*>(po + t.n_partials * TF_D);
+    uint16_t* o = static_cast<uint16_t*>(out);
+    int rc = launch_attn_partials<true>(t, attn_layer, static_cast<const uint16_t*>(q), po, pml, stream, o,
+                                        full ? 1 : 0);
+    if (rc != TF_OK || t.n_merge_rows == 0) return rc;
+    return launch_attn_merge<true>(t, po, pml, o, stream, true);
+}
+
 extern "C" int tf_attn_merge(const tf_segments* seg, const void* partials, float* out, tf_cuda_stream stream) {
     using namespace tf;
-    if (!seg) return TF_EINVAL;
+    if (!seg || seg->paged) return TF_EINVAL;
     const SegTable& t = seg->dev;
     if (t.R == 0) return TF_OK;
     if (!partials || !out || !aligned16(partials) || !aligned16(out)) return TF_EINVAL;

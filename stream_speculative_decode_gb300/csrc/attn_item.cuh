@@ -36,6 +36,21 @@ constexpr float kTau = 8.f;             // lazy-rescale threshold, log2 units
 
 __host__ __device__ constexpr int smem_bytes(int mt) { return kStages * kStageB + 16 * mt * kRowB; }
 
+// Paged tables: the chunk's page ids sit in shared memory behind the item's
+// own part. A chunk holds at most 512 * TF_MAX_ROWS = 8,192 keys (256 * 32 for
+// a prompt's windows), 512 pages of 16 keys.
+constexpr int kMaxChunkPages = 512;
+constexpr int kPageIdsB = kMaxChunkPages * 4;
+
+// The page ids of keys [c0, c0 + nkeys) of a stream into `ids`, by `nthreads`
+// threads (the caller synchronises them). c0 is a multiple of every page size.
+__device__ __forceinline__ void load_page_ids(const SegTable& t, int stream, int c0, int nkeys, int32_t* ids, int tid,
+                                              int nthreads) {
+    const int32_t* src = t.pages + t.page_first[stream] + (c0 >> t.page_shift);
+    const int n = (nkeys + (1 << t.page_shift) - 1) >> t.page_shift;
+    for (int i = tid; i < n; i += nthreads) ids[i] = src[i];
+}
+
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
@@ -127,11 +142,14 @@ __device__ __forceinline__ bool bar_and(int id, bool x) {
 //   V below 2^-14 round, by at most 2^-25 each.
 //   trigger: let the stream's next kernel launch once the passes are done.
 // The caller has passed griddepcontrol.wait.
-template <int MT, bool kFast, int kBar>
+// kPaged: the chunk's keys lie in the pages `page_ids` (shared memory,
+// load_page_ids) of the layer's pools, and the output is bf16.
+template <int MT, bool kFast, int kBar, bool kPaged = false>
 __device__ __forceinline__ void attn_item(const SegTable& t, int layer, const AttnItem item, const SegStream& st,
                                           int g, const uint16_t* __restrict__ q, float* __restrict__ part_o,
-                                          float2* __restrict__ part_ml, float* __restrict__ out, int mode, int full,
-                                          unsigned char* smem, int tid, bool trigger) {
+                                          float2* __restrict__ part_ml, OutT<kPaged>* __restrict__ out, int mode,
+                                          int full, unsigned char* smem, int tid, bool trigger,
+                                          const int32_t* page_ids = nullptr) {
     constexpr bool kQReg = MT <= 2;
     constexpr int bar = kBar;
     const int nq_all = st.rows * 4;
@@ -141,8 +159,10 @@ __device__ __forceinline__ void attn_item(const SegTable& t, int layer, const At
     const int nkeys = min(st.chunk_keys, st.keys - c0);
     const int nst = (nkeys + kKT - 1) / kKT;
     const size_t slot = size_t(layer) * t.S + item.stream;
-    const uint16_t* Kg = static_cast<const uint16_t*>(t.k_cache[slot]) + (size_t(g) * st.cap + c0) * TF_D;
-    const uint16_t* Vg = static_cast<const uint16_t*>(t.v_cache[slot]) + (size_t(g) * st.cap + c0) * TF_D;
+    // the chunk's first key of the head, or (paged) the layer's pool
+    const size_t base = kPaged ? 0 : (size_t(g) * st.cap + c0) * TF_D;
+    const uint16_t* Kg = static_cast<const uint16_t*>(t.k_cache[slot]) + base;
+    const uint16_t* Vg = static_cast<const uint16_t*>(t.v_cache[slot]) + base;
     unsigned char* sKV = smem;
     unsigned char* sQ = smem + kStages * kStageB;
     const uint32_t sKV32 = smem_u32(sKV), sQ32 = smem_u32(sQ);
@@ -165,7 +185,12 @@ __device__ __forceinline__ void attn_item(const SegTable& t, int layer, const At
             const int idx = tid + k * kThreads;
             const int r = idx >> 3, ch = idx & 7;
             const bool valid = key0 + r < nkeys;
-            const size_t off = size_t(key0 + r) * TF_D + ch * 8;
+            size_t off = size_t(key0 + r) * TF_D + ch * 8;
+            if constexpr (kPaged) {   // slot of the key's page; a page id is read only for a key of the chunk
+                const int key = key0 + r, ps = t.page_shift;
+                const int64_t head = int64_t(valid ? page_ids[key >> ps] : 0) * TF_NKV + g;
+                off = ((size_t(head) << ps) + (key & ((1 << ps) - 1))) * TF_D + ch * 8;
+            }
             cp_async16(buf + swz(r, ch), valid ? Kg + off : Kg, valid);
             cp_async16(buf + kKT * kRowB + swz(r, ch), valid ? Vg + off : Vg, valid);
         }
@@ -454,8 +479,8 @@ __device__ __forceinline__ void attn_item(const SegTable& t, int layer, const At
         }
         if (mode == kMergeDirect) {   // the stream's only chunk: the output itself
             const float inv = 1.f / L;
-            *reinterpret_cast<float4*>(out_row(out, st, g, q0 + qi) + d4) =
-                make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+            store_out4(out_row(out, st, g, q0 + qi) + d4,
+                       make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
         } else {
             *reinterpret_cast<float4*>(part_o + (rec0 + qi) * TF_D + d4) = acc;
             if (d4 == 0) part_ml[rec0 + qi] = make_float2(M, L);

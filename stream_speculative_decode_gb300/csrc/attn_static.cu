@@ -51,7 +51,7 @@ int partials_address(void** out) {
 extern "C" int tf_attn_static(const tf_segments* seg, int attn_layer, const void* q, float* out,
                               tf_cuda_stream stream) {
     using namespace tf;
-    if (!seg) return TF_EINVAL;
+    if (!seg || seg->paged) return TF_EINVAL;
     const SegTable& t = seg->dev;
     if (attn_layer < 0 || attn_layer >= t.n_attn) return TF_EINVAL;
     if (seg->plan.partials_bytes > int64_t(TF_STATIC_SCRATCH_BYTES)) return TF_ERANGE;

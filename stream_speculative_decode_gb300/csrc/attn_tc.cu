@@ -53,6 +53,15 @@
 // At the end (m, l, O) is renormalised to the true running max and written
 // as the chunk's partial records.
 //
+// Paged tables (kPaged): a 64-key tile is one box of the layer's pool map
+// (pages of 64 keys or more) or 64 / page boxes side by side (smaller pages;
+// box offsets are multiples of 2 KB, whole swizzle atoms); the producer reads a
+// tile's page ids one tile ahead of its boxes, so their latency hides behind
+// the ring. A tile's boxes past the stream's last page read that page again, and
+// a last page may hold anything past the stream's keys: such K columns are
+// masked like the causal edge, such V rows are zeroed by the converter (0 * NaN
+// would reach the sums).
+//
 // Every wait on an mbarrier is bounded (the library's wait limit, 2 s of
 // %globaltimer unless tf_set_wait_limit_ns changed it); on a timeout the CTA
 // raises a shared abort flag, waits (bounded) for its TMA copies and MMAs in
@@ -136,6 +145,7 @@ struct Unit {
     const CUtensorMap* vmap;
     int stream, chunk, g, c0, T;
 };
+template <bool kPaged>
 __device__ __forceinline__ Unit unit_of(const SegTable& t, int layer, int u) {
     Unit U;
     const AttnItem it = t.items[t.n_items_mma + u / TF_NKV];   // tensor-core items follow the mma.sync ones
@@ -145,10 +155,34 @@ __device__ __forceinline__ Unit unit_of(const SegTable& t, int layer, int u) {
     U.st = t.streams[it.stream];
     U.c0 = it.chunk * U.st.chunk_keys;
     U.T = (min(U.st.chunk_keys, U.st.keys - U.c0) + kKT - 1) / kKT;
-    const size_t slot = size_t(layer) * t.S + it.stream;
+    const size_t slot = kPaged ? size_t(layer) : size_t(layer) * t.S + it.stream;
     U.kmap = t.k_maps + slot;
     U.vmap = t.v_maps + slot;
     return U;
+}
+
+// The page ids of tile j of a unit (x only for pages of 64 keys or more, x and
+// y for 32-key pages, all four for 16-key pages).
+__device__ __forceinline__ int4 tile_pages(const SegTable& t, const Unit& U, int j) {
+    const int32_t* ids = t.pages + t.page_first[U.stream] + ((U.c0 + j * kKT) >> t.page_shift);
+    if (t.page_shift == 4) return __ldg(reinterpret_cast<const int4*>(ids));
+    if (t.page_shift == 5) {
+        const int2 p = __ldg(reinterpret_cast<const int2*>(ids));
+        return make_int4(p.x, p.y, 0, 0);
+    }
+    return make_int4(__ldg(ids), 0, 0, 0);
+}
+// Tile j of a paged unit: f(offset in the tile, slot in the page, page) for each of its boxes.
+template <typename F>
+__device__ __forceinline__ void tile_boxes(const SegTable& t, const Unit& U, int j, int4 id, F&& f) {
+    const int ps = t.page_shift;
+    f(0u, ps >= 6 ? (U.c0 + j * kKT) & ((1 << ps) - 1) : 0, id.x);
+    if (ps == 5) f(32u * 128u, 0, id.y);
+    if (ps == 4) {
+        f(16u * 128u, 0, id.y);
+        f(32u * 128u, 0, id.z);
+        f(48u * 128u, 0, id.w);
+    }
 }
 
 // Blackwell's three-input max and paired fp32 FMA / add: each of these does
@@ -400,17 +434,26 @@ __device__ __forceinline__ void issue_q(uint32_t sQ, const CUtensorMap* qmap, co
 // item code on its exact path (V in bf16, P split into two bf16 parts),
 // writing the unit's records or output again; then the unit's deferred merge
 // arrival (a last-CTA merge runs here when it completes the count).
+template <bool kPaged>
 __device__ __noinline__ void recompute_exact(const SegTable& t, int layer, const uint16_t* q, float* part_o,
-                                             float2* part_ml, float* out, int full, unsigned char* smem, int tid) {
+                                             float2* part_ml, OutT<kPaged>* out, int full, unsigned char* smem,
+                                             int tid) {
     const int n = *reinterpret_cast<volatile const int32_t*>(t.tc_redo);
     __shared__ int last_flag;
     for (int k = 0; k < n; ++k) {
-        const Unit U = unit_of(t, layer, __ldcg(t.tc_redo + 1 + k));
+        const Unit U = unit_of<kPaged>(t, layer, __ldcg(t.tc_redo + 1 + k));
         const int mode = out ? U.st.merge_mode : kMergeKernel;
+        int32_t* page_ids = nullptr;
+        if constexpr (kPaged) {
+            static_assert(item::smem_bytes(2) + item::kPageIdsB <= kQB + kStages * kStageB, "shared memory");
+            page_ids = reinterpret_cast<int32_t*>(smem + item::smem_bytes(2));
+            item::load_page_ids(t, U.stream, U.c0, min(U.st.chunk_keys, U.st.keys - U.c0), page_ids, tid, 128);
+            item::bar_sync(1);
+        }
         for (int q0 = 0; q0 < 4 * U.st.rows; q0 += 32) {
             const AttnItem it{U.stream, U.chunk, q0, 0};
-            item::attn_item<2, false, 1>(t, layer, it, U.st, U.g, q, part_o, part_ml, out, mode, full, smem, tid,
-                                         false);
+            item::attn_item<2, false, 1, kPaged>(t, layer, it, U.st, U.g, q, part_o, part_ml, out, mode, full, smem,
+                                                 tid, false, page_ids);
             item::bar_sync(1);   // the item's shared memory is reused by the next group
         }
         if (mode == kMergeLastCta) {
@@ -437,9 +480,10 @@ __device__ __noinline__ void recompute_exact(const SegTable& t, int layer, const
 // TMA producer and the MMA thread run into the next unit's tiles while the
 // softmax warps finish the previous unit (records, merges); the ring stages, S
 // buffers and their mbarrier phases follow one running tile count.
+template <bool kPaged>
 __global__ void __launch_bounds__(kThreads, 2)
 attn_partials_tc_kernel(SegTable t, int layer, const uint16_t* __restrict__ q, float* __restrict__ part_o,
-                        float2* __restrict__ part_ml, float* __restrict__ out, int full, int n_units,
+                        float2* __restrict__ part_ml, OutT<kPaged>* __restrict__ out, int full, int n_units,
                         const __grid_constant__ CUtensorMap qmap) {
     extern __shared__ unsigned char smem_raw[];
     const uint32_t raw = su32(smem_raw);
@@ -480,10 +524,17 @@ attn_partials_tc_kernel(SegTable t, int layer, const uint16_t* __restrict__ q, f
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (tid == 0 && int(blockIdx.x) < n_units) {   // the first unit's first tiles into L2 meanwhile
-        const Unit U = unit_of(t, layer, blockIdx.x);
+        const Unit U = unit_of<kPaged>(t, layer, blockIdx.x);
         for (int j = 0; j < U.T && j < kStages; ++j) {
-            tma_prefetch_3d(U.kmap, 0, U.c0 + j * kKT, U.g);
-            tma_prefetch_3d(U.vmap, 0, U.c0 + j * kKT, U.g);
+            if constexpr (kPaged) {
+                tile_boxes(t, U, j, tile_pages(t, U, j), [&](uint32_t, int slot, int page) {
+                    tma_prefetch_3d(U.kmap, 0, slot, page * TF_NKV + U.g);
+                    tma_prefetch_3d(U.vmap, 0, slot, page * TF_NKV + U.g);
+                });
+            } else {
+                tma_prefetch_3d(U.kmap, 0, U.c0 + j * kKT, U.g);
+                tma_prefetch_3d(U.vmap, 0, U.c0 + j * kKT, U.g);
+            }
         }
     }
     pdl_wait();   // the table above; queries and caches below
@@ -510,11 +561,11 @@ attn_partials_tc_kernel(SegTable t, int layer, const uint16_t* __restrict__ q, f
             bool ok = true;
             int gt = 0, n = 0, q_issued = 0;
             if (int(blockIdx.x) < n_units) {
-                issue_q(sQ, &qmap, unit_of(t, layer, blockIdx.x), su32(&bars->q_ready));
+                issue_q(sQ, &qmap, unit_of<kPaged>(t, layer, blockIdx.x), su32(&bars->q_ready));
                 q_issued = 1;
             }
             for (int u = blockIdx.x; u >= 0 && ok; ++n) {
-                const int T = unit_of(t, layer, u).T;
+                const int T = unit_of<kPaged>(t, layer, u).T;
                 ok = mbar_wait(su32(&bars->q_ready), n & 1, abortp);   // the unit's queries landed
                 if (!ok) break;
                 tc_fence_after();
@@ -542,7 +593,7 @@ attn_partials_tc_kernel(SegTable t, int layer, const uint16_t* __restrict__ q, f
                 if (u >= 0) {
                     ok = mbar_wait(su32(&bars->q_free), n & 1, abortp);
                     if (ok) {
-                        issue_q(sQ, &qmap, unit_of(t, layer, u), su32(&bars->q_ready));
+                        issue_q(sQ, &qmap, unit_of<kPaged>(t, layer, u), su32(&bars->q_ready));
                         ++q_issued;
                     }
                 }
@@ -559,7 +610,7 @@ attn_partials_tc_kernel(SegTable t, int layer, const uint16_t* __restrict__ q, f
             bool ok = true;
             int gt = 0, n = 0;
             for (int u = blockIdx.x; u >= 0 && ok; ++n) {
-                const int T = unit_of(t, layer, u).T;
+                const int T = unit_of<kPaged>(t, layer, u).T;
                 for (int j = 0; j < T && ok; ++j) {
                     const int g2 = gt + j, s = g2 % kStages, b = g2 % kSBuf;
                     ok = mbar_wait(su32(&bars->p_full[b]), (g2 / kSBuf) & 1, abortp);
@@ -593,7 +644,9 @@ attn_partials_tc_kernel(SegTable t, int layer, const uint16_t* __restrict__ q, f
             int gt = 0;
             bool ok = true;
             for (int u = blockIdx.x, m = 0; u >= 0 && ok; ++m) {
-                const Unit U = unit_of(t, layer, u);
+                const Unit U = unit_of<kPaged>(t, layer, u);
+                int4 pid = make_int4(0, 0, 0, 0);
+                if constexpr (kPaged) pid = tile_pages(t, U, 0);
                 for (int j = 0; j < U.T; ++j, ++gt) {
                     const int s = gt % kStages;
                     if (gt >= kStages &&   // the stage is free once the P.V of tile gt - kStages completed
@@ -603,8 +656,17 @@ attn_partials_tc_kernel(SegTable t, int layer, const uint16_t* __restrict__ q, f
                     }
                     const uint32_t bar = su32(&bars->kv_full[s]);
                     mbar_expect_tx(bar, kStageB);
-                    tma_load_3d_hint(sStage + s * kStageB, U.kmap, 0, U.c0 + j * kKT, U.g, bar, once);
-                    tma_load_3d_hint(sStage + s * kStageB + kTileB, U.vmap, 0, U.c0 + j * kKT, U.g, bar, once);
+                    if constexpr (kPaged) {
+                        tile_boxes(t, U, j, pid, [&](uint32_t off, int slot, int page) {
+                            const int head = page * TF_NKV + U.g;
+                            tma_load_3d_hint(sStage + s * kStageB + off, U.kmap, 0, slot, head, bar, once);
+                            tma_load_3d_hint(sStage + s * kStageB + kTileB + off, U.vmap, 0, slot, head, bar, once);
+                        });
+                        if (j + 1 < U.T) pid = tile_pages(t, U, j + 1);
+                    } else {
+                        tma_load_3d_hint(sStage + s * kStageB, U.kmap, 0, U.c0 + j * kKT, U.g, bar, once);
+                        tma_load_3d_hint(sStage + s * kStageB + kTileB, U.vmap, 0, U.c0 + j * kKT, U.g, bar, once);
+                    }
                 }
                 if (!ok) break;
                 // the next unit of the launch, for this CTA's roles
@@ -626,7 +688,8 @@ attn_partials_tc_kernel(SegTable t, int layer, const uint16_t* __restrict__ q, f
         int gt = 0;
         bool ok = true;
         for (int u = blockIdx.x, m = 0; u >= 0 && ok; ++m) {
-            const int T = unit_of(t, layer, u).T;
+            const Unit U = unit_of<kPaged>(t, layer, u);
+            const int T = U.T;
             for (int j = 0; j < T; ++j, ++gt) {
                 const int s = gt % kStages;
                 if (!mbar_wait_warp(su32(&bars->kv_full[s]), (gt / kStages) & 1, abortp)) {
@@ -640,6 +703,14 @@ attn_partials_tc_kernel(SegTable t, int layer, const uint16_t* __restrict__ q, f
                 uint4 v[NC];
 #pragma unroll
                 for (int c = 0; c < NC; ++c) v[c] = lds128(vs + uint32_t(32 * c) * 16u);
+                if constexpr (kPaged) {   // rows past the stream's keys: whatever the page holds there, zero
+                    const int left = U.st.keys - U.c0 - j * kKT;
+                    if (left < kKT) {
+#pragma unroll
+                        for (int c = 0; c < NC; ++c)
+                            if (4 * c + (lane >> 3) >= left) v[c] = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                }
 #pragma unroll
                 for (int c = 0; c < NC; ++c) {
                     v[c].x = bf2_to_h2(v[c].x);
@@ -661,7 +732,7 @@ attn_partials_tc_kernel(SegTable t, int layer, const uint16_t* __restrict__ q, f
         int gt = 0, gph = 0;
         const uint32_t trow = tmem + (uint32_t(warp * 32) << 16);
         for (int u = blockIdx.x, m = 0; u >= 0; ++m) {
-            const Unit U = unit_of(t, layer, u);
+            const Unit U = unit_of<kPaged>(t, layer, u);
             const SegStream& st = U.st;
             const int nq = st.rows * 4, per = q_per(st.rows);
             const bool dual = per == 16;
@@ -727,13 +798,13 @@ attn_partials_tc_kernel(SegTable t, int layer, const uint16_t* __restrict__ q, f
                         t.tc_redo[1 + atomicAdd(t.tc_redo, 1)] = u;
                     if (qvalid && mode == kMergeDirect) {   // the stream's only chunk: the output itself
                         const float inv = aborted ? NAN : 1.f / lsum;   // a row always sees key 0 of its stream
-                        float4* dst = reinterpret_cast<float4*>(out_row(out, st, U.g, qi) + d0);
+                        auto* dst = out_row(out, st, U.g, qi) + d0;
 #pragma unroll
                         for (int c = 0; c < ND / 4; ++c)
-                            dst[c] = make_float4(__uint_as_float(ro[4 * c]) * inv,
-                                                 __uint_as_float(ro[4 * c + 1]) * inv,
-                                                 __uint_as_float(ro[4 * c + 2]) * inv,
-                                                 __uint_as_float(ro[4 * c + 3]) * inv);
+                            store_out4(dst + 4 * c, make_float4(__uint_as_float(ro[4 * c]) * inv,
+                                                                __uint_as_float(ro[4 * c + 1]) * inv,
+                                                                __uint_as_float(ro[4 * c + 2]) * inv,
+                                                                __uint_as_float(ro[4 * c + 3]) * inv));
                     } else if (qvalid) {
                         const int64_t rec = st.pbase + (int64_t(U.chunk) * TF_NKV + U.g) * nq + qi;
                         const bool empty = ss.mref == -INFINITY;
@@ -812,7 +883,7 @@ attn_partials_tc_kernel(SegTable t, int layer, const uint16_t* __restrict__ q, f
     __syncthreads();
     if (bars->is_last) {
         __threadfence();   // every CTA queued its units before it counted itself done
-        if (warp < 4) recompute_exact(t, layer, q, part_o, part_ml, out, full, gbase, tid);
+        if (warp < 4) recompute_exact<kPaged>(t, layer, q, part_o, part_ml, out, full, gbase, tid);
         __syncthreads();
         if (tid == 0) t.tc_redo[0] = 0;
     }
@@ -821,13 +892,16 @@ attn_partials_tc_kernel(SegTable t, int layer, const uint16_t* __restrict__ q, f
 }  // namespace
 
 int attn_tc_prepare() {
-    cudaError_t e = cudaFuncSetAttribute(attn_partials_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t e = cudaFuncSetAttribute(attn_partials_tc_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          kSmemBytes);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(attn_partials_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     return e == cudaSuccess ? TF_OK : cuda_fail(e);
 }
 
+template <bool kPaged>
 int launch_attn_partials_tc(const SegTable& t0, int layer, const uint16_t* q, float* po, float2* pml,
-                            cudaStream_t stream, float* out, int full, int grid_cap) {
+                            cudaStream_t stream, OutT<kPaged>* out, int full, int grid_cap) {
     if (!t0.k_maps || !t0.v_maps) return TF_EINVAL;
     SegTable t = t0;
     t.wait_ns = wait_limit_ns();
@@ -836,8 +910,13 @@ int launch_attn_partials_tc(const SegTable& t0, int layer, const uint16_t* q, fl
     const int grid = n_units < slots ? n_units : slots;
     CUtensorMap qmap;
     if (!encode_q_map(&qmap, q, t.R)) return cuda_fail(cudaErrorInvalidValue);
-    return launch_pdl(attn_partials_tc_kernel, dim3(grid), dim3(kThreads), kSmemBytes, stream, t, layer, q, po, pml,
-                      out, full, n_units, qmap);
+    return launch_pdl(attn_partials_tc_kernel<kPaged>, dim3(grid), dim3(kThreads), kSmemBytes, stream, t, layer, q, po,
+                      pml, out, full, n_units, qmap);
 }
+
+template int launch_attn_partials_tc<false>(const SegTable&, int, const uint16_t*, float*, float2*, cudaStream_t,
+                                            float*, int, int);
+template int launch_attn_partials_tc<true>(const SegTable&, int, const uint16_t*, float*, float2*, cudaStream_t,
+                                           uint16_t*, int, int);
 
 }  // namespace tf

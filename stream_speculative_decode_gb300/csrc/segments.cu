@@ -11,6 +11,7 @@
 #include <atomic>
 #include <cstdlib>
 #include <cstring>
+#include <memory>
 #include <mutex>
 #include <new>
 
@@ -71,6 +72,22 @@ bool encode_kv_map(CUtensorMap* out, const void* base, int keys, int cap) {
     const cuuint64_t dims[3] = {cuuint64_t(TF_D), cuuint64_t(keys), cuuint64_t(TF_NKV)};
     const cuuint64_t strides[2] = {cuuint64_t(TF_D) * 2, cuuint64_t(cap) * TF_D * 2};
     const cuuint32_t box[3] = {cuuint32_t(TF_D), 64u, 1u};
+    const cuuint32_t estr[3] = {1u, 1u, 1u};
+    CUresult r = enc(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
+// TMA map of one layer's pool of K or V pages, bf16 [n_pages][8][page_keys][64],
+// as a 3-D tensor (d, slot, page * 8 + head); a box is one head's 64 slots (or
+// the whole of a smaller page).
+bool encode_pool_map(CUtensorMap* out, const void* base, int page_keys, int n_pages) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {cuuint64_t(TF_D), cuuint64_t(page_keys), cuuint64_t(n_pages) * TF_NKV};
+    const cuuint64_t strides[2] = {cuuint64_t(TF_D) * 2, cuuint64_t(page_keys) * TF_D * 2};
+    const cuuint32_t box[3] = {cuuint32_t(TF_D), cuuint32_t(std::min(page_keys, 64)), 1u};
     const cuuint32_t estr[3] = {1u, 1u, 1u};
     CUresult r = enc(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -183,14 +200,76 @@ int plan_windows(const tf_stream* streams, int n_streams, tf_plan* out, int max_
 
 namespace {
 
+// The page side of a paged build: the caller's lists (stream after stream,
+// kv_capacity / page_keys entries each) and pools; k_cache and v_cache hold
+// one pool a layer then.
+struct Paged {
+    const int32_t* pages;
+    int32_t page_keys, n_pages;
+};
+
+// The checks of a paged build that need no look at the streams' state: page
+// size, pool size, pools set, aligned and apart (n_attn pools of K and of V).
+int check_pools(const Paged& pg, const void* const* k_pool, const void* const* v_pool, int n_attn) {
+    using namespace tf;
+    const int P = pg.page_keys;
+    if (P < TF_MIN_PAGE_KEYS || P > TF_MAX_PAGE_KEYS || (P & (P - 1)) || pg.n_pages < 1) return TF_EINVAL;
+    if (pg.n_pages > TF_MAX_PAGES) return TF_ERANGE;
+    std::vector<Interval> iv;
+    const size_t bytes = size_t(pg.n_pages) * TF_NKV * P * TF_D * 2;
+    for (int i = 0; i < 2 * n_attn; ++i) {
+        const void* p = i < n_attn ? k_pool[i] : v_pool[i - n_attn];
+        if (!p || !aligned16(p)) return TF_EINVAL;
+        const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+        iv.push_back({a, a + bytes});
+    }
+    return any_overlap(iv) ? TF_EINVAL : TF_OK;
+}
+
+// The page lists of `n` caches (their streams' rows, keys and capacity), checked
+// and laid out for the device: every id names a page of the pool, and a page
+// that holds window rows (they are appended there) occurs once in all lists.
+int lay_out_pages(const Paged& pg, const tf_stream* caches, int n, std::vector<int32_t>& ids,
+                  std::vector<int32_t>& first) {
+    const int P = pg.page_keys;
+    std::vector<int32_t> written;
+    int64_t total = 0;
+    for (int s = 0; s < n; ++s) {
+        const tf_stream& st = caches[s];
+        if (st.kv_capacity % P) return TF_EINVAL;
+        if (total + st.kv_capacity / P > TF_MAX_PAGE_IDS) return TF_ERANGE;
+        const int32_t* list = pg.pages + total;
+        const int cap = st.kv_capacity / P, used = (st.keys + P - 1) / P;
+        for (int i = 0; i < cap; ++i)
+            if (list[i] < 0 || list[i] >= pg.n_pages) return TF_EINVAL;
+        for (int i = (st.keys - st.rows) / P; i < used; ++i) written.push_back(list[i]);
+        first.push_back(int32_t(ids.size()));
+        ids.insert(ids.end(), list, list + used);
+        // whole 64-key tiles (the kernels' page reads are whole tiles), 16-byte starts
+        while ((ids.size() - first.back()) * P % 64 || ids.size() % 4) ids.push_back(ids.back());
+        total += cap;
+    }
+    std::sort(written.begin(), written.end());
+    size_t uses = 0;
+    for (int64_t i = 0; i < total; ++i)
+        uses += std::binary_search(written.begin(), written.end(), pg.pages[i]);
+    return uses == written.size() && std::adjacent_find(written.begin(), written.end()) == written.end() ? TF_OK
+                                                                                                         : TF_EINVAL;
+}
+
 // The rest of a build, shared by the verify and the prompt tables: sort the
-// attention items, lay out and upload the blob, encode the TMA maps. `seg`
-// (with its plan) is owned here from now on: freed on failure.
-int finish_build(tf_segments* seg, std::vector<tf::SegStream>& ss, std::vector<int32_t>& row_stream,
+// attention items, lay out and upload the blob, encode the TMA maps. `owned`
+// (with its plan) is freed on failure. Paged tables (pg): page_ids holds the
+// lists, page_first their starts, one a stream of the table.
+int finish_build(std::unique_ptr<tf_segments> owned, std::vector<tf::SegStream>& ss, std::vector<int32_t>& row_stream,
                  std::vector<tf::ConvTile>& tiles, std::vector<tf::AttnItem>& items,
                  const void* const* conv_state, const void* const* conv_hist, const void* const* k_cache,
-                 const void* const* v_cache, int n_conv, int n_attn, tf_cuda_stream stream, tf_segments** out) {
+                 const void* const* v_cache, int n_conv, int n_attn, tf_cuda_stream stream, tf_segments** out,
+                 const Paged* pg = nullptr, const std::vector<int32_t>* page_ids = nullptr,
+                 const std::vector<int32_t>* page_first = nullptr) {
     using namespace tf;
+    tf_segments* const seg = owned.get();
+    seg->paged = pg != nullptr;
     const int S = int(ss.size());
     const int R = int(row_stream.size());
     const tf_plan& plan = seg->plan;
@@ -239,9 +318,12 @@ int finish_build(tf_segments* seg, std::vector<tf::SegStream>& ss, std::vector<i
     const size_t o_ch = off;       off = align_up(off + (conv_hist ? sizeof(void*) * n_cp : 0), 256);
     const size_t o_k = off;        off = align_up(off + sizeof(void*) * n_ap, 256);
     const size_t o_v = off;        off = align_up(off + sizeof(void*) * n_ap, 256);
-    const size_t n_maps = size_t(n_items_mma) < items.size() ? n_ap : 0;
+    const size_t n_maps = size_t(n_items_mma) < items.size() ? (pg ? size_t(n_attn) : n_ap) : 0;
     const size_t o_km = off;       off = align_up(off + sizeof(CUtensorMap) * n_maps, 256);
     const size_t o_vm = off;       off = align_up(off + sizeof(CUtensorMap) * n_maps, 256);
+    const size_t n_ids = pg ? page_ids->size() : 0;
+    const size_t o_pg = off;       off = align_up(off + sizeof(int32_t) * n_ids, 256);
+    const size_t o_pf = off;       off = align_up(off + (pg ? sizeof(int32_t) * S : 0), 256);
     const size_t o_ctr = off;      off = align_up(off + sizeof(int32_t) * n_ap * TF_NKV, 256);
     const size_t n_groups = (size_t(S) + 127) / 128;   // Markov step: 128 streams per group
     const size_t o_mkk = off;      off = align_up(off + sizeof(unsigned long long) * S, 256);
@@ -264,18 +346,30 @@ int finish_build(tf_segments* seg, std::vector<tf::SegStream>& ss, std::vector<i
     if (!items.empty()) std::memcpy(h + o_items, items.data(), sizeof(AttnItem) * items.size());
     if (n_cp) std::memcpy(h + o_cs, conv_state, sizeof(void*) * n_cp);
     if (n_cp && conv_hist) std::memcpy(h + o_ch, conv_hist, sizeof(void*) * n_cp);
-    if (n_ap) {
+    if (n_ap && !pg) {
         std::memcpy(h + o_k, k_cache, sizeof(void*) * n_ap);
         std::memcpy(h + o_v, v_cache, sizeof(void*) * n_ap);
+    } else {   // every stream of a layer names the layer's pools
+        for (size_t i = 0; i < n_ap; ++i) {
+            std::memcpy(h + o_k + i * sizeof(void*), &k_cache[i / S], sizeof(void*));
+            std::memcpy(h + o_v + i * sizeof(void*), &v_cache[i / S], sizeof(void*));
+        }
+    }
+    if (pg) {
+        if (n_ids) std::memcpy(h + o_pg, page_ids->data(), sizeof(int32_t) * n_ids);
+        if (S) std::memcpy(h + o_pf, page_first->data(), sizeof(int32_t) * S);
     }
     for (size_t i = 0; i < n_maps; ++i) {
-        const SegStream& st = ss[i % S];
         CUtensorMap km, vm;   // aligned locals, copied into the image
-        if (!encode_kv_map(&km, k_cache[i], st.keys, st.cap) ||
-            !encode_kv_map(&vm, v_cache[i], st.keys, st.cap)) {
-            delete seg;
-            return cuda_fail(cudaErrorInvalidValue);
+        bool ok;
+        if (pg) {
+            ok = encode_pool_map(&km, k_cache[i], pg->page_keys, pg->n_pages) &&
+                 encode_pool_map(&vm, v_cache[i], pg->page_keys, pg->n_pages);
+        } else {
+            const SegStream& st = ss[i % S];
+            ok = encode_kv_map(&km, k_cache[i], st.keys, st.cap) && encode_kv_map(&vm, v_cache[i], st.keys, st.cap);
         }
+        if (!ok) return cuda_fail(cudaErrorInvalidValue);
         std::memcpy(h + o_km + i * sizeof(CUtensorMap), &km, sizeof(CUtensorMap));
         std::memcpy(h + o_vm + i * sizeof(CUtensorMap), &vm, sizeof(CUtensorMap));
     }
@@ -301,14 +395,12 @@ int finish_build(tf_segments* seg, std::vector<tf::SegStream>& ss, std::vector<i
     if (total > 0 && S > 0) {
         cudaError_t e = cudaMalloc(&seg->blob, total);
         if (e != cudaSuccess) {
-            delete seg;
             cuda_fail(e);
             return e == cudaErrorMemoryAllocation ? TF_ENOMEM : TF_ECUDA;
         }
         e = cudaMemcpyAsync(seg->blob, h, total, cudaMemcpyHostToDevice, stream);
         if (e != cudaSuccess) {
             cudaFree(seg->blob);
-            delete seg;
             return cuda_fail(e);
         }
         unsigned char* b = static_cast<unsigned char*>(seg->blob);
@@ -322,6 +414,11 @@ int finish_build(tf_segments* seg, std::vector<tf::SegStream>& ss, std::vector<i
         t.v_cache = reinterpret_cast<const void* const*>(b + o_v);
         t.k_maps = n_maps ? reinterpret_cast<const CUtensorMap*>(b + o_km) : nullptr;
         t.v_maps = n_maps ? reinterpret_cast<const CUtensorMap*>(b + o_vm) : nullptr;
+        if (pg) {
+            t.pages = reinterpret_cast<const int32_t*>(b + o_pg);
+            t.page_first = reinterpret_cast<const int32_t*>(b + o_pf);
+            while ((1 << t.page_shift) < pg->page_keys) ++t.page_shift;
+        }
         t.counters = reinterpret_cast<int32_t*>(b + o_ctr);   // zero in the image
         t.mk_keys = reinterpret_cast<unsigned long long*>(b + o_mkk);   // zero in the image
         t.mk_flags = reinterpret_cast<uint32_t*>(b + o_mkf);
@@ -357,11 +454,10 @@ int finish_build(tf_segments* seg, std::vector<tf::SegStream>& ss, std::vector<i
         }
         if (rc != TF_OK) {
             cudaFree(seg->blob);
-            delete seg;
             return rc;
         }
     }
-    *out = seg;
+    *out = owned.release();
     return TF_OK;
 }
 
@@ -378,10 +474,14 @@ int tf_segments_plan(const tf_stream* streams, int n_streams, tf_plan* out) {
     return tf::plan_windows(streams, n_streams, out, TF_MAX_ROWS);
 }
 
-int tf_segments_build(const tf_stream* streams, int n_streams,
-                      const void* const* conv_state, const void* const* conv_hist,
-                      const void* const* k_cache, const void* const* v_cache,
-                      int n_conv, int n_attn, tf_cuda_stream stream, tf_segments** out) {
+}  // extern "C"
+
+namespace {
+
+// tf_segments_build and (pg) tf_paged_build.
+int build_verify(const tf_stream* streams, int n_streams, const void* const* conv_state, const void* const* conv_hist,
+                 const void* const* k_cache, const void* const* v_cache, int n_conv, int n_attn, tf_cuda_stream stream,
+                 tf_segments** out, const Paged* pg) {
     using namespace tf;
     if (!out) return TF_EINVAL;
     *out = nullptr;
@@ -392,6 +492,13 @@ int tf_segments_build(const tf_stream* streams, int n_streams,
     const int S = n_streams;
     if (S > 0 && n_conv > 0 && !conv_state) return TF_EINVAL;
     if (S > 0 && n_attn > 0 && (!k_cache || !v_cache)) return TF_EINVAL;
+    std::vector<int32_t> page_ids, page_first;
+    if (pg && S > 0) {
+        if (!pg->pages) return TF_EINVAL;
+        rc = check_pools(*pg, k_cache, v_cache, n_attn);
+        if (rc == TF_OK) rc = lay_out_pages(*pg, streams, S, page_ids, page_first);
+        if (rc != TF_OK) return rc;
+    }
 
     // ---- pointer checks: non-null, 16-byte aligned, no two buffers overlap
     std::vector<Interval> conv_iv, kv_iv;
@@ -413,7 +520,7 @@ int tf_segments_build(const tf_stream* streams, int n_streams,
             }
         }
     }
-    for (int l = 0; l < n_attn; ++l) {
+    for (int l = 0; l < (pg ? 0 : n_attn); ++l) {
         for (int s = 0; s < S; ++s) {
             const void* k = k_cache[size_t(l) * S + s];
             const void* v = v_cache[size_t(l) * S + s];
@@ -426,8 +533,7 @@ int tf_segments_build(const tf_stream* streams, int n_streams,
     }
     if (any_overlap(conv_iv) || any_overlap(kv_iv)) return TF_EINVAL;
 
-    tf_segments* seg = new (std::nothrow) tf_segments();
-    if (!seg) return TF_ENOMEM;
+    auto seg = std::make_unique<tf_segments>();
     seg->plan = plan;
     const int R = plan.n_rows;
 
@@ -456,13 +562,14 @@ int tf_segments_build(const tf_stream* streams, int n_streams,
             tiles.push_back({s, r0, std::min(kConvTileRows, st.rows - r0), 0});
         for (int c = 0; c < d.n_chunks; ++c) items.push_back({s, c, 0, 0});
     }
-    return finish_build(seg, ss, row_stream, tiles, items, conv_state, conv_hist, k_cache, v_cache, n_conv, n_attn,
-                        stream, out);
+    return finish_build(std::move(seg), ss, row_stream, tiles, items, conv_state, conv_hist, k_cache, v_cache, n_conv,
+                        n_attn, stream, out, pg, &page_ids, &page_first);
 }
 
-int tf_prompt_build(int32_t rows, int32_t keys, int32_t kv_capacity, const void* const* conv_state,
-                    const void* const* k_cache, const void* const* v_cache, int n_conv, int n_attn,
-                    tf_cuda_stream stream, tf_segments** out) {
+// tf_prompt_build and (pg) tf_paged_prompt_build.
+int build_prompt(int32_t rows, int32_t keys, int32_t kv_capacity, const void* const* conv_state,
+                 const void* const* k_cache, const void* const* v_cache, int n_conv, int n_attn,
+                 tf_cuda_stream stream, tf_segments** out, const Paged* pg) {
     using namespace tf;
     if (!out) return TF_EINVAL;
     *out = nullptr;
@@ -470,6 +577,14 @@ int tf_prompt_build(int32_t rows, int32_t keys, int32_t kv_capacity, const void*
     if (rows < 1 || keys < rows || kv_capacity < keys) return TF_EINVAL;
     if (rows > TF_MAX_PROMPT_ROWS || kv_capacity > TF_MAX_KEYS) return TF_ERANGE;
     if ((n_conv > 0 && !conv_state) || (n_attn > 0 && (!k_cache || !v_cache))) return TF_EINVAL;
+    std::vector<int32_t> page_ids, page_first;
+    if (pg) {   // one cache: one list, which every window of the table shares
+        if (!pg->pages) return TF_EINVAL;
+        const tf_stream cache = {rows, 0, keys, kv_capacity};
+        int rc = check_pools(*pg, k_cache, v_cache, n_attn);
+        if (rc == TF_OK) rc = lay_out_pages(*pg, &cache, 1, page_ids, page_first);
+        if (rc != TF_OK) return rc;
+    }
     std::vector<Interval> conv_iv, kv_iv;
     for (int l = 0; l < n_conv; ++l) {
         const void* p = conv_state[l];
@@ -478,7 +593,7 @@ int tf_prompt_build(int32_t rows, int32_t keys, int32_t kv_capacity, const void*
         conv_iv.push_back({a, a + size_t(2) * TF_H * 2});
     }
     const size_t kv_bytes = size_t(TF_NKV) * kv_capacity * TF_D * 2;
-    for (int l = 0; l < n_attn; ++l) {
+    for (int l = 0; l < (pg ? 0 : n_attn); ++l) {
         const void* k = k_cache[l];
         const void* v = v_cache[l];
         if (!k || !v || !aligned16(k) || !aligned16(v)) return TF_EINVAL;
@@ -504,10 +619,10 @@ int tf_prompt_build(int32_t rows, int32_t keys, int32_t kv_capacity, const void*
     plan.n_streams = 1;
     plan.n_conv_tiles = (rows + kConvTileRows - 1) / kConvTileRows;
 
-    tf_segments* seg = new (std::nothrow) tf_segments();
-    if (!seg) return TF_ENOMEM;
+    auto seg = std::make_unique<tf_segments>();
     seg->plan = plan;
     seg->prompt = true;
+    page_first.resize(pg ? S : 0, 0);
     std::vector<SegStream> ss(S);
     std::vector<int32_t> row_stream(rows);
     std::vector<ConvTile> tiles;
@@ -537,13 +652,68 @@ int tf_prompt_build(int32_t rows, int32_t keys, int32_t kv_capacity, const void*
     std::vector<const void*> cs(size_t(n_conv) * S), kc(size_t(n_attn) * S), vc(size_t(n_attn) * S);
     for (int l = 0; l < n_conv; ++l)
         for (int s = 0; s < S; ++s) cs[size_t(l) * S + s] = conv_state[l];
-    for (int l = 0; l < n_attn; ++l)
+    for (int l = 0; l < (pg ? 0 : n_attn); ++l)
         for (int s = 0; s < S; ++s) {
             kc[size_t(l) * S + s] = k_cache[l];
             vc[size_t(l) * S + s] = v_cache[l];
         }
-    return finish_build(seg, ss, row_stream, tiles, items, n_conv ? cs.data() : nullptr, nullptr,
-                        n_attn ? kc.data() : nullptr, n_attn ? vc.data() : nullptr, n_conv, n_attn, stream, out);
+    return finish_build(std::move(seg), ss, row_stream, tiles, items, n_conv ? cs.data() : nullptr, nullptr,
+                        pg ? k_cache : n_attn ? kc.data() : nullptr, pg ? v_cache : n_attn ? vc.data() : nullptr,
+                        n_conv, n_attn, stream, out, pg, &page_ids, &page_first);
+}
+
+// A build runs out of host memory: TF_ENOMEM, no exception past the C entry.
+template <typename F>
+int guarded(F&& build) {
+    try {
+        return build();
+    } catch (...) {
+        return TF_ENOMEM;
+    }
+}
+
+}  // namespace
+
+extern "C" {
+
+int tf_segments_build(const tf_stream* streams, int n_streams,
+                      const void* const* conv_state, const void* const* conv_hist,
+                      const void* const* k_cache, const void* const* v_cache,
+                      int n_conv, int n_attn, tf_cuda_stream stream, tf_segments** out) {
+    return guarded([&] {
+        return build_verify(streams, n_streams, conv_state, conv_hist, k_cache, v_cache, n_conv, n_attn, stream, out,
+                            nullptr);
+    });
+}
+
+int tf_prompt_build(int32_t rows, int32_t keys, int32_t kv_capacity, const void* const* conv_state,
+                    const void* const* k_cache, const void* const* v_cache, int n_conv, int n_attn,
+                    tf_cuda_stream stream, tf_segments** out) {
+    return guarded([&] {
+        return build_prompt(rows, keys, kv_capacity, conv_state, k_cache, v_cache, n_conv, n_attn, stream, out,
+                            nullptr);
+    });
+}
+
+int tf_paged_build(const tf_stream* streams, int n_streams, const void* const* conv_state,
+                   const void* const* conv_hist, const int32_t* pages, int32_t page_keys, int32_t n_pages,
+                   const void* const* k_pool, const void* const* v_pool, int n_conv, int n_attn,
+                   tf_cuda_stream stream, tf_segments** out) {
+    return guarded([&] {
+        const Paged pg = {pages, page_keys, n_pages};
+        return build_verify(streams, n_streams, conv_state, conv_hist, k_pool, v_pool, n_conv, n_attn, stream, out,
+                            &pg);
+    });
+}
+
+int tf_paged_prompt_build(int32_t rows, int32_t keys, int32_t kv_capacity, const void* const* conv_state,
+                          const int32_t* pages, int32_t page_keys, int32_t n_pages, const void* const* k_pool,
+                          const void* const* v_pool, int n_conv, int n_attn, tf_cuda_stream stream,
+                          tf_segments** out) {
+    return guarded([&] {
+        const Paged pg = {pages, page_keys, n_pages};
+        return build_prompt(rows, keys, kv_capacity, conv_state, k_pool, v_pool, n_conv, n_attn, stream, out, &pg);
+    });
 }
 
 int tf_segments_free(tf_segments* seg) {

@@ -7,6 +7,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <stdint.h>
+#include <type_traits>
 #include <vector>
 
 #include "../../include/tf.h"
@@ -89,7 +90,15 @@ struct SegTable {
     cudaStream_t side;
     cudaEvent_t ev_fork, ev_join;
     int32_t tc_grid_mixed;
-    int32_t pad3_;
+    // Paged tables (tf_paged_build, tf_paged_prompt_build): key t of stream s
+    // is slot t % 2^page_shift of page pages[page_first[s] + (t >> page_shift)]
+    // of the layer's pools; k_cache / v_cache name the layer's pools, and
+    // k_maps / v_maps hold one map a layer. Every list starts at a multiple of 4
+    // entries and is padded to whole 64-key tiles with its last page.
+    // page_shift is 0 in a table of dense caches.
+    int32_t page_shift;
+    const int32_t* pages;
+    const int32_t* page_first;        // [S]
 };
 
 // The Markov chain's scratch: 64 words of barrier state, then three
@@ -126,6 +135,7 @@ struct tf_segments {
     std::vector<tf::SegStream> streams;
     tf_plan plan{};
     bool prompt = false;               // built by tf_prompt_build (conv + attention only)
+    bool paged = false;                // built by tf_paged_build / tf_paged_prompt_build
     size_t scratch_off = 0;            // the blob's cross-CTA scratch and status word:
     size_t scratch_bytes = 0;          // zero in the image, zeroed again by tf_segments_status
 };
@@ -189,14 +199,20 @@ int launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cud
 // With out != nullptr the partials kernels also finish the streams whose
 // merge_mode is kMergeDirect or kMergeLastCta (the one-call form). full != 0:
 // the drafter's non-causal block form, every window row seeing all keys.
+// kPaged: a paged table's kernels; they write bf16 outputs (OutT).
+template <bool kPaged>
+using OutT = std::conditional_t<kPaged, uint16_t, float>;
+template <bool kPaged = false>
 int launch_attn_partials(const SegTable& t, int layer, const uint16_t* q, float* po, float2* pml,
-                         cudaStream_t stream, float* out = nullptr, int full = 0);
-int launch_attn_merge(const SegTable& t, const float* po, const float2* pml, float* out, cudaStream_t stream,
+                         cudaStream_t stream, OutT<kPaged>* out = nullptr, int full = 0);
+template <bool kPaged = false>
+int launch_attn_merge(const SegTable& t, const float* po, const float2* pml, OutT<kPaged>* out, cudaStream_t stream,
                       bool kernel_mode_only = false);
 
 // attn_tc.cu: the tensor-core partials kernel (same records as the mma.sync kernel).
+template <bool kPaged>
 int launch_attn_partials_tc(const SegTable& t, int layer, const uint16_t* q, float* po, float2* pml,
-                            cudaStream_t stream, float* out, int full,
+                            cudaStream_t stream, OutT<kPaged>* out, int full,
                             int grid = 0);   // items [n_items_mma, n_items); grid 0: two CTAs per SM
 int attn_tc_prepare();
 
@@ -228,8 +244,18 @@ __device__ __forceinline__ uint32_t absmax_bf2(uint32_t a, uint32_t b) {
 __device__ __forceinline__ bool v_tile_exact(uint32_t m) { return m >= 0x4780u || m < 0x3C80u; }
 
 // Output address of query row qi (window row qi/4, head 4g + qi%4) of a stream.
-__device__ __forceinline__ float* out_row(float* out, const SegStream& st, int g, int qi) {
+template <typename O>
+__device__ __forceinline__ O* out_row(O* out, const SegStream& st, int g, int qi) {
     return out + (size_t(st.row_offset + (qi >> 2)) * TF_NQ + 4 * g + (qi & 3)) * TF_D;
+}
+// Four consecutive dimensions of an output row: fp32, or (paged tables) one
+// rounding of the finished fp32 value to bf16, the type the next projection
+// reads.
+__device__ __forceinline__ void store_out4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void store_out4(uint16_t* p, float4 v) {
+    __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+    *reinterpret_cast<uint2*>(p) =
+        make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
 }
 
 // Log-sum-exp merge of the chunk records of one (stream, KV head) into the
@@ -238,9 +264,9 @@ __device__ __forceinline__ float* out_row(float* out, const SegStream& st, int g
 // dimensions) items at once and issues all their loads before using any
 // (kU = 1: one item at a time). The records were written by other CTAs: they
 // are read through L2 (ld.global.cg).
-template <int kB, int kU = 1>   // records in flight per item, items per thread at once
+template <int kB, int kU = 1, typename O>   // records in flight per item, items per thread at once
 __device__ __forceinline__ void merge_stream_head(const SegStream& st, int g, const float* part_o,
-                                                  const float2* part_ml, float* out, int tid, int nthreads) {
+                                                  const float2* part_ml, O* out, int tid, int nthreads) {
     const int nq = st.rows * 4;
     const int n_items = nq * (TF_D / 4);
     const int64_t stride = int64_t(TF_NKV) * nq;
@@ -305,8 +331,8 @@ __device__ __forceinline__ void merge_stream_head(const SegStream& st, int g, co
             if (idx < n_items) {
                 const int qi = idx >> 4, d4 = (idx & 15) * 4;
                 const float inv = 1.f / L[u];
-                *reinterpret_cast<float4*>(out_row(out, st, g, qi) + d4) =
-                    make_float4(acc[u].x * inv, acc[u].y * inv, acc[u].z * inv, acc[u].w * inv);
+                store_out4(out_row(out, st, g, qi) + d4,
+                           make_float4(acc[u].x * inv, acc[u].y * inv, acc[u].z * inv, acc[u].w * inv));
             }
         }
     }
@@ -316,9 +342,9 @@ __device__ __forceinline__ void merge_stream_head(const SegStream& st, int g, co
 // CTA of (stream, KV head) counts its arrival after its records are visible;
 // the last one merges and resets the counter for the next launch. All threads
 // of the CTA call this.
-template <int kB = 8>
+template <int kB = 8, typename O>
 __device__ __forceinline__ void finish_last_cta(const SegTable& t, int layer, int s, const SegStream& st, int g,
-                                                const float* part_o, const float2* part_ml, float* out,
+                                                const float* part_o, const float2* part_ml, O* out,
                                                 int* smem_flag) {
     __threadfence();
     __syncthreads();

@@ -9,6 +9,7 @@ Build the library with ``python -m stream_speculative_decode_gb300.build`` (or
 ``__graft_entry__.build()``).
 """
 
+import array
 import ctypes
 import os
 
@@ -22,6 +23,8 @@ TF_MAX_STREAMS = 65536
 TF_MAX_PROMPT_ROWS = 65536
 TF_PROMPT_WINDOW_ROWS = 32
 TF_MK = 256
+TF_MIN_PAGE_KEYS, TF_MAX_PAGE_KEYS = 16, 256
+TF_MAX_PAGES, TF_MAX_PAGE_IDS = 1 << 24, 1 << 28
 TF_DFLAG_BAD_PENDING, TF_DFLAG_BAD_DRAFT = 1, 2
 TF_OK, TF_EINVAL, TF_ERANGE, TF_ENOMEM, TF_ECUDA, TF_ETIMEOUT = 0, 1, 2, 3, 4, 5
 TF_WAIT_LIMIT_DEFAULT_NS = 2000000000
@@ -34,7 +37,7 @@ EXPORTS = ("tf_chunk_keys", "tf_segments_plan", "tf_segments_build", "tf_segment
            "tf_attn_merge", "tf_attn", "tf_attn_static", "tf_attn_block_partials", "tf_attn_block",
            "tf_argmax_rows", "tf_accept", "tf_markov_chain", "tf_draft_ids", "tf_prompt_build",
            "tf_strerror", "tf_last_cuda_error", "tf_set_wait_limit_ns", "tf_wait_limit_ns",
-           "tf_segments_status")
+           "tf_segments_status", "tf_paged_build", "tf_paged_prompt_build", "tf_attn_paged")
 TF_STATIC_SCRATCH_BYTES = 16 << 20
 
 
@@ -85,6 +88,11 @@ def _load():
         "tf_attn": (i32, [vp, i32, vp, vp, vp, vp]),
         "tf_attn_block_partials": (i32, [vp, i32, vp, vp, vp]),
         "tf_attn_block": (i32, [vp, i32, vp, vp, vp, vp]),
+        "tf_paged_build": (i32, [P(tf_stream), i32, P(vp), P(vp), P(ctypes.c_int32), ctypes.c_int32, ctypes.c_int32,
+                                 P(vp), P(vp), i32, i32, vp, P(vp)]),
+        "tf_paged_prompt_build": (i32, [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, P(vp), P(ctypes.c_int32),
+                                        ctypes.c_int32, ctypes.c_int32, P(vp), P(vp), i32, i32, vp, P(vp)]),
+        "tf_attn_paged": (i32, [vp, i32, vp, vp, vp, i32, vp]),
         "tf_markov_chain": (i32, [vp, vp, vp, i32, vp, i64, vp, vp, vp, vp]),
         "tf_draft_ids": (i32, [vp, vp, vp, vp, i32, vp, vp, vp]),
         "tf_argmax_rows": (i32, [vp, i32, i32, i64, vp, vp, vp]),
@@ -221,6 +229,67 @@ def tf_prompt_build(rows, keys, kv_capacity, conv_state, k_cache, v_cache, n_con
     return Segments(handle)
 
 
+def _int32_array(x, n=None):
+    """A host int32 array for the library: a contiguous numpy int32 array or CPU
+    torch tensor is passed as it is, any other sequence is copied. ``n``: the
+    entries the call will read."""
+    if x is None:
+        return None
+    if hasattr(x, "numpy"):
+        if x.device.type != "cpu":
+            raise ValueError("a host array is needed, not a device tensor")
+        x = x.numpy()
+    if not (hasattr(x, "ctypes") and x.dtype.name == "int32" and x.flags.c_contiguous):
+        x = array.array("i", (int(v) for v in x))
+        size, ptr = len(x), (ctypes.c_int32 * max(len(x), 1)).from_buffer(x if len(x) else array.array("i", [0]))
+    else:
+        size, ptr = x.size, x.ctypes.data_as(ctypes.POINTER(ctypes.c_int32))
+    if n is not None and size < n:
+        raise ValueError(f"{size} entries where the call reads {n}")
+    return ptr
+
+
+def tf_paged_build_status(streams, conv_state, conv_hist, pages, page_keys, n_pages, k_pool, v_pool, n_conv, n_attn,
+                          stream=None):
+    """Raw status and handle of tf_paged_build; ``pages``: the streams' page ids
+    one after another, ``k_pool``/``v_pool``: a pool a layer."""
+    out = ctypes.c_void_p()
+    n = sum(st[3] // page_keys for st in streams) if page_keys > 0 else 0
+    rc = _lib.tf_paged_build(_streams_array(streams), len(streams), _ptr_array(conv_state), _ptr_array(conv_hist),
+                             _int32_array(pages, n), page_keys, n_pages, _ptr_array(k_pool), _ptr_array(v_pool),
+                             n_conv, n_attn, _stream(stream), ctypes.byref(out))
+    return rc, out.value
+
+
+def tf_paged_build(streams, conv_state, conv_hist, pages, page_keys, n_pages, k_pool, v_pool, n_conv, n_attn,
+                   stream=None):
+    """A verify table whose streams keep their keys in pages of shared pools."""
+    rc, handle = tf_paged_build_status(streams, conv_state, conv_hist, pages, page_keys, n_pages, k_pool, v_pool,
+                                       n_conv, n_attn, stream)
+    _check("tf_paged_build", rc)
+    return Segments(handle)
+
+
+def tf_paged_prompt_build_status(rows, keys, kv_capacity, conv_state, pages, page_keys, n_pages, k_pool, v_pool,
+                                 n_conv, n_attn, stream=None):
+    """Raw status and handle of tf_paged_prompt_build."""
+    out = ctypes.c_void_p()
+    n = kv_capacity // page_keys if page_keys > 0 else 0
+    rc = _lib.tf_paged_prompt_build(rows, keys, kv_capacity, _ptr_array(conv_state), _int32_array(pages, n), page_keys,
+                                    n_pages, _ptr_array(k_pool), _ptr_array(v_pool), n_conv, n_attn, _stream(stream),
+                                    ctypes.byref(out))
+    return rc, out.value
+
+
+def tf_paged_prompt_build(rows, keys, kv_capacity, conv_state, pages, page_keys, n_pages, k_pool, v_pool, n_conv,
+                          n_attn, stream=None):
+    """A prompt call's table over the pages of one stream."""
+    rc, handle = tf_paged_prompt_build_status(rows, keys, kv_capacity, conv_state, pages, page_keys, n_pages, k_pool,
+                                              v_pool, n_conv, n_attn, stream)
+    _check("tf_paged_prompt_build", rc)
+    return Segments(handle)
+
+
 def tf_segments_free(seg):
     seg.free()
 
@@ -266,6 +335,13 @@ def tf_attn_block(seg, attn_layer, q, partials, out, stream=None):
     """One layer of the drafter's non-causal block attention in one call."""
     _check("tf_attn_block", _lib.tf_attn_block(_h(seg), attn_layer, _ptr(q), _ptr(partials), _ptr(out),
                                                _stream(stream)))
+
+
+def tf_attn_paged(seg, attn_layer, q, partials, out, full=False, stream=None):
+    """One attention layer over a paged table, bf16 output; ``full``: every row
+    sees all keys (the drafter's block form)."""
+    _check("tf_attn_paged", _lib.tf_attn_paged(_h(seg), attn_layer, _ptr(q), _ptr(partials), _ptr(out),
+                                               1 if full else 0, _stream(stream)))
 
 
 def tf_markov_chain(seg, W1, W2, vocab, base, base_stride, prev, pick, flag, stream=None):
