@@ -430,6 +430,35 @@ int tf_paged_prompt_build(int32_t rows, int32_t keys, int32_t kv_capacity,
 int tf_attn_paged(const tf_segments* seg, int attn_layer, const void* q, void* partials,
                   void* out, int full, tf_cuda_stream stream);
 
+/* The attention inputs of one layer from its projections, over every row of a
+ * table (dense or paged, verify or prompt): each query and key head normed and
+ * rotated, and the rows' keys and values appended to their streams' caches,
+ * where the layer's attention call reads them. It goes between the layer's
+ * projections and tf_attn / tf_attn_block / tf_attn_paged, which take q_out.
+ * Window row i of a stream has position p = keys - rows + i. For a head's 64
+ * values x with norm weight w, in fp32:
+ *   n = x * w / sqrt(mean(x^2) + eps)
+ *   y[j]    = n[j] cos(p f_j) - n[j+32] sin(p f_j)      f_j = theta^(-2j/64),
+ *   y[j+32] = n[j+32] cos(p f_j) + n[j] sin(p f_j)      j < 32 (half-split)
+ * rounded once to bf16 (angles to 2^-32 of a turn at every position). The rest
+ * of the caches is left as it is.
+ *   q   bf16, row r's TF_NQ heads at q + r*q_stride (elements)
+ *   k, v  bf16, row r's TF_NKV heads at k + r*k_stride, v + r*v_stride: the
+ *         three may be slices of one projection's rows. v is copied.
+ *   q_norm, k_norm  bf16 [TF_D], one weight for all query and all key heads
+ *   q_out  bf16 [R][TF_NQ][TF_D]; may be q itself when q_stride is
+ *          TF_NQ*TF_D. k and v must not lie in the caches.
+ * A NaN or infinity in a head spreads over that head only. Strides are
+ * multiples of 8. Calls on different layers may overlap; a call that appends
+ * to a layer must not overlap attention on that layer. Errors: TF_EINVAL
+ * (null, misaligned, stride below the row or no multiple of 8, q_out
+ * overlapping an input, eps not positive and finite, theta below 1 or not
+ * finite), TF_ERANGE (a stride beyond 2^32). */
+int tf_qk_rows(const tf_segments* seg, int attn_layer, const void* q, int64_t q_stride,
+               const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+               const void* q_norm, const void* k_norm, float eps, double theta,
+               void* q_out, tf_cuda_stream stream);
+
 /* ---- failures on the device ------------------------------------------------
  * The tensor-core attention kernel (tf_attn*, streams of 9 rows or more and
  * prompt windows) and the Markov chain (tf_markov_chain) wait on barriers

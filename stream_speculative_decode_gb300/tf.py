@@ -37,7 +37,8 @@ EXPORTS = ("tf_chunk_keys", "tf_segments_plan", "tf_segments_build", "tf_segment
            "tf_attn_merge", "tf_attn", "tf_attn_static", "tf_attn_block_partials", "tf_attn_block",
            "tf_argmax_rows", "tf_accept", "tf_markov_chain", "tf_draft_ids", "tf_prompt_build",
            "tf_strerror", "tf_last_cuda_error", "tf_set_wait_limit_ns", "tf_wait_limit_ns",
-           "tf_segments_status", "tf_paged_build", "tf_paged_prompt_build", "tf_attn_paged")
+           "tf_segments_status", "tf_paged_build", "tf_paged_prompt_build", "tf_attn_paged",
+           "tf_qk_rows")
 TF_STATIC_SCRATCH_BYTES = 16 << 20
 
 
@@ -93,6 +94,7 @@ def _load():
         "tf_paged_prompt_build": (i32, [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, P(vp), P(ctypes.c_int32),
                                         ctypes.c_int32, ctypes.c_int32, P(vp), P(vp), i32, i32, vp, P(vp)]),
         "tf_attn_paged": (i32, [vp, i32, vp, vp, vp, i32, vp]),
+        "tf_qk_rows": (i32, [vp, i32, vp, i64, vp, i64, vp, i64, vp, vp, ctypes.c_float, ctypes.c_double, vp, vp]),
         "tf_markov_chain": (i32, [vp, vp, vp, i32, vp, i64, vp, vp, vp, vp]),
         "tf_draft_ids": (i32, [vp, vp, vp, vp, i32, vp, vp, vp]),
         "tf_argmax_rows": (i32, [vp, i32, i32, i64, vp, vp, vp]),
@@ -342,6 +344,13 @@ def tf_attn_paged(seg, attn_layer, q, partials, out, full=False, stream=None):
     sees all keys (the drafter's block form)."""
     _check("tf_attn_paged", _lib.tf_attn_paged(_h(seg), attn_layer, _ptr(q), _ptr(partials), _ptr(out),
                                                1 if full else 0, _stream(stream)))
+
+
+def tf_qk_rows(seg, attn_layer, q, q_stride, k, k_stride, v, v_stride, q_norm, k_norm, eps, theta, q_out, stream=None):
+    """Norm and rotation of one layer's queries and keys, and the append of its
+    keys and values to the table's caches."""
+    _check("tf_qk_rows", _lib.tf_qk_rows(_h(seg), attn_layer, _ptr(q), q_stride, _ptr(k), k_stride, _ptr(v), v_stride,
+                                         _ptr(q_norm), _ptr(k_norm), eps, theta, _ptr(q_out), _stream(stream)))
 
 
 def tf_markov_chain(seg, W1, W2, vocab, base, base_stride, prev, pick, flag, stream=None):
