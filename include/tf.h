@@ -459,6 +459,27 @@ int tf_qk_rows(const tf_segments* seg, int attn_layer, const void* q, int64_t q_
                const void* q_norm, const void* k_norm, float eps, double theta,
                void* q_out, tf_cuda_stream stream);
 
+/* Copies between pages of paged pools, in every given pool alike: keys
+ * [0, keys[i]) of page src[i] to page dst[i], i < n_copies. For a fork (the
+ * child's own copy of the parent's partly filled last page, before either
+ * appends to it) and for moving pages (a compaction).
+ *   pools   host array [n_pools] of device pointers, each a bf16 pool
+ *           [n_pages][TF_NKV][page_keys][TF_D] (the K and V pools of any layers)
+ *   src, dst  host arrays [n_copies] of page ids in [0, n_pages). A page may be
+ *           a source several times; a destination is no other copy's source or
+ *           destination (the copies run in no order). Chained moves take
+ *           several calls.
+ *   keys    host array [n_copies], 0..page_keys each, or NULL for whole pages;
+ *           the rest of a destination page is left as it is
+ * The lists are read before the call returns and travel with the launches, so
+ * a captured graph repeats them. Errors: TF_EINVAL (null, misaligned or
+ * overlapping pools, a bad page size, an id or a key count out of range, a
+ * destination used twice or read), TF_ERANGE (n_pages > TF_MAX_PAGES, more
+ * than 8,192 pools), TF_ENOMEM (host memory). */
+int tf_pages_copy(void* const* pools, int n_pools, int32_t page_keys, int32_t n_pages,
+                  const int32_t* src, const int32_t* dst, const int32_t* keys,
+                  int n_copies, tf_cuda_stream stream);
+
 /* ---- failures on the device ------------------------------------------------
  * The tensor-core attention kernel (tf_attn*, streams of 9 rows or more and
  * prompt windows) and the Markov chain (tf_markov_chain) wait on barriers

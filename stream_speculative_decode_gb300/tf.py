@@ -38,7 +38,7 @@ EXPORTS = ("tf_chunk_keys", "tf_segments_plan", "tf_segments_build", "tf_segment
            "tf_argmax_rows", "tf_accept", "tf_markov_chain", "tf_draft_ids", "tf_prompt_build",
            "tf_strerror", "tf_last_cuda_error", "tf_set_wait_limit_ns", "tf_wait_limit_ns",
            "tf_segments_status", "tf_paged_build", "tf_paged_prompt_build", "tf_attn_paged",
-           "tf_qk_rows")
+           "tf_qk_rows", "tf_pages_copy")
 TF_STATIC_SCRATCH_BYTES = 16 << 20
 
 
@@ -95,6 +95,8 @@ def _load():
                                         ctypes.c_int32, ctypes.c_int32, P(vp), P(vp), i32, i32, vp, P(vp)]),
         "tf_attn_paged": (i32, [vp, i32, vp, vp, vp, i32, vp]),
         "tf_qk_rows": (i32, [vp, i32, vp, i64, vp, i64, vp, i64, vp, vp, ctypes.c_float, ctypes.c_double, vp, vp]),
+        "tf_pages_copy": (i32, [P(vp), i32, ctypes.c_int32, ctypes.c_int32, P(ctypes.c_int32), P(ctypes.c_int32),
+                                P(ctypes.c_int32), i32, vp]),
         "tf_markov_chain": (i32, [vp, vp, vp, i32, vp, i64, vp, vp, vp, vp]),
         "tf_draft_ids": (i32, [vp, vp, vp, vp, i32, vp, vp, vp]),
         "tf_argmax_rows": (i32, [vp, i32, i32, i64, vp, vp, vp]),
@@ -344,6 +346,14 @@ def tf_attn_paged(seg, attn_layer, q, partials, out, full=False, stream=None):
     sees all keys (the drafter's block form)."""
     _check("tf_attn_paged", _lib.tf_attn_paged(_h(seg), attn_layer, _ptr(q), _ptr(partials), _ptr(out),
                                                1 if full else 0, _stream(stream)))
+
+
+def tf_pages_copy(pools, page_keys, n_pages, src, dst, keys=None, stream=None):
+    """Copy keys [0, keys[i]) (all of them without ``keys``) of page src[i] to
+    page dst[i] in every pool."""
+    n = len(src)
+    _check("tf_pages_copy", _lib.tf_pages_copy(_ptr_array(pools), len(pools), page_keys, n_pages, _int32_array(src, n),
+                                               _int32_array(dst, n), _int32_array(keys, n), n, _stream(stream)))
 
 
 def tf_qk_rows(seg, attn_layer, q, q_stride, k, k_stride, v, v_stride, q_norm, k_norm, eps, theta, q_out, stream=None):
