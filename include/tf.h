@@ -280,6 +280,44 @@ int tf_attn_static(const tf_segments* seg, int attn_layer, const void* q, float*
 int tf_argmax_rows(const void* logits, int R, int V, int64_t row_stride,
                    int32_t* pick, uint8_t* flag, tf_cuda_stream stream);
 
+/* Sampled pick of each row of bf16 logits, for rows that a temperature draws
+ * instead of tf_argmax_rows' greedy pick; the picks and flags go to tf_accept
+ * in the same way (a draft is accepted where the target's draw equals it, so a
+ * drafted reply is distributed as an undrafted one). Per row, with its own
+ * settings:
+ *   - tokens in order of (logit descending, id ascending; -0 equals +0), each
+ *     of weight w = exp((x - max) / T);
+ *   - top-k keeps the first top_k tokens, of mass Z;
+ *   - top-p keeps the shortest prefix of mass at least top_p * Z (one token at
+ *     least), min-p the tokens of w >= min_p; the kept tokens are the shortest
+ *     prefix of the three;
+ *   - the pick is the first token at which the cumulative mass exceeds u times
+ *     the mass of the kept tokens.
+ * T == 0 picks the first token (the greedy pick). Masses are exact to 64-bit
+ * fixed point, so a pick equals the float64 definition's except where u lies
+ * within about 1e-12 of a border.
+ *   logits      as in tf_argmax_rows; -Inf is a masked token (never picked)
+ *   temperature float [R] or NULL (1); 0 <= T < inf
+ *   top_k       int32 [R] or NULL; off where <= 0 or >= V
+ *   top_p       float [R] or NULL; off where >= 1; <= 0 keeps one token
+ *   min_p       float [R] or NULL; off where <= 0; at most 1
+ *   u           float [R] in [0, 1)
+ *   pick        int32 [R]; -1 when the row is flagged
+ *   prob        float [R] or NULL: w of the pick over the kept mass (1 when
+ *               T == 0, 0 when flagged)
+ *   flag        uint8 [R]: TF_SAMPLE_NO_LOGITS a NaN or +Inf in the row, or
+ *               every token masked; TF_SAMPLE_BAD_SETTING a setting outside
+ *               its range or NaN
+ * Needs no table. R == 0 is a no-op. Errors: TF_EINVAL (null, V < 1,
+ * row_stride < V), TF_ERANGE (V > TF_SAMPLE_MAX_VOCAB, R > 2^24). */
+#define TF_SAMPLE_MAX_VOCAB (1 << 19)
+#define TF_SAMPLE_NO_LOGITS   1
+#define TF_SAMPLE_BAD_SETTING 2
+int tf_sample_rows(const void* logits, int R, int V, int64_t row_stride,
+                   const float* temperature, const int32_t* top_k, const float* top_p,
+                   const float* min_p, const float* u, int32_t* pick, float* prob,
+                   uint8_t* flag, tf_cuda_stream stream);
+
 /* a5. Greedy verify of every stream: the accepted-draft prefix length
  * ([DSP]: the target verifies every draft; [SRD] verifyFn takes the pick
  * for greedy rows, flagged rows are drawn on the host).

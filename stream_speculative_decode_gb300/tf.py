@@ -25,6 +25,8 @@ TF_PROMPT_WINDOW_ROWS = 32
 TF_MK = 256
 TF_MIN_PAGE_KEYS, TF_MAX_PAGE_KEYS = 16, 256
 TF_MAX_PAGES, TF_MAX_PAGE_IDS = 1 << 24, 1 << 28
+TF_SAMPLE_MAX_VOCAB = 1 << 19
+TF_SAMPLE_NO_LOGITS, TF_SAMPLE_BAD_SETTING = 1, 2
 TF_DFLAG_BAD_PENDING, TF_DFLAG_BAD_DRAFT = 1, 2
 TF_OK, TF_EINVAL, TF_ERANGE, TF_ENOMEM, TF_ECUDA, TF_ETIMEOUT = 0, 1, 2, 3, 4, 5
 TF_WAIT_LIMIT_DEFAULT_NS = 2000000000
@@ -38,7 +40,7 @@ EXPORTS = ("tf_chunk_keys", "tf_segments_plan", "tf_segments_build", "tf_segment
            "tf_argmax_rows", "tf_accept", "tf_markov_chain", "tf_draft_ids", "tf_prompt_build",
            "tf_strerror", "tf_last_cuda_error", "tf_set_wait_limit_ns", "tf_wait_limit_ns",
            "tf_segments_status", "tf_paged_build", "tf_paged_prompt_build", "tf_attn_paged",
-           "tf_qk_rows", "tf_pages_copy")
+           "tf_qk_rows", "tf_pages_copy", "tf_sample_rows")
 TF_STATIC_SCRATCH_BYTES = 16 << 20
 
 
@@ -100,6 +102,7 @@ def _load():
         "tf_markov_chain": (i32, [vp, vp, vp, i32, vp, i64, vp, vp, vp, vp]),
         "tf_draft_ids": (i32, [vp, vp, vp, vp, i32, vp, vp, vp]),
         "tf_argmax_rows": (i32, [vp, i32, i32, i64, vp, vp, vp]),
+        "tf_sample_rows": (i32, [vp, i32, i32, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp]),
         "tf_accept": (i32, [vp, vp, vp, vp, i32, vp, vp, vp, vp, i32, vp]),
         "tf_strerror": (ctypes.c_char_p, [i32]),
         "tf_last_cuda_error": (i32, []),
@@ -378,6 +381,14 @@ def tf_draft_ids(seg, prev, drafts, draft_flag, vocab, ids, dflag, stream=None):
 
 def tf_argmax_rows(logits, R, V, row_stride, pick, flag, stream=None):
     _check("tf_argmax_rows", _lib.tf_argmax_rows(_ptr(logits), R, V, row_stride, _ptr(pick), _ptr(flag),
+                                                 _stream(stream)))
+
+
+def tf_sample_rows(logits, R, V, row_stride, temperature, top_k, top_p, min_p, u, pick, prob, flag, stream=None):
+    """A draw from each row of logits by its uniform number; any of temperature,
+    top_k, top_p, min_p and prob may be None."""
+    _check("tf_sample_rows", _lib.tf_sample_rows(_ptr(logits), R, V, row_stride, _ptr(temperature), _ptr(top_k),
+                                                 _ptr(top_p), _ptr(min_p), _ptr(u), _ptr(pick), _ptr(prob), _ptr(flag),
                                                  _stream(stream)))
 
 
