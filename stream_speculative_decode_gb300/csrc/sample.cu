@@ -13,25 +13,45 @@
 // are integers (a histogram in shared memory, so the order of its atomics does
 // not matter) and the weights are 64-bit fixed point. Masses of up to V tokens
 // of weight 1 fit 64 bits at 63 - log2(V) fraction bits (46 at V = 128,000: a
-// weight is off by at most 2^-47 of the largest).
+// weight is off by about 2^-46 of the largest).
 //
-// Values are handled as signed magnitudes (key = +-(bits & 0x7FFF), so -0 is
-// +0 and keys rise with values), in windows of 4,096 keys from the largest key
-// down; a window covers 32 powers of two, so N(0, 3) logits take two.
+// One pass over a row: its tokens are counted as they arrive, in a folded
+// window of both signs' magnitudes (2^-33, 128) and zero, which needs no maximum
+// first; the largest occupied value is the maximum. A row with any other finite
+// value (one N(0, 3) row in 250,000) is counted again in windows of 10,240
+// consecutive values from its largest down. A second pass, from L2, finds the
+// picked value's j-th token.
+//
+// A row is shared by a cluster of 1 to 8 CTAs. Each counts a part of the
+// tokens, then sums one slice of the sorted values over the cluster
+// (distributed shared memory), weighs it, and every CTA learns the slices'
+// totals: all of them follow the same steps with the same numbers.
 #include <cmath>
 
+#include <cooperative_groups.h>
+
 #include "tf_internal.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace tf {
 namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kWindow = 4096;                    // keys of a window
-constexpr int kBins = kWindow / kThreads;        // keys of a window a thread scans
-constexpr int kMaxWindows = 2 * 0x7F80 / kWindow + 2;
+constexpr int kUnroll = 4;                       // 16-byte loads a thread asks for at a time, counting
+constexpr int kSearch = 4;                       // and searching
+constexpr int kSide = 5120;                      // positions a side of the sorted window
+constexpr int kTopMag = 0x42FF;                  // the folded window's largest magnitude, just below 128
+constexpr int kLowMag = kTopMag - kSide + 2;     // and its smallest, just above 2^-33: kSide - 1 of them
+constexpr int kValues = 2 * kSide;               // sorted positions of a window
+constexpr int kGroup = 8;                        // of which a thread weighs so many at a time
+constexpr int kMaxWindows = 2 * 0x7F80 / kValues + 2;
 constexpr int kMinKey = -0x7F80;                 // the key of -infinity: a masked token
 constexpr int kInfKey = 0x7F80;
+constexpr int kBadKey = 0x10000;                 // stands for a NaN or +infinity
+constexpr int kMaxCluster = 8;
+static_assert((kLowMag - 1) % 128 == 0 && kSide % kGroup == 0 && kValues % (kGroup * kMaxCluster) == 0 && kSide <= 8192, "");
 
 using u64 = unsigned long long;
 
@@ -65,22 +85,24 @@ constexpr ExpTables make_tables() {
 }
 __device__ const ExpTables kExpTables = make_tables();
 
-// 2^-y in units of 2^-frac, y >= 0: the integer part shifts, the next two
-// groups of six bits look up, and the rest, r < 2^-12, is 1 - a + a^2/2 - a^3/6
-// with a = r ln 2 (the next term is below 2^-54).
-__device__ __forceinline__ u64 weight(double y, int frac, const ExpTables& tab) {
-    if (!(y < 62.0)) return 0;
-    const u64 fx = __double2ull_rz(y * 0x1p52);
-    const int n = int(fx >> 52);
-    const u64 c = tab.coarse[(fx >> 46) & 63], f = tab.fine[(fx >> 40) & 63];
-    const u64 a = __umul64hi(fx << 24, 0xB17217F7D1CF79ABull) >> 12;   // r ln 2 in units of 2^-64
-    const u64 a2 = __umul64hi(a, a), a3 = __umul64hi(a2, a);
-    const u64 poly = (u64(1) << 63) - (a >> 1) + (a2 >> 2) - a3 / 12;
+// 2^-y in units of 2^-frac for y in units of 2^-52: the integer part shifts, the
+// next two groups of six bits look up, and the rest, r < 2^-12, is
+// 1 - a + a^2/2 - a^3/6 with a = r ln 2 (the next term is below 2^-54).
+constexpr u64 kYLimit = u64(62) << 52;   // beyond it a weight is 0
+__device__ __forceinline__ u64 weight(u64 y, int frac, const ExpTables& tab) {
+    if (y >= kYLimit) return 0;
+    const u64 a = __umul64hi(y << 24, 0xB17217F7D1CF79ABull) >> 12;   // r ln 2 in units of 2^-64
+    const uint32_t ah = uint32_t(a >> 20);                             // < 2^32, in units of 2^-44
+    const uint32_t a2 = __umulhi(ah, ah);                              // a^2 in units of 2^-56
+    const uint32_t a3 = __umulhi(a2, ah);                              // a^3 in units of 2^-68
+    const u64 poly = (u64(1) << 63) - (a >> 1) + (u64(a2) << 6) - (a3 / 12 >> 4);
+    const u64 c = tab.coarse[(y >> 46) & 63], f = tab.fine[(y >> 40) & 63];
     const u64 w = __umul64hi(__umul64hi(c, f) << 1, poly) << 1;        // 2^-(fraction of y), units of 2^-63
-    const int shift = 63 - frac + n;
+    const int shift = 63 - frac + int(y >> 52);
     return shift > 63 ? 0 : (w + (u64(1) << shift >> 1)) >> shift;
 }
 
+// Values are handled as keys, signed magnitudes: -0 is +0 and keys rise with values.
 __device__ __forceinline__ int key_of(uint32_t bits) {
     const int mag = int(bits & 0x7FFFu);
     return bits & 0x8000u ? -mag : mag;
@@ -89,66 +111,110 @@ __device__ __forceinline__ double value_of(int key) {
     const float v = __uint_as_float(uint32_t(key < 0 ? -key : key) << 16);
     return key < 0 ? -double(v) : double(v);
 }
-
-struct Shared {
-    ExpTables tab;
-    uint32_t hist[kWindow];
-    int32_t top[kMaxWindows];          // windows used, from the largest key down
-    u64 mass_before[kMaxWindows];
-    int32_t count_before[kMaxWindows];
-    u64 warp_mass[kWarps];
-    int32_t warp_int[kWarps];
-    u64 mass[4];
-    int32_t num[4];
-};
-
-__device__ __forceinline__ int block_max(int v, Shared& sh) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) sh.warp_int[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = sh.warp_int[threadIdx.x & (kWarps - 1)];
-#pragma unroll
-    for (int o = kWarps / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-    return __shfl_sync(0xFFFFFFFFu, v, 0);
+// A folded window's value in units of 2^-40 (0, or 8 significant bits shifted by up to 39).
+__device__ __forceinline__ long long fixed_of(int key) {
+    const int mag = key < 0 ? -key : key;
+    const long long x = mag ? (long long)((mag & 0x7F) | 0x80) << ((mag >> 7) - (kLowMag >> 7)) : 0;
+    return key < 0 ? -x : x;
 }
 
-// Sums over the threads before this one, and the block's totals.
-struct Scan {
-    int32_t count, total;
-    u64 mass, total_mass;
+// Sorted positions, largest value first. Folded: the positive magnitudes, zero
+// at kSide - 1, (kSide is empty,) the negative ones. Otherwise kValues
+// consecutive keys from `top` down.
+template <bool kFold>
+__device__ __forceinline__ int key_at(int pos, int top) {
+    if constexpr (!kFold) return top - pos;
+    if (pos < kSide) return pos == kSide - 1 ? 0 : kTopMag - pos;
+    return kSide + 1 - kLowMag - pos;
+}
+// The histogram's word of a position: downwards from word kSide - 1, then
+// upwards from word 8,192, so that a folded token's byte offset is its
+// magnitude above kLowMag - 1 times 4, its sign as bit 15, and zero's is 0. The
+// gap between holds the rest of the shared memory's contents.
+__device__ __forceinline__ int word_of(int pos) { return pos < kSide ? kSide - 1 - pos : 8192 - kSide + pos; }
+
+// What a row's settings give: log2(e) / T, as a double and as a 64-bit fraction
+// with a shift, and -log2(min_p) in units of 2^-52. Doubles run at a 64th of the
+// fp32 rate, so one warp works these out while the others count.
+struct Setting {
+    double per;
+    u64 mant, y_min;
+    int shift;
 };
-__device__ __forceinline__ Scan block_scan(int32_t c, u64 m, Shared& sh) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int32_t ci = c;
-    u64 mi = m;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int32_t c2 = __shfl_up_sync(0xFFFFFFFFu, ci, o);
-        const u64 m2 = __shfl_up_sync(0xFFFFFFFFu, mi, o);
-        if (lane >= o) {
-            ci += c2;
-            mi += m2;
-        }
+__device__ __forceinline__ Setting setting_of(float T, float min_p) {
+    Setting s = {0.0, 0, kYLimit, 0};
+    if (T > 0.f) {
+        s.per = 1.4426950408889634074 / double(T);
+        // y 2^52 = d 2^12 per = d mant 2^(e - 64), d the difference in units of 2^-40
+        int e;
+        s.mant = u64(frexp(s.per * 4096.0, &e) * 0x1p64);
+        s.shift = e - 15;
     }
-    __syncthreads();
-    if (lane == 31) {
-        sh.warp_int[warp] = ci;
-        sh.warp_mass[warp] = mi;
-    }
-    __syncthreads();
-    Scan s = {ci - c, 0, mi - m, 0};
-    for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) {
-            s.count += sh.warp_int[w];
-            s.mass += sh.warp_mass[w];
-        }
-        s.total += sh.warp_int[w];
-        s.total_mass += sh.warp_mass[w];
+    if (min_p > 0.f) {
+        const double y = -log2(double(min_p));
+        if (y < 62.0) s.y_min = __double2ull_rz(y * 0x1p52);
     }
     return s;
 }
+
+// y = (max - x) log2(e) / T of a key, in units of 2^-52.
+struct Scale {
+    double vmax, per;     // any value
+    long long xmax;       // folded window: the difference is an integer
+    u64 mant;
+    int shift;
+    __device__ __forceinline__ u64 y_of(u64 d) const {   // of a difference
+        const u64 p = __umul64hi(d << 15, mant);
+        if (shift <= 0) return shift < -63 ? 0 : p >> -shift;
+        return shift > 57 ? (p ? kYLimit : 0) : p >= (kYLimit >> shift) ? kYLimit : p << shift;
+    }
+    template <bool kFold>
+    __device__ __forceinline__ u64 y(int key) const {
+        if constexpr (kFold) return y_of(u64(xmax - fixed_of(key)));
+        const double v = (vmax - value_of(key)) * per;
+        return v < 62.0 ? __double2ull_rz(v * 0x1p52) : kYLimit;
+    }
+};
+__device__ __forceinline__ Scale scale_of(int top_key, bool fold, const Setting& s) {
+    return {value_of(top_key), s.per, fold ? fixed_of(top_key) : 0, s.mant, s.shift};
+}
+
+// floor(x m) of a float x in [0, 1) and a 64-bit m (the fraction cut at 2^-64), and the ceiling.
+__device__ __forceinline__ u64 part_of(float x, u64 m) { return __umul64hi(__float2ull_rz(x * 0x1p64f), m); }
+__device__ __forceinline__ u64 part_up(float x, u64 m) {
+    const u64 f = __float2ull_rz(x * 0x1p64f);
+    return __umul64hi(f, m) + (f * m != 0);
+}
+
+// n / d for a quotient below 2^34: a float quotient, its remainder's, and a last step of one.
+__device__ __forceinline__ u64 quotient(u64 n, u64 d) {
+    const float inv = 1.f / __ull2float_rn(d);
+    u64 q = __float2ull_rz(__ull2float_rn(n) * inv);
+    q += (long long)(__ll2float_rn((long long)(n - q * d)) * inv);
+    const long long rest = (long long)(n - q * d);
+    return rest < 0 ? q - 1 : u64(rest) >= d ? q + 1 : q;
+}
+
+struct Shared {
+    ExpTables tab;
+    Setting set;
+    u64 ratio[kSide / 128];   // folded: the weight of one step of each power of two, in units of 2^-63
+    u64 warp_mass[kWarps];
+    int32_t warp_int[3][kWarps];
+    // what the cluster's CTAs tell one another, by rank
+    u64 mass[kMaxCluster];
+    int32_t first[kMaxCluster], count[kMaxCluster], other[kMaxCluster], found[kMaxCluster];
+    u64 cut[2];             // mass kept by top-p and by min-p, each from the CTA that found it
+    int32_t pick_key, want;
+    u64 before[kValues / kGroup + 1];   // the mass before each group of the slice, and its whole
+};
+static_assert(kSide * 4 + sizeof(Shared) <= 32768, "the gap");
+// Behind the histogram: the windows of a row outside the folded one.
+struct Windows {
+    u64 mass_before[kMaxWindows + 1];
+    int32_t top[kMaxWindows], count_before[kMaxWindows];
+};
+constexpr int kSmemBytes = 32768 + kSide * 4 + int(sizeof(Windows));
 
 struct Args {
     const uint16_t* logits;
@@ -161,191 +227,645 @@ struct Args {
     int32_t* pick;
     float* prob;
     uint8_t* flag;
-    int32_t V;
-    int32_t frac;
+    int32_t V, frac;
+    int32_t chunk;       // tokens a CTA of the cluster counts, a multiple of 8
 };
 
-__global__ void __launch_bounds__(kThreads)
-sample_rows_kernel(Args a) {
-    __shared__ Shared sh;
-    const int row = blockIdx.x, tid = threadIdx.x;
-    const uint16_t* p = a.logits + size_t(row) * size_t(a.stride);
-    if (tid < 64) {
-        sh.tab.coarse[tid] = kExpTables.coarse[tid];
-        sh.tab.fine[tid] = kExpTables.fine[tid];
-    }
-    pdl_wait();
-    const float T = a.temperature ? a.temperature[row] : 1.f;
-    const float tp = a.top_p ? a.top_p[row] : 1.f, mp = a.min_p ? a.min_p[row] : 0.f, u = a.u[row];
-    const int32_t tk = a.top_k ? a.top_k[row] : 0;
-    const int32_t K = tk > 0 && tk < a.V ? tk : a.V;
-    const bool bad_setting = !(T >= 0.f && T < INFINITY) || isnan(tp) || isnan(mp) || !(mp <= 1.f) ||
-                             !(u >= 0.f && u < 1.f);
-
-    int hi = kMinKey;
-    for (int i = tid; i < a.V; i += kThreads) {
-        const int k = key_of(p[i]);
-        hi = max(hi, k >= kInfKey || k < kMinKey ? 0x10000 : k);   // NaN or +infinity: beyond every key
-    }
-    hi = block_max(hi, sh);
-    if (hi == 0x10000 || hi == kMinKey || bad_setting) {
-        if (tid == 0) {
-            a.pick[row] = -1;
-            if (a.prob) a.prob[row] = 0.f;
-            a.flag[row] = uint8_t((hi == 0x10000 || hi == kMinKey ? TF_SAMPLE_NO_LOGITS : 0) |
-                                  (bad_setting ? TF_SAMPLE_BAD_SETTING : 0));
+// f(word of two tokens) over 16-byte vectors, f1(bits) for the rest of [begin, end).
+template <bool kVec, typename F, typename F1>
+__device__ __forceinline__ void for_tokens(const uint16_t* p, int begin, int end, F&& f, F1&& f1) {
+    if constexpr (kVec) {
+        const int nvec = (end - begin) >> 3;
+        const uint4* pv = reinterpret_cast<const uint4*>(p + begin);
+        // the next vectors are asked for before the ones at hand are used
+        uint4 v[kUnroll], next[kUnroll];
+        auto load = [&](uint4 (&x)[kUnroll], int i) {
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u)
+                if (i + u * kThreads < nvec) x[u] = __ldg(pv + i + u * kThreads);
+        };
+        load(v, threadIdx.x);
+        for (int i = threadIdx.x; i < nvec; i += kUnroll * kThreads) {
+            load(next, i + kUnroll * kThreads);
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                if (i + u * kThreads >= nvec) break;
+                f(v[u].x);
+                f(v[u].y);
+                f(v[u].z);
+                f(v[u].w);
+            }
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) v[u] = next[u];
         }
-        return;
+        begin += nvec * 8;
     }
-    const double vmax = value_of(hi), per = T > 0.f ? 1.4426950408889634074 / double(T) : 0.0;   // log2(e) / T
-    // log2 of the smallest kept weight, negated
-    const double y_min = mp > 0.f ? -log2(double(mp)) : 2e308;
+    for (int i = begin + threadIdx.x; i < end; i += kThreads) f1(uint32_t(p[i]));
+}
 
-    int32_t want = 0, pick_key = hi;   // the pick: the want-th token (by id) of value pick_key
-    float prob = 1.f;
-    if (T > 0.f) {
-        // counts of window `top` into the histogram; the largest key below it
-        auto count = [&](int top) {
-            __syncthreads();
-            for (int i = tid; i < kWindow; i += kThreads) sh.hist[i] = 0;
-            __syncthreads();
-            int below = kMinKey;
-            for (int i = tid; i < a.V; i += kThreads) {
-                const int k = key_of(p[i]);
-                if (k > top || k == kMinKey) continue;
-                if (top - k < kWindow) atomicAdd(&sh.hist[top - k], 1u);
-                else below = max(below, k);
-            }
-            return block_max(below, sh);   // a barrier: the histogram is complete
-        };
-        // f(key, tokens kept by top-k, tokens before, mass before, weight) of this thread's values of
-        // window w, in descending order; the masses of the whole window
-        auto walk = [&](int w, auto&& f) {
-            const int top = sh.top[w];
-            int32_t c[kBins], cs = 0;
-            u64 wt[kBins], ms = 0;
-#pragma unroll
-            for (int j = 0; j < kBins; ++j) {
-                c[j] = int32_t(sh.hist[tid * kBins + j]);
-                cs += c[j];
-            }
-            const Scan sc = block_scan(cs, 0, sh);
-            int32_t before = sh.count_before[w] + sc.count;
-            const int32_t before0 = before;
-#pragma unroll
-            for (int j = 0; j < kBins; ++j) {
-                wt[j] = c[j] ? weight((vmax - value_of(top - tid * kBins - j)) * per, a.frac, sh.tab) : 0;
-                const int32_t n = max(0, min(c[j], K - before));
-                before += c[j];
-                c[j] = n;
-                ms += u64(n) * wt[j];
-            }
-            const Scan sm = block_scan(0, ms, sh);
-            u64 mass = sh.mass_before[w] + sm.mass;
-            before = min(before0, K);
-#pragma unroll
-            for (int j = 0; j < kBins; ++j) {
-                if (c[j]) f(top - tid * kBins - j, c[j], before, mass, wt[j]);
-                before += c[j];
-                mass += u64(c[j]) * wt[j];
-            }
-            return Scan{0, sc.total, 0, sm.total_mass};
-        };
+// One CTA's part in its row. Every step that ends in sync() is taken by all
+// threads of all CTAs of the cluster, with the same numbers.
+template <bool kVec>
+struct Row {
+    const Args& a;
+    unsigned char* dyn;
+    Shared& sh;
+    int ncl, rank;
+    int begin, end;      // this CTA's tokens
+    int s0, s1;          // and its slice of the sorted positions
+    const uint16_t* p;
+    float tp;
+    int32_t K;
+    int top_key;
 
-        // windows down to the k-th token, and the mass Z of the first k
-        int nw = 0;
-        for (int top = hi, counted = 0;;) {
-            const int below = count(top);
+    __device__ __forceinline__ uint32_t* hist() const { return reinterpret_cast<uint32_t*>(dyn); }
+    __device__ __forceinline__ u64* before() const { return sh.before; }
+    __device__ __forceinline__ void sync() const {
+        if (ncl > 1) cg::this_cluster().sync();
+        else __syncthreads();
+    }
+    // the block's value v (the same in every thread) into every CTA's `mine`; called by all threads
+    template <typename X>
+    __device__ __forceinline__ void tell(X& mine, X v) const {
+        if (int(threadIdx.x) < ncl) *cg::this_cluster().map_shared_rank(&mine, threadIdx.x) = v;
+    }
+    // one thread's value into every CTA's `mine`
+    template <typename X>
+    __device__ __forceinline__ void tell_alone(X& mine, X v) const {
+        for (int r = 0; r < ncl; ++r) *cg::this_cluster().map_shared_rank(&mine, r) = v;
+    }
+
+    __device__ __forceinline__ void clear() const {
+        uint4* h = reinterpret_cast<uint4*>(dyn);
+        for (int i = threadIdx.x; i < kSide / 2; i += kThreads)
+            h[i < kSide / 4 ? i : 2048 + i - kSide / 4] = make_uint4(0, 0, 0, 0);
+        __syncthreads();
+    }
+
+    // The counts of group g of the slice, in sorted order; whether there are any.
+    __device__ __forceinline__ bool load_group(int g, uint32_t (&n)[kGroup]) const {
+        const int pos = s0 + kGroup * g;
+        const bool down = pos < kSide;   // the group's words run down, or up
+        uint32_t any = 0;
+#pragma unroll
+        for (int k = 0; k < kGroup / 4; ++k) {
+            const uint4 c = *reinterpret_cast<const uint4*>(hist() + (down ? word_of(pos + 4 * k) - 3 : word_of(pos + 4 * k)));
+            n[4 * k] = down ? c.w : c.x;
+            n[4 * k + 1] = down ? c.z : c.y;
+            n[4 * k + 2] = down ? c.y : c.z;
+            n[4 * k + 3] = down ? c.x : c.w;
+            any |= c.x | c.y | c.z | c.w;
+        }
+        return any != 0;
+    }
+    __device__ __forceinline__ int groups() const { return (s1 - s0) / kGroup; }
+
+    // After the count: sums the slice over the cluster and surveys it. The
+    // window's first occupied position and tokens, the largest of every
+    // thread's `other`.
+    struct Survey {
+        int first, count, other;
+    };
+    __device__ __forceinline__ Survey survey(int other) const {
+        sync();
+        if (ncl > 1) {
+            for (int i = s0 / 4 + int(threadIdx.x); i < s1 / 4; i += kThreads) {
+                const int w4 = min(word_of(4 * i), word_of(4 * i + 3)) / 4;   // 4 positions are 4 words
+                uint4 c = reinterpret_cast<uint4*>(hist())[w4], o[kMaxCluster];
+#pragma unroll
+                for (int r = 1; r < kMaxCluster; ++r) {   // every peer's words asked for before any is used
+                    const int peer = rank + r < ncl ? rank + r : rank + r - ncl;
+                    o[r] = make_uint4(0, 0, 0, 0);
+                    if (r < ncl) o[r] = reinterpret_cast<uint4*>(cg::this_cluster().map_shared_rank(hist(), peer))[w4];
+                }
+#pragma unroll
+                for (int r = 1; r < kMaxCluster; ++r) {
+                    c.x += o[r].x;
+                    c.y += o[r].y;
+                    c.z += o[r].z;
+                    c.w += o[r].w;
+                }
+                reinterpret_cast<uint4*>(hist())[w4] = c;
+            }
             __syncthreads();
-            if (tid == 0) {
-                sh.top[nw] = top;
-                if (nw == 0) {
-                    sh.count_before[0] = 0;
-                    sh.mass_before[0] = 0;
+        }
+        int first = kValues, n = 0;
+        for (int g = int(threadIdx.x); g < groups(); g += kThreads) {
+            uint32_t c[kGroup];
+            if (!load_group(g, c)) continue;
+#pragma unroll
+            for (int j = kGroup - 1; j >= 0; --j) {
+                n += c[j];
+                if (c[j]) first = min(first, s0 + kGroup * g + j);
+            }
+        }
+        first = __reduce_min_sync(0xFFFFFFFFu, first);
+        n = __reduce_add_sync(0xFFFFFFFFu, n);
+        other = __reduce_max_sync(0xFFFFFFFFu, other);
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        if (lane == 0) {
+            sh.warp_int[0][warp] = first;
+            sh.warp_int[1][warp] = n;
+            sh.warp_int[2][warp] = other;
+        }
+        __syncthreads();
+        Survey s;
+        s.first = __reduce_min_sync(0xFFFFFFFFu, sh.warp_int[0][lane % kWarps]);
+        s.count = __reduce_add_sync(0xFFFFFFFFu, lane < kWarps ? sh.warp_int[1][lane] : 0);
+        s.other = __reduce_max_sync(0xFFFFFFFFu, sh.warp_int[2][lane % kWarps]);
+        if (ncl == 1) {
+            if (threadIdx.x == 0) sh.count[0] = s.count;
+            __syncthreads();
+            return s;
+        }
+        tell(sh.first[rank], s.first);
+        tell(sh.count[rank], s.count);
+        tell(sh.other[rank], s.other);
+        sync();
+        s = {kValues, 0, kMinKey};
+        for (int r = 0; r < ncl; ++r) {
+            s.first = min(s.first, sh.first[r]);
+            s.count += sh.count[r];
+            s.other = max(s.other, sh.other[r]);
+        }
+        return s;
+    }
+
+    // before()[g] of every group of the slice (written, with the threads synchronised, by any
+    // thread) into the sum of the groups before g; before()[groups()] becomes the whole.
+    __device__ __forceinline__ u64 prefix() const {
+        const int G = groups(), per = (G + kThreads - 1) / kThreads;
+        const int g0 = min(G, int(threadIdx.x) * per), g1 = min(G, g0 + per);
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        u64 sum = 0;
+        for (int g = g0; g < g1; ++g) sum += before()[g];
+        u64 incl = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const u64 t = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+            if (lane >= o) incl += t;
+        }
+        if (lane == 31) sh.warp_mass[warp] = incl;
+        __syncthreads();
+        u64 w = sh.warp_mass[lane % kWarps];
+#pragma unroll
+        for (int o = 1; o < kWarps; o <<= 1) {
+            const u64 t = __shfl_up_sync(0xFFFFFFFFu, w, o, kWarps);
+            if (lane % kWarps >= o) w += t;
+        }
+        const u64 total = __shfl_sync(0xFFFFFFFFu, w, kWarps - 1), prev = __shfl_sync(0xFFFFFFFFu, w, warp ? warp - 1 : 0);
+        u64 at = (warp ? prev : 0) + incl - sum;
+        for (int g = g0; g < g1; ++g) {
+            const u64 v = before()[g];
+            before()[g] = at;
+            at += v;
+        }
+        if (threadIdx.x == 0) before()[G] = total;
+        __syncthreads();
+        return total;
+    }
+
+    // Cuts the slice's counts to the first K tokens (`counted` come before the window) and
+    // weighs it: before() holds the mass before each group, relative to the slice's. The
+    // window's mass, and the mass of the slices before this one in `slice_at`.
+    template <bool kFold>
+    __device__ __forceinline__ u64 weigh(const Scale& scale, int top, int32_t counted, u64& slice_at) const {
+        if (K < a.V) {
+            for (int r = 0; r < rank; ++r) counted += sh.count[r];
+            for (int g = int(threadIdx.x); g < groups(); g += kThreads) {
+                uint32_t c[kGroup];
+                load_group(g, c);
+                u64 n = 0;
+#pragma unroll
+                for (int j = 0; j < kGroup; ++j) n += c[j];
+                before()[g] = n;
+            }
+            __syncthreads();
+            prefix();
+            for (int g = int(threadIdx.x); g < groups(); g += kThreads) {
+                if (counted + int64_t(before()[g + 1]) <= K) continue;
+                int32_t left = K - counted - int32_t(before()[g]);
+#pragma unroll 1
+                for (int pos = s0 + kGroup * g; pos < s0 + kGroup * (g + 1); ++pos) {
+                    const int32_t c = int32_t(hist()[word_of(pos)]);
+                    if (c > left) hist()[word_of(pos)] = uint32_t(max(left, 0));
+                    left -= c;
                 }
             }
             __syncthreads();
-            const Scan s = walk(nw, [](int, int32_t, int32_t, u64, u64) {});
-            counted += s.total;
-            ++nw;
-            if (tid == 0) {
-                sh.count_before[nw] = counted;
-                sh.mass_before[nw] = sh.mass_before[nw - 1] + s.total_mass;
-            }
-            if (below == kMinKey || counted >= K) break;
-            top = below;
         }
-        int held = nw - 1;   // the window whose counts the histogram holds
+#pragma unroll 1
+        for (int g = int(threadIdx.x); g < groups(); g += kThreads) {
+            u64 m = 0;
+            uint32_t n[kGroup];
+            if (load_group(g, n)) {
+                u64 w[kGroup];
+                group_weights<kFold>(g, scale, top, w);
+#pragma unroll
+                for (int j = 0; j < kGroup; ++j) m += n[j] * w[j];
+            }
+            before()[g] = m;
+        }
         __syncthreads();
-        const u64 Z = sh.mass_before[nw];
-        auto hold = [&](int w) {
-            if (held != w) count(sh.top[w]);
-            held = w;
-        };
+        const u64 mine = prefix();
+        slice_at = 0;
+        if (ncl == 1) return mine;
+        tell(sh.mass[rank], mine);
+        sync();
+        u64 total = 0;
+        for (int r = 0; r < ncl; ++r) {
+            if (r < rank) slice_at += sh.mass[r];
+            total += sh.mass[r];
+        }
+        return total;
+    }
 
-        // the kept mass: of the shortest prefix
+    // The weights of group g's positions. A group of a folded window lies in one power of two
+    // (the zero's aside), so its values are equal steps apart and each weight is the one before
+    // times the step's, ratio[exponent]. Positions above the largest value hold no tokens.
+    template <bool kFold>
+    __device__ __forceinline__ void group_weights(int g, const Scale& scale, int top, u64 (&w)[kGroup]) const {
+        const int pos = s0 + kGroup * g;
+        if constexpr (!kFold) {
+#pragma unroll 1
+            for (int j = 0; j < kGroup; ++j) w[j] = weight_of<kFold>(scale, min(key_at<kFold>(pos + j, top), top_key), a.frac, sh.tab);
+            return;
+        }
+        const int key = key_at<true>(pos, 0), round = 63 - a.frac;
+        const u64 ratio = sh.ratio[(abs(key) >> 7) - (kLowMag >> 7)];
+        u64 x = weight(scale.template y<true>(min(key, top_key)), 63, sh.tab);
+#pragma unroll
+        for (int j = 0; j < kGroup; ++j) {
+            if (j > 0 && key - j < top_key) x = __umul64hi(x, ratio) << 1;
+            w[j] = (x + (u64(1) << round >> 1)) >> round;
+        }
+        if (pos == kSide - kGroup) w[kGroup - 1] = weight_of<true>(scale, min(0, top_key), a.frac, sh.tab);
+    }
+
+    // The weight of one key, out of line: the searches below are not worth a copy each.
+    template <bool kFold>
+    __device__ __noinline__ static u64 weight_of(const Scale& scale, int key, int frac, const ExpTables& tab) {
+        return weight(scale.template y<kFold>(key), frac, tab);
+    }
+
+    // f(key, mass before, weight) by the one thread that holds the value whose masses
+    // (before, after] hold m; `at` precedes the slice.
+    template <bool kFold, typename F>
+    __device__ __forceinline__ void find(u64 m, u64 at, const Scale& scale, int top, F&& f) const {
+        if (m <= at || m > at + before()[groups()]) return;
+        for (int g = int(threadIdx.x); g < groups(); g += kThreads) {
+            if (!(at + before()[g] < m && m <= at + before()[g + 1])) continue;
+            u64 x = at + before()[g], w[kGroup], hit = 0, hit_w = 0;
+            uint32_t n[kGroup];
+            int hit_pos = -1;
+            load_group(g, n);
+            group_weights<kFold>(g, scale, top, w);
+#pragma unroll
+            for (int j = 0; j < kGroup; ++j) {
+                const u64 x1 = x + n[j] * w[j];
+                if (x < m && m <= x1) {
+                    hit_pos = s0 + kGroup * g + j;
+                    hit = x;
+                    hit_w = w[j];
+                }
+                x = x1;
+            }
+            if (hit_pos >= 0) f(key_at<kFold>(hit_pos, top), hit, hit_w);
+        }
+    }
+    // The first prefix mass of at least `least`, into every CTA's cut[0].
+    template <bool kFold>
+    __device__ __forceinline__ void top_p_cut(u64 Z, u64 at, const Scale& scale, int top) const {
+        const u64 least = least_of(Z);
+        find<kFold>(least, at, scale, top, [&](int, u64 x, u64 w) { tell_alone(sh.cut[0], x + quotient(least - x + w - 1, w) * w); });
+    }
+    __device__ __forceinline__ u64 least_of(u64 Z) const { return max(u64(1), part_up(fmaxf(tp, 0.f), Z)); }
+    // The mass of the window's values with y <= y_min, and what precedes it, into every
+    // CTA's cut[1]: the last such position is found by bisection (y rises with positions)
+    // in the slice that holds it; `Z` is the mass up to the window's end.
+    template <bool kFold>
+    __device__ __forceinline__ void min_p_cut(u64 Z, u64 at, const Scale& scale, int top) const {
+        if (threadIdx.x >= 32) return;
+        const u64 y_min = sh.set.y_min;
+        auto keeps = [&](int pos) {
+            const int key = key_at<kFold>(pos, top);
+            return key >= top_key || (key >= kMinKey && scale.template y<kFold>(key) <= y_min);
+        };
+        int lo = 0;   // positions below lo are kept; 32 looked at a time, 320, 10 and 1 apart
+#pragma unroll 1
+        for (int step = kValues / 32; step; step = step == 1 ? 0 : step / 32 > 1 ? step / 32 : 1) {
+            const int pos = lo + int(threadIdx.x) * step;
+            const bool k = pos < kValues && keeps(pos);
+            const uint32_t kept = __ballot_sync(0xFFFFFFFFu, k);
+            if (step > 1) lo += kept ? (31 - __clz(kept)) * step : 0;   // the last kept one
+            else lo += __popc(kept);
+        }
+        if (threadIdx.x != 0) return;
+        if (lo == kValues) {
+            if (rank == ncl - 1) tell_alone(sh.cut[1], Z);
+            return;
+        }
+        if (lo < s0 || lo >= s1) return;
+        const int g = (lo - s0) / kGroup;
+        u64 x = at + before()[g], w[kGroup];
+        uint32_t n[kGroup];
+        load_group(g, n);
+        group_weights<kFold>(g, scale, top, w);
+#pragma unroll
+        for (int j = 0; j < kGroup; ++j)
+            if (s0 + kGroup * g + j < lo) x += n[j] * w[j];
+        tell_alone(sh.cut[1], x);
+    }
+    // The pick at cumulative mass `target`, into every CTA.
+    template <bool kFold>
+    __device__ __forceinline__ void pick_at(u64 target, u64 at, const Scale& scale, int top) const {
+        find<kFold>(target + 1, at, scale, top, [&](int key, u64 x, u64 w) {
+            tell_alone(sh.pick_key, key);
+            tell_alone(sh.want, int32_t(quotient(target - x, w)));
+        });
+    }
+
+    // A row outside the folded window: windows of kValues keys from its largest down.
+    // The kept mass; the pick goes to pick_key and want.
+    __device__ __noinline__ u64 general(const Scale& scale, float mp, float u) const {
+        u64 slice_at = 0;
+        Windows& win = *reinterpret_cast<Windows*>(dyn + 32768 + kSide * 4);
+        // counts of the window of kValues keys from `top` down, and the largest key below it
+        auto count = [&](int top) {
+            sync();   // every CTA is done with the counts so far
+            clear();
+            int below = kMinKey;
+            auto one = [&](uint32_t b) {
+                const int k = key_of(b);
+                if (k > top || k == kMinKey) return;
+                if (top - k < kValues) atomicAdd(hist() + word_of(top - k), 1u);
+                else below = max(below, k);
+            };
+            for_tokens<kVec>(p, begin, end, [&](uint32_t w) {
+                one(w & 0xFFFFu);
+                one(w >> 16);
+            }, one);
+            return survey(below);
+        };
+        int nw = 0;
+        u64 Z = 0;
+        for (int top = top_key, counted = 0;;) {   // windows down to the K-th token
+            const Survey s = count(top);
+            if (threadIdx.x == 0) {
+                win.top[nw] = top;
+                win.count_before[nw] = counted;
+                win.mass_before[nw] = Z;
+            }
+            Z += weigh<false>(scale, top, counted, slice_at);
+            counted += s.count;
+            ++nw;
+            if (s.other == kMinKey || counted >= K) break;
+            top = s.other;
+        }
+        if (threadIdx.x == 0) win.mass_before[nw] = Z;
+        __syncthreads();
+        int held = nw - 1;
+        auto hold = [&](int w) {   // window w's counts and masses; the mass before this CTA's slice
+            if (held != w) {
+                count(win.top[w]);
+                weigh<false>(scale, win.top[w], win.count_before[w], slice_at);
+                held = w;
+            }
+            return win.mass_before[w] + slice_at;
+        };
         u64 kept = Z;
         if (tp < 1.f) {
-            const double need = double(fmaxf(tp, 0.f)) * double(Z);
-            const u64 least = max(u64(1), u64(ceil(need)));   // the first prefix of at least this mass
             int w = 0;
-            while (sh.mass_before[w + 1] < least) ++w;
-            hold(w);
-            walk(w, [&](int, int32_t n, int32_t, u64 m, u64 wt) {
-                if (m < least && least <= m + u64(n) * wt) sh.mass[0] = m + (least - m + wt - 1) / wt * wt;
-            });
-            __syncthreads();
-            kept = min(kept, sh.mass[0]);
+            while (win.mass_before[w + 1] < least_of(Z)) ++w;
+            top_p_cut<false>(Z, hold(w), scale, win.top[w]);
+            sync();
+            kept = min(kept, sh.cut[0]);
         }
         if (mp > 0.f) {
             // the last window whose largest value is kept holds the cut
             int w = 0;
-            while (w + 1 < nw && (vmax - value_of(sh.top[w + 1])) * per <= y_min) ++w;
-            hold(w);
-            if (tid == 0) sh.mass[1] = 0;
-            __syncthreads();
-            walk(w, [&](int key, int32_t n, int32_t, u64 m, u64 wt) {
-                if ((vmax - value_of(key)) * per <= y_min) atomicMax(&sh.mass[1], m + u64(n) * wt);
-            });
-            __syncthreads();
-            kept = min(kept, sh.mass[1]);
+            while (w + 1 < nw && scale.y<false>(win.top[w + 1]) <= sh.set.y_min) ++w;
+            const u64 at = hold(w);
+            min_p_cut<false>(win.mass_before[w + 1], at, scale, win.top[w]);
+            sync();
+            kept = min(kept, sh.cut[1]);
         }
-        const u64 target = min(u64(double(u) * double(kept)), kept - 1);
-        {
-            int w = 0;
-            while (sh.mass_before[w + 1] <= target) ++w;
-            hold(w);
-            walk(w, [&](int key, int32_t n, int32_t, u64 m, u64 wt) {
-                if (m <= target && target < m + u64(n) * wt) {
-                    sh.num[0] = key;
-                    sh.num[1] = int32_t((target - m) / wt);
-                }
-            });
-            __syncthreads();
-            pick_key = sh.num[0];
-            want = sh.num[1];
-            // the pick's weight again, to all 63 bits
-            const u64 w63 = weight((vmax - value_of(pick_key)) * per, 63, sh.tab);
-            prob = float(ldexp(double(w63), a.frac - 63) / double(kept));
+        const u64 target = part_of(u, kept);
+        int w = 0;
+        while (win.mass_before[w + 1] <= target) ++w;
+        pick_at<false>(target, hold(w), scale, win.top[w]);
+        sync();
+        return kept;
+    }
+};
+
+template <bool kVec>
+__global__ void __launch_bounds__(kThreads, 2)
+sample_rows_kernel(const __grid_constant__ Args a) {
+    extern __shared__ __align__(128) unsigned char dyn[];
+    Shared& sh = *reinterpret_cast<Shared*>(dyn + kSide * 4);
+    const int row = blockIdx.y, tid = threadIdx.x;
+    const int ncl = gridDim.x, rank = blockIdx.x;   // a cluster is one row's CTAs
+    const int begin = min(a.V, rank * a.chunk), end = min(a.V, begin + a.chunk);
+    const int slice = kValues / ncl;
+    const uint16_t* p = a.logits + size_t(row) * size_t(a.stride);
+    Row<kVec> R{a, dyn, sh, ncl, rank, begin, end, rank * slice, (rank + 1) * slice, p, 1.f, a.V, kMinKey};
+    uint32_t* const hist = R.hist();
+    if (tid < 64) {
+        sh.tab.coarse[tid] = kExpTables.coarse[tid];
+        sh.tab.fine[tid] = kExpTables.fine[tid];
+    }
+    R.clear();
+    pdl_wait();
+    const float T = a.temperature ? a.temperature[row] : 1.f;
+    const float tp = a.top_p ? a.top_p[row] : 1.f, mp = a.min_p ? a.min_p[row] : 0.f, u = a.u[row];
+    const int32_t tk = a.top_k ? a.top_k[row] : 0;
+    R.K = tk > 0 && tk < a.V ? tk : a.V;
+    R.tp = tp;
+    const bool bad_setting = !(T >= 0.f && T < INFINITY) || isnan(tp) || isnan(mp) || !(mp <= 1.f) ||
+                             !(u >= 0.f && u < 1.f);
+    if (tid == kThreads - 1) sh.set = setting_of(T, mp);   // read after the count's barriers
+
+    // ---- the first pass: the folded window
+    int other = kMinKey;   // the largest other value
+    auto count_one = [&](uint32_t b) {
+        const int d = int(b & 0x7FFFu) - kLowMag;
+        if (uint32_t(d) < uint32_t(kSide - 1)) {
+            atomicAdd(hist + (b & 0x8000u ? 8193 + d : 1 + d), 1u);
+        } else if (b != 0xFF80u) {
+            const int k = key_of(b);
+            if (k == 0) atomicAdd(hist, 1u);
+            else other = max(other, k >= kInfKey || k < kMinKey ? kBadKey : k);
         }
+    };
+    for_tokens<kVec>(
+        p, begin, end,
+        [&](uint32_t w) {
+            // halves: 0x8000 + magnitude - kLowMag, and the same less the window's size (no borrow crosses
+            // a half); both tokens lie in the window when the first keeps bit 15 and the second loses it
+            const uint32_t r = (w | 0x80008000u) - uint32_t(kLowMag) * 0x10001u;
+            if ((r & ~(r - uint32_t(kSide - 1) * 0x10001u) & 0x80008000u) == 0x80008000u) {
+                const uint32_t e = (w & 0x80008000u) | (r << 2 & 0x7FFF7FFFu);   // byte offsets less 4; the low
+                atomicAdd(reinterpret_cast<uint32_t*>(dyn + (e & 0xFFFFu) + 4), 1u);  // half's bit 15 adds 2
+                atomicAdd(reinterpret_cast<uint32_t*>(dyn + (e >> 16) + 2), 1u);      // to the high one's
+            } else {
+                count_one(w & 0xFFFFu);
+                count_one(w >> 16);
+            }
+        },
+        count_one);
+
+    const auto found = R.survey(other);
+    const bool fold = found.other == kMinKey;
+    const int top_key = max(found.first < kValues ? key_at<true>(found.first, 0) : kMinKey, found.other);
+    R.top_key = top_key;
+    if (top_key == kBadKey || top_key == kMinKey || bad_setting) {
+        if (tid == 0 && rank == 0) {
+            a.pick[row] = -1;
+            if (a.prob) a.prob[row] = 0.f;
+            a.flag[row] = uint8_t((top_key == kBadKey || top_key == kMinKey ? TF_SAMPLE_NO_LOGITS : 0) |
+                                  (bad_setting ? TF_SAMPLE_BAD_SETTING : 0));
+        }
+        return;   // the cluster's last exchange was the survey's
+    }
+
+    const Scale scale = scale_of(top_key, fold, sh.set);
+    u64 kept = 0;
+    int pick_key = top_key, want = 0;   // the pick: the want-th token (by id) of value pick_key
+    if (T > 0.f) {
+        if (fold) {
+            if (tid < kSide / 128) sh.ratio[tid] = weight(scale.y_of(u64(1) << tid), 63, sh.tab);
+            __syncthreads();
+            u64 at;
+            const u64 Z = R.template weigh<true>(scale, 0, 0, at);
+            kept = Z;
+            if (tp < 1.f || mp > 0.f) {
+                if (tp < 1.f) R.template top_p_cut<true>(Z, at, scale, 0);
+                if (mp > 0.f) R.template min_p_cut<true>(Z, at, scale, 0);
+                R.sync();
+                if (tp < 1.f) kept = min(kept, sh.cut[0]);
+                if (mp > 0.f) kept = min(kept, sh.cut[1]);
+            }
+            R.template pick_at<true>(part_of(u, kept), at, scale, 0);
+            R.sync();
+        } else {
+            kept = R.general(scale, mp, u);
+        }
+        pick_key = sh.pick_key;
+        want = sh.want;
     }
     pdl_trigger();
 
-    // the want-th token of value pick_key, in id order: contiguous ranges a thread
-    const int per_thread = (a.V + kThreads - 1) / kThreads;
-    const int i0 = min(a.V, tid * per_thread), i1 = min(a.V, i0 + per_thread);
-    int32_t n = 0;
-    for (int i = i0; i < i1; ++i) n += key_of(p[i]) == pick_key;
-    const Scan s = block_scan(n, 0, sh);
-    if (s.count <= want && want < s.count + n) {
-        int32_t left = want - s.count;
-        int i = i0;
-        for (;; ++i)
-            if (key_of(p[i]) == pick_key && left-- == 0) break;
-        a.pick[row] = i;
+    const int lane = tid & 31, warp = tid >> 5;
+    if (tid == kThreads - 1 && rank == 0) {
+        float prob = 1.f;
+        if (T > 0.f) {
+            // the weight's first 64 bits over the mass's first 32 (2^-31 of it off at most),
+            // the remainder as the quotient's last bit, so that the one rounding sees it
+            const u64 w = fold ? R.template weight_of<true>(scale, pick_key, 63, sh.tab)
+                               : R.template weight_of<false>(scale, pick_key, 63, sh.tab);
+            const int wu = __clzll((long long)w), ku = __clzll((long long)kept);
+            const u64 den = (kept << ku) >> 32, q = quotient(w << wu, den);
+            prob = ldexpf(float(q | u64(q * den != w << wu)), ku - wu + a.frac - 63 - 32);
+        }
         if (a.prob) a.prob[row] = prob;
         a.flag[row] = 0;
     }
+
+    // ---- the second pass: the want-th token of value pick_key. A warp counts one
+    // contiguous part of the CTA's tokens in steps of kStep, lane j keeping step
+    // j's count, so the counts of the CTAs, warps and steps before a token say how
+    // many come before its step, which one more read searches.
+    constexpr int kStep = kSearch * 32 * 8;
+    static_assert(TF_SAMPLE_MAX_VOCAB <= kStep * 32 * kWarps, "a lane a step");
+    const uint32_t bits = uint32_t(pick_key < 0 ? -pick_key | 0x8000 : pick_key);
+    const int part = ((end - begin + kWarps - 1) / kWarps + 7) / 8 * 8;
+    const int w0 = min(end, begin + warp * part), w1 = min(end, w0 + part);
+    const uint32_t both = bits * 0x10001u;
+    const __nv_bfloat162 ref = *reinterpret_cast<const __nv_bfloat162*>(&both);
+    // the lane's 8 tokens from i on (those before w1) that are the pick's value, a bit each
+    auto hits_at = [&](int i, const uint4& v) {
+        uint32_t h = 0;
+        if (kVec && i + 8 <= w1) {
+            const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                h |= (__heq2_mask(*reinterpret_cast<const __nv_bfloat162*>(&x[k]), ref) & 0x10001u) << 2 * k;
+            h = (h | h >> 15) & 0xFFu;   // the high tokens' bits between the low ones'
+        } else {
+#pragma unroll 1
+            for (int k = 0; k < 8; ++k)
+                if (i + k < w1 && key_of(p[i + k]) == pick_key) h |= 1u << k;
+        }
+        return h;
+    };
+    auto load = [&](uint4 (&v)[kSearch], int i0) {
+#pragma unroll
+        for (int k = 0; k < kSearch; ++k)
+            if (kVec && i0 + 256 * k + 8 * lane + 8 <= w1)
+                v[k] = __ldg(reinterpret_cast<const uint4*>(p + i0 + 256 * k + 8 * lane));
+    };
+    int32_t n = 0, steps = 0;   // the warp's count, this lane's step's
+    uint4 v[kSearch], next[kSearch];
+    load(v, w0);
+    for (int i0 = w0, j = 0; i0 < w1; i0 += kStep, ++j) {
+        load(next, i0 + kStep);
+        int32_t c = 0;
+#pragma unroll
+        for (int k = 0; k < kSearch; ++k) c += __popc(hits_at(i0 + 256 * k + 8 * lane, v[k]));
+#pragma unroll
+        for (int k = 0; k < kSearch; ++k) v[k] = next[k];
+        c = __reduce_add_sync(0xFFFFFFFFu, c);
+        if (lane == j) steps = c;
+        n += c;
+    }
+    if (lane == 0) sh.warp_int[0][warp] = n;
+    __syncthreads();
+    const int32_t x = lane < kWarps ? sh.warp_int[0][lane] : 0;
+    int32_t before = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? x : 0);
+    if (ncl > 1) {
+        R.tell(sh.found[rank], __reduce_add_sync(0xFFFFFFFFu, x));
+        R.sync();   // the last use of another CTA's memory
+        for (int r = 0; r < rank; ++r) before += sh.found[r];
+    }
+    if (before <= want && want < before + n) {
+        // the step, then 8 tokens a lane of it at a time
+        int32_t left = want - before, incl = steps;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int32_t t = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+            if (lane >= o) incl += t;
+        }
+        const int j = __ffs(__ballot_sync(0xFFFFFFFFu, left < incl)) - 1;
+        left -= __shfl_sync(0xFFFFFFFFu, incl - steps, j);
+        const int i0 = w0 + j * kStep;
+        load(v, i0);
+#pragma unroll
+        for (int k = 0; k < kSearch; ++k) {
+            const int i = i0 + 256 * k + 8 * lane;
+            uint32_t h = hits_at(i, v[k]);
+            const int32_t c = __popc(h);
+            int32_t upto = c;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int32_t t = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+                if (lane >= o) upto += t;
+            }
+            if (left >= upto - c && left < upto) {
+                for (int q = upto - c; q < left; ++q) h &= h - 1;
+                a.pick[row] = i + __ffs(h) - 1;
+            }
+            left -= __shfl_sync(0xFFFFFFFFu, upto, 31);
+            if (left < 0) break;
+        }
+    }
+}
+
+template <bool kVec>
+int prepare() {
+    const cudaError_t r = cudaFuncSetAttribute(sample_rows_kernel<kVec>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               kSmemBytes);
+    return r == cudaSuccess ? TF_OK : cuda_fail(r);
 }
 
 }  // namespace
@@ -361,7 +881,46 @@ extern "C" int tf_sample_rows(const void* logits, int R, int V, int64_t row_stri
     if (V > TF_SAMPLE_MAX_VOCAB || R > (1 << 24)) return TF_ERANGE;
     int bits = 0;
     while ((int64_t(1) << bits) < V) ++bits;
-    const Args a = {static_cast<const uint16_t*>(logits), row_stride, temperature, top_k, top_p, min_p, u,
-                    pick, prob, flag, V, 63 - bits};
-    return launch_pdl(sample_rows_kernel, dim3(R), dim3(kThreads), 0, stream, a);
+    const bool vec = aligned16(logits) && row_stride % 8 == 0;
+    int rc = vec ? prepare<true>() : prepare<false>();
+    if (rc != TF_OK) return rc;
+    // CTAs a row: as many as one wave holds, at two an SM, while each has 16,384 tokens
+    int cl = kMaxCluster;
+    while (cl > 1 && (int64_t(R) * cl > 2 * sm_count() || V < cl * 16384)) cl /= 2;
+    Args a = {static_cast<const uint16_t*>(logits), row_stride, temperature, top_k, top_p, min_p, u,
+              pick, prob, flag, V, 63 - bits, ((V + cl - 1) / cl + 7) / 8 * 8};
+
+    // rows go in grid.y, at most 65,535 a launch
+    constexpr int kRowsPerLaunch = 65535;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cl;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    for (int r0 = 0; r0 < R; r0 += kRowsPerLaunch) {
+        const int nr = R - r0 < kRowsPerLaunch ? R - r0 : kRowsPerLaunch;
+        cfg.gridDim = dim3(cl, nr, 1);
+        Args b = a;
+        b.logits += size_t(r0) * size_t(row_stride);
+        for (const float** f : {&b.temperature, &b.top_p, &b.min_p, &b.u})
+            if (*f) *f += r0;
+        if (b.top_k) b.top_k += r0;
+        b.pick += r0;
+        if (b.prob) b.prob += r0;
+        b.flag += r0;
+        cudaError_t e = vec ? cudaLaunchKernelEx(&cfg, sample_rows_kernel<true>, b)
+                            : cudaLaunchKernelEx(&cfg, sample_rows_kernel<false>, b);
+        if (e != cudaSuccess) return cuda_fail(e);
+        rc = launch_status();
+        if (rc != TF_OK) return rc;
+    }
+    return TF_OK;
 }
