@@ -97,16 +97,26 @@ int copy_pages(void* const* pools, int n_pools, int page_keys, int n_pages, cons
     for (size_t p = 1; p < at.size(); ++p)
         if (at[p] - at[p - 1] < bytes) return TF_EINVAL;
     // ids in the pool; no page written twice, none both read and written
-    std::vector<int32_t> written;
     for (int i = 0; i < n; ++i) {
         if (src[i] < 0 || src[i] >= n_pages || dst[i] < 0 || dst[i] >= n_pages) return TF_EINVAL;
         if (keys && (keys[i] < 0 || keys[i] > page_keys)) return TF_EINVAL;
-        written.push_back(dst[i]);
     }
-    std::sort(written.begin(), written.end());
-    if (std::adjacent_find(written.begin(), written.end()) != written.end()) return TF_EINVAL;
-    for (int i = 0; i < n; ++i)
-        if (std::binary_search(written.begin(), written.end(), src[i])) return TF_EINVAL;
+    if (n_pages <= int64_t(1024) * (n + 64)) {   // a bit a page, unless the pool is huge beside the lists
+        std::vector<uint64_t> written(n_pages / 64 + 1);
+        for (int i = 0; i < n; ++i) {
+            const uint64_t bit = uint64_t(1) << (dst[i] & 63);
+            if (written[dst[i] >> 6] & bit) return TF_EINVAL;
+            written[dst[i] >> 6] |= bit;
+        }
+        for (int i = 0; i < n; ++i)
+            if (written[src[i] >> 6] >> (src[i] & 63) & 1) return TF_EINVAL;
+    } else {
+        std::vector<int32_t> written(dst, dst + n);
+        std::sort(written.begin(), written.end());
+        if (std::adjacent_find(written.begin(), written.end()) != written.end()) return TF_EINVAL;
+        for (int i = 0; i < n; ++i)
+            if (std::binary_search(written.begin(), written.end(), src[i])) return TF_EINVAL;
+    }
     if (n_pools == 0) return TF_OK;
     // few copies travel in a small argument block
     constexpr int kFew = 64, kMany = 2400;

@@ -91,14 +91,13 @@ def _load():
         "tf_attn": (i32, [vp, i32, vp, vp, vp, vp]),
         "tf_attn_block_partials": (i32, [vp, i32, vp, vp, vp]),
         "tf_attn_block": (i32, [vp, i32, vp, vp, vp, vp]),
-        "tf_paged_build": (i32, [P(tf_stream), i32, P(vp), P(vp), P(ctypes.c_int32), ctypes.c_int32, ctypes.c_int32,
+        "tf_paged_build": (i32, [P(tf_stream), i32, P(vp), P(vp), vp, ctypes.c_int32, ctypes.c_int32,
                                  P(vp), P(vp), i32, i32, vp, P(vp)]),
-        "tf_paged_prompt_build": (i32, [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, P(vp), P(ctypes.c_int32),
+        "tf_paged_prompt_build": (i32, [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, P(vp), vp,
                                         ctypes.c_int32, ctypes.c_int32, P(vp), P(vp), i32, i32, vp, P(vp)]),
         "tf_attn_paged": (i32, [vp, i32, vp, vp, vp, i32, vp]),
         "tf_qk_rows": (i32, [vp, i32, vp, i64, vp, i64, vp, i64, vp, vp, ctypes.c_float, ctypes.c_double, vp, vp]),
-        "tf_pages_copy": (i32, [P(vp), i32, ctypes.c_int32, ctypes.c_int32, P(ctypes.c_int32), P(ctypes.c_int32),
-                                P(ctypes.c_int32), i32, vp]),
+        "tf_pages_copy": (i32, [P(vp), i32, ctypes.c_int32, ctypes.c_int32, vp, vp, vp, i32, vp]),
         "tf_markov_chain": (i32, [vp, vp, vp, i32, vp, i64, vp, vp, vp, vp]),
         "tf_draft_ids": (i32, [vp, vp, vp, vp, i32, vp, vp, vp]),
         "tf_argmax_rows": (i32, [vp, i32, i32, i64, vp, vp, vp]),
@@ -126,20 +125,35 @@ def lib():
 
 
 def _ptr(x):
-    if x is None:
-        return None
-    if isinstance(x, int):
+    if x is None or isinstance(x, int):
         return x
     return x.data_ptr()
 
 
 def _stream(s):
     if s is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(s, int):
         return s
     return s.cuda_stream
+
+
+def _current_stream():
+    """The current PyTorch stream of the current device, as an integer (found
+    once how; a call's host time is a few microseconds)."""
+    global _current_stream
+    import torch
+
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is None:
+        def _current_stream():
+            return torch.cuda.current_stream().cuda_stream
+    else:
+        device = torch.cuda.current_device
+
+        def _current_stream():
+            return raw(device())
+    return _current_stream()
 
 
 def _check(fn, rc):
@@ -197,10 +211,8 @@ class Segments:
 def _ptr_array(ptrs):
     if ptrs is None:
         return None
-    arr = (ctypes.c_void_p * max(len(ptrs), 1))()
-    for i, p in enumerate(ptrs):
-        arr[i] = _ptr(p)
-    return arr
+    at = array.array("Q", [p if p.__class__ is int else 0 if p is None else p.data_ptr() for p in ptrs] or [0])
+    return (ctypes.c_void_p * len(at)).from_buffer(at)
 
 
 def tf_segments_build_status(streams, conv_state, conv_hist, k_cache, v_cache, n_conv, n_attn, stream=None):
@@ -237,23 +249,23 @@ def tf_prompt_build(rows, keys, kv_capacity, conv_state, k_cache, v_cache, n_con
 
 
 def _int32_array(x, n=None):
-    """A host int32 array for the library: a contiguous numpy int32 array or CPU
-    torch tensor is passed as it is, any other sequence is copied. ``n``: the
-    entries the call will read."""
+    """Address of a host int32 array and what keeps it alive: a contiguous numpy
+    int32 array or CPU torch tensor is used as it is, any other sequence is
+    copied. ``n``: the entries the call will read."""
     if x is None:
-        return None
+        return None, None
     if hasattr(x, "numpy"):
         if x.device.type != "cpu":
             raise ValueError("a host array is needed, not a device tensor")
         x = x.numpy()
-    if not (hasattr(x, "ctypes") and x.dtype.name == "int32" and x.flags.c_contiguous):
+    if getattr(x, "dtype", None) != "int32" or not x.flags.c_contiguous:
         x = array.array("i", (int(v) for v in x))
-        size, ptr = len(x), (ctypes.c_int32 * max(len(x), 1)).from_buffer(x if len(x) else array.array("i", [0]))
+        at = x.buffer_info()[0]
     else:
-        size, ptr = x.size, x.ctypes.data_as(ctypes.POINTER(ctypes.c_int32))
-    if n is not None and size < n:
-        raise ValueError(f"{size} entries where the call reads {n}")
-    return ptr
+        at = x.ctypes.data
+    if n is not None and len(x) < n:
+        raise ValueError(f"{len(x)} entries where the call reads {n}")
+    return at, x
 
 
 def tf_paged_build_status(streams, conv_state, conv_hist, pages, page_keys, n_pages, k_pool, v_pool, n_conv, n_attn,
@@ -262,8 +274,9 @@ def tf_paged_build_status(streams, conv_state, conv_hist, pages, page_keys, n_pa
     one after another, ``k_pool``/``v_pool``: a pool a layer."""
     out = ctypes.c_void_p()
     n = sum(st[3] // page_keys for st in streams) if page_keys > 0 else 0
+    at, _keep = _int32_array(pages, n)
     rc = _lib.tf_paged_build(_streams_array(streams), len(streams), _ptr_array(conv_state), _ptr_array(conv_hist),
-                             _int32_array(pages, n), page_keys, n_pages, _ptr_array(k_pool), _ptr_array(v_pool),
+                             at, page_keys, n_pages, _ptr_array(k_pool), _ptr_array(v_pool),
                              n_conv, n_attn, _stream(stream), ctypes.byref(out))
     return rc, out.value
 
@@ -282,7 +295,8 @@ def tf_paged_prompt_build_status(rows, keys, kv_capacity, conv_state, pages, pag
     """Raw status and handle of tf_paged_prompt_build."""
     out = ctypes.c_void_p()
     n = kv_capacity // page_keys if page_keys > 0 else 0
-    rc = _lib.tf_paged_prompt_build(rows, keys, kv_capacity, _ptr_array(conv_state), _int32_array(pages, n), page_keys,
+    at, _keep = _int32_array(pages, n)
+    rc = _lib.tf_paged_prompt_build(rows, keys, kv_capacity, _ptr_array(conv_state), at, page_keys,
                                     n_pages, _ptr_array(k_pool), _ptr_array(v_pool), n_conv, n_attn, _stream(stream),
                                     ctypes.byref(out))
     return rc, out.value
@@ -355,8 +369,9 @@ def tf_pages_copy(pools, page_keys, n_pages, src, dst, keys=None, stream=None):
     """Copy keys [0, keys[i]) (all of them without ``keys``) of page src[i] to
     page dst[i] in every pool."""
     n = len(src)
-    _check("tf_pages_copy", _lib.tf_pages_copy(_ptr_array(pools), len(pools), page_keys, n_pages, _int32_array(src, n),
-                                               _int32_array(dst, n), _int32_array(keys, n), n, _stream(stream)))
+    (s, _s), (d, _d), (k, _k) = _int32_array(src, n), _int32_array(dst, n), _int32_array(keys, n)
+    _check("tf_pages_copy", _lib.tf_pages_copy(_ptr_array(pools), len(pools), page_keys, n_pages, s, d, k, n,
+                                               _stream(stream)))
 
 
 def tf_qk_rows(seg, attn_layer, q, q_stride, k, k_stride, v, v_stride, q_norm, k_norm, eps, theta, q_out, stream=None):

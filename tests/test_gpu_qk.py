@@ -163,6 +163,26 @@ def test_prompt(mods, page, rows, cached):
     c.seg.free()
 
 
+@pytest.mark.parametrize("page", [0, 16, 128])
+@pytest.mark.parametrize("streams", [64, 14, 15])
+def test_many_rows(mods, page, streams):
+    """1,024 rows, and rows about the 512 from which a warp takes a whole row (504 and 540)."""
+    shape = [(16, 20 + 61 * s) for s in range(64)] if streams == 64 else STREAMS * streams
+    c = Case(mods, shape, page, seed=streams + page, pads=(8, 0, 0))
+    before = c.copies()
+    c.run(mods)
+    c.check(mods, before)
+    c.seg.free()
+
+
+def test_many_rows_in_place(mods):
+    c = Case(mods, STREAMS * 20, 64, seed=30)
+    before, q = c.copies(), c.q.clone()
+    c.run(mods, out=c.qb)
+    c.check(mods, before, q=q, out=c.qb)
+    c.seg.free()
+
+
 @pytest.mark.parametrize("pads", [(64, 0, 8), (8, 128, 512), (0, 8, 0)])
 def test_row_strides(mods, pads):
     c = Case(mods, STREAMS, 16, seed=3, pads=pads)

@@ -28,6 +28,9 @@ def status(T, pools=(P0, P0 + POOL), page=16, n_pages=8, src=(0, 1), dst=(2, 3),
     dict(dst=(2, 2)),                                               # written twice
     dict(dst=(2, 0)), dict(src=(0, 3)), dict(src=(2, 1)),           # written and read
     dict(keys=[16, 17]), dict(keys=[-1, 4]),
+    dict(n_pages=1 << 20, dst=(1 << 19, 1 << 19)),                  # the same in a pool far larger than the lists
+    dict(n_pages=1 << 20, dst=(2, 0)), dict(n_pages=1 << 20, src=(9, 1 << 19), dst=(1 << 19, 3)),
+    dict(n_pages=1 << 20, src=(0, 1 << 20)),
 ])
 def test_refused(T, change):
     assert status(T, **change) == T.TF_EINVAL
