@@ -39,8 +39,7 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kUnroll = 4;                       // 16-byte loads a thread asks for at a time, counting
-constexpr int kSearch = 4;                       // and searching
+constexpr int kUnroll = 4;                       // 16-byte loads a thread asks for at a time
 constexpr int kSide = 5120;                      // positions a side of the sorted window
 constexpr int kTopMag = 0x42FF;                  // the folded window's largest magnitude, just below 128
 constexpr int kLowMag = kTopMag - kSide + 2;     // and its smallest, just above 2^-33: kSide - 1 of them
@@ -430,6 +429,7 @@ struct Row {
     // window's mass, and the mass of the slices before this one in `slice_at`.
     template <bool kFold>
     __device__ __forceinline__ u64 weigh(const Scale& scale, int top, int32_t counted, u64& slice_at) const {
+        uint32_t keep = ~0u;   // this thread's groups that top-k leaves tokens in, a bit a round
         if (K < a.V) {
             for (int r = 0; r < rank; ++r) counted += sh.count[r];
             for (int g = int(threadIdx.x); g < groups(); g += kThreads) {
@@ -442,23 +442,26 @@ struct Row {
             }
             __syncthreads();
             prefix();
-            for (int g = int(threadIdx.x); g < groups(); g += kThreads) {
-                if (counted + int64_t(before()[g + 1]) <= K) continue;
+            keep = 0;
+            for (int g = int(threadIdx.x), bit = 0; g < groups(); g += kThreads, ++bit) {
                 int32_t left = K - counted - int32_t(before()[g]);
+                if (left <= 0) break;
+                keep |= 1u << bit;
+                if (left >= int32_t(before()[g + 1] - before()[g])) continue;
 #pragma unroll 1
-                for (int pos = s0 + kGroup * g; pos < s0 + kGroup * (g + 1); ++pos) {
+                for (int pos = s0 + kGroup * g; pos < s0 + kGroup * (g + 1); ++pos) {   // the K-th token's group
                     const int32_t c = int32_t(hist()[word_of(pos)]);
-                    if (c > left) hist()[word_of(pos)] = uint32_t(max(left, 0));
-                    left -= c;
+                    if (c > left) hist()[word_of(pos)] = uint32_t(left);
+                    left -= min(c, left);
                 }
             }
             __syncthreads();
         }
 #pragma unroll 1
-        for (int g = int(threadIdx.x); g < groups(); g += kThreads) {
+        for (int g = int(threadIdx.x); g < groups(); g += kThreads, keep >>= 1) {
             u64 m = 0;
             uint32_t n[kGroup];
-            if (load_group(g, n)) {
+            if ((keep & 1u) && load_group(g, n)) {
                 u64 w[kGroup];
                 group_weights<kFold>(g, scale, top, w);
 #pragma unroll
@@ -574,6 +577,7 @@ struct Row {
 #pragma unroll
         for (int j = 0; j < kGroup; ++j)
             if (s0 + kGroup * g + j < lo) x += n[j] * w[j];
+        x = min(x, at + before()[g + 1]);   // a group past the K-th token weighs nothing
         tell_alone(sh.cut[1], x);
     }
     // The pick at cumulative mass `target`, into every CTA.
@@ -708,7 +712,7 @@ sample_rows_kernel(const __grid_constant__ Args a) {
                 const uint32_t e = (w & 0x80008000u) | (r << 2 & 0x7FFF7FFFu);   // byte offsets less 4; the low
                 atomicAdd(reinterpret_cast<uint32_t*>(dyn + (e & 0xFFFFu) + 4), 1u);  // half's bit 15 adds 2
                 atomicAdd(reinterpret_cast<uint32_t*>(dyn + (e >> 16) + 2), 1u);      // to the high one's
-            } else {
+            } else if (w != 0xFF80FF80u) {   // not two masked tokens
                 count_one(w & 0xFFFFu);
                 count_one(w >> 16);
             }
@@ -772,78 +776,51 @@ sample_rows_kernel(const __grid_constant__ Args a) {
         a.flag[row] = 0;
     }
 
-    // ---- the second pass: the want-th token of value pick_key. A warp counts one
-    // contiguous part of the CTA's tokens in steps of kStep, lane j keeping step
-    // j's count, so the counts of the CTAs, warps and steps before a token say how
-    // many come before its step, which one more read searches.
-    constexpr int kStep = kSearch * 32 * 8;
-    static_assert(TF_SAMPLE_MAX_VOCAB <= kStep * 32 * kWarps, "a lane a step");
-    const uint32_t bits = uint32_t(pick_key < 0 ? -pick_key | 0x8000 : pick_key);
-    const int part = ((end - begin + kWarps - 1) / kWarps + 7) / 8 * 8;
-    const int w0 = min(end, begin + warp * part), w1 = min(end, w0 + part);
-    const uint32_t both = bits * 0x10001u;
+    // ---- the second pass: the want-th token of value pick_key, over the CTA's
+    // tokens in chunks, a step of each warp's in turn, the next chunk's loads in
+    // flight. A CTA alone in its row stops at the chunk that holds the token, half way
+    // through the row on average; in a cluster each counts all of its chunks, and the
+    // one that holds the token reads its step again.
+    constexpr int kStep = kUnroll * 32 * 8, kChunk = kStep * kWarps;
+    static_assert(TF_SAMPLE_MAX_VOCAB / kChunk * kWarps <= kSide, "the counts go over the histogram");
+    const uint32_t bits = uint32_t(pick_key < 0 ? -pick_key | 0x8000 : pick_key), both = bits * 0x10001u;
     const __nv_bfloat162 ref = *reinterpret_cast<const __nv_bfloat162*>(&both);
-    // the lane's 8 tokens from i on (those before w1) that are the pick's value, a bit each
+    // the lane's 8 tokens from i on that are the pick's value, a bit each
     auto hits_at = [&](int i, const uint4& v) {
         uint32_t h = 0;
-        if (kVec && i + 8 <= w1) {
+        if (kVec && i + 8 <= end) {
             const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+            uint32_t m[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                h |= (__heq2_mask(*reinterpret_cast<const __nv_bfloat162*>(&x[k]), ref) & 0x10001u) << 2 * k;
-            h = (h | h >> 15) & 0xFFu;   // the high tokens' bits between the low ones'
+            for (int k = 0; k < 4; ++k) m[k] = __heq2_mask(*reinterpret_cast<const __nv_bfloat162*>(&x[k]), ref);
+            if (m[0] | m[1] | m[2] | m[3]) {   // rarely
+#pragma unroll
+                for (int k = 0; k < 4; ++k) h |= (m[k] & 0x10001u) << 2 * k;
+                h = (h | h >> 15) & 0xFFu;   // the high tokens' bits between the low ones'
+            }
         } else {
 #pragma unroll 1
             for (int k = 0; k < 8; ++k)
-                if (i + k < w1 && key_of(p[i + k]) == pick_key) h |= 1u << k;
+                if (i + k < end && key_of(p[i + k]) == pick_key) h |= 1u << k;
         }
         return h;
     };
-    auto load = [&](uint4 (&v)[kSearch], int i0) {
+    auto load = [&](uint4 (&v)[kUnroll], int i0) {
 #pragma unroll
-        for (int k = 0; k < kSearch; ++k)
-            if (kVec && i0 + 256 * k + 8 * lane + 8 <= w1)
+        for (int k = 0; k < kUnroll; ++k)
+            if (kVec && i0 + 256 * k + 8 * lane + 8 <= end)
                 v[k] = __ldg(reinterpret_cast<const uint4*>(p + i0 + 256 * k + 8 * lane));
     };
-    int32_t n = 0, steps = 0;   // the warp's count, this lane's step's
-    uint4 v[kSearch], next[kSearch];
-    load(v, w0);
-    for (int i0 = w0, j = 0; i0 < w1; i0 += kStep, ++j) {
-        load(next, i0 + kStep);
-        int32_t c = 0;
-#pragma unroll
-        for (int k = 0; k < kSearch; ++k) c += __popc(hits_at(i0 + 256 * k + 8 * lane, v[k]));
-#pragma unroll
-        for (int k = 0; k < kSearch; ++k) v[k] = next[k];
-        c = __reduce_add_sync(0xFFFFFFFFu, c);
-        if (lane == j) steps = c;
-        n += c;
-    }
-    if (lane == 0) sh.warp_int[0][warp] = n;
-    __syncthreads();
-    const int32_t x = lane < kWarps ? sh.warp_int[0][lane] : 0;
-    int32_t before = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? x : 0);
-    if (ncl > 1) {
-        R.tell(sh.found[rank], __reduce_add_sync(0xFFFFFFFFu, x));
-        R.sync();   // the last use of another CTA's memory
-        for (int r = 0; r < rank; ++r) before += sh.found[r];
-    }
-    if (before <= want && want < before + n) {
-        // the step, then 8 tokens a lane of it at a time
-        int32_t left = want - before, incl = steps;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int32_t t = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-            if (lane >= o) incl += t;
-        }
-        const int j = __ffs(__ballot_sync(0xFFFFFFFFu, left < incl)) - 1;
-        left -= __shfl_sync(0xFFFFFFFFu, incl - steps, j);
-        const int i0 = w0 + j * kStep;
-        load(v, i0);
-#pragma unroll
-        for (int k = 0; k < kSearch; ++k) {
+    // the left-th of the warp's tokens of the pick's value, in its step from i0 on
+    auto finish = [&](int i0, const uint4 (&v)[kUnroll], int32_t left) {
+#pragma unroll 1
+        for (int k = 0; k < kUnroll; ++k) {
             const int i = i0 + 256 * k + 8 * lane;
-            uint32_t h = hits_at(i, v[k]);
+            uint4 x = v[0];
+#pragma unroll
+            for (int j = 1; j < kUnroll; ++j)
+                if (j == k) x = v[j];
+            uint32_t h = hits_at(i, x);
             const int32_t c = __popc(h);
             int32_t upto = c;
 #pragma unroll
@@ -858,6 +835,54 @@ sample_rows_kernel(const __grid_constant__ Args a) {
             left -= __shfl_sync(0xFFFFFFFFu, upto, 31);
             if (left < 0) break;
         }
+    };
+    int32_t* const counts = reinterpret_cast<int32_t*>(hist);   // [chunk][warp]; the histogram is done with
+    const int chunks = (end - begin + kChunk - 1) / kChunk;
+    int32_t before = 0;    // tokens of the value in the chunks so far
+    uint4 v[kUnroll], next[kUnroll];
+    load(v, begin + warp * kStep);
+    for (int j = 0; j < chunks; ++j) {
+        const int i0 = begin + j * kChunk + warp * kStep;
+        load(next, i0 + kChunk);
+        int32_t c = 0;
+#pragma unroll
+        for (int k = 0; k < kUnroll; ++k)
+            if (const uint32_t h = hits_at(i0 + 256 * k + 8 * lane, v[k])) c += __popc(h);
+        c = __reduce_add_sync(0xFFFFFFFFu, c);
+        if (lane == 0) counts[j * kWarps + warp] = c;
+        if (ncl == 1) {
+            __syncthreads();
+            const int32_t x = lane < kWarps ? counts[j * kWarps + lane] : 0;
+            const int32_t all = __reduce_add_sync(0xFFFFFFFFu, x);
+            if (want < before + all) {
+                const int32_t left = want - before - __reduce_add_sync(0xFFFFFFFFu, lane < warp ? x : 0);
+                if (0 <= left && left < c) finish(i0, v, left);
+                return;
+            }
+            before += all;
+        }
+#pragma unroll
+        for (int k = 0; k < kUnroll; ++k) v[k] = next[k];
+    }
+    __syncthreads();
+    // this CTA's count; then the counts of the CTAs before it
+    int32_t n = 0;
+    for (int i = lane; i < chunks * kWarps; i += 32) n += counts[i];
+    n = __reduce_add_sync(0xFFFFFFFFu, n);
+    R.tell(sh.found[rank], n);
+    R.sync();   // the last use of another CTA's memory
+    for (int r = 0; r < rank; ++r) before += sh.found[r];
+    if (want < before || want >= before + n) return;
+    for (int j = 0; j < chunks; ++j) {   // the warp whose step it is
+        const int32_t x = lane < kWarps ? counts[j * kWarps + lane] : 0;
+        const int32_t at = before + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? x : 0);
+        if (at <= want && want < at + __shfl_sync(0xFFFFFFFFu, x, warp)) {
+            const int i0 = begin + j * kChunk + warp * kStep;
+            load(v, i0);
+            finish(i0, v, want - at);
+            return;
+        }
+        before += __reduce_add_sync(0xFFFFFFFFu, x);
     }
 }
 
