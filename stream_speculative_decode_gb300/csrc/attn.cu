@@ -30,10 +30,10 @@
 // all of the stream's keys instead of its causal count; nothing else changes,
 // and the merge is shared (it reads only the records).
 //
-// Paged tables (tf_attn_paged) run the same kernels with kPaged set: the
-// chunk's page ids are read into shared memory before the dependency wait (the
-// table is immutable), every 16-byte copy finds its page there, and the output
-// is bf16. A page holds at least 16 keys, so each 2 KB of a head's K or V is
+// Paged tables (tf_attn_paged) run the same kernels with kPaged set: where each
+// 16 keys of the chunk lie is worked out into shared memory before the
+// dependency wait (the table is immutable), every 16-byte copy finds its
+// address there, and the output is bf16. A page holds at least 16 keys, so each 2 KB of a head's K or V is
 // still contiguous and the copies stay whole 128-byte lines.
 #include "attn_item.cuh"
 
@@ -58,23 +58,22 @@ attn_partials_kernel(SegTable t, int layer, const uint16_t* __restrict__ q,
     const int g = blockIdx.x % TF_NKV;
     const AttnItem it = t.items[blockIdx.x / TF_NKV];
     const SegStream st = t.streams[it.stream];
-    int32_t* page_ids = nullptr;
+    uint32_t* blocks = nullptr;
     if constexpr (kPaged) {
-        page_ids = reinterpret_cast<int32_t*>(smem + smem_bytes(MT));
-        const int c0 = it.chunk * st.chunk_keys;
-        item::load_page_ids(t, it.stream, c0, min(st.chunk_keys, st.keys - c0), page_ids, threadIdx.x, kThreads);
-        __syncthreads();
-    }
-    if constexpr (MT == 1 && kPaged) {   // the same prefetch, a page a thread (at most 12 pages)
+        blocks = reinterpret_cast<uint32_t*>(smem + smem_bytes(MT));
         const int nkeys = min(st.chunk_keys, st.keys - it.chunk * st.chunk_keys);
-        const int k0 = int(threadIdx.x) << t.page_shift;
-        const int n = min(min(nkeys, (item::kStages - 1) * item::kKT) - k0, 1 << t.page_shift);
-        if (n > 0) {
-            const size_t slot = size_t(layer) * t.S + it.stream;
-            const size_t off = ((size_t(page_ids[threadIdx.x]) * TF_NKV + g) << t.page_shift) * TF_D;
-            l2_prefetch_bulk(static_cast<const uint16_t*>(t.k_cache[slot]) + off, uint32_t(n) * item::kRowB);
-            l2_prefetch_bulk(static_cast<const uint16_t*>(t.v_cache[slot]) + off, uint32_t(n) * item::kRowB);
+        item::load_blocks(t, it, nkeys, g, blocks, threadIdx.x, kThreads);
+        if constexpr (MT == 1) {   // the same prefetch, a block a thread (12 of them)
+            const int k0 = int(threadIdx.x) * item::kBlockKeys;
+            const int n = min(min(nkeys, (item::kStages - 1) * item::kKT) - k0, item::kBlockKeys);
+            if (n > 0) {
+                const size_t slot = size_t(layer) * t.S + it.stream;
+                const size_t off = size_t(blocks[threadIdx.x]) * item::kBlockElems;
+                l2_prefetch_bulk(static_cast<const uint16_t*>(t.k_cache[slot]) + off, uint32_t(n) * item::kRowB);
+                l2_prefetch_bulk(static_cast<const uint16_t*>(t.v_cache[slot]) + off, uint32_t(n) * item::kRowB);
+            }
         }
+        __syncthreads();
     }
     if constexpr (MT == 1 && !kPaged) {
         // narrow windows (one m-tile: short launches, one wave): the first
@@ -94,7 +93,7 @@ attn_partials_kernel(SegTable t, int layer, const uint16_t* __restrict__ q,
     pdl_wait();   // the table above; queries and caches below
     const int mode = out ? st.merge_mode : kMergeKernel;   // records only in the two-call form
     item::attn_item<MT, true, 0, kPaged>(t, layer, it, st, g, q, part_o, part_ml, out, mode, full, smem, threadIdx.x,
-                                         true, page_ids);
+                                         true, blocks);
     if (mode == kMergeLastCta) {
         __shared__ int last_flag;
         finish_last_cta<MT == 1 ? 8 : 16>(t, layer, it.stream, st, g, part_o, part_ml, out, &last_flag);
@@ -223,7 +222,7 @@ attn_merge_kernel(SegTable t, const float* __restrict__ part_o, const float2* __
 }
 
 template <int MT, bool kPaged>
-constexpr int partials_smem() { return smem_bytes(MT) + (kPaged ? item::kPageIdsB : 0); }
+constexpr int partials_smem() { return smem_bytes(MT) + (kPaged ? item::kBlocksB : 0); }
 
 template <int MT, bool kPaged>
 int prepare_one() {

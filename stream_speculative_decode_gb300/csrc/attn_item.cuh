@@ -36,19 +36,26 @@ constexpr float kTau = 8.f;             // lazy-rescale threshold, log2 units
 
 __host__ __device__ constexpr int smem_bytes(int mt) { return kStages * kStageB + 16 * mt * kRowB; }
 
-// Paged tables: the chunk's page ids sit in shared memory behind the item's
-// own part. A chunk holds at most 512 * TF_MAX_ROWS = 8,192 keys (256 * 32 for
-// a prompt's windows), 512 pages of 16 keys.
-constexpr int kMaxChunkPages = 512;
-constexpr int kPageIdsB = kMaxChunkPages * 4;
+// Paged tables: where each 16 keys of the chunk lie in head g of the layer's
+// pools, counted in such blocks of 2 KB (at most 2^31 a pool), sits in shared
+// memory behind the item's own part: a stage's four blocks are one load, a
+// copy's address one multiply-add. A chunk holds at most 512 * TF_MAX_ROWS =
+// 8,192 keys (256 * 32 for a prompt's windows), 512 blocks.
+constexpr int kBlockKeys = TF_MIN_PAGE_KEYS;
+constexpr int kBlocksB = 512 * TF_MAX_ROWS / kBlockKeys * 4;
+constexpr int kBlockElems = kBlockKeys * TF_D;
+static_assert(int64_t(TF_MAX_PAGES) * TF_NKV * (TF_MAX_PAGE_KEYS / kBlockKeys) <= int64_t(1) << 31, "32-bit blocks");
+static_assert(kKT / kBlockKeys == 4 && kThreads / 8 == kBlockKeys, "a stage's blocks, a thread's row of each");
 
-// The page ids of keys [c0, c0 + nkeys) of a stream into `ids`, by `nthreads`
-// threads (the caller synchronises them). c0 is a multiple of every page size.
-__device__ __forceinline__ void load_page_ids(const SegTable& t, int stream, int c0, int nkeys, int32_t* ids, int tid,
-                                              int nthreads) {
-    const int32_t* src = t.pages + t.page_first[stream] + (c0 >> t.page_shift);
-    const int n = (nkeys + (1 << t.page_shift) - 1) >> t.page_shift;
-    for (int i = tid; i < n; i += nthreads) ids[i] = src[i];
+// The blocks of an item's chunk of nkeys keys, to whole stages (block 0 past the
+// last key), by `nthreads` threads (the caller synchronises them).
+__device__ __forceinline__ void load_blocks(const SegTable& t, const AttnItem& item, int nkeys, int g,
+                                            uint32_t* blocks, int tid, int nthreads) {
+    const int32_t* pages = t.pages + item.pages;
+    const int bs = t.page_shift - 4;   // blocks a page, log2
+    for (int i = tid; i < (nkeys + kKT - 1) / kKT * 4; i += nthreads)
+        blocks[i] = i * kBlockKeys < nkeys
+                        ? ((uint32_t(__ldg(pages + (i >> bs))) * TF_NKV + g) << bs) + (i & ((1 << bs) - 1)) : 0u;
 }
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
@@ -142,14 +149,14 @@ __device__ __forceinline__ bool bar_and(int id, bool x) {
 //   V below 2^-14 round, by at most 2^-25 each.
 //   trigger: let the stream's next kernel launch once the passes are done.
 // The caller has passed griddepcontrol.wait.
-// kPaged: the chunk's keys lie in the pages `page_ids` (shared memory,
-// load_page_ids) of the layer's pools, and the output is bf16.
+// kPaged: the chunk's keys lie at `blocks` (shared memory, load_blocks) of the
+// layer's pools, and the output is bf16.
 template <int MT, bool kFast, int kBar, bool kPaged = false>
 __device__ __forceinline__ void attn_item(const SegTable& t, int layer, const AttnItem item, const SegStream& st,
                                           int g, const uint16_t* __restrict__ q, float* __restrict__ part_o,
                                           float2* __restrict__ part_ml, OutT<kPaged>* __restrict__ out, int mode,
                                           int full, unsigned char* smem, int tid, bool trigger,
-                                          const int32_t* page_ids = nullptr) {
+                                          const uint32_t* blocks = nullptr) {
     constexpr bool kQReg = MT <= 2;
     constexpr int bar = kBar;
     const int nq_all = st.rows * 4;
@@ -180,16 +187,25 @@ __device__ __forceinline__ void attn_item(const SegTable& t, int layer, const At
     auto issue = [&](int s) {
         const uint32_t buf = sKV32 + (s % kStages) * kStageB;
         const int key0 = s * kKT;
+        uint32_t block[4];
+        if constexpr (kPaged) {
+            const uint4 b = reinterpret_cast<const uint4*>(blocks)[s];
+            block[0] = b.x;
+            block[1] = b.y;
+            block[2] = b.z;
+            block[3] = b.w;
+        }
 #pragma unroll
         for (int k = 0; k < (kKT * 8) / kThreads; ++k) {
             const int idx = tid + k * kThreads;
             const int r = idx >> 3, ch = idx & 7;
             const bool valid = key0 + r < nkeys;
             size_t off = size_t(key0 + r) * TF_D + ch * 8;
-            if constexpr (kPaged) {   // slot of the key's page; a page id is read only for a key of the chunk
-                const int key = key0 + r, ps = t.page_shift;
-                const int64_t head = int64_t(valid ? page_ids[key >> ps] : 0) * TF_NKV + g;
-                off = ((size_t(head) << ps) + (key & ((1 << ps) - 1))) * TF_D + ch * 8;
+            if constexpr (kPaged) {   // row r is row tid / 8 of block k
+                off = size_t(block[k]) * kBlockElems + (tid >> 3) * TF_D + (tid & 7) * 8;
+                cp_async16(buf + swz(r, ch), Kg + off, valid);
+                cp_async16(buf + kKT * kRowB + swz(r, ch), Vg + off, valid);
+                continue;
             }
             cp_async16(buf + swz(r, ch), valid ? Kg + off : Kg, valid);
             cp_async16(buf + kKT * kRowB + swz(r, ch), valid ? Vg + off : Vg, valid);

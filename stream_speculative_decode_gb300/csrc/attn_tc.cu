@@ -144,6 +144,7 @@ struct Unit {
     const CUtensorMap* kmap;
     const CUtensorMap* vmap;
     int stream, chunk, g, c0, T;
+    int pages;   // paged: the list entry of the chunk's first key
 };
 template <bool kPaged>
 __device__ __forceinline__ Unit unit_of(const SegTable& t, int layer, int u) {
@@ -153,6 +154,7 @@ __device__ __forceinline__ Unit unit_of(const SegTable& t, int layer, int u) {
     U.stream = it.stream;
     U.chunk = it.chunk;
     U.st = t.streams[it.stream];
+    U.pages = it.pages;
     U.c0 = it.chunk * U.st.chunk_keys;
     U.T = (min(U.st.chunk_keys, U.st.keys - U.c0) + kKT - 1) / kKT;
     const size_t slot = kPaged ? size_t(layer) : size_t(layer) * t.S + it.stream;
@@ -164,7 +166,7 @@ __device__ __forceinline__ Unit unit_of(const SegTable& t, int layer, int u) {
 // The page ids of tile j of a unit (x only for pages of 64 keys or more, x and
 // y for 32-key pages, all four for 16-key pages).
 __device__ __forceinline__ int4 tile_pages(const SegTable& t, const Unit& U, int j) {
-    const int32_t* ids = t.pages + t.page_first[U.stream] + ((U.c0 + j * kKT) >> t.page_shift);
+    const int32_t* ids = t.pages + U.pages + ((j * kKT) >> t.page_shift);   // c0 starts a page
     if (t.page_shift == 4) return __ldg(reinterpret_cast<const int4*>(ids));
     if (t.page_shift == 5) {
         const int2 p = __ldg(reinterpret_cast<const int2*>(ids));
@@ -443,17 +445,18 @@ __device__ __noinline__ void recompute_exact(const SegTable& t, int layer, const
     for (int k = 0; k < n; ++k) {
         const Unit U = unit_of<kPaged>(t, layer, __ldcg(t.tc_redo + 1 + k));
         const int mode = out ? U.st.merge_mode : kMergeKernel;
-        int32_t* page_ids = nullptr;
+        uint32_t* blocks = nullptr;
         if constexpr (kPaged) {
-            static_assert(item::smem_bytes(2) + item::kPageIdsB <= kQB + kStages * kStageB, "shared memory");
-            page_ids = reinterpret_cast<int32_t*>(smem + item::smem_bytes(2));
-            item::load_page_ids(t, U.stream, U.c0, min(U.st.chunk_keys, U.st.keys - U.c0), page_ids, tid, 128);
+            static_assert(item::smem_bytes(2) + item::kBlocksB <= kQB + kStages * kStageB, "shared memory");
+            blocks = reinterpret_cast<uint32_t*>(smem + item::smem_bytes(2));
+            item::load_blocks(t, AttnItem{U.stream, U.chunk, 0, U.pages}, min(U.st.chunk_keys, U.st.keys - U.c0), U.g,
+                              blocks, tid, 128);
             item::bar_sync(1);
         }
         for (int q0 = 0; q0 < 4 * U.st.rows; q0 += 32) {
-            const AttnItem it{U.stream, U.chunk, q0, 0};
+            const AttnItem it{U.stream, U.chunk, q0, U.pages};
             item::attn_item<2, false, 1, kPaged>(t, layer, it, U.st, U.g, q, part_o, part_ml, out, mode, full, smem,
-                                                 tid, false, page_ids);
+                                                 tid, false, blocks);
             item::bar_sync(1);   // the item's shared memory is reused by the next group
         }
         if (mode == kMergeLastCta) {
@@ -690,6 +693,8 @@ attn_partials_tc_kernel(SegTable t, int layer, const uint16_t* __restrict__ q, f
         for (int u = blockIdx.x, m = 0; u >= 0 && ok; ++m) {
             const Unit U = unit_of<kPaged>(t, layer, u);
             const int T = U.T;
+            // 16-byte pieces of the last tile's V that hold keys
+            const int first_zero = 8 * (min(U.st.chunk_keys, U.st.keys - U.c0) - (T - 1) * kKT);
             for (int j = 0; j < T; ++j, ++gt) {
                 const int s = gt % kStages;
                 if (!mbar_wait_warp(su32(&bars->kv_full[s]), (gt / kStages) & 1, abortp)) {
@@ -697,20 +702,20 @@ attn_partials_tc_kernel(SegTable t, int layer, const uint16_t* __restrict__ q, f
                     break;
                 }
                 const uint32_t vs = sStage + s * kStageB + kTileB + uint32_t(lane) * 16u;
+                if constexpr (kPaged) {
+                    // the last tile's rows past the stream's keys: whatever the page holds there, zero
+                    if (j + 1 == T) {
+                        for (int i = first_zero + lane; i < kTileB / 16; i += 32)
+                            sts128(sStage + s * kStageB + kTileB + uint32_t(i) * 16u, make_uint4(0u, 0u, 0u, 0u));
+                        __syncwarp();
+                    }
+                }
                 // all 16 loads first: one shared-memory round trip a tile, not
                 // one per 16 bytes (the volatile loads and stores keep their order)
                 constexpr int NC = kTileB / 16 / 32;
                 uint4 v[NC];
 #pragma unroll
                 for (int c = 0; c < NC; ++c) v[c] = lds128(vs + uint32_t(32 * c) * 16u);
-                if constexpr (kPaged) {   // rows past the stream's keys: whatever the page holds there, zero
-                    const int left = U.st.keys - U.c0 - j * kKT;
-                    if (left < kKT) {
-#pragma unroll
-                        for (int c = 0; c < NC; ++c)
-                            if (4 * c + (lane >> 3) >= left) v[c] = make_uint4(0u, 0u, 0u, 0u);
-                    }
-                }
 #pragma unroll
                 for (int c = 0; c < NC; ++c) {
                     v[c].x = bf2_to_h2(v[c].x);

@@ -288,6 +288,9 @@ int finish_build(std::unique_ptr<tf_segments> owned, std::vector<tf::SegStream>&
         }
         items.swap(groups);
     }
+    if (pg)
+        for (AttnItem& it : items)
+            it.pages = (*page_first)[it.stream] + it.chunk * ss[it.stream].chunk_keys / pg->page_keys;
     // mma.sync items first, then tensor-core items; within each, largest
     // chunks first so the long work starts early in the grid
     std::stable_sort(items.begin(), items.end(), [&](const AttnItem& a, const AttnItem& b) {

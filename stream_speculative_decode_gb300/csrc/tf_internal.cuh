@@ -37,9 +37,10 @@ struct ConvTile {
 // An attention work item: one key chunk of one stream (for every KV head) and,
 // on the mma.sync path, one group of at most kMmaGroupRows window rows: query
 // rows [q0, q0 + 4*kMmaGroupRows) of the KV head (q0 = 0 on the tensor-core
-// path, which takes the whole window).
+// path, which takes the whole window). pages: paged tables, the entry of the
+// table's page lists that holds the chunk's first key.
 struct AttnItem {
-    int32_t stream, chunk, q0, pad;
+    int32_t stream, chunk, q0, pages;
 };
 
 // Window rows of one mma.sync item: two 16-row query m-tiles, the most that
