@@ -203,8 +203,9 @@ struct Shared {
     // what the cluster's CTAs tell one another, by rank
     u64 mass[kMaxCluster];
     int32_t first[kMaxCluster], count[kMaxCluster], other[kMaxCluster], found[kMaxCluster];
-    u64 cut[2];             // mass kept by top-p and by min-p, each from the CTA that found it
-    int32_t pick_key, want;
+    u64 min_p_mass;         // mass kept by min-p
+    int32_t hit_key;        // the value that find() found, the mass before it and its weight
+    u64 hit_mass, hit_weight;
     u64 before[kValues / kGroup + 1];   // the mass before each group of the slice, and its whole
 };
 static_assert(kSide * 4 + sizeof(Shared) <= 32768, "the gap");
@@ -230,7 +231,7 @@ struct Args {
     int32_t chunk;       // tokens a CTA of the cluster counts, a multiple of 8
 };
 
-// f(word of two tokens) over 16-byte vectors, f1(bits) for the rest of [begin, end).
+// f(16 bytes, 8 tokens) and f1(bits) for the rest of [begin, end).
 template <bool kVec, typename F, typename F1>
 __device__ __forceinline__ void for_tokens(const uint16_t* p, int begin, int end, F&& f, F1&& f1) {
     if constexpr (kVec) {
@@ -244,22 +245,79 @@ __device__ __forceinline__ void for_tokens(const uint16_t* p, int begin, int end
                 if (i + u * kThreads < nvec) x[u] = __ldg(pv + i + u * kThreads);
         };
         load(v, threadIdx.x);
+#pragma unroll 1
         for (int i = threadIdx.x; i < nvec; i += kUnroll * kThreads) {
             load(next, i + kUnroll * kThreads);
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {
                 if (i + u * kThreads >= nvec) break;
-                f(v[u].x);
-                f(v[u].y);
-                f(v[u].z);
-                f(v[u].w);
+                f(v[u]);
             }
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) v[u] = next[u];
         }
         begin += nvec * 8;
     }
+#pragma unroll 1
     for (int i = begin + threadIdx.x; i < end; i += kThreads) f1(uint32_t(p[i]));
+}
+
+// Counts into the folded window; `other` becomes the largest value outside it
+// (NaN and +infinity as kBadKey), masked tokens aside.
+__device__ __forceinline__ int count_one(uint32_t* hist, uint32_t b, int other) {
+    const int d = int(b & 0x7FFFu) - kLowMag;
+    if (uint32_t(d) < uint32_t(kSide - 1)) {
+        atomicAdd(hist + (b & 0x8000u ? 8193 + d : 1 + d), 1u);
+    } else if (b != 0xFF80u) {
+        const int k = key_of(b);
+        if (k == 0) atomicAdd(hist, 1u);
+        else other = max(other, k >= kInfKey || k < kMinKey ? kBadKey : k);
+    }
+    return other;
+}
+// Halves of a word: 0x8000 + magnitude - kLowMag. Both tokens lie in the window
+// when these keep bit 15 and lose it with the window's size subtracted (no borrow
+// crosses a half).
+__device__ __forceinline__ uint32_t above_low(uint32_t w) { return (w | 0x80008000u) - uint32_t(kLowMag) * 0x10001u; }
+__device__ __forceinline__ uint32_t inside(uint32_t r) { return r & ~(r - uint32_t(kSide - 1) * 0x10001u); }
+__device__ __forceinline__ void count_word(unsigned char* dyn, uint32_t w, uint32_t r) {
+    const uint32_t e = (w & 0x80008000u) | (r << 2 & 0x7FFF7FFFu);        // byte offsets less 4; the low half's
+    atomicAdd(reinterpret_cast<uint32_t*>(dyn + (e & 0xFFFFu) + 4), 1u);  // bit 15 adds 2 to the high one's
+    atomicAdd(reinterpret_cast<uint32_t*>(dyn + (e >> 16) + 2), 1u);
+}
+// A word with a token outside that is not masked.
+__device__ __noinline__ int count_odd(uint32_t w, int other) {
+    extern __shared__ __align__(128) unsigned char dyn[];
+#pragma unroll 1
+    for (int k = 0; k < 2; ++k, w >>= 16)
+        if (!(inside(above_low(w & 0xFFFFu)) & 0x8000u)) other = count_one(reinterpret_cast<uint32_t*>(dyn), w & 0xFFFFu, other);
+    return other;
+}
+// 8 tokens of which some lie outside, or are masked, which all rows under a
+// grammar's mask hold (out of line: the counting loop has a copy a vector in
+// flight, and the kernel's code has to stay in the instruction caches).
+__device__ __noinline__ int count_mixed(uint4 v, int other) {
+    extern __shared__ __align__(128) unsigned char dyn[];
+    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t w = x[k], r = above_low(w), in = inside(r);
+        const uint32_t e = (w & 0x80008000u) | (r << 2 & 0x7FFF7FFFu), masked = w ^ 0xFF80FF80u;
+        // a half out of the window keeps the low half's two bits out of the high one's offset by the mask
+        if (in & 0x8000u) atomicAdd(reinterpret_cast<uint32_t*>(dyn + (e & 0xFFFCu) + 4), 1u);
+        if (in & 0x80000000u) atomicAdd(reinterpret_cast<uint32_t*>(dyn + (e >> 16 & 0xFFFCu) + 4), 1u);
+        if ((!(in & 0x8000u) && masked & 0xFFFFu) || (!(in & 0x80000000u) && masked >> 16)) other = count_odd(w, other);
+    }
+    return other;
+}
+
+// Tokens [i, min(i + 8, end)) one by one, `none` in the place of the others.
+__device__ __noinline__ uint4 load_part(const uint16_t* p, int i, int end, uint32_t none) {
+    uint32_t x[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        x[k / 2] |= ((i + k < end ? uint32_t(p[i + k]) : none) & 0xFFFFu) << 16 * (k & 1);
+    return make_uint4(x[0], x[1], x[2], x[3]);
 }
 
 // One CTA's part in its row. Every step that ends in sync() is taken by all
@@ -291,11 +349,13 @@ struct Row {
     // one thread's value into every CTA's `mine`
     template <typename X>
     __device__ __forceinline__ void tell_alone(X& mine, X v) const {
+#pragma unroll 1
         for (int r = 0; r < ncl; ++r) *cg::this_cluster().map_shared_rank(&mine, r) = v;
     }
 
     __device__ __forceinline__ void clear() const {
         uint4* h = reinterpret_cast<uint4*>(dyn);
+#pragma unroll 1
         for (int i = threadIdx.x; i < kSide / 2; i += kThreads)
             h[i < kSide / 4 ? i : 2048 + i - kSide / 4] = make_uint4(0, 0, 0, 0);
         __syncthreads();
@@ -328,6 +388,7 @@ struct Row {
     __device__ __forceinline__ Survey survey(int other) const {
         sync();
         if (ncl > 1) {
+#pragma unroll 1
             for (int i = s0 / 4 + int(threadIdx.x); i < s1 / 4; i += kThreads) {
                 const int w4 = min(word_of(4 * i), word_of(4 * i + 3)) / 4;   // 4 positions are 4 words
                 uint4 c = reinterpret_cast<uint4*>(hist())[w4], o[kMaxCluster];
@@ -349,6 +410,7 @@ struct Row {
             __syncthreads();
         }
         int first = kValues, n = 0;
+#pragma unroll 1
         for (int g = int(threadIdx.x); g < groups(); g += kThreads) {
             uint32_t c[kGroup];
             if (!load_group(g, c)) continue;
@@ -382,6 +444,7 @@ struct Row {
         tell(sh.other[rank], s.other);
         sync();
         s = {kValues, 0, kMinKey};
+#pragma unroll 1
         for (int r = 0; r < ncl; ++r) {
             s.first = min(s.first, sh.first[r]);
             s.count += sh.count[r];
@@ -397,6 +460,7 @@ struct Row {
         const int g0 = min(G, int(threadIdx.x) * per), g1 = min(G, g0 + per);
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
         u64 sum = 0;
+#pragma unroll 1
         for (int g = g0; g < g1; ++g) sum += before()[g];
         u64 incl = sum;
 #pragma unroll
@@ -414,6 +478,7 @@ struct Row {
         }
         const u64 total = __shfl_sync(0xFFFFFFFFu, w, kWarps - 1), prev = __shfl_sync(0xFFFFFFFFu, w, warp ? warp - 1 : 0);
         u64 at = (warp ? prev : 0) + incl - sum;
+#pragma unroll 1
         for (int g = g0; g < g1; ++g) {
             const u64 v = before()[g];
             before()[g] = at;
@@ -430,19 +495,35 @@ struct Row {
     template <bool kFold>
     __device__ __forceinline__ u64 weigh(const Scale& scale, int top, int32_t counted, u64& slice_at) const {
         uint32_t keep = ~0u;   // this thread's groups that top-k leaves tokens in, a bit a round
-        if (K < a.V) {
-            for (int r = 0; r < rank; ++r) counted += sh.count[r];
-            for (int g = int(threadIdx.x); g < groups(); g += kThreads) {
-                uint32_t c[kGroup];
-                load_group(g, c);
-                u64 n = 0;
+        u64 mine;
+        // counts first where top-k may cut them, then masses
+#pragma unroll 1
+        for (int masses = K < a.V ? 0 : 1;; masses = 1) {
+            uint32_t left_in = keep;
+#pragma unroll 1
+            for (int g = int(threadIdx.x); g < groups(); g += kThreads, left_in >>= 1) {
+                u64 m = 0;
+                uint32_t n[kGroup];
+                if ((left_in & 1u) && load_group(g, n)) {
+                    u64 w[kGroup];
+                    if (masses) {
+                        group_weights<kFold>(g, scale, top, w);
+                    } else {
 #pragma unroll
-                for (int j = 0; j < kGroup; ++j) n += c[j];
-                before()[g] = n;
+                        for (int j = 0; j < kGroup; ++j) w[j] = 1;
+                    }
+#pragma unroll
+                    for (int j = 0; j < kGroup; ++j) m += n[j] * w[j];
+                }
+                before()[g] = m;
             }
             __syncthreads();
-            prefix();
+            mine = prefix();
+            if (masses) break;
+#pragma unroll 1
+            for (int r = 0; r < rank; ++r) counted += sh.count[r];
             keep = 0;
+#pragma unroll 1
             for (int g = int(threadIdx.x), bit = 0; g < groups(); g += kThreads, ++bit) {
                 int32_t left = K - counted - int32_t(before()[g]);
                 if (left <= 0) break;
@@ -457,25 +538,12 @@ struct Row {
             }
             __syncthreads();
         }
-#pragma unroll 1
-        for (int g = int(threadIdx.x); g < groups(); g += kThreads, keep >>= 1) {
-            u64 m = 0;
-            uint32_t n[kGroup];
-            if ((keep & 1u) && load_group(g, n)) {
-                u64 w[kGroup];
-                group_weights<kFold>(g, scale, top, w);
-#pragma unroll
-                for (int j = 0; j < kGroup; ++j) m += n[j] * w[j];
-            }
-            before()[g] = m;
-        }
-        __syncthreads();
-        const u64 mine = prefix();
         slice_at = 0;
         if (ncl == 1) return mine;
         tell(sh.mass[rank], mine);
         sync();
         u64 total = 0;
+#pragma unroll 1
         for (int r = 0; r < ncl; ++r) {
             if (r < rank) slice_at += sh.mass[r];
             total += sh.mass[r];
@@ -486,65 +554,86 @@ struct Row {
     // The weights of group g's positions. A group of a folded window lies in one power of two
     // (the zero's aside), so its values are equal steps apart and each weight is the one before
     // times the step's, ratio[exponent]. Positions above the largest value hold no tokens.
+    struct Weights {
+        u64 x, ratio;     // a position's weight and the step's, in units of 2^-63
+        int key, round;
+    };
+    template <bool kFold>
+    __device__ __forceinline__ Weights first_weight(int pos, const Scale& scale, int top) const {
+        const int key = key_at<kFold>(pos, top);
+        return {weight(scale.template y<kFold>(min(key, top_key)), 63, sh.tab),
+                kFold ? sh.ratio[(abs(key) >> 7) - (kLowMag >> 7)] : 0, key, 63 - a.frac};
+    }
+    // The position's weight, and on to the next position's.
+    template <bool kFold>
+    __device__ __forceinline__ u64 next_weight(Weights& w, int pos, const Scale& scale) const {
+        const u64 x = (w.x + (u64(1) << w.round >> 1)) >> w.round;
+        --w.key;
+        if constexpr (kFold) {
+            if (w.key < top_key) w.x = __umul64hi(w.x, w.ratio) << 1;
+            return pos == kSide - 1 ? zero_weight(scale) : x;
+        }
+        w.x = weight(scale.template y<false>(min(w.key, top_key)), 63, sh.tab);
+        return x;
+    }
     template <bool kFold>
     __device__ __forceinline__ void group_weights(int g, const Scale& scale, int top, u64 (&w)[kGroup]) const {
         const int pos = s0 + kGroup * g;
-        if constexpr (!kFold) {
-#pragma unroll 1
-            for (int j = 0; j < kGroup; ++j) w[j] = weight_of<kFold>(scale, min(key_at<kFold>(pos + j, top), top_key), a.frac, sh.tab);
-            return;
-        }
-        const int key = key_at<true>(pos, 0), round = 63 - a.frac;
-        const u64 ratio = sh.ratio[(abs(key) >> 7) - (kLowMag >> 7)];
-        u64 x = weight(scale.template y<true>(min(key, top_key)), 63, sh.tab);
-#pragma unroll
-        for (int j = 0; j < kGroup; ++j) {
-            if (j > 0 && key - j < top_key) x = __umul64hi(x, ratio) << 1;
-            w[j] = (x + (u64(1) << round >> 1)) >> round;
-        }
-        if (pos == kSide - kGroup) w[kGroup - 1] = weight_of<true>(scale, min(0, top_key), a.frac, sh.tab);
-    }
-
-    // The weight of one key, out of line: the searches below are not worth a copy each.
-    template <bool kFold>
-    __device__ __noinline__ static u64 weight_of(const Scale& scale, int key, int frac, const ExpTables& tab) {
-        return weight(scale.template y<kFold>(key), frac, tab);
-    }
-
-    // f(key, mass before, weight) by the one thread that holds the value whose masses
-    // (before, after] hold m; `at` precedes the slice.
-    template <bool kFold, typename F>
-    __device__ __forceinline__ void find(u64 m, u64 at, const Scale& scale, int top, F&& f) const {
-        if (m <= at || m > at + before()[groups()]) return;
-        for (int g = int(threadIdx.x); g < groups(); g += kThreads) {
-            if (!(at + before()[g] < m && m <= at + before()[g + 1])) continue;
-            u64 x = at + before()[g], w[kGroup], hit = 0, hit_w = 0;
-            uint32_t n[kGroup];
-            int hit_pos = -1;
-            load_group(g, n);
-            group_weights<kFold>(g, scale, top, w);
+        Weights at = first_weight<kFold>(pos, scale, top);
+        if constexpr (kFold) {
 #pragma unroll
             for (int j = 0; j < kGroup; ++j) {
-                const u64 x1 = x + n[j] * w[j];
-                if (x < m && m <= x1) {
-                    hit_pos = s0 + kGroup * g + j;
-                    hit = x;
-                    hit_w = w[j];
+                w[j] = (at.x + (u64(1) << at.round >> 1)) >> at.round;
+                if (--at.key < top_key) at.x = __umul64hi(at.x, at.ratio) << 1;
+            }
+            if (pos == kSide - kGroup) w[kGroup - 1] = zero_weight(scale);
+        } else {
+#pragma unroll
+            for (int j = 0; j < kGroup; ++j) w[j] = 0;
+#pragma unroll 1
+            for (int j = 0; j < kGroup; ++j) {   // a register a turn
+                const u64 x = next_weight<false>(at, pos + j, scale);
+#pragma unroll
+                for (int i = 0; i + 1 < kGroup; ++i) w[i] = w[i + 1];
+                w[kGroup - 1] = x;
+            }
+        }
+    }
+    __device__ __forceinline__ u64 zero_weight(const Scale& scale) const {
+        return weight(scale.template y<true>(min(0, top_key)), a.frac, sh.tab);
+    }
+
+    // The value whose masses (before, after] hold m into every CTA's hit_*, by the one thread that
+    // holds it; `at` precedes the slice. A sync() has to follow.
+    template <bool kFold>
+    __device__ __forceinline__ void find(u64 m, u64 at, const Scale& scale, int top) const {
+        if (m <= at || m > at + before()[groups()]) return;
+#pragma unroll 1
+        for (int g = int(threadIdx.x); g < groups(); g += kThreads) {
+            if (!(at + before()[g] < m && m <= at + before()[g + 1])) continue;
+            const int pos = s0 + kGroup * g;
+            Weights next = first_weight<kFold>(pos, scale, top);
+            u64 x = at + before()[g];
+#pragma unroll 1
+            for (int j = 0; j < kGroup; ++j) {
+                const u64 w = next_weight<kFold>(next, pos + j, scale), x1 = x + hist()[word_of(pos + j)] * w;
+                if (m <= x1) {
+                    tell_alone(sh.hit_key, key_at<kFold>(pos + j, top));
+                    tell_alone(sh.hit_mass, x);
+                    tell_alone(sh.hit_weight, w);
+                    break;
                 }
                 x = x1;
             }
-            if (hit_pos >= 0) f(key_at<kFold>(hit_pos, top), hit, hit_w);
         }
     }
-    // The first prefix mass of at least `least`, into every CTA's cut[0].
-    template <bool kFold>
-    __device__ __forceinline__ void top_p_cut(u64 Z, u64 at, const Scale& scale, int top) const {
-        const u64 least = least_of(Z);
-        find<kFold>(least, at, scale, top, [&](int, u64 x, u64 w) { tell_alone(sh.cut[0], x + quotient(least - x + w - 1, w) * w); });
-    }
     __device__ __forceinline__ u64 least_of(u64 Z) const { return max(u64(1), part_up(fmaxf(tp, 0.f), Z)); }
+    // After find(least): the first prefix mass of at least `least`.
+    __device__ __forceinline__ u64 top_p_mass(u64 least) const {
+        return sh.hit_mass + quotient(least - sh.hit_mass + sh.hit_weight - 1, sh.hit_weight) * sh.hit_weight;
+    }
     // The mass of the window's values with y <= y_min, and what precedes it, into every
-    // CTA's cut[1]: the last such position is found by bisection (y rises with positions)
+    // CTA's min_p_mass: the last such position is found by bisection (y rises with positions)
     // in the slice that holds it; `Z` is the mass up to the window's end.
     template <bool kFold>
     __device__ __forceinline__ void min_p_cut(u64 Z, u64 at, const Scale& scale, int top) const {
@@ -564,104 +653,105 @@ struct Row {
             else lo += __popc(kept);
         }
         if (threadIdx.x != 0) return;
-        if (lo == kValues) {
-            if (rank == ncl - 1) tell_alone(sh.cut[1], Z);
+        if (lo == kValues) {   // all of it: the last CTA's to tell
+            if (rank == ncl - 1) tell_alone(sh.min_p_mass, Z);
             return;
         }
         if (lo < s0 || lo >= s1) return;
-        const int g = (lo - s0) / kGroup;
-        u64 x = at + before()[g], w[kGroup];
-        uint32_t n[kGroup];
-        load_group(g, n);
-        group_weights<kFold>(g, scale, top, w);
-#pragma unroll
-        for (int j = 0; j < kGroup; ++j)
-            if (s0 + kGroup * g + j < lo) x += n[j] * w[j];
-        x = min(x, at + before()[g + 1]);   // a group past the K-th token weighs nothing
-        tell_alone(sh.cut[1], x);
-    }
-    // The pick at cumulative mass `target`, into every CTA.
-    template <bool kFold>
-    __device__ __forceinline__ void pick_at(u64 target, u64 at, const Scale& scale, int top) const {
-        find<kFold>(target + 1, at, scale, top, [&](int key, u64 x, u64 w) {
-            tell_alone(sh.pick_key, key);
-            tell_alone(sh.want, int32_t(quotient(target - x, w)));
-        });
+        const int g = (lo - s0) / kGroup, pos = s0 + kGroup * g;
+        Weights next = first_weight<kFold>(pos, scale, top);
+        u64 x = at + before()[g];
+#pragma unroll 1
+        for (int j = 0; pos + j < lo; ++j) x += hist()[word_of(pos + j)] * next_weight<kFold>(next, pos + j, scale);
+        tell_alone(sh.min_p_mass, min(x, at + before()[g + 1]));   // a group past the K-th token weighs nothing
     }
 
-    // A row outside the folded window: windows of kValues keys from its largest down.
-    // The kept mass; the pick goes to pick_key and want.
-    __device__ __noinline__ u64 general(const Scale& scale, float mp, float u) const {
-        u64 slice_at = 0;
-        Windows& win = *reinterpret_cast<Windows*>(dyn + 32768 + kSide * 4);
-        // counts of the window of kValues keys from `top` down, and the largest key below it
-        auto count = [&](int top) {
-            sync();   // every CTA is done with the counts so far
-            clear();
-            int below = kMinKey;
-            auto one = [&](uint32_t b) {
-                const int k = key_of(b);
-                if (k > top || k == kMinKey) return;
-                if (top - k < kValues) atomicAdd(hist() + word_of(top - k), 1u);
-                else below = max(below, k);
-            };
-            for_tokens<kVec>(p, begin, end, [&](uint32_t w) {
-                one(w & 0xFFFFu);
-                one(w >> 16);
-            }, one);
-            return survey(below);
+    // The counts of the window of kValues keys from `top` down, surveyed: `other` is the largest key below it.
+    __device__ __forceinline__ Survey count_window(int top) const {
+        sync();   // every CTA is done with the counts so far
+        clear();
+        int below = kMinKey;
+        auto one = [&](uint32_t b) {
+            const int k = key_of(b);
+            if (k > top || k == kMinKey) return;
+            if (top - k < kValues) atomicAdd(hist() + word_of(top - k), 1u);
+            else below = max(below, k);
         };
-        int nw = 0;
-        u64 Z = 0;
-        for (int top = top_key, counted = 0;;) {   // windows down to the K-th token
-            const Survey s = count(top);
-            if (threadIdx.x == 0) {
-                win.top[nw] = top;
-                win.count_before[nw] = counted;
-                win.mass_before[nw] = Z;
+        for_tokens<kVec>(p, begin, end, [&](uint4 v) {
+#pragma unroll 1
+            for (int k = 0; k < 4; ++k) {
+                one(v.x & 0xFFFFu);
+                one(v.x >> 16);
+                v = make_uint4(v.y, v.z, v.w, 0);
             }
-            Z += weigh<false>(scale, top, counted, slice_at);
+        }, one);
+        return survey(below);
+    }
+
+};
+
+// A row outside the folded window: windows of kValues keys from its largest
+// down. The kept mass; hit_* describe the pick at u of it. (Out of line, with its
+// own copy of the row's variables, and one site of each step in its loop: few
+// rows come here, and the others' code has to stay in the instruction caches.)
+template <bool kVec>
+__device__ __noinline__ u64 general(const Row<kVec> R, const Scale scale, float mp, float u) {
+    Shared& sh = R.sh;
+    Windows& win = *reinterpret_cast<Windows*>(R.dyn + 32768 + kSide * 4);
+    u64 slice_at = 0, Z = 0, kept = 0;
+    int nw = 0, held = 0;
+    bool building = true;
+    int step = 0;
+#pragma unroll 1
+    for (int top = R.top_key, counted = 0; step < 3;) {
+        // windows down to the K-th token; afterwards the one that a step needs
+        const auto s = R.count_window(top);
+        if (building && threadIdx.x == 0) {
+            win.top[nw] = top;
+            win.count_before[nw] = counted;
+            win.mass_before[nw] = Z;
+        }
+        const u64 m = R.template weigh<false>(scale, top, building ? counted : win.count_before[held], slice_at);
+        if (building) {
+            Z += m;
             counted += s.count;
             ++nw;
-            if (s.other == kMinKey || counted >= K) break;
-            top = s.other;
-        }
-        if (threadIdx.x == 0) win.mass_before[nw] = Z;
-        __syncthreads();
-        int held = nw - 1;
-        auto hold = [&](int w) {   // window w's counts and masses; the mass before this CTA's slice
-            if (held != w) {
-                count(win.top[w]);
-                weigh<false>(scale, win.top[w], win.count_before[w], slice_at);
-                held = w;
+            if (s.other != kMinKey && counted < R.K) {
+                top = s.other;
+                continue;
             }
-            return win.mass_before[w] + slice_at;
-        };
-        u64 kept = Z;
-        if (tp < 1.f) {
-            int w = 0;
-            while (win.mass_before[w + 1] < least_of(Z)) ++w;
-            top_p_cut<false>(Z, hold(w), scale, win.top[w]);
-            sync();
-            kept = min(kept, sh.cut[0]);
+            building = false;
+            held = nw - 1;
+            kept = Z;
+            if (threadIdx.x == 0) win.mass_before[nw] = Z;
+            __syncthreads();
         }
-        if (mp > 0.f) {
-            // the last window whose largest value is kept holds the cut
+        // the top-p cut, the min-p cut and the pick, each in the window that holds it
+#pragma unroll 1
+        for (; step < 3; ++step) {
+            if ((step == 0 && !(R.tp < 1.f)) || (step == 1 && !(mp > 0.f))) continue;
+            const u64 to = step == 0 ? R.least_of(Z) : part_of(u, kept) + 1;
             int w = 0;
-            while (w + 1 < nw && scale.y<false>(win.top[w + 1]) <= sh.set.y_min) ++w;
-            const u64 at = hold(w);
-            min_p_cut<false>(win.mass_before[w + 1], at, scale, win.top[w]);
-            sync();
-            kept = min(kept, sh.cut[1]);
+            if (step == 1) {   // the last window whose largest value is kept
+                while (w + 1 < nw && scale.y<false>(win.top[w + 1]) <= sh.set.y_min) ++w;
+            } else {
+                while (win.mass_before[w + 1] < to) ++w;
+            }
+            if (held != w) {
+                held = w;
+                top = win.top[w];
+                break;
+            }
+            const u64 at = win.mass_before[w] + slice_at;
+            if (step == 1) R.template min_p_cut<false>(win.mass_before[w + 1], at, scale, win.top[w]);
+            else R.template find<false>(to, at, scale, win.top[w]);
+            R.sync();
+            if (step < 2) kept = min(kept, step == 0 ? R.top_p_mass(to) : sh.min_p_mass);
+            R.sync();   // hit_* are read before the next find
         }
-        const u64 target = part_of(u, kept);
-        int w = 0;
-        while (win.mass_before[w + 1] <= target) ++w;
-        pick_at<false>(target, hold(w), scale, win.top[w]);
-        sync();
-        return kept;
     }
-};
+    return kept;
+}
 
 template <bool kVec>
 __global__ void __launch_bounds__(kThreads, 2)
@@ -688,36 +778,30 @@ sample_rows_kernel(const __grid_constant__ Args a) {
     R.tp = tp;
     const bool bad_setting = !(T >= 0.f && T < INFINITY) || isnan(tp) || isnan(mp) || !(mp <= 1.f) ||
                              !(u >= 0.f && u < 1.f);
-    if (tid == kThreads - 1) sh.set = setting_of(T, mp);   // read after the count's barriers
+    if (tid >= kThreads - 32) {   // one warp; read after the count's barriers
+        const Setting set = setting_of(T, mp);
+        const Scale step = scale_of(0, true, set);
+        if (tid == kThreads - 32) sh.set = set;
+#pragma unroll 1
+        for (int e = tid % 32; e < kSide / 128; e += 32) sh.ratio[e] = weight(step.y_of(u64(1) << e), 63, kExpTables);
+    }
 
     // ---- the first pass: the folded window
-    int other = kMinKey;   // the largest other value
-    auto count_one = [&](uint32_t b) {
-        const int d = int(b & 0x7FFFu) - kLowMag;
-        if (uint32_t(d) < uint32_t(kSide - 1)) {
-            atomicAdd(hist + (b & 0x8000u ? 8193 + d : 1 + d), 1u);
-        } else if (b != 0xFF80u) {
-            const int k = key_of(b);
-            if (k == 0) atomicAdd(hist, 1u);
-            else other = max(other, k >= kInfKey || k < kMinKey ? kBadKey : k);
-        }
-    };
+    int other = kMinKey;   // the largest value outside it
     for_tokens<kVec>(
         p, begin, end,
-        [&](uint32_t w) {
-            // halves: 0x8000 + magnitude - kLowMag, and the same less the window's size (no borrow crosses
-            // a half); both tokens lie in the window when the first keeps bit 15 and the second loses it
-            const uint32_t r = (w | 0x80008000u) - uint32_t(kLowMag) * 0x10001u;
-            if ((r & ~(r - uint32_t(kSide - 1) * 0x10001u) & 0x80008000u) == 0x80008000u) {
-                const uint32_t e = (w & 0x80008000u) | (r << 2 & 0x7FFF7FFFu);   // byte offsets less 4; the low
-                atomicAdd(reinterpret_cast<uint32_t*>(dyn + (e & 0xFFFFu) + 4), 1u);  // half's bit 15 adds 2
-                atomicAdd(reinterpret_cast<uint32_t*>(dyn + (e >> 16) + 2), 1u);      // to the high one's
-            } else if (w != 0xFF80FF80u) {   // not two masked tokens
-                count_one(w & 0xFFFFu);
-                count_one(w >> 16);
+        [&](const uint4& v) {
+            const uint32_t r[4] = {above_low(v.x), above_low(v.y), above_low(v.z), above_low(v.w)};
+            if ((inside(r[0]) & inside(r[1]) & inside(r[2]) & inside(r[3]) & 0x80008000u) == 0x80008000u) {
+                count_word(dyn, v.x, r[0]);
+                count_word(dyn, v.y, r[1]);
+                count_word(dyn, v.z, r[2]);
+                count_word(dyn, v.w, r[3]);
+            } else {
+                other = count_mixed(v, other);
             }
         },
-        count_one);
+        [&](uint32_t b) { other = count_one(hist, b, other); });
 
     const auto found = R.survey(other);
     const bool fold = found.other == kMinKey;
@@ -738,25 +822,29 @@ sample_rows_kernel(const __grid_constant__ Args a) {
     int pick_key = top_key, want = 0;   // the pick: the want-th token (by id) of value pick_key
     if (T > 0.f) {
         if (fold) {
-            if (tid < kSide / 128) sh.ratio[tid] = weight(scale.y_of(u64(1) << tid), 63, sh.tab);
-            __syncthreads();
             u64 at;
             const u64 Z = R.template weigh<true>(scale, 0, 0, at);
             kept = Z;
-            if (tp < 1.f || mp > 0.f) {
-                if (tp < 1.f) R.template top_p_cut<true>(Z, at, scale, 0);
-                if (mp > 0.f) R.template min_p_cut<true>(Z, at, scale, 0);
+            if (mp > 0.f) R.template min_p_cut<true>(Z, at, scale, 0);
+            // the top-p cut, if there is one, and the pick
+#pragma unroll 1
+            for (int pick = tp < 1.f ? 0 : 1; pick < 2; ++pick) {
+                if (pick && mp > 0.f) {
+                    if (!(tp < 1.f)) R.sync();
+                    kept = min(kept, sh.min_p_mass);
+                }
+                const u64 to = pick ? part_of(u, kept) + 1 : R.least_of(Z);
+                R.template find<true>(to, at, scale, 0);
                 R.sync();
-                if (tp < 1.f) kept = min(kept, sh.cut[0]);
-                if (mp > 0.f) kept = min(kept, sh.cut[1]);
+                if (pick) break;
+                kept = min(kept, R.top_p_mass(to));
+                R.sync();   // hit_* are read before the next find
             }
-            R.template pick_at<true>(part_of(u, kept), at, scale, 0);
-            R.sync();
         } else {
-            kept = R.general(scale, mp, u);
+            kept = general<kVec>(R, scale, mp, u);
         }
-        pick_key = sh.pick_key;
-        want = sh.want;
+        pick_key = sh.hit_key;
+        want = int(quotient(part_of(u, kept) - sh.hit_mass, sh.hit_weight));
     }
     pdl_trigger();
 
@@ -766,8 +854,7 @@ sample_rows_kernel(const __grid_constant__ Args a) {
         if (T > 0.f) {
             // the weight's first 64 bits over the mass's first 32 (2^-31 of it off at most),
             // the remainder as the quotient's last bit, so that the one rounding sees it
-            const u64 w = fold ? R.template weight_of<true>(scale, pick_key, 63, sh.tab)
-                               : R.template weight_of<false>(scale, pick_key, 63, sh.tab);
+            const u64 w = weight(fold ? scale.y<true>(pick_key) : scale.y<false>(pick_key), 63, sh.tab);
             const int wu = __clzll((long long)w), ku = __clzll((long long)kept);
             const u64 den = (kept << ku) >> 32, q = quotient(w << wu, den);
             prob = ldexpf(float(q | u64(q * den != w << wu)), ku - wu + a.frac - 63 - 32);
@@ -785,69 +872,41 @@ sample_rows_kernel(const __grid_constant__ Args a) {
     static_assert(TF_SAMPLE_MAX_VOCAB / kChunk * kWarps <= kSide, "the counts go over the histogram");
     const uint32_t bits = uint32_t(pick_key < 0 ? -pick_key | 0x8000 : pick_key), both = bits * 0x10001u;
     const __nv_bfloat162 ref = *reinterpret_cast<const __nv_bfloat162*>(&both);
-    // the lane's 8 tokens from i on that are the pick's value, a bit each
-    auto hits_at = [&](int i, const uint4& v) {
-        uint32_t h = 0;
-        if (kVec && i + 8 <= end) {
-            const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-            uint32_t m[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) m[k] = __heq2_mask(*reinterpret_cast<const __nv_bfloat162*>(&x[k]), ref);
-            if (m[0] | m[1] | m[2] | m[3]) {   // rarely
-#pragma unroll
-                for (int k = 0; k < 4; ++k) h |= (m[k] & 0x10001u) << 2 * k;
-                h = (h | h >> 15) & 0xFFu;   // the high tokens' bits between the low ones'
-            }
-        } else {
-#pragma unroll 1
-            for (int k = 0; k < 8; ++k)
-                if (i + k < end && key_of(p[i + k]) == pick_key) h |= 1u << k;
-        }
-        return h;
-    };
     auto load = [&](uint4 (&v)[kUnroll], int i0) {
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k)
-            if (kVec && i0 + 256 * k + 8 * lane + 8 <= end)
-                v[k] = __ldg(reinterpret_cast<const uint4*>(p + i0 + 256 * k + 8 * lane));
-    };
-    // the left-th of the warp's tokens of the pick's value, in its step from i0 on
-    auto finish = [&](int i0, const uint4 (&v)[kUnroll], int32_t left) {
-#pragma unroll 1
         for (int k = 0; k < kUnroll; ++k) {
             const int i = i0 + 256 * k + 8 * lane;
-            uint4 x = v[0];
-#pragma unroll
-            for (int j = 1; j < kUnroll; ++j)
-                if (j == k) x = v[j];
-            uint32_t h = hits_at(i, x);
-            const int32_t c = __popc(h);
-            int32_t upto = c;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int32_t t = __shfl_up_sync(0xFFFFFFFFu, upto, o);
-                if (lane >= o) upto += t;
-            }
-            if (left >= upto - c && left < upto) {
-                for (int q = upto - c; q < left; ++q) h &= h - 1;
-                a.pick[row] = i + __ffs(h) - 1;
-            }
-            left -= __shfl_sync(0xFFFFFFFFu, upto, 31);
-            if (left < 0) break;
+            if (kVec && i + 8 <= end) v[k] = __ldg(reinterpret_cast<const uint4*>(p + i));
+            else v[k] = load_part(p, i, end, ~bits);   // no other token equals the pick's value
         }
+    };
+    // a lane's 8 tokens that are the pick's value, a bit each
+    auto hits = [&](const uint4& v) {
+        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+        uint32_t m[4], h = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) m[k] = __heq2_mask(*reinterpret_cast<const __nv_bfloat162*>(&x[k]), ref);
+        if (m[0] | m[1] | m[2] | m[3]) {   // rarely
+#pragma unroll
+            for (int k = 0; k < 4; ++k) h |= (m[k] & 0x10001u) << 2 * k;
+            h = (h | h >> 15) & 0xFFu;   // the high tokens' bits between the low ones'
+        }
+        return h;
     };
     int32_t* const counts = reinterpret_cast<int32_t*>(hist);   // [chunk][warp]; the histogram is done with
     const int chunks = (end - begin + kChunk - 1) / kChunk;
     int32_t before = 0;    // tokens of the value in the chunks so far
+    int32_t left = -1;     // the pick is the left-th of this warp's tokens of the value in chunk `mine`
+    int mine = 0;
     uint4 v[kUnroll], next[kUnroll];
     load(v, begin + warp * kStep);
+#pragma unroll 1
     for (int j = 0; j < chunks; ++j) {
-        const int i0 = begin + j * kChunk + warp * kStep;
-        load(next, i0 + kChunk);
+        load(next, begin + (j + 1) * kChunk + warp * kStep);
         int32_t c = 0;
 #pragma unroll
         for (int k = 0; k < kUnroll; ++k)
-            if (const uint32_t h = hits_at(i0 + 256 * k + 8 * lane, v[k])) c += __popc(h);
+            if (const uint32_t h = hits(v[k])) c += __popc(h);
         c = __reduce_add_sync(0xFFFFFFFFu, c);
         if (lane == 0) counts[j * kWarps + warp] = c;
         if (ncl == 1) {
@@ -855,34 +914,58 @@ sample_rows_kernel(const __grid_constant__ Args a) {
             const int32_t x = lane < kWarps ? counts[j * kWarps + lane] : 0;
             const int32_t all = __reduce_add_sync(0xFFFFFFFFu, x);
             if (want < before + all) {
-                const int32_t left = want - before - __reduce_add_sync(0xFFFFFFFFu, lane < warp ? x : 0);
-                if (0 <= left && left < c) finish(i0, v, left);
-                return;
+                left = want - before - __reduce_add_sync(0xFFFFFFFFu, lane < warp ? x : 0);
+                if (left >= c) left = -1;
+                mine = j;
+                break;
             }
             before += all;
         }
 #pragma unroll
         for (int k = 0; k < kUnroll; ++k) v[k] = next[k];
     }
-    __syncthreads();
-    // this CTA's count; then the counts of the CTAs before it
-    int32_t n = 0;
-    for (int i = lane; i < chunks * kWarps; i += 32) n += counts[i];
-    n = __reduce_add_sync(0xFFFFFFFFu, n);
-    R.tell(sh.found[rank], n);
-    R.sync();   // the last use of another CTA's memory
-    for (int r = 0; r < rank; ++r) before += sh.found[r];
-    if (want < before || want >= before + n) return;
-    for (int j = 0; j < chunks; ++j) {   // the warp whose step it is
-        const int32_t x = lane < kWarps ? counts[j * kWarps + lane] : 0;
-        const int32_t at = before + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? x : 0);
-        if (at <= want && want < at + __shfl_sync(0xFFFFFFFFu, x, warp)) {
-            const int i0 = begin + j * kChunk + warp * kStep;
-            load(v, i0);
-            finish(i0, v, want - at);
-            return;
+    if (ncl > 1) {
+        __syncthreads();
+        // this CTA's count; then the counts of the CTAs before it
+        int32_t n = 0;
+#pragma unroll 1
+        for (int i = lane; i < chunks * kWarps; i += 32) n += counts[i];
+        n = __reduce_add_sync(0xFFFFFFFFu, n);
+        R.tell(sh.found[rank], n);
+        R.sync();   // the last use of another CTA's memory
+#pragma unroll 1
+        for (int r = 0; r < rank; ++r) before += sh.found[r];
+#pragma unroll 1
+        for (; mine < chunks && left < 0; ++mine) {   // the warp whose step it is
+            const int32_t x = lane < kWarps ? counts[mine * kWarps + lane] : 0;
+            const int32_t at = before + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? x : 0);
+            before += __reduce_add_sync(0xFFFFFFFFu, x);
+            if (at <= want && want < at + __shfl_sync(0xFFFFFFFFu, x, warp)) {
+                left = want - at;
+                break;
+            }
         }
-        before += __reduce_add_sync(0xFFFFFFFFu, x);
+    }
+    if (left < 0) return;
+    load(v, begin + mine * kChunk + warp * kStep);
+#pragma unroll 1
+    for (int k = 0; k < kUnroll; ++k) {
+        uint32_t h = hits(v[0]);
+#pragma unroll
+        for (int j = 0; j + 1 < kUnroll; ++j) v[j] = v[j + 1];
+        const int32_t c = __popc(h);
+        int32_t upto = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int32_t t = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+            if (lane >= o) upto += t;
+        }
+        if (left >= upto - c && left < upto) {
+            for (int q = upto - c; q < left; ++q) h &= h - 1;
+            a.pick[row] = begin + mine * kChunk + warp * kStep + 256 * k + 8 * lane + __ffs(h) - 1;
+        }
+        left -= __shfl_sync(0xFFFFFFFFu, upto, 31);
+        if (left < 0) break;
     }
 }
 
