@@ -113,6 +113,55 @@ def test_vocabulary_rows(mods):
     check(mods, x, 128000, u, **kw)
 
 
+@pytest.mark.parametrize("R,V", [(1, 140000), (2, 131072), (5, 70001), (40, 33000), (100, 20000), (400, 9000)])
+@pytest.mark.parametrize("outside", [False, True])
+def test_clusters(mods, R, V, outside):
+    """Rows shared by 8, 8, 4, 2, 1 and 1 CTAs, with values outside the folded window
+    (large, tiny, both signs) in some rows or none."""
+    x = normal(mods[1], R, V, 3.0, V)
+    if outside:
+        x[::2, 11:5000:7] = 300.0
+        x[::2, 3] = -2.0 ** -60
+        x[::3, V - 1] = 2.0 ** -40
+        x[R - 1, V // 2] = -9000.0
+    kw, u = settings(R, V + 1)
+    kw["temperature"] = np.where(kw["temperature"] > 0, kw["temperature"] * (20 if outside else 1), 0)
+    check(mods, x, V, u)
+    check(mods, x, V, u, **kw)
+
+
+def test_same_value_everywhere_at_a_border(mods):
+    """Values at the folded window's edges: 127.5, 128, 2^-33 and its neighbours, both signs."""
+    torch = mods[1]
+    edge = [127.5, 128.0, 2.0 ** -33, 2.0 ** -33 * (1 + 2.0 ** -7), 2.0 ** -33 * (1 - 2.0 ** -8), 0.0, -0.0, 1.0]
+    vals = torch.tensor([s * e for e in edge for s in (1, -1)], device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(31)
+    x = vals[torch.randint(0, len(vals), (64, 3000), generator=g, device="cuda")].to(torch.bfloat16)
+    for r in range(16):                    # rows of one edge value and ones, so that they stay inside or not
+        x[r] = torch.where(torch.rand(3000, generator=g, device="cuda") < 0.5, vals[r], torch.ones_like(vals[r])).to(torch.bfloat16)
+    kw, u = settings(64, 32)
+    kw["temperature"] = kw["temperature"] * 50
+    check(mods, x, 3000, u, **kw)
+    check(mods, x, 3000, u, temperature=np.full(64, 200.0))
+
+
+def test_two_streams_at_once(mods):
+    """Calls on two streams share nothing."""
+    tf, torch = mods
+    xs = [normal(torch, 300, 30000, 3.0, s) for s in (33, 34)]
+    us = [torch.rand(300, device="cuda") * 0.999 for _ in xs]
+    outs = [(torch.empty(300, dtype=torch.int32, device="cuda"), torch.empty(300, dtype=torch.uint8, device="cuda")) for _ in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    for _ in range(4):
+        for x, u, o, s in zip(xs, us, outs, streams):
+            tf.tf_sample_rows(x, 300, 30000, 30000, None, None, None, None, u, o[0], None, o[1], stream=s)
+    torch.cuda.synchronize()
+    for x, u, o in zip(xs, us, outs):
+        rp, _, _ = OS.sample_rows(host_bits(x, 30000), u.cpu().numpy())
+        assert np.array_equal(o[0].cpu().numpy(), rp)
+
+
 def test_largest_vocabulary(mods):
     x = normal(mods[1], 3, 1 << 19, 2.0, 9)
     check(mods, x, 1 << 19, [0.2, 0.6, 0.99999], temperature=[1.0, 3.0, 0.8])
