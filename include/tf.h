@@ -296,7 +296,8 @@ int tf_argmax_rows(const void* logits, int R, int V, int64_t row_stride,
  * T == 0 picks the first token (the greedy pick). Masses are exact to 64-bit
  * fixed point, so a pick equals the float64 definition's except where u lies
  * within about 1e-12 of a border.
- *   logits      as in tf_argmax_rows; -Inf is a masked token (never picked)
+ *   logits      as in tf_argmax_rows (any 2-byte address and stride); -Inf is a
+ *               masked token (never picked)
  *   temperature float [R] or NULL (1); 0 <= T < inf
  *   top_k       int32 [R] or NULL; off where <= 0 or >= V
  *   top_p       float [R] or NULL; off where >= 1; <= 0 keeps one token
@@ -308,8 +309,8 @@ int tf_argmax_rows(const void* logits, int R, int V, int64_t row_stride,
  *   flag        uint8 [R]: TF_SAMPLE_NO_LOGITS a NaN or +Inf in the row, or
  *               every token masked; TF_SAMPLE_BAD_SETTING a setting outside
  *               its range or NaN
- * Needs no table. R == 0 is a no-op. Errors: TF_EINVAL (null, V < 1,
- * row_stride < V), TF_ERANGE (V > TF_SAMPLE_MAX_VOCAB, R > 2^24). */
+ * Needs no table. R == 0 is a no-op. Errors: TF_EINVAL (null, an odd address,
+ * V < 1, row_stride < V), TF_ERANGE (V > TF_SAMPLE_MAX_VOCAB, R > 2^24). */
 #define TF_SAMPLE_MAX_VOCAB (1 << 19)
 #define TF_SAMPLE_NO_LOGITS   1
 #define TF_SAMPLE_BAD_SETTING 2

@@ -231,35 +231,35 @@ struct Args {
     int32_t chunk;       // tokens a CTA of the cluster counts, a multiple of 8
 };
 
-// f(16 bytes, 8 tokens) and f1(bits) for the rest of [begin, end).
-template <bool kVec, typename F, typename F1>
-__device__ __forceinline__ void for_tokens(const uint16_t* p, int begin, int end, F&& f, F1&& f1) {
-    if constexpr (kVec) {
-        const int nvec = (end - begin) >> 3;
-        const uint4* pv = reinterpret_cast<const uint4*>(p + begin);
-        // the next vectors are asked for before the ones at hand are used
-        uint4 v[kUnroll], next[kUnroll];
-        auto load = [&](uint4 (&x)[kUnroll], int i) {
+// f(16 bytes, 8 tokens) and f1(bits) for the rest of a row's [begin, end): the
+// tokens before the first 16-byte boundary and after the last (`head` and 8 of
+// them at most).
+template <typename F, typename F1>
+__device__ __forceinline__ void for_tokens(const uint16_t* p, int begin, int end, int head, F&& f, F1&& f1) {
+    const int body = min(end, begin + head), nvec = (end - body) >> 3;
+    const uint4* pv = reinterpret_cast<const uint4*>(p + body);
+    // the next vectors are asked for before the ones at hand are used
+    uint4 v[kUnroll], next[kUnroll];
+    auto load = [&](uint4 (&x)[kUnroll], int i) {
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u)
-                if (i + u * kThreads < nvec) x[u] = __ldg(pv + i + u * kThreads);
-        };
-        load(v, threadIdx.x);
+        for (int u = 0; u < kUnroll; ++u)
+            if (i + u * kThreads < nvec) x[u] = __ldg(pv + i + u * kThreads);
+    };
+    load(v, threadIdx.x);
 #pragma unroll 1
-        for (int i = threadIdx.x; i < nvec; i += kUnroll * kThreads) {
-            load(next, i + kUnroll * kThreads);
+    for (int i = threadIdx.x; i < nvec; i += kUnroll * kThreads) {
+        load(next, i + kUnroll * kThreads);
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                if (i + u * kThreads >= nvec) break;
-                f(v[u]);
-            }
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u) v[u] = next[u];
+        for (int u = 0; u < kUnroll; ++u) {
+            if (i + u * kThreads >= nvec) break;
+            f(v[u]);
         }
-        begin += nvec * 8;
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) v[u] = next[u];
     }
-#pragma unroll 1
-    for (int i = begin + threadIdx.x; i < end; i += kThreads) f1(uint32_t(p[i]));
+    const int tail = body + nvec * 8, t = int(threadIdx.x);
+    if (t < body - begin) f1(uint32_t(p[begin + t]));
+    if (t < end - tail) f1(uint32_t(p[tail + t]));
 }
 
 // Counts into the folded window; `other` becomes the largest value outside it
@@ -311,24 +311,24 @@ __device__ __noinline__ int count_mixed(uint4 v, int other) {
     return other;
 }
 
-// Tokens [i, min(i + 8, end)) one by one, `none` in the place of the others.
-__device__ __noinline__ uint4 load_part(const uint16_t* p, int i, int end, uint32_t none) {
+// The tokens of [i, i + 8) that lie in [begin, end) one by one, `none` in the place of the others.
+__device__ __noinline__ uint4 load_part(const uint16_t* p, int i, int begin, int end, uint32_t none) {
     uint32_t x[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-        x[k / 2] |= ((i + k < end ? uint32_t(p[i + k]) : none) & 0xFFFFu) << 16 * (k & 1);
+        x[k / 2] |= ((i + k >= begin && i + k < end ? uint32_t(p[i + k]) : none) & 0xFFFFu) << 16 * (k & 1);
     return make_uint4(x[0], x[1], x[2], x[3]);
 }
 
 // One CTA's part in its row. Every step that ends in sync() is taken by all
 // threads of all CTAs of the cluster, with the same numbers.
-template <bool kVec>
 struct Row {
     const Args& a;
     unsigned char* dyn;
     Shared& sh;
     int ncl, rank;
-    int begin, end;      // this CTA's tokens
+    int begin, end;      // this CTA's tokens,
+    int head;            // and those of them before a 16-byte boundary
     int s0, s1;          // and its slice of the sorted positions
     const uint16_t* p;
     float tp;
@@ -561,7 +561,7 @@ struct Row {
     template <bool kFold>
     __device__ __forceinline__ Weights first_weight(int pos, const Scale& scale, int top) const {
         const int key = key_at<kFold>(pos, top);
-        return {weight(scale.template y<kFold>(min(key, top_key)), 63, sh.tab),
+        return {weight(scale.y<kFold>(min(key, top_key)), 63, sh.tab),
                 kFold ? sh.ratio[(abs(key) >> 7) - (kLowMag >> 7)] : 0, key, 63 - a.frac};
     }
     // The position's weight, and on to the next position's.
@@ -573,7 +573,7 @@ struct Row {
             if (w.key < top_key) w.x = __umul64hi(w.x, w.ratio) << 1;
             return pos == kSide - 1 ? zero_weight(scale) : x;
         }
-        w.x = weight(scale.template y<false>(min(w.key, top_key)), 63, sh.tab);
+        w.x = weight(scale.y<false>(min(w.key, top_key)), 63, sh.tab);
         return x;
     }
     template <bool kFold>
@@ -600,7 +600,7 @@ struct Row {
         }
     }
     __device__ __forceinline__ u64 zero_weight(const Scale& scale) const {
-        return weight(scale.template y<true>(min(0, top_key)), a.frac, sh.tab);
+        return weight(scale.y<true>(min(0, top_key)), a.frac, sh.tab);
     }
 
     // The value whose masses (before, after] hold m into every CTA's hit_*, by the one thread that
@@ -641,7 +641,7 @@ struct Row {
         const u64 y_min = sh.set.y_min;
         auto keeps = [&](int pos) {
             const int key = key_at<kFold>(pos, top);
-            return key >= top_key || (key >= kMinKey && scale.template y<kFold>(key) <= y_min);
+            return key >= top_key || (key >= kMinKey && scale.y<kFold>(key) <= y_min);
         };
         int lo = 0;   // positions below lo are kept; 32 looked at a time, 320, 10 and 1 apart
 #pragma unroll 1
@@ -677,7 +677,7 @@ struct Row {
             if (top - k < kValues) atomicAdd(hist() + word_of(top - k), 1u);
             else below = max(below, k);
         };
-        for_tokens<kVec>(p, begin, end, [&](uint4 v) {
+        for_tokens(p, begin, end, head, [&](uint4 v) {
 #pragma unroll 1
             for (int k = 0; k < 4; ++k) {
                 one(v.x & 0xFFFFu);
@@ -694,8 +694,7 @@ struct Row {
 // down. The kept mass; hit_* describe the pick at u of it. (Out of line, with its
 // own copy of the row's variables, and one site of each step in its loop: few
 // rows come here, and the others' code has to stay in the instruction caches.)
-template <bool kVec>
-__device__ __noinline__ u64 general(const Row<kVec> R, const Scale scale, float mp, float u) {
+__device__ __noinline__ u64 general(const Row R, const Scale scale, float mp, float u) {
     Shared& sh = R.sh;
     Windows& win = *reinterpret_cast<Windows*>(R.dyn + 32768 + kSide * 4);
     u64 slice_at = 0, Z = 0, kept = 0;
@@ -711,7 +710,7 @@ __device__ __noinline__ u64 general(const Row<kVec> R, const Scale scale, float 
             win.count_before[nw] = counted;
             win.mass_before[nw] = Z;
         }
-        const u64 m = R.template weigh<false>(scale, top, building ? counted : win.count_before[held], slice_at);
+        const u64 m = R.weigh<false>(scale, top, building ? counted : win.count_before[held], slice_at);
         if (building) {
             Z += m;
             counted += s.count;
@@ -743,8 +742,8 @@ __device__ __noinline__ u64 general(const Row<kVec> R, const Scale scale, float 
                 break;
             }
             const u64 at = win.mass_before[w] + slice_at;
-            if (step == 1) R.template min_p_cut<false>(win.mass_before[w + 1], at, scale, win.top[w]);
-            else R.template find<false>(to, at, scale, win.top[w]);
+            if (step == 1) R.min_p_cut<false>(win.mass_before[w + 1], at, scale, win.top[w]);
+            else R.find<false>(to, at, scale, win.top[w]);
             R.sync();
             if (step < 2) kept = min(kept, step == 0 ? R.top_p_mass(to) : sh.min_p_mass);
             R.sync();   // hit_* are read before the next find
@@ -753,17 +752,19 @@ __device__ __noinline__ u64 general(const Row<kVec> R, const Scale scale, float 
     return kept;
 }
 
-template <bool kVec>
 __global__ void __launch_bounds__(kThreads, 2)
 sample_rows_kernel(const __grid_constant__ Args a) {
     extern __shared__ __align__(128) unsigned char dyn[];
     Shared& sh = *reinterpret_cast<Shared*>(dyn + kSide * 4);
     const int row = blockIdx.y, tid = threadIdx.x;
     const int ncl = gridDim.x, rank = blockIdx.x;   // a cluster is one row's CTAs
-    const int begin = min(a.V, rank * a.chunk), end = min(a.V, begin + a.chunk);
     const int slice = kValues / ncl;
     const uint16_t* p = a.logits + size_t(row) * size_t(a.stride);
-    Row<kVec> R{a, dyn, sh, ncl, rank, begin, end, rank * slice, (rank + 1) * slice, p, 1.f, a.V, kMinKey};
+    // the row's tokens before a 16-byte boundary are the first CTA's, the parts begin at boundaries
+    const int skew = int(-reinterpret_cast<uintptr_t>(p) & 15u) / 2;
+    const int begin = rank ? min(a.V, skew + rank * a.chunk) : 0;
+    const int end = rank == ncl - 1 ? a.V : min(a.V, skew + (rank + 1) * a.chunk);
+    Row R{a, dyn, sh, ncl, rank, begin, end, rank ? 0 : skew, rank * slice, (rank + 1) * slice, p, 1.f, a.V, kMinKey};
     uint32_t* const hist = R.hist();
     if (tid < 64) {
         sh.tab.coarse[tid] = kExpTables.coarse[tid];
@@ -788,8 +789,8 @@ sample_rows_kernel(const __grid_constant__ Args a) {
 
     // ---- the first pass: the folded window
     int other = kMinKey;   // the largest value outside it
-    for_tokens<kVec>(
-        p, begin, end,
+    for_tokens(
+        p, begin, end, R.head,
         [&](const uint4& v) {
             const uint32_t r[4] = {above_low(v.x), above_low(v.y), above_low(v.z), above_low(v.w)};
             if ((inside(r[0]) & inside(r[1]) & inside(r[2]) & inside(r[3]) & 0x80008000u) == 0x80008000u) {
@@ -823,9 +824,9 @@ sample_rows_kernel(const __grid_constant__ Args a) {
     if (T > 0.f) {
         if (fold) {
             u64 at;
-            const u64 Z = R.template weigh<true>(scale, 0, 0, at);
+            const u64 Z = R.weigh<true>(scale, 0, 0, at);
             kept = Z;
-            if (mp > 0.f) R.template min_p_cut<true>(Z, at, scale, 0);
+            if (mp > 0.f) R.min_p_cut<true>(Z, at, scale, 0);
             // the top-p cut, if there is one, and the pick
 #pragma unroll 1
             for (int pick = tp < 1.f ? 0 : 1; pick < 2; ++pick) {
@@ -834,14 +835,14 @@ sample_rows_kernel(const __grid_constant__ Args a) {
                     kept = min(kept, sh.min_p_mass);
                 }
                 const u64 to = pick ? part_of(u, kept) + 1 : R.least_of(Z);
-                R.template find<true>(to, at, scale, 0);
+                R.find<true>(to, at, scale, 0);
                 R.sync();
                 if (pick) break;
                 kept = min(kept, R.top_p_mass(to));
                 R.sync();   // hit_* are read before the next find
             }
         } else {
-            kept = general<kVec>(R, scale, mp, u);
+            kept = general(R, scale, mp, u);
         }
         pick_key = sh.hit_key;
         want = int(quotient(part_of(u, kept) - sh.hit_mass, sh.hit_weight));
@@ -869,15 +870,15 @@ sample_rows_kernel(const __grid_constant__ Args a) {
     // through the row on average; in a cluster each counts all of its chunks, and the
     // one that holds the token reads its step again.
     constexpr int kStep = kUnroll * 32 * 8, kChunk = kStep * kWarps;
-    static_assert(TF_SAMPLE_MAX_VOCAB / kChunk * kWarps <= kSide, "the counts go over the histogram");
+    static_assert((TF_SAMPLE_MAX_VOCAB / kChunk + 2) * kWarps <= kSide, "the counts go over the histogram");
     const uint32_t bits = uint32_t(pick_key < 0 ? -pick_key | 0x8000 : pick_key), both = bits * 0x10001u;
     const __nv_bfloat162 ref = *reinterpret_cast<const __nv_bfloat162*>(&both);
     auto load = [&](uint4 (&v)[kUnroll], int i0) {
 #pragma unroll
         for (int k = 0; k < kUnroll; ++k) {
             const int i = i0 + 256 * k + 8 * lane;
-            if (kVec && i + 8 <= end) v[k] = __ldg(reinterpret_cast<const uint4*>(p + i));
-            else v[k] = load_part(p, i, end, ~bits);   // no other token equals the pick's value
+            if (i >= begin && i + 8 <= end) v[k] = __ldg(reinterpret_cast<const uint4*>(p + i));
+            else v[k] = load_part(p, i, begin, end, ~bits);   // which no pick equals
         }
     };
     // a lane's 8 tokens that are the pick's value, a bit each
@@ -894,15 +895,16 @@ sample_rows_kernel(const __grid_constant__ Args a) {
         return h;
     };
     int32_t* const counts = reinterpret_cast<int32_t*>(hist);   // [chunk][warp]; the histogram is done with
-    const int chunks = (end - begin + kChunk - 1) / kChunk;
+    const int from = R.head ? R.head - 8 : begin;   // a 16-byte boundary at or before the first token
+    const int chunks = (end - from + kChunk - 1) / kChunk;
     int32_t before = 0;    // tokens of the value in the chunks so far
     int32_t left = -1;     // the pick is the left-th of this warp's tokens of the value in chunk `mine`
     int mine = 0;
     uint4 v[kUnroll], next[kUnroll];
-    load(v, begin + warp * kStep);
+    load(v, from + warp * kStep);
 #pragma unroll 1
     for (int j = 0; j < chunks; ++j) {
-        load(next, begin + (j + 1) * kChunk + warp * kStep);
+        load(next, from + (j + 1) * kChunk + warp * kStep);
         int32_t c = 0;
 #pragma unroll
         for (int k = 0; k < kUnroll; ++k)
@@ -947,7 +949,7 @@ sample_rows_kernel(const __grid_constant__ Args a) {
         }
     }
     if (left < 0) return;
-    load(v, begin + mine * kChunk + warp * kStep);
+    load(v, from + mine * kChunk + warp * kStep);
 #pragma unroll 1
     for (int k = 0; k < kUnroll; ++k) {
         uint32_t h = hits(v[0]);
@@ -962,17 +964,15 @@ sample_rows_kernel(const __grid_constant__ Args a) {
         }
         if (left >= upto - c && left < upto) {
             for (int q = upto - c; q < left; ++q) h &= h - 1;
-            a.pick[row] = begin + mine * kChunk + warp * kStep + 256 * k + 8 * lane + __ffs(h) - 1;
+            a.pick[row] = from + mine * kChunk + warp * kStep + 256 * k + 8 * lane + __ffs(h) - 1;
         }
         left -= __shfl_sync(0xFFFFFFFFu, upto, 31);
         if (left < 0) break;
     }
 }
 
-template <bool kVec>
 int prepare() {
-    const cudaError_t r = cudaFuncSetAttribute(sample_rows_kernel<kVec>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               kSmemBytes);
+    const cudaError_t r = cudaFuncSetAttribute(sample_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     return r == cudaSuccess ? TF_OK : cuda_fail(r);
 }
 
@@ -986,11 +986,11 @@ extern "C" int tf_sample_rows(const void* logits, int R, int V, int64_t row_stri
     if (R < 0) return TF_EINVAL;
     if (R == 0) return TF_OK;
     if (!logits || !u || !pick || !flag || V < 1 || row_stride < V) return TF_EINVAL;
+    if (reinterpret_cast<uintptr_t>(logits) & 1) return TF_EINVAL;
     if (V > TF_SAMPLE_MAX_VOCAB || R > (1 << 24)) return TF_ERANGE;
     int bits = 0;
     while ((int64_t(1) << bits) < V) ++bits;
-    const bool vec = aligned16(logits) && row_stride % 8 == 0;
-    int rc = vec ? prepare<true>() : prepare<false>();
+    int rc = prepare();
     if (rc != TF_OK) return rc;
     // CTAs a row: as many as one wave holds, at two an SM, while each has 16,384 tokens
     int cl = kMaxCluster;
@@ -1024,8 +1024,7 @@ extern "C" int tf_sample_rows(const void* logits, int R, int V, int64_t row_stri
         b.pick += r0;
         if (b.prob) b.prob += r0;
         b.flag += r0;
-        cudaError_t e = vec ? cudaLaunchKernelEx(&cfg, sample_rows_kernel<true>, b)
-                            : cudaLaunchKernelEx(&cfg, sample_rows_kernel<false>, b);
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, sample_rows_kernel, b);
         if (e != cudaSuccess) return cuda_fail(e);
         rc = launch_status();
         if (rc != TF_OK) return rc;

@@ -81,6 +81,7 @@ def test_refusals(T):
 
     for i in (0, 8, 9, 11):                       # logits, u, pick, flag
         assert status(**{f"a{i}": None}) == T.TF_EINVAL
+    assert status(a0=P + 1) == T.TF_EINVAL        # an odd address
     assert status(a1=-1) == T.TF_EINVAL and status(a2=0) == T.TF_EINVAL and status(a3=99) == T.TF_EINVAL
     assert status(a2=(1 << 19) + 1, a3=1 << 20) == T.TF_ERANGE
     assert status(a1=(1 << 24) + 1) == T.TF_ERANGE
