@@ -440,6 +440,10 @@ int tf_prompt_build(int32_t rows, int32_t keys, int32_t kv_capacity,
  * tf_paged_prompt_build is tf_prompt_build for pages: one list of kv_capacity /
  * page_keys entries.
  *
+ * The calls on tables below (tf_attn_paged, tf_qk_rows) refuse a table that was
+ * built with another device current (TF_EINVAL); tf_pages_copy and
+ * tf_sample_rows refuse pools and logits in another device's memory.
+ *
  * Either table serves every call that a dense table of its kind serves, except
  * that its attention is tf_attn_paged: tf_attn, tf_attn_block, their partials
  * forms, tf_attn_merge and tf_attn_static refuse it (TF_EINVAL). */

@@ -362,6 +362,7 @@ extern "C" int tf_attn_paged(const tf_segments* seg, int attn_layer, const void*
     const SegTable& t = seg->dev;
     if (attn_layer < 0 || attn_layer >= t.n_attn) return TF_EINVAL;
     if (t.R == 0) return TF_OK;
+    if (!on_this_device(seg)) return TF_EINVAL;
     if (!q || !partials || !out || !aligned16(q) || !aligned16(partials) || !aligned16(out)) return TF_EINVAL;
     float* po = static_cast<float*>(partials);
     float2* pml = reinterpret_cast<float2*>(po + t.n_partials * TF_D);

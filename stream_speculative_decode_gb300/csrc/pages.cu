@@ -118,7 +118,9 @@ int copy_pages(void* const* pools, int n_pools, int page_keys, int n_pages, cons
         for (int i = 0; i < n; ++i)
             if (std::binary_search(written.begin(), written.end(), src[i])) return TF_EINVAL;
     }
-    if (n_pools == 0) return TF_OK;
+    if (n_pools == 0 || n == 0) return TF_OK;
+    for (int p = 0; p < n_pools; ++p)
+        if (!on_this_device(pools[p])) return TF_EINVAL;
     // few copies travel in a small argument block
     constexpr int kFew = 64, kMany = 2400;
     return n <= kFew ? launch_batches<kFew>(pools, n_pools, page_keys, src, dst, keys, n, stream)

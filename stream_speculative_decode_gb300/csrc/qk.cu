@@ -224,6 +224,7 @@ extern "C" int tf_qk_rows(const tf_segments* seg, int attn_layer, const void* q,
     if (attn_layer < 0 || attn_layer >= t.n_attn) return TF_EINVAL;
     if (!(eps > 0.f) || !std::isfinite(eps) || !(theta >= 1.0) || !std::isfinite(theta)) return TF_EINVAL;
     if (t.R == 0) return TF_OK;
+    if (!on_this_device(seg)) return TF_EINVAL;
     for (const void* p : {q, k, v, q_norm, k_norm, static_cast<const void*>(q_out)})
         if (!p || !aligned16(p)) return TF_EINVAL;
     constexpr int64_t kQ = TF_NQ * TF_D, kKV = TF_NKV * TF_D, kMaxStride = int64_t(1) << 32;

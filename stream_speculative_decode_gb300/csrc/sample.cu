@@ -993,6 +993,7 @@ extern "C" int tf_sample_rows(const void* logits, int R, int V, int64_t row_stri
     if (!logits || !u || !pick || !flag || V < 1 || row_stride < V) return TF_EINVAL;
     if (reinterpret_cast<uintptr_t>(logits) & 1) return TF_EINVAL;
     if (V > TF_SAMPLE_MAX_VOCAB || R > (1 << 24)) return TF_ERANGE;
+    if (!on_this_device(logits)) return TF_EINVAL;
     int bits = 0;
     while ((int64_t(1) << bits) < V) ++bits;
     int rc = prepare();

@@ -44,6 +44,21 @@ int sm_count() {
     return cache[dev];
 }
 
+bool on_this_device(const tf_segments* seg) {
+    int dev = -1;
+    return cudaGetDevice(&dev) == cudaSuccess && dev == seg->device;
+}
+
+bool on_this_device(const void* memory) {
+    int dev = -1;
+    cudaPointerAttributes a;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaPointerGetAttributes(&a, memory) != cudaSuccess) {
+        cudaGetLastError();   // no device, or nothing known of the address: the launch will say
+        return true;
+    }
+    return a.type != cudaMemoryTypeDevice || a.device == dev;
+}
+
 int attn_prepare();   // attn.cu: kernel attributes
 
 namespace {
@@ -270,6 +285,7 @@ int finish_build(std::unique_ptr<tf_segments> owned, std::vector<tf::SegStream>&
     using namespace tf;
     tf_segments* const seg = owned.get();
     seg->paged = pg != nullptr;
+    cudaGetDevice(&seg->device);
     const int S = int(ss.size());
     const int R = int(row_stream.size());
     const tf_plan& plan = seg->plan;

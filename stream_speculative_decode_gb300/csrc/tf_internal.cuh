@@ -137,6 +137,7 @@ struct tf_segments {
     tf_plan plan{};
     bool prompt = false;               // built by tf_prompt_build (conv + attention only)
     bool paged = false;                // built by tf_paged_build / tf_paged_prompt_build
+    int device = 0;                    // current device of the build
     size_t scratch_off = 0;            // the blob's cross-CTA scratch and status word:
     size_t scratch_bytes = 0;          // zero in the image, zeroed again by tf_segments_status
 };
@@ -159,6 +160,11 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 
 // Number of SMs of the current device (cached per device).
 int sm_count();
+
+// False for a table, or for device memory, of another device than the current
+// one: a launch here would read addresses that mean nothing on this device.
+bool on_this_device(const tf_segments* seg);
+bool on_this_device(const void* memory);
 
 // ---- programmatic dependent launch ---------------------------------------
 // Every kernel of the library is launched with programmatic stream

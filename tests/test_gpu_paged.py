@@ -256,3 +256,51 @@ def test_whole_step_on_pages(mods):
     assert torch.equal(out.cpu(), torch.from_numpy(want["out"][0]).to(torch.bfloat16))
     d.free()
     e.free()
+
+
+@pytest.mark.parametrize("page", [16, 64])
+def test_wait_that_runs_out(mods, page):
+    """The tensor-core kernel's bounded waits over pages: a limit of 0 gives up without
+    a fault, the status word says so, and the next call is right again."""
+    tf, inputs, _, torch = mods
+    from paged import PagedAttn
+    inp = inputs.make_inputs(work(inputs, [16, 12, 2], [9000, 700, 40]), backend="numpy")
+    p = PagedAttn(tf, inp, page)
+    try:
+        for _ in range(5):
+            tf.tf_set_wait_limit_ns(0)
+            p.run()
+            tf.tf_set_wait_limit_ns(tf.TF_WAIT_LIMIT_DEFAULT_NS)
+            torch.cuda.synchronize()
+            rc, bits = tf.tf_segments_status(p.seg)
+            if rc == tf.TF_ETIMEOUT:
+                break
+        assert rc == tf.TF_ETIMEOUT and bits & tf.TF_STATUS_ATTN_TIMEOUT
+    finally:
+        tf.tf_set_wait_limit_ns(tf.TF_WAIT_LIMIT_DEFAULT_NS)
+    out = [inputs.to_numpy_bits(x) for x in p.run()]
+    torch.cuda.synchronize()
+    assert tf.tf_segments_status(p.seg) == (tf.TF_OK, 0)
+    check_exact(out[0], dense_bits(mods, inp)[0], "after a wait ran out")
+    p.seg.free()
+
+
+def test_two_rounds_at_once(mods):
+    """Two tables over the same pools, their calls on two streams at once (scratch apart)."""
+    tf, inputs, _, torch = mods
+    from paged import PagedAttn
+    inp = inputs.make_inputs(work(inputs, [16, 1, 8, 10], [4000, 900, 2100, 65]), backend="numpy")
+    a = PagedAttn(tf, inp, 32)
+    table = [(r, o, k, len(x) * 32) for (r, o, k), x in zip(inp.streams, a.lists)]
+    seg = tf.tf_paged_build(table, None, None, np.concatenate(a.lists), 32, a.n_pages, a.K, a.V, 0, 1)
+    out, partials = torch.empty_like(a.out[0]), torch.empty_like(a.partials)
+    torch.cuda.synchronize()
+    s = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(6):
+        tf.tf_attn_paged(a.seg, 0, a.q[0], a.partials, a.out[0], stream=s[0])
+        tf.tf_attn_paged(seg, 0, a.q[0], partials, out, stream=s[1])
+    torch.cuda.synchronize()
+    check_exact(inputs.to_numpy_bits(out), inputs.to_numpy_bits(a.out[0]), "two at once")
+    check_exact(inputs.to_numpy_bits(out), dense_bits(mods, inp)[0], "two at once, dense")
+    seg.free()
+    a.seg.free()

@@ -108,3 +108,29 @@ def test_short_list_is_refused_by_the_binding(T):
 
 def test_attn_paged_refuses_no_table(T):
     assert T.lib().tf_attn_paged(None, 0, P0, P0, P0, 0, None) == T.TF_EINVAL
+
+
+def test_host_arrays(T):
+    """The binding's int32 arrays: used in place where they fit, copied where not."""
+    import ctypes
+
+    import torch
+
+    def read(x, n):
+        at, keep = T._int32_array(x, n)
+        return list((ctypes.c_int32 * n).from_address(at))
+
+    a = np.arange(6, dtype=np.int32)
+    assert T._int32_array(a, 6)[0] == a.ctypes.data
+    frozen = a.copy()
+    frozen.setflags(write=False)
+    assert read(frozen, 6) == read(a, 6) == list(range(6))
+    for x in (a[::2], a[::2].astype(np.int64), [0, 2, 4], (0, 2, 4), torch.tensor([0, 2, 4]),
+              torch.tensor([0, 2, 4], dtype=torch.int32)):
+        assert read(x, 3) == [0, 2, 4]
+    assert T._int32_array(None) == (None, None)
+    T._int32_array(np.array([], np.int32), 0)
+    with pytest.raises(ValueError):
+        T._int32_array(a, 7)
+    with pytest.raises(OverflowError):
+        T._int32_array([1 << 31], 1)
