@@ -483,8 +483,9 @@ int tf_attn_paged(const tf_segments* seg, int attn_layer, const void* q, void* p
  *   n = x * w / sqrt(mean(x^2) + eps)
  *   y[j]    = n[j] cos(p f_j) - n[j+32] sin(p f_j)      f_j = theta^(-2j/64),
  *   y[j+32] = n[j+32] cos(p f_j) + n[j] sin(p f_j)      j < 32 (half-split)
- * rounded once to bf16 (angles to 2^-32 of a turn at every position). The rest
- * of the caches is left as it is.
+ * rounded once to bf16. Angles are reduced exactly (p times a 64-bit fraction of
+ * a turn) before they become fp32, so far positions are as good as near ones.
+ * The rest of the caches is left as it is.
  *   q   bf16, row r's TF_NQ heads at q + r*q_stride (elements)
  *   k, v  bf16, row r's TF_NKV heads at k + r*k_stride, v + r*v_stride: the
  *         three may be slices of one projection's rows. v is copied.
