@@ -17,9 +17,10 @@
 // position 2^22 is good to 2^-33 of a turn); its top 32 bits go to sincospif.
 //
 // A warp works on a group of 8 heads (of a row's 4 groups of queries, 1 of K, 1 of
-// V): one warp a group, a CTA a row, or for many rows a warp a row. A head is 4 lanes, each holding dimensions 8l..8l+7 and 32+8l.. of it, so a
-// rotation needs no exchange, and two shuffles sum the squares. Lane j computes
-// the sine and cosine of f_j, read by shuffles.
+// V): one warp a group, a CTA a row, or for many rows a warp a row. A head is 4
+// lanes, each holding dimensions 8l..8l+7 and 32+8l.. of it, so a rotation needs
+// no exchange, and two shuffles sum the squares. Lane j computes the sine and
+// cosine of f_j, read by shuffles.
 // HBM bound: 6,144 bytes in and as many out a row.
 #include <cmath>
 
