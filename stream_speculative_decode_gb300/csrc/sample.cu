@@ -138,15 +138,16 @@ __device__ __forceinline__ int key_at(int pos, int top) {
 __device__ __forceinline__ int word_of(int pos) { return pos < kSide ? kSide - 1 - pos : 8192 - kSide + pos; }
 
 // What a row's settings give: log2(e) / T, as a double and as a 64-bit fraction
-// with a shift, and -log2(min_p) in units of 2^-52. Doubles run at a 64th of the
-// fp32 rate, so one warp works these out while the others count.
+// with a shift, -log2(min_p) in units of 2^-52, and top_p and u in units of 2^-64
+// (cut there). Doubles run at a 64th of the fp32 rate and so do conversions to and
+// from 64 bits, so one warp works these out while the others count.
 struct Setting {
     double per;
-    u64 mant, y_min;
+    u64 mant, y_min, p, u;
     int shift;
 };
-__device__ __forceinline__ Setting setting_of(float T, float min_p) {
-    Setting s = {0.0, 0, kYLimit, 0};
+__device__ __forceinline__ Setting setting_of(float T, float top_p, float min_p, float u) {
+    Setting s = {0.0, 0, kYLimit, __float2ull_rz(fmaxf(top_p, 0.f) * 0x1p64f), __float2ull_rz(u * 0x1p64f), 0};
     if (T > 0.f) {
         s.per = 1.4426950408889634074 / double(T);
         // y 2^52 = d 2^12 per = d mant 2^(e - 64), d the difference in units of 2^-40
@@ -166,7 +167,10 @@ struct Scale {
     double vmax, per;     // any value
     long long xmax;       // folded window: the difference is an integer
     u64 mant;
-    int shift;
+    int shift, top_key;
+    __device__ __forceinline__ Scale any(const Setting& s) const {
+        return {value_of(top_key), s.per, xmax, mant, shift, top_key};
+    }
     __device__ __forceinline__ u64 y_of(u64 d) const {   // of a difference
         const u64 p = __umul64hi(d << 15, mant);
         if (shift <= 0) return shift < -63 ? 0 : p >> -shift;
@@ -180,15 +184,12 @@ struct Scale {
     }
 };
 __device__ __forceinline__ Scale scale_of(int top_key, bool fold, const Setting& s) {
-    return {value_of(top_key), s.per, fold ? fixed_of(top_key) : 0, s.mant, s.shift};
+    return {0.0, 0.0, fold ? fixed_of(top_key) : 0, s.mant, s.shift, top_key};   // any(): for the rows that need it
 }
 
-// floor(x m) of a float x in [0, 1) and a 64-bit m (the fraction cut at 2^-64), and the ceiling.
-__device__ __forceinline__ u64 part_of(float x, u64 m) { return __umul64hi(__float2ull_rz(x * 0x1p64f), m); }
-__device__ __forceinline__ u64 part_up(float x, u64 m) {
-    const u64 f = __float2ull_rz(x * 0x1p64f);
-    return __umul64hi(f, m) + (f * m != 0);
-}
+// The floor of a part of m, f in units of 2^-64, and the ceiling.
+__device__ __forceinline__ u64 part_of(u64 f, u64 m) { return __umul64hi(f, m); }
+__device__ __forceinline__ u64 part_up(u64 f, u64 m) { return __umul64hi(f, m) + (f * m != 0); }
 
 // n / d for a quotient below 2^34: a float quotient, its remainder's, and a last step of one.
 __device__ __forceinline__ u64 quotient(u64 n, u64 d) {
@@ -209,8 +210,9 @@ struct Shared {
     u64 mass[kMaxCluster];
     int32_t first[kMaxCluster], count[kMaxCluster], other[kMaxCluster], found[kMaxCluster];
     u64 min_p_mass;         // mass kept by min-p
-    int32_t hit_key;        // the value that find() found, the mass before it and its weight
-    u64 hit_mass, hit_weight;
+    // the token that find() found: its value, its number among the value's tokens and the mass up to its end
+    int32_t hit_key, hit_rank;
+    u64 hit_mass;
     u64 before[kValues / kGroup + 1];   // the mass before each group of the slice, and its whole
 };
 static_assert(kSide * 4 + sizeof(Shared) <= 32768, "the gap");
@@ -608,8 +610,9 @@ struct Row {
         return weight(scale.y<true>(min(0, top_key)), a.frac, sh.tab);
     }
 
-    // The value whose masses (before, after] hold m into every CTA's hit_*, by the one thread that
-    // holds it; `at` precedes the slice. A sync() has to follow.
+    // The token whose masses (before, after] hold m into every CTA's hit_*, by the one thread that
+    // holds it; `at` precedes the slice. A sync() has to follow. (The division by all threads took
+    // 4,500 cycles.)
     template <bool kFold>
     __device__ __forceinline__ void find(u64 m, u64 at, const Scale& scale, int top) const {
         if (m <= at || m > at + before()[groups()]) return;
@@ -624,19 +627,17 @@ struct Row {
                 const u64 w = next_weight<kFold>(next, pos + j, scale), x1 = x + hist()[word_of(pos + j)] * w;
                 if (m <= x1) {
                     tell_alone(sh.hit_key, key_at<kFold>(pos + j, top));
-                    tell_alone(sh.hit_mass, x);
-                    tell_alone(sh.hit_weight, w);
+                    const u64 n = quotient(m - 1 - x, w);
+                    tell_alone(sh.hit_rank, int32_t(n));
+                    tell_alone(sh.hit_mass, x + (n + 1) * w);
                     break;
                 }
                 x = x1;
             }
         }
     }
-    __device__ __forceinline__ u64 least_of(u64 Z) const { return max(u64(1), part_up(fmaxf(tp, 0.f), Z)); }
-    // After find(least): the first prefix mass of at least `least`.
-    __device__ __forceinline__ u64 top_p_mass(u64 least) const {
-        return sh.hit_mass + quotient(least - sh.hit_mass + sh.hit_weight - 1, sh.hit_weight) * sh.hit_weight;
-    }
+    // The mass that a top-p prefix has at least.
+    __device__ __forceinline__ u64 least_of(u64 Z) const { return max(u64(1), part_up(sh.set.p, Z)); }
     // The mass of the window's values with y <= y_min, and what precedes it, into every
     // CTA's min_p_mass: the last such position is found by bisection (y rises with positions)
     // in the slice that holds it; `Z` is the mass up to the window's end.
@@ -699,9 +700,10 @@ struct Row {
 // down. The kept mass; hit_* describe the pick at u of it. (Out of line, with its
 // own copy of the row's variables, and one site of each step in its loop: few
 // rows come here, and the others' code has to stay in the instruction caches.)
-__device__ __noinline__ u64 general(const Row R, const Scale scale, float mp, float u) {
+__device__ __noinline__ u64 general(const Row R, Scale scale, float mp) {
     Shared& sh = R.sh;
     Windows& win = *reinterpret_cast<Windows*>(R.dyn + 32768 + kSide * 4);
+    scale = scale.any(sh.set);
     u64 slice_at = 0, Z = 0, kept = 0;
     int nw = 0, held = 0;
     bool building = true;
@@ -734,7 +736,7 @@ __device__ __noinline__ u64 general(const Row R, const Scale scale, float mp, fl
 #pragma unroll 1
         for (; step < 3; ++step) {
             if ((step == 0 && !(R.tp < 1.f)) || (step == 1 && !(mp > 0.f))) continue;
-            const u64 to = step == 0 ? R.least_of(Z) : part_of(u, kept) + 1;
+            const u64 to = step == 0 ? R.least_of(Z) : part_of(sh.set.u, kept) + 1;
             int w = 0;
             if (step == 1) {   // the last window whose largest value is kept
                 while (w + 1 < nw && scale.y<false>(win.top[w + 1]) <= sh.set.y_min) ++w;
@@ -750,7 +752,7 @@ __device__ __noinline__ u64 general(const Row R, const Scale scale, float mp, fl
             if (step == 1) R.min_p_cut<false>(win.mass_before[w + 1], at, scale, win.top[w]);
             else R.find<false>(to, at, scale, win.top[w]);
             R.sync();
-            if (step < 2) kept = min(kept, step == 0 ? R.top_p_mass(to) : sh.min_p_mass);
+            if (step < 2) kept = min(kept, step == 0 ? sh.hit_mass : sh.min_p_mass);
             R.sync();   // hit_* are read before the next find
         }
     }
@@ -785,7 +787,7 @@ sample_rows_kernel(const __grid_constant__ Args a) {
     const bool bad_setting = !(T >= 0.f && T < INFINITY) || isnan(tp) || isnan(mp) || !(mp <= 1.f) ||
                              !(u >= 0.f && u < 1.f);
     if (tid >= kThreads - 32) {   // one warp; read after the count's barriers
-        const Setting set = setting_of(T, mp);
+        const Setting set = setting_of(T, tp, mp, u);
         const Scale step = scale_of(0, true, set);
         if (tid == kThreads - 32) sh.set = set;
 #pragma unroll 1
@@ -839,18 +841,18 @@ sample_rows_kernel(const __grid_constant__ Args a) {
                     if (!(tp < 1.f)) R.sync();
                     kept = min(kept, sh.min_p_mass);
                 }
-                const u64 to = pick ? part_of(u, kept) + 1 : R.least_of(Z);
+                const u64 to = pick ? part_of(sh.set.u, kept) + 1 : R.least_of(Z);
                 R.find<true>(to, at, scale, 0);
                 R.sync();
                 if (pick) break;
-                kept = min(kept, R.top_p_mass(to));
+                kept = min(kept, sh.hit_mass);
                 R.sync();   // hit_* are read before the next find
             }
         } else {
-            kept = general(R, scale, mp, u);
+            kept = general(R, scale, mp);
         }
         pick_key = sh.hit_key;
-        want = int(quotient(part_of(u, kept) - sh.hit_mass, sh.hit_weight));
+        want = sh.hit_rank;
     }
     pdl_trigger();
 
@@ -860,7 +862,7 @@ sample_rows_kernel(const __grid_constant__ Args a) {
         if (T > 0.f) {
             // the weight's first 64 bits over the mass's first 32 (2^-31 of it off at most),
             // the remainder as the quotient's last bit, so that the one rounding sees it
-            const u64 w = weight(fold ? scale.y<true>(pick_key) : scale.y<false>(pick_key), 63, sh.tab);
+            const u64 w = weight(fold ? scale.y<true>(pick_key) : scale.any(sh.set).y<false>(pick_key), 63, sh.tab);
             const int wu = __clzll((long long)w), ku = __clzll((long long)kept);
             const u64 den = (kept << ku) >> 32, q = quotient(w << wu, den);
             prob = ldexpf(float(q | u64(q * den != w << wu)), ku - wu + a.frac - 63 - 32);
