@@ -213,6 +213,10 @@ struct Shared {
     // the token that find() found: its value, its number among the value's tokens and the mass up to its end
     int32_t hit_key, hit_rank;
     u64 hit_mass;
+    // what one thread keeps for the end
+    Scale scale;
+    u64 kept;
+    int32_t pick_key, fold;
     u64 before[kValues / kGroup + 1];   // the mass before each group of the slice, and its whole
 };
 static_assert(kSide * 4 + sizeof(Shared) <= 32768, "the gap");
@@ -759,6 +763,22 @@ __device__ __noinline__ u64 general(const Row R, Scale scale, float mp) {
     return kept;
 }
 
+// The row's prob and flag.
+__device__ __noinline__ void report(const Args& a, int row, const Shared& sh) {
+    float prob = 1.f;
+    if (sh.kept) {
+        // the weight's first 64 bits over the mass's first 32 (2^-31 of it off at most),
+        // the remainder as the quotient's last bit, so that the one rounding sees it
+        const u64 y = sh.fold ? sh.scale.y<true>(sh.pick_key) : sh.scale.any(sh.set).y<false>(sh.pick_key);
+        const u64 w = weight(y, 63, sh.tab);
+        const int wu = __clzll((long long)w), ku = __clzll((long long)sh.kept);
+        const u64 den = (sh.kept << ku) >> 32, q = quotient(w << wu, den);
+        prob = ldexpf(float(q | u64(q * den != w << wu)), ku - wu + a.frac - 63 - 32);
+    }
+    if (a.prob) a.prob[row] = prob;
+    a.flag[row] = 0;
+}
+
 __global__ void __launch_bounds__(kThreads, 2)
 sample_rows_kernel(const __grid_constant__ Args a) {
     extern __shared__ __align__(128) unsigned char dyn[];
@@ -857,18 +877,11 @@ sample_rows_kernel(const __grid_constant__ Args a) {
     pdl_trigger();
 
     const int lane = tid & 31, warp = tid >> 5;
-    if (tid == kThreads - 1 && rank == 0) {
-        float prob = 1.f;
-        if (T > 0.f) {
-            // the weight's first 64 bits over the mass's first 32 (2^-31 of it off at most),
-            // the remainder as the quotient's last bit, so that the one rounding sees it
-            const u64 w = weight(fold ? scale.y<true>(pick_key) : scale.any(sh.set).y<false>(pick_key), 63, sh.tab);
-            const int wu = __clzll((long long)w), ku = __clzll((long long)kept);
-            const u64 den = (kept << ku) >> 32, q = quotient(w << wu, den);
-            prob = ldexpf(float(q | u64(q * den != w << wu)), ku - wu + a.frac - 63 - 32);
-        }
-        if (a.prob) a.prob[row] = prob;
-        a.flag[row] = 0;
+    if (tid == kThreads - 1) {   // for report(), below
+        sh.scale = scale;
+        sh.fold = fold;
+        sh.kept = T > 0.f ? kept : 0;
+        sh.pick_key = pick_key;
     }
 
     // ---- the second pass: the want-th token of value pick_key, over the CTA's
@@ -956,6 +969,7 @@ sample_rows_kernel(const __grid_constant__ Args a) {
             }
         }
     }
+    if (tid == kThreads - 1 && rank == 0) report(a, row, sh);   // now, as the search's steps wait for every warp
     if (left < 0) return;
     load(v, from + mine * kChunk + warp * kStep);
 #pragma unroll 1
