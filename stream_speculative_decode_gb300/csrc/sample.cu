@@ -201,6 +201,7 @@ __device__ __forceinline__ u64 quotient(u64 n, u64 d) {
 }
 
 struct Shared {
+    uint32_t above[4];        // the window's words for positive tokens outside
     ExpTables tab;
     Setting set;
     u64 ratio[kSide / 128];   // folded: the weight of one step of each power of two, in units of 2^-63
@@ -220,8 +221,10 @@ struct Shared {
     u64 before[kValues / kGroup + 1];   // the mass before each group of the slice, and its whole
 };
 static_assert(kSide * 4 + sizeof(Shared) <= 32768, "the gap");
-// Behind the histogram: the windows of a row outside the folded one.
+// Behind the histogram: its words for negative tokens outside, and the windows of
+// a row outside the folded one.
 struct Windows {
+    uint32_t above[4];
     u64 mass_before[kMaxWindows + 1];
     int32_t top[kMaxWindows], count_before[kMaxWindows];
 };
@@ -286,38 +289,32 @@ __device__ __forceinline__ int count_one(uint32_t* hist, uint32_t b, int other) 
     }
     return other;
 }
-// Halves of a word: 0x8000 + magnitude - kLowMag. Both tokens lie in the window
-// when these keep bit 15 and lose it with the window's size subtracted (no borrow
-// crosses a half).
-__device__ __forceinline__ uint32_t above_low(uint32_t w) { return (w | 0x80008000u) - uint32_t(kLowMag) * 0x10001u; }
-__device__ __forceinline__ uint32_t inside(uint32_t r) { return r & ~(r - uint32_t(kSide - 1) * 0x10001u); }
-__device__ __forceinline__ void count_word(unsigned char* dyn, uint32_t w, uint32_t r) {
-    const uint32_t e = (w & 0x80008000u) | (r << 2 & 0x7FFF7FFFu);        // byte offsets less 4; the low half's
-    atomicAdd(reinterpret_cast<uint32_t*>(dyn + (e & 0xFFFFu) + 4), 1u);  // bit 15 adds 2 to the high one's
-    atomicAdd(reinterpret_cast<uint32_t*>(dyn + (e >> 16) + 2), 1u);
+// The magnitudes of a word's two tokens above kLowMag, modulo 2^16: kSide - 1 or
+// more for a token outside the window.
+__device__ __forceinline__ uint32_t above_low(uint32_t w) {
+    return __vadd2(w & 0x7FFF7FFFu, uint32_t(0x10000 - kLowMag) * 0x10001u);
 }
-// A word with a token outside that is not masked.
-__device__ __noinline__ int count_odd(uint32_t w, int other) {
+constexpr uint32_t kOutside = uint32_t(kSide - 1) * 0x10001u;
+// Counts both, those outside in a word behind their side's positions, so that masked tokens cost no branch.
+__device__ __forceinline__ void count_word(unsigned char* dyn, uint32_t w, uint32_t d) {
+    const uint32_t e = (w & 0x80008000u) | __vminu2(d, kOutside) << 2;   // byte offsets less 4
+    atomicAdd(reinterpret_cast<uint32_t*>(dyn + (e & 0xFFFFu) + 4), 1u);
+    atomicAdd(reinterpret_cast<uint32_t*>(dyn + (e >> 16) + 4), 1u);
+}
+// Whether some token is outside and not masked.
+__device__ __forceinline__ bool is_odd(uint32_t w) {
+    const uint32_t d = above_low(w);
+    return ((d & 0xFFFFu) >= kSide - 1 && (w & 0xFFFFu) != 0xFF80u) || (d >> 16 >= kSide - 1 && w >> 16 != 0xFF80u);
+}
+// 8 tokens' part in `other`, and their zeros.
+__device__ __noinline__ int count_odd(uint4 v, int other) {
     extern __shared__ __align__(128) unsigned char dyn[];
 #pragma unroll 1
-    for (int k = 0; k < 2; ++k, w >>= 16)
-        if (!(inside(above_low(w & 0xFFFFu)) & 0x8000u)) other = count_one(reinterpret_cast<uint32_t*>(dyn), w & 0xFFFFu, other);
-    return other;
-}
-// 8 tokens of which some lie outside, or are masked, which all rows under a
-// grammar's mask hold (out of line: the counting loop has a copy a vector in
-// flight, and the kernel's code has to stay in the instruction caches).
-__device__ __noinline__ int count_mixed(uint4 v, int other) {
-    extern __shared__ __align__(128) unsigned char dyn[];
-    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const uint32_t w = x[k], r = above_low(w), in = inside(r);
-        const uint32_t e = (w & 0x80008000u) | (r << 2 & 0x7FFF7FFFu), masked = w ^ 0xFF80FF80u;
-        // a half out of the window keeps the low half's two bits out of the high one's offset by the mask
-        if (in & 0x8000u) atomicAdd(reinterpret_cast<uint32_t*>(dyn + (e & 0xFFFCu) + 4), 1u);
-        if (in & 0x80000000u) atomicAdd(reinterpret_cast<uint32_t*>(dyn + (e >> 16 & 0xFFFCu) + 4), 1u);
-        if ((!(in & 0x8000u) && masked & 0xFFFFu) || (!(in & 0x80000000u) && masked >> 16)) other = count_odd(w, other);
+    for (int k = 0; k < 8; ++k) {
+        const uint32_t b = v.x & 0xFFFFu;
+        if ((above_low(b) & 0xFFFFu) >= kSide - 1) other = count_one(reinterpret_cast<uint32_t*>(dyn), b, other);
+        v.x = k & 1 ? v.y : v.x >> 16;
+        if (k & 1) v.y = v.z, v.z = v.w;
     }
     return other;
 }
@@ -819,15 +816,14 @@ sample_rows_kernel(const __grid_constant__ Args a) {
     for_tokens(
         p, begin, end, R.head,
         [&](const uint4& v) {
-            const uint32_t r[4] = {above_low(v.x), above_low(v.y), above_low(v.z), above_low(v.w)};
-            if ((inside(r[0]) & inside(r[1]) & inside(r[2]) & inside(r[3]) & 0x80008000u) == 0x80008000u) {
-                count_word(dyn, v.x, r[0]);
-                count_word(dyn, v.y, r[1]);
-                count_word(dyn, v.z, r[2]);
-                count_word(dyn, v.w, r[3]);
-            } else {
-                other = count_mixed(v, other);
-            }
+            const uint32_t d[4] = {above_low(v.x), above_low(v.y), above_low(v.z), above_low(v.w)};
+            count_word(dyn, v.x, d[0]);
+            count_word(dyn, v.y, d[1]);
+            count_word(dyn, v.z, d[2]);
+            count_word(dyn, v.w, d[3]);
+            const uint32_t most = __vmaxu2(__vmaxu2(d[0], d[1]), __vmaxu2(d[2], d[3]));
+            if (max(most & 0xFFFFu, most >> 16) >= kSide - 1 && (is_odd(v.x) || is_odd(v.y) || is_odd(v.z) || is_odd(v.w)))
+                other = count_odd(v, other);
         },
         [&](uint32_t b) { other = count_one(hist, b, other); });
 
