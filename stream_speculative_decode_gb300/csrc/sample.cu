@@ -19,7 +19,8 @@
 // window of both signs' magnitudes (2^-33, 128) and zero, which needs no maximum
 // first; the largest occupied value is the maximum. A row with any other finite
 // value (one N(0, 3) row in 250,000) is counted again in windows of 10,240
-// consecutive values from its largest down. A second pass, from L2, finds the
+// consecutive values from its largest down, unless what is outside has no weight
+// (a mask by a large negative number). A second pass, from L2, finds the
 // picked value's j-th token.
 //
 // A row is shared by a cluster of 1 to 8 CTAs. Each counts a part of the
@@ -111,10 +112,11 @@ __device__ __forceinline__ int key_of(uint32_t bits) {
     const int mag = int(bits & 0x7FFFu);
     return bits & 0x8000u ? -mag : mag;
 }
-__device__ __forceinline__ double value_of(int key) {
+__device__ __forceinline__ float float_of(int key) {
     const float v = __uint_as_float(uint32_t(key < 0 ? -key : key) << 16);
-    return key < 0 ? -double(v) : double(v);
+    return key < 0 ? -v : v;
 }
+__device__ __forceinline__ double value_of(int key) { return double(float_of(key)); }
 // A folded window's value in units of 2^-40 (0, or 8 significant bits shifted by up to 39).
 __device__ __forceinline__ long long fixed_of(int key) {
     const int mag = key < 0 ? -key : key;
@@ -145,11 +147,13 @@ struct Setting {
     double per;
     u64 mant, y_min, p, u;
     int shift;
+    float per_f;
 };
 __device__ __forceinline__ Setting setting_of(float T, float top_p, float min_p, float u) {
-    Setting s = {0.0, 0, kYLimit, __float2ull_rz(fmaxf(top_p, 0.f) * 0x1p64f), __float2ull_rz(u * 0x1p64f), 0};
+    Setting s = {0.0, 0, kYLimit, __float2ull_rz(fmaxf(top_p, 0.f) * 0x1p64f), __float2ull_rz(u * 0x1p64f), 0, 0.f};
     if (T > 0.f) {
         s.per = 1.4426950408889634074 / double(T);
+        s.per_f = float(s.per);
         // y 2^52 = d 2^12 per = d mant 2^(e - 64), d the difference in units of 2^-40
         int e;
         s.mant = u64(frexp(s.per * 4096.0, &e) * 0x1p64);
@@ -301,11 +305,10 @@ __device__ __forceinline__ void count_word(unsigned char* dyn, uint32_t w, uint3
     atomicAdd(reinterpret_cast<uint32_t*>(dyn + (e & 0xFFFFu) + 4), 1u);
     atomicAdd(reinterpret_cast<uint32_t*>(dyn + (e >> 16) + 4), 1u);
 }
-// Whether some token is outside and not masked.
-__device__ __forceinline__ bool is_odd(uint32_t w) {
-    const uint32_t d = above_low(w);
-    return ((d & 0xFFFFu) >= kSide - 1 && (w & 0xFFFFu) != 0xFF80u) || (d >> 16 >= kSide - 1 && w >> 16 != 0xFF80u);
-}
+// Of a word with a token outside: finite ones from -128 down, and masked ones,
+// are 0 to kMasked here, in order of their magnitudes, all others more.
+constexpr uint32_t kMasked = 0xFF80 - 0xC300;
+__device__ __forceinline__ uint32_t below_low(uint32_t w) { return __vadd2(w, (0x10000u - 0xC300u) * 0x10001u); }
 // 8 tokens' part in `other`, and their zeros.
 __device__ __noinline__ int count_odd(uint4 v, int other) {
     extern __shared__ __align__(128) unsigned char dyn[];
@@ -822,14 +825,27 @@ sample_rows_kernel(const __grid_constant__ Args a) {
             count_word(dyn, v.z, d[2]);
             count_word(dyn, v.w, d[3]);
             const uint32_t most = __vmaxu2(__vmaxu2(d[0], d[1]), __vmaxu2(d[2], d[3]));
-            if (max(most & 0xFFFFu, most >> 16) >= kSide - 1 && (is_odd(v.x) || is_odd(v.y) || is_odd(v.z) || is_odd(v.w)))
-                other = count_odd(v, other);
+            if (max(most & 0xFFFFu, most >> 16) < kSide - 1) return;
+            uint32_t x[4] = {v.x, v.y, v.z, v.w}, below = ~0u, odd = 0;   // the largest of what only a token outside that is not below reaches
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                asm volatile("" : "+r"(x[k]));   // d is not kept for this branch: its registers cost 3 us
+                const uint32_t b = below_low(x[k]);
+                below = __vminu2(below, b);
+                odd = __vmaxu2(odd, __vminu2(above_low(x[k]), kOutside) + __vminu2(b, (kMasked + 1) * 0x10001u));
+            }
+            below = min(below & 0xFFFFu, below >> 16);
+            if (below < kMasked) other = max(other, -int(below + 0x4300));
+            if (max(odd & 0xFFFFu, odd >> 16) == kSide + kMasked) other = count_odd(v, other);
         },
         [&](uint32_t b) { other = count_one(hist, b, other); });
 
     const auto found = R.survey(other);
-    const bool fold = found.other == kMinKey;
-    const int top_key = max(found.first < kValues ? key_at<true>(found.first, 0) : kMinKey, found.other);
+    const int most = found.first < kValues ? key_at<true>(found.first, 0) : kMinKey, top_key = max(most, found.other);
+    // what lies outside does not matter if it has no weight, as a mask by a large negative number has not (62 would
+    // be the limit; a row just above it is right either way)
+    const bool fold = found.other == kMinKey ||
+                      (most > found.other && (float_of(most) - float_of(found.other)) * sh.set.per_f > 62.1f);
     R.top_key = top_key;
     if (top_key == kBadKey || top_key == kMinKey || bad_setting) {
         if (tid == 0 && rank == 0) {

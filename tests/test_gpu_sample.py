@@ -226,6 +226,25 @@ def test_masks(mods):
     check(mods, x, 3001, u)
 
 
+@pytest.mark.parametrize("mask", [-128.0, -133.0, -500.0, -1e4, -1e9, -3.3895313892515355e38])
+def test_finite_masks(mods, mask):
+    """Large negative numbers in masked places, from where they still have weight to where they have none."""
+    tf, torch = mods
+    R, V = 96, 3001
+    x = normal(torch, R, V, 3.0, 40)
+    g = torch.Generator(device="cuda").manual_seed(41)
+    off = torch.rand(x.shape, generator=g, device="cuda") < torch.linspace(0, 1, R, device="cuda")[:, None]
+    x = torch.where(off, mask, x.float()).to(torch.bfloat16)
+    x[0::8, 17] = 0.0                     # with zeros, masked ones by -Inf, tiny and large ones beside them
+    x[1::8, ::3] = -math.inf
+    x[2::8, 100] = 2.0 ** -60
+    x[3::8, 2000] = 130.0
+    kw, u = settings(R, 42)
+    check(mods, x, V, u, **kw)
+    for t in (1.0, 2.9, 3.1, 3.3, 50.0, 1e3, 1e8, 1e30, 3.4e38):
+        check(mods, x, V, u, **(kw | dict(temperature=np.full(R, t))))
+
+
 def test_nonfinite_rows_and_bad_settings(mods):
     tf, torch = mods
     R, V = 24, 2000
