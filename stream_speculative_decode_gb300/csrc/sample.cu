@@ -28,10 +28,11 @@
 // (distributed shared memory), weighs it, and every CTA learns the slices'
 // totals: all of them follow the same steps with the same numbers.
 //
-// Measured on a GB300 (1,024 rows of 128,000 N(0, 3) logits): 105 us, 2.5 TB/s,
-// 37 % of the copy rate; a CTA's row takes 55,000 cycles, two CTAs an SM, of which
-// the count is 24,000 (HBM and shared-memory atomics), the weights 9,000, the
-// search 9,000. 16 rows, 4 CTAs each: 17 us, a chain of latencies.
+// Measured on a GB300 (1,024 rows of 128,000 N(0, 3) logits): 99 us, 2.6 TB/s,
+// 39 % of the copy rate; masked rows 94 to 101. A CTA's row takes 52,000 cycles,
+// two CTAs an SM, of which the count is 24,000 (HBM and shared-memory atomics),
+// the weights 9,000, the search 9,000. 16 rows, 4 CTAs each: 15 us, a chain of
+// latencies.
 #include <cmath>
 
 #include <cooperative_groups.h>
@@ -826,10 +827,11 @@ sample_rows_kernel(const __grid_constant__ Args a) {
             count_word(dyn, v.w, d[3]);
             const uint32_t most = __vmaxu2(__vmaxu2(d[0], d[1]), __vmaxu2(d[2], d[3]));
             if (max(most & 0xFFFFu, most >> 16) < kSide - 1) return;
-            uint32_t x[4] = {v.x, v.y, v.z, v.w}, below = ~0u, odd = 0;   // the largest of what only a token outside that is not below reaches
+            uint32_t x[4] = {v.x, v.y, v.z, v.w}, below = ~0u;
+            uint32_t odd = 0;   // its largest value is that of tokens outside which are not below
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                asm volatile("" : "+r"(x[k]));   // d is not kept for this branch: its registers cost 3 us
+                asm volatile("" : "+r"(x[k]));   // d is not kept for this branch: the registers cost 3 us
                 const uint32_t b = below_low(x[k]);
                 below = __vminu2(below, b);
                 odd = __vmaxu2(odd, __vminu2(above_low(x[k]), kOutside) + __vminu2(b, (kMasked + 1) * 0x10001u));
@@ -842,8 +844,8 @@ sample_rows_kernel(const __grid_constant__ Args a) {
 
     const auto found = R.survey(other);
     const int most = found.first < kValues ? key_at<true>(found.first, 0) : kMinKey, top_key = max(most, found.other);
-    // what lies outside does not matter if it has no weight, as a mask by a large negative number has not (62 would
-    // be the limit; a row just above it is right either way)
+    // what lies outside does not matter if it has no weight, as a large negative number has
+    // none (y >= 62; a row close to that is right either way)
     const bool fold = found.other == kMinKey ||
                       (most > found.other && (float_of(most) - float_of(found.other)) * sh.set.per_f > 62.1f);
     R.top_key = top_key;
