@@ -11,9 +11,13 @@
 // few hundredth row, so masses are exact to 64 bits: bf16 logits take few
 // distinct values, a value's mass is its count times one weight, the counts
 // are integers (a histogram in shared memory, so the order of its atomics does
-// not matter) and the weights are 64-bit fixed point. Masses of up to V tokens
-// of weight 1 fit 64 bits at 63 - log2(V) fraction bits (46 at V = 128,000: a
-// weight is off by about 2^-46 of the largest).
+// not matter) and the weights are 64-bit fixed point. A row has as many fraction
+// bits as its whole mass M leaves room for, 63 - ceil(log2 M) or up to two fewer (M
+// from 1, its largest value's weight, to V; a rough float sum over the counts says
+// which). With bits for M = V a peak before a long flat tail would have its borders
+// off by up to V^2 2^-64 (2^-26 at 2^19 tokens); with its own a weight is off by
+// M 2^-61 at most and a border by V 2^-59 of the kept mass, the weights below 2^-62,
+// which are 0, among it (9e-13 at 2^19 tokens).
 //
 // One pass over a row: its tokens are counted as they arrive, in a folded
 // window of both signs' magnitudes (2^-33, 128) and zero, which needs no maximum
@@ -33,6 +37,7 @@
 // two CTAs an SM, of which the count is 24,000 (HBM and shared-memory atomics),
 // the weights 9,000, the search 9,000. 16 rows, 4 CTAs each: 15 us, a chain of
 // latencies.
+#include <cfloat>
 #include <cmath>
 
 #include <cooperative_groups.h>
@@ -108,6 +113,12 @@ __device__ __forceinline__ u64 weight(u64 y, int frac, const ExpTables& tab) {
     return shift > 63 ? 0 : (w + (u64(1) << shift >> 1)) >> shift;
 }
 
+__device__ __forceinline__ float exp2_of(float x) {   // 2^x, good to 2^-22 of it, for the rough mass
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // Values are handled as keys, signed magnitudes: -0 is +0 and keys rise with values.
 __device__ __forceinline__ int key_of(uint32_t bits) {
     const int mag = int(bits & 0x7FFFu);
@@ -154,7 +165,7 @@ __device__ __forceinline__ Setting setting_of(float T, float top_p, float min_p,
     Setting s = {0.0, 0, kYLimit, __float2ull_rz(fmaxf(top_p, 0.f) * 0x1p64f), __float2ull_rz(u * 0x1p64f), 0, 0.f};
     if (T > 0.f) {
         s.per = 1.4426950408889634074 / double(T);
-        s.per_f = float(s.per);
+        s.per_f = fminf(float(s.per), FLT_MAX);
         // y 2^52 = d 2^12 per = d mant 2^(e - 64), d the difference in units of 2^-40
         int e;
         s.mant = u64(frexp(s.per * 4096.0, &e) * 0x1p64);
@@ -215,6 +226,7 @@ struct Shared {
     // what the cluster's CTAs tell one another, by rank
     u64 mass[kMaxCluster];
     int32_t first[kMaxCluster], count[kMaxCluster], other[kMaxCluster], found[kMaxCluster];
+    float part[kMaxCluster];   // of the row's rough mass
     u64 min_p_mass;         // mass kept by min-p
     // the token that find() found: its value, its number among the value's tokens and the mass up to its end
     int32_t hit_key, hit_rank;
@@ -222,7 +234,7 @@ struct Shared {
     // what one thread keeps for the end
     Scale scale;
     u64 kept;
-    int32_t pick_key, fold;
+    int32_t pick_key, fold, frac;
     u64 before[kValues / kGroup + 1];   // the mass before each group of the slice, and its whole
 };
 static_assert(kSide * 4 + sizeof(Shared) <= 32768, "the gap");
@@ -246,7 +258,7 @@ struct Args {
     int32_t* pick;
     float* prob;
     uint8_t* flag;
-    int32_t V, frac;
+    int32_t V;
     int32_t chunk;       // tokens a CTA of the cluster counts, a multiple of 8
 };
 
@@ -346,6 +358,7 @@ struct Row {
     float tp;
     int32_t K;
     int top_key;
+    int frac;            // fraction bits of the row's weights
 
     __device__ __forceinline__ uint32_t* hist() const { return reinterpret_cast<uint32_t*>(dyn); }
     __device__ __forceinline__ u64* before() const { return sh.before; }
@@ -391,12 +404,45 @@ struct Row {
     }
     __device__ __forceinline__ int groups() const { return (s1 - s0) / kGroup; }
 
+    // The weight of a value relative to that of one not below it.
+    __device__ __forceinline__ float relative(float from, float to) const { return exp2_of((to - from) * sh.set.per_f); }
+    // The mass of a folded group's n tokens (c, by position) relative to the weight of the value
+    // `ref`, that of `first`, the first occupied position here or in an earlier group. Where the
+    // group's weights are within a factor of 2, all get the largest; otherwise, as its values are
+    // equal steps apart (zero aside), a polynomial in the step's weight, from the last position up.
+    __device__ __forceinline__ float group_mass(int pos, int first, float ref, int n,
+                                                const uint32_t (&c)[kGroup]) const {
+        const int key = key_at<true>(pos, 0);
+        const float from = fminf(ref, float_of(key));   // position max(pos, first)'s value
+        const float step = __uint_as_float((uint32_t(abs(key)) >> 7) - 7 << 23) * sh.set.per_f;
+        float m = float(n);
+        if (7.f * step > 1.f || pos == kSide - kGroup) {
+            const float w = exp2_of(-step);
+            m = 0.f;
+#pragma unroll
+            for (int j = kGroup - 1; j >= 0; --j) {
+                if (pos + j < first) continue;
+                m *= w;
+                if (pos + j != kSide - 1) m += float(c[j]);
+            }
+            if (pos == kSide - kGroup) m += float(c[kGroup - 1]) * relative(from, 0.f);
+        }
+        return m * relative(ref, from);
+    }
+    // The warp's sum of masses m, each relative to the weight of its lane's value v, relative to `top`'s.
+    __device__ __forceinline__ uint32_t rough_sum(float m, float v, float top) const {
+        return __reduce_add_sync(0xFFFFFFFFu, __float2uint_ru(m * relative(top, v)));
+    }
+
     // After the count: sums the slice over the cluster and surveys it. The
     // window's first occupied position and tokens, the largest of every
-    // thread's `other`.
+    // thread's `other`, and (folded) the tokens' mass, of which the first position's
+    // tokens have 1 each: too large by a factor of 2 1/4 at most, too small by 2^-14 of it.
     struct Survey {
         int first, count, other;
+        float mass;
     };
+    template <bool kFold>
     __device__ __forceinline__ Survey survey(int other) const {
         sync();
         if (ncl > 1) {
@@ -422,28 +468,50 @@ struct Row {
             __syncthreads();
         }
         int first = kValues, n = 0;
+        float mass = 0.f, ref = -INFINITY;   // the thread's, relative to its first position's value
 #pragma unroll 1
         for (int g = int(threadIdx.x); g < groups(); g += kThreads) {
             uint32_t c[kGroup];
             if (!load_group(g, c)) continue;
+            int in_group = 0;
 #pragma unroll
             for (int j = kGroup - 1; j >= 0; --j) {
-                n += c[j];
+                in_group += c[j];
                 if (c[j]) first = min(first, s0 + kGroup * g + j);
+            }
+            n += in_group;
+            if constexpr (kFold) {
+                if (mass == 0.f) ref = float_of(key_at<true>(first, 0));
+                mass += group_mass(s0 + kGroup * g, first, ref, in_group, c);
             }
         }
         first = __reduce_min_sync(0xFFFFFFFFu, first);
         n = __reduce_add_sync(0xFFFFFFFFu, n);
         other = __reduce_max_sync(0xFFFFFFFFu, other);
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        float top = -INFINITY;
+        uint32_t rough = 0;   // the sums in units of 2^-12, rounded up
+        if constexpr (kFold) {
+            if (first < kValues) top = float_of(key_at<true>(first, 0));
+            rough = rough_sum(mass * 4096.f, ref, top);
+        }
         if (lane == 0) {
             sh.warp_int[0][warp] = first;
             sh.warp_int[1][warp] = n;
             sh.warp_int[2][warp] = other;
+            if constexpr (kFold) sh.warp_mass[warp] = u64(__float_as_uint(top)) << 32 | rough;
         }
         __syncthreads();
         Survey s;
-        s.first = __reduce_min_sync(0xFFFFFFFFu, sh.warp_int[0][lane % kWarps]);
+        const int theirs = sh.warp_int[0][lane % kWarps];
+        s.first = __reduce_min_sync(0xFFFFFFFFu, theirs);
+        s.mass = 0.f;
+        if constexpr (kFold) {
+            const u64 x = sh.warp_mass[lane % kWarps];
+            const float m = lane < kWarps ? float(uint32_t(x)) : 0.f, v = __uint_as_float(uint32_t(x >> 32));
+            if (s.first < kValues) top = float_of(key_at<true>(s.first, 0));
+            s.mass = float(rough_sum(m, v, top)) * 0x1p-12f;
+        }
         s.count = __reduce_add_sync(0xFFFFFFFFu, lane < kWarps ? sh.warp_int[1][lane] : 0);
         s.other = __reduce_max_sync(0xFFFFFFFFu, sh.warp_int[2][lane % kWarps]);
         if (ncl == 1) {
@@ -454,13 +522,21 @@ struct Row {
         tell(sh.first[rank], s.first);
         tell(sh.count[rank], s.count);
         tell(sh.other[rank], s.other);
+        if constexpr (kFold) tell(sh.part[rank], s.mass);
         sync();
-        s = {kValues, 0, kMinKey};
+        s = {kValues, 0, kMinKey, 0.f};
 #pragma unroll 1
         for (int r = 0; r < ncl; ++r) {
             s.first = min(s.first, sh.first[r]);
             s.count += sh.count[r];
             s.other = max(s.other, sh.other[r]);
+        }
+        if constexpr (kFold) {
+            const float top = float_of(key_at<true>(s.first, 0));
+#pragma unroll 1
+            for (int r = 0; r < ncl; ++r)
+                if (sh.first[r] < kValues)
+                    s.mass += sh.part[r] * relative(top, float_of(key_at<true>(sh.first[r], 0)));
         }
         return s;
     }
@@ -574,7 +650,7 @@ struct Row {
     __device__ __forceinline__ Weights first_weight(int pos, const Scale& scale, int top) const {
         const int key = key_at<kFold>(pos, top);
         return {weight(scale.y<kFold>(min(key, top_key)), 63, sh.tab),
-                kFold ? sh.ratio[(abs(key) >> 7) - (kLowMag >> 7)] : 0, key, 63 - a.frac};
+                kFold ? sh.ratio[(abs(key) >> 7) - (kLowMag >> 7)] : 0, key, 63 - frac};
     }
     // The position's weight, and on to the next position's.
     template <bool kFold>
@@ -612,7 +688,7 @@ struct Row {
         }
     }
     __device__ __forceinline__ u64 zero_weight(const Scale& scale) const {
-        return weight(scale.y<true>(min(0, top_key)), a.frac, sh.tab);
+        return weight(scale.y<true>(min(0, top_key)), frac, sh.tab);
     }
 
     // The token whose masses (before, after] hold m into every CTA's hit_*, by the one thread that
@@ -696,10 +772,54 @@ struct Row {
                 v = make_uint4(v.y, v.z, v.w, 0);
             }
         }, one);
-        return survey(below);
+        return survey<false>(below);
     }
 
 };
+
+// The fraction bits of a row of rough mass m (1 or more): m 2^frac <= 2^63, so that half
+// a unit more for each of its tokens passes no 2^64.
+__device__ __forceinline__ int frac_of(float m) {
+    return 63 + 126 - (__float_as_int(m * (1.f + 0x1p-8f)) >> 23);
+}
+
+// The mass of all of a row's tokens, any values; for all threads of the cluster.
+__device__ __noinline__ float mass_of_all(const Row R) {
+    Shared& sh = R.sh;
+    const float per = sh.set.per_f;
+    if (!(per < 1e38f)) return float(R.a.V);   // log2(e) / T may not be a float: the most there can be
+    const float half = 0.5f * float_of(R.top_key);   // halves: the difference may not be a float either
+    float m = 0.f;
+    auto one = [&](uint32_t b) {
+        if (b == 0xFF80u) return;
+        const float d = half - 0.5f * float_of(key_of(b));
+        m += d > 0.f ? exp2_of(-2.f * (d * per)) : 1.f;
+    };
+    for_tokens(R.p, R.begin, R.end, R.head, [&](uint4 v) {
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k) {
+            one(v.x & 0xFFFFu);
+            one(v.x >> 16);
+            v = make_uint4(v.y, v.z, v.w, 0);
+        }
+    }, one);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 16; o; o /= 2) m += __shfl_xor_sync(0xFFFFFFFFu, m, o);
+    if (lane == 0) sh.warp_mass[warp] = __float_as_uint(m);
+    __syncthreads();
+    m = __uint_as_float(uint32_t(sh.warp_mass[lane % kWarps]));
+#pragma unroll
+    for (int o = kWarps / 2; o; o /= 2) m += __shfl_xor_sync(0xFFFFFFFFu, m, o);
+    if (R.ncl == 1) return m;
+    R.sync();   // the parts of the survey are read
+    R.tell(sh.part[R.rank], m);
+    R.sync();
+    m = 0.f;
+#pragma unroll 1
+    for (int r = 0; r < R.ncl; ++r) m += sh.part[r];
+    return m;
+}
 
 // A row outside the folded window: windows of kValues keys from its largest
 // down. The kept mass; hit_* describe the pick at u of it. (Out of line, with its
@@ -774,7 +894,7 @@ __device__ __noinline__ void report(const Args& a, int row, const Shared& sh) {
         const u64 w = weight(y, 63, sh.tab);
         const int wu = __clzll((long long)w), ku = __clzll((long long)sh.kept);
         const u64 den = (sh.kept << ku) >> 32, q = quotient(w << wu, den);
-        prob = ldexpf(float(q | u64(q * den != w << wu)), ku - wu + a.frac - 63 - 32);
+        prob = ldexpf(float(q | u64(q * den != w << wu)), ku - wu + sh.frac - 63 - 32);
     }
     if (a.prob) a.prob[row] = prob;
     a.flag[row] = 0;
@@ -792,7 +912,8 @@ sample_rows_kernel(const __grid_constant__ Args a) {
     const int skew = int(-reinterpret_cast<uintptr_t>(p) & 15u) / 2;
     const int begin = rank ? min(a.V, skew + rank * a.chunk) : 0;
     const int end = rank == ncl - 1 ? a.V : min(a.V, skew + (rank + 1) * a.chunk);
-    Row R{a, dyn, sh, ncl, rank, begin, end, rank ? 0 : skew, rank * slice, (rank + 1) * slice, p, 1.f, a.V, kMinKey};
+    Row R{a, dyn, sh, ncl, rank, begin, end, rank ? 0 : skew, rank * slice, (rank + 1) * slice, p, 1.f, a.V,
+          kMinKey, 0};
     uint32_t* const hist = R.hist();
     if (tid < 64) {
         sh.tab.coarse[tid] = kExpTables.coarse[tid];
@@ -842,7 +963,7 @@ sample_rows_kernel(const __grid_constant__ Args a) {
         },
         [&](uint32_t b) { other = count_one(hist, b, other); });
 
-    const auto found = R.survey(other);
+    const auto found = R.survey<true>(other);
     const int most = found.first < kValues ? key_at<true>(found.first, 0) : kMinKey, top_key = max(most, found.other);
     // what lies outside does not matter if it has no weight, as a large negative number has
     // none (y >= 62; a row close to that is right either way)
@@ -863,6 +984,7 @@ sample_rows_kernel(const __grid_constant__ Args a) {
     u64 kept = 0;
     int pick_key = top_key, want = 0;   // the pick: the want-th token (by id) of value pick_key
     if (T > 0.f) {
+        R.frac = frac_of(fold ? found.mass : mass_of_all(R));
         if (fold) {
             u64 at;
             const u64 Z = R.weigh<true>(scale, 0, 0, at);
@@ -894,6 +1016,7 @@ sample_rows_kernel(const __grid_constant__ Args a) {
     if (tid == kThreads - 1) {   // for report(), below
         sh.scale = scale;
         sh.fold = fold;
+        sh.frac = R.frac;
         sh.kept = T > 0.f ? kept : 0;
         sh.pick_key = pick_key;
     }
@@ -1025,8 +1148,6 @@ extern "C" int tf_sample_rows(const void* logits, int R, int V, int64_t row_stri
     if (reinterpret_cast<uintptr_t>(logits) & 1) return TF_EINVAL;
     if (V > TF_SAMPLE_MAX_VOCAB || R > (1 << 24)) return TF_ERANGE;
     if (!on_this_device(logits)) return TF_EINVAL;
-    int bits = 0;
-    while ((int64_t(1) << bits) < V) ++bits;
     int rc = prepare();
     if (rc != TF_OK) return rc;
     // CTAs a row: up to 8 while they have an SM each and 16,384 tokens each (128,000 tokens: 16 rows 16.0 us with
@@ -1034,7 +1155,7 @@ extern "C" int tf_sample_rows(const void* logits, int R, int V, int64_t row_stri
     int cl = kMaxCluster;
     while (cl > 1 && (int64_t(R) * cl > sm_count() || V < cl * 16384)) cl /= 2;
     Args a = {static_cast<const uint16_t*>(logits), row_stride, temperature, top_k, top_p, min_p, u,
-              pick, prob, flag, V, 63 - bits, ((V + cl - 1) / cl + 7) / 8 * 8};
+              pick, prob, flag, V, ((V + cl - 1) / cl + 7) / 8 * 8};
 
     // rows go in grid.y, at most 65,535 a launch
     constexpr int kRowsPerLaunch = 65535;
