@@ -152,24 +152,27 @@ __device__ __forceinline__ int key_at(int pos, int top) {
 __device__ __forceinline__ int word_of(int pos) { return pos < kSide ? kSide - 1 - pos : 8192 - kSide + pos; }
 
 // What a row's settings give: log2(e) / T, as a double and as a 64-bit fraction
-// with a shift, -log2(min_p) in units of 2^-52, and top_p and u in units of 2^-64
-// (cut there). Doubles run at a 64th of the fp32 rate and so do conversions to and
-// from 64 bits, so one warp works these out while the others count.
+// with its product's shifts, -log2(min_p) in units of 2^-52, and top_p and u in
+// units of 2^-64 (cut there). Doubles run at a 64th of the fp32 rate and so do
+// conversions to and from 64 bits, so one warp works these out while the others count.
 struct Setting {
     double per;
     u64 mant, y_min, p, u;
-    int shift;
+    int shift;   // left, before the product (the low 8 bits), and right, after it
     float per_f;
 };
 __device__ __forceinline__ Setting setting_of(float T, float top_p, float min_p, float u) {
-    Setting s = {0.0, 0, kYLimit, __float2ull_rz(fmaxf(top_p, 0.f) * 0x1p64f), __float2ull_rz(u * 0x1p64f), 0, 0.f};
+    Setting s = {0.0, 0, kYLimit, __float2ull_rz(fmaxf(top_p, 0.f) * 0x1p64f), __float2ull_rz(u * 0x1p64f), 15, 0.f};
     if (T > 0.f) {
         s.per = 1.4426950408889634074 / double(T);
         s.per_f = fminf(float(s.per), FLT_MAX);
         // y 2^52 = d 2^12 per = d mant 2^(e - 64), d the difference in units of 2^-40
         int e;
         s.mant = u64(frexp(s.per * 4096.0, &e) * 0x1p64);
-        s.shift = e - 15;
+        // d goes up by e + 5, so that the product's upper half holds all of y's 58 bits and 5 more
+        // (15 for T above 5.8: any difference, 2^49 at most, fits)
+        const int up = max(15, min(e + 5, 63));
+        s.shift = up | max(0, up - e) << 8;
     }
     if (min_p > 0.f) {
         const double y = -log2(double(min_p));
@@ -187,10 +190,11 @@ struct Scale {
     __device__ __forceinline__ Scale any(const Setting& s) const {
         return {value_of(top_key), s.per, xmax, mant, shift, top_key};
     }
-    __device__ __forceinline__ u64 y_of(u64 d) const {   // of a difference
-        const u64 p = __umul64hi(d << 15, mant);
-        if (shift <= 0) return shift < -63 ? 0 : p >> -shift;
-        return shift > 57 ? (p ? kYLimit : 0) : p >= (kYLimit >> shift) ? kYLimit : p << shift;
+    __device__ __forceinline__ u64 y_of(u64 d) const {   // of a difference, cut to whole units
+        const int up = shift & 255, right = shift >> 8;
+        if (d >> (64 - up)) return kYLimit;
+        const u64 p = __umul64hi(d << up, mant);
+        return right > 63 ? 0 : p >> right;
     }
     template <bool kFold>
     __device__ __forceinline__ u64 y(int key) const {

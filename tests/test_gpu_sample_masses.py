@@ -95,3 +95,9 @@ def test_a_whole_row_of_one_value(mods, V):
     tf.tf_sample_rows(x, rows, V, V, None, None, None, None, torch.from_numpy(u).cuda(), pick, prob, flag)
     torch.cuda.synchronize()
     assert np.array_equal(pick.cpu().numpy(), j) and (prob.cpu().numpy() == np.float32(1 / V)).all()
+
+
+@pytest.mark.parametrize("T,peak,tail", [(1e-6, 1.2e-5, 0.0), (1e-8, 1.5e-7, 2.0 ** -25), (1e-9, -2.0 ** -26, -2.7e-8)])
+def test_flat_tail_at_small_temperatures(mods, T, peak, tail):
+    """Differences of a few T, with T far below the values' usual distances."""
+    ask(mods, 1 << 19, T, peak, tail)
