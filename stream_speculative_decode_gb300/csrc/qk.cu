@@ -207,10 +207,10 @@ qk_rows_many_kernel(SegTable t, int layer, Rows in, const uint16_t* __restrict__
     pdl_trigger();
 }
 
-// Whether `rows` rows of `width` bf16 at a stride and the dense output overlap.
-bool overlaps(const void* p, int64_t stride, int64_t rows, int64_t width, const void* out) {
+// Whether `rows` rows of `width` bf16 at a stride and the dense output's rows overlap.
+bool overlaps(const void* p, int64_t stride, int64_t rows, int64_t width, const void* out, int64_t out_rows) {
     const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(out);
-    return a < b + uintptr_t(rows) * TF_NQ * TF_D * 2 && b < a + uintptr_t((rows - 1) * stride + width) * 2;
+    return a < b + uintptr_t(out_rows) * TF_NQ * TF_D * 2 && b < a + uintptr_t((rows - 1) * stride + width) * 2;
 }
 
 }  // namespace
@@ -232,9 +232,11 @@ extern "C" int tf_qk_rows(const tf_segments* seg, int attn_layer, const void* q,
     if (q_stride < kQ || k_stride < kKV || v_stride < kKV || (q_stride | k_stride | v_stride) % 8) return TF_EINVAL;
     if (q_stride > kMaxStride || k_stride > kMaxStride || v_stride > kMaxStride) return TF_ERANGE;
     const bool in_place = q == q_out && q_stride == kQ;   // each head is read and written by its own lanes
-    if ((!in_place && overlaps(q, q_stride, t.R, kQ, q_out)) || overlaps(k, k_stride, t.R, kKV, q_out) ||
-        overlaps(v, v_stride, t.R, kKV, q_out))
+    if ((!in_place && overlaps(q, q_stride, t.R, kQ, q_out, t.R)) || overlaps(k, k_stride, t.R, kKV, q_out, t.R) ||
+        overlaps(v, v_stride, t.R, kKV, q_out, t.R))
         return TF_EINVAL;
+    for (const void* w : {q_norm, k_norm})   // TF_D weights: rows would be normed with what others wrote
+        if (overlaps(w, 0, 1, TF_D, q_out, t.R)) return TF_EINVAL;
     Turns turns;
     for (int j = 0; j < TF_D / 2; ++j)
         turns.f[j] = uint64_t(std::ldexp(std::pow(theta, -2.0 * j / TF_D) * 0.15915494309189533577, 64));   // 1 / (2 pi)

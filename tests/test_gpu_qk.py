@@ -303,3 +303,20 @@ def test_refusals(mods):
     assert tf.lib().tf_qk_rows(None, 0, c.qb.data_ptr(), 2048, c.kb.data_ptr(), 512, c.vb.data_ptr(), 512,
                                c.qw.data_ptr(), c.kw.data_ptr(), EPS, THETA, c.out.data_ptr(), None) == tf.TF_EINVAL
     c.seg.free()
+
+
+def test_output_over_the_norm_weights_is_refused(mods):
+    """q_out must not hold an input: rows would be normed with what others wrote."""
+    tf, torch = mods
+    c = Case(mods, [(2, 20)], 16, seed=11)
+    buf = torch.ones(2 * 2048 + 64, dtype=torch.bfloat16, device="cuda")      # q_out's rows and 64 more
+    for name, at in (("q_norm", 0), ("k_norm", 0), ("q_norm", 1000), ("k_norm", 4096 - 8)):
+        qw, kw = (buf[at:at + 64] if name == n else w for n, w in (("q_norm", c.qw), ("k_norm", c.kw)))
+        with pytest.raises(tf.TFError) as e:
+            tf.tf_qk_rows(c.seg, 0, c.qb, 2048, c.kb, 512, c.vb, 512, qw, kw, EPS, THETA, buf)
+        assert e.value.status == tf.TF_EINVAL, (name, at)
+    c.kw, c.qw = buf[4096:], c.kw                                            # right behind it: allowed
+    before = c.copies()
+    c.run(mods, out=buf)
+    c.check(mods, before, out=buf[:4096])
+    c.seg.free()
