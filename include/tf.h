@@ -309,8 +309,9 @@ int tf_argmax_rows(const void* logits, int R, int V, int64_t row_stride,
  *   flag        uint8 [R]: TF_SAMPLE_NO_LOGITS a NaN or +Inf in the row, or
  *               every token masked; TF_SAMPLE_BAD_SETTING a setting outside
  *               its range or NaN
- * Needs no table. R == 0 is a no-op. Errors: TF_EINVAL (null, an odd address,
- * V < 1, row_stride < V), TF_ERANGE (V > TF_SAMPLE_MAX_VOCAB, R > 2^24). */
+ * Needs no table. R == 0 is a no-op. Errors: TF_EINVAL (null, an odd address
+ * of the logits, one that is no multiple of 4 of a 4-byte array, V < 1,
+ * row_stride < V), TF_ERANGE (V > TF_SAMPLE_MAX_VOCAB, R > 2^24). */
 #define TF_SAMPLE_MAX_VOCAB (1 << 19)
 #define TF_SAMPLE_NO_LOGITS   1
 #define TF_SAMPLE_BAD_SETTING 2

@@ -1150,6 +1150,10 @@ extern "C" int tf_sample_rows(const void* logits, int R, int V, int64_t row_stri
     if (R == 0) return TF_OK;
     if (!logits || !u || !pick || !flag || V < 1 || row_stride < V) return TF_EINVAL;
     if (reinterpret_cast<uintptr_t>(logits) & 1) return TF_EINVAL;
+    for (const void* x : {static_cast<const void*>(temperature), static_cast<const void*>(top_k),
+                          static_cast<const void*>(top_p), static_cast<const void*>(min_p), static_cast<const void*>(u),
+                          static_cast<const void*>(pick), static_cast<const void*>(prob)})
+        if (reinterpret_cast<uintptr_t>(x) & 3) return TF_EINVAL;
     if (V > TF_SAMPLE_MAX_VOCAB || R > (1 << 24)) return TF_ERANGE;
     if (!on_this_device(logits)) return TF_EINVAL;
     int rc = prepare();

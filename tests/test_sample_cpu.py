@@ -86,3 +86,18 @@ def test_refusals(T):
     assert status(a2=(1 << 19) + 1, a3=1 << 20) == T.TF_ERANGE
     assert status(a1=(1 << 24) + 1) == T.TF_ERANGE
     assert status(a1=0, a0=None) == T.TF_OK       # no rows: nothing to do
+
+
+def test_misaligned_arrays_are_refused(T):
+    """The 4-byte arrays: an address that is no multiple of 4 would fault on the device.
+    (With a vocabulary beyond the limit too, so that no answer to this call is a launch.)"""
+    P = 0x7F0000000000
+    f = T.lib().tf_sample_rows
+    call = [P, 4, (1 << 19) + 1, 1 << 20, P, P, P, P, P, P, P, P, None]
+    assert f(*call) == T.TF_ERANGE
+    for i in (4, 5, 6, 7, 8, 9, 10):              # temperature, top_k, top_p, min_p, u, pick, prob
+        for off in (1, 2, 3):
+            a = list(call)
+            a[i] = P + off
+            assert f(*a) == T.TF_EINVAL, (i, off)
+    assert f(*call[:11], P + 1, None) == T.TF_ERANGE          # flag holds bytes
