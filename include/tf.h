@@ -469,8 +469,9 @@ int tf_paged_prompt_build(int32_t rows, int32_t keys, int32_t kv_capacity,
  *        (what the output projection reads; the probabilities are fp16, which
  *        leaves the fp32 result about 2e-4 of its size, a tenth of that
  *        rounding)
- * Errors: TF_EINVAL (a table that is not paged, attn_layer out of range, null
- * or misaligned pointers). */
+ * q, partials and out lie apart (queries may be read again after outputs are
+ * written). Errors: TF_EINVAL (a table that is not paged, attn_layer out of
+ * range, null, misaligned or overlapping buffers). */
 int tf_attn_paged(const tf_segments* seg, int attn_layer, const void* q, void* partials,
                   void* out, int full, tf_cuda_stream stream);
 

@@ -297,6 +297,13 @@ template int launch_attn_partials<false>(const SegTable&, int, const uint16_t*, 
                                          int);
 template int launch_attn_merge<false>(const SegTable&, const float*, const float2*, float*, cudaStream_t, bool);
 
+namespace {
+bool overlap(const void* p, size_t np, const void* q, size_t nq) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return a < b + nq && b < a + np;
+}
+}  // namespace
+
 }  // namespace tf
 
 extern "C" int tf_attn_partials(const tf_segments* seg, int attn_layer, const void* q, void* partials,
@@ -364,6 +371,10 @@ extern "C" int tf_attn_paged(const tf_segments* seg, int attn_layer, const void*
     if (t.R == 0) return TF_OK;
     if (!on_this_device(seg)) return TF_EINVAL;
     if (!q || !partials || !out || !aligned16(q) || !aligned16(partials) || !aligned16(out)) return TF_EINVAL;
+    // queries are read again after outputs are written (the exact recompute), records throughout
+    const size_t rows = size_t(t.R) * TF_NQ * TF_D * 2, records = size_t(seg->plan.partials_bytes);
+    if (overlap(q, rows, out, rows) || overlap(q, rows, partials, records) || overlap(out, rows, partials, records))
+        return TF_EINVAL;
     float* po = static_cast<float*>(partials);
     float2* pml = reinterpret_cast<float2*>(po + t.n_partials * TF_D);
     uint16_t* o = static_cast<uint16_t*>(out);

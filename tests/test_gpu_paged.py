@@ -304,3 +304,27 @@ def test_two_rounds_at_once(mods):
     check_exact(inputs.to_numpy_bits(out), dense_bits(mods, inp)[0], "two at once, dense")
     seg.free()
     a.seg.free()
+
+
+def test_refuses_an_output_over_its_inputs(mods):
+    """bf16 in and out have one size, but queries are read again after outputs are
+    written (the exact recompute), and so are the records: all three lie apart."""
+    tf, inputs, _, torch = mods
+    from paged import PagedAttn
+    inp = inputs.make_inputs(work(inputs, [16, 2], [9000, 40]), backend="numpy")
+    p = PagedAttn(tf, inp, 16)
+    n, scratch = p.q[0].numel() * 2, p.seg.partials_bytes
+    buf = torch.zeros(2 * n + 32 + max(scratch, n), dtype=torch.uint8, device="cuda")
+    at = buf.data_ptr()
+    for q, partials, out in ((at, p.partials, at), (at, p.partials, at + 16), (at + n - 16, p.partials, at),
+                             (p.q[0], at, at), (p.q[0], at, at + scratch - 16), (p.q[0], at + n - 16, at),
+                             (at, at, p.out[0]), (at + scratch - 16, at, p.out[0]), (at, at + n - 16, p.out[0])):
+        with pytest.raises(tf.TFError) as e:
+            tf.tf_attn_paged(p.seg, 0, q, partials, out)
+        assert e.value.status == tf.TF_EINVAL
+    buf[:n].copy_(p.q[0].view(-1).view(torch.uint8))
+    tf.tf_attn_paged(p.seg, 0, at, p.partials, at + n)          # side by side: allowed
+    want = p.run()[0]
+    torch.cuda.synchronize()
+    assert torch.equal(buf[n:2 * n], want.view(-1).view(torch.uint8))
+    p.seg.free()
