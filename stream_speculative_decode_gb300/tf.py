@@ -248,23 +248,27 @@ def tf_prompt_build(rows, keys, kv_capacity, conv_state, k_cache, v_cache, n_con
     return Segments(handle)
 
 
-def _int32_array(x, n=None):
+def _int32_array(x, n=None, table=False):
     """Address of a host int32 array and what keeps it alive: a contiguous numpy
     int32 array or CPU torch tensor is used as it is, any other sequence is
-    copied. ``n``: the entries the call will read."""
+    copied. ``n``: the entries the call will read. ``table``: an array of two
+    dimensions goes row after row (otherwise it is refused)."""
     if x is None:
         return None, None
+    dims = getattr(x, "ndim", None)
+    if hasattr(x, "numpy"):
+        if x.device.type != "cpu":
+            raise ValueError("a host array is needed, not a device tensor")
+        x = x.numpy()
+    if dims is not None and dims != 1:
+        if not table or dims != 2:
+            raise ValueError(f"an array of {dims} dimensions where the call reads a list")
+        x = x.reshape(-1)
     try:   # a numpy array that is one already
-        fits = x.dtype.char == "i" and x.flags.c_contiguous
+        fits = x.dtype.char == "i" and x.flags.c_contiguous and x.dtype.isnative
     except AttributeError:
         fits = False
     if not fits:
-        if hasattr(x, "numpy"):
-            if x.device.type != "cpu":
-                raise ValueError("a host array is needed, not a device tensor")
-            x = x.numpy()
-            if x.dtype.char == "i" and x.flags.c_contiguous:
-                return _int32_array(x, n)
         x = array.array("i", (int(v) for v in x))
     if n is not None and len(x) < n:
         raise ValueError(f"{len(x)} entries where the call reads {n}")
@@ -277,10 +281,10 @@ def _int32_array(x, n=None):
 def tf_paged_build_status(streams, conv_state, conv_hist, pages, page_keys, n_pages, k_pool, v_pool, n_conv, n_attn,
                           stream=None):
     """Raw status and handle of tf_paged_build; ``pages``: the streams' page ids
-    one after another, ``k_pool``/``v_pool``: a pool a layer."""
+    one after another (lists of one length may be a [streams][pages] array), ``k_pool``/``v_pool``: a pool a layer."""
     out = ctypes.c_void_p()
     n = sum(st[3] // page_keys for st in streams) if page_keys > 0 else 0
-    at, _keep = _int32_array(pages, n)
+    at, _keep = _int32_array(pages, n, table=True)
     rc = _lib.tf_paged_build(_streams_array(streams), len(streams), _ptr_array(conv_state), _ptr_array(conv_hist),
                              at, page_keys, n_pages, _ptr_array(k_pool), _ptr_array(v_pool),
                              n_conv, n_attn, _stream(stream), ctypes.byref(out))
@@ -301,7 +305,7 @@ def tf_paged_prompt_build_status(rows, keys, kv_capacity, conv_state, pages, pag
     """Raw status and handle of tf_paged_prompt_build."""
     out = ctypes.c_void_p()
     n = kv_capacity // page_keys if page_keys > 0 else 0
-    at, _keep = _int32_array(pages, n)
+    at, _keep = _int32_array(pages, n, table=True)
     rc = _lib.tf_paged_prompt_build(rows, keys, kv_capacity, _ptr_array(conv_state), at, page_keys,
                                     n_pages, _ptr_array(k_pool), _ptr_array(v_pool), n_conv, n_attn, _stream(stream),
                                     ctypes.byref(out))

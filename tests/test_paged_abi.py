@@ -134,3 +134,37 @@ def test_host_arrays(T):
         T._int32_array(a, 7)
     with pytest.raises(OverflowError):
         T._int32_array([1 << 31], 1)
+
+
+def test_block_tables_and_foreign_byte_orders(T):
+    """Page lists as a [streams][pages] array are read row after row, other lists have one
+    dimension; other byte orders are converted."""
+    import ctypes
+
+    import torch
+
+    def read(x, n, **kw):
+        at, keep = T._int32_array(x, n, **kw)
+        return list((ctypes.c_int32 * n).from_address(at))
+
+    a = np.arange(6, dtype=np.int32)
+    wide = np.arange(12, dtype=np.int32).reshape(2, 6)
+    for x in (a.reshape(2, 3), a.reshape(3, 2).astype(np.int64), torch.arange(6).view(2, 3),
+              torch.arange(6, dtype=torch.int32).view(3, 2), a.reshape(2, 3).astype(">i4"), a):
+        assert read(x, 6, table=True) == list(range(6))
+    assert read(wide[:, ::2], 6, table=True) == [0, 2, 4, 6, 8, 10]
+    assert read(wide[:, 1:3], 4, table=True) == [1, 2, 7, 8]
+    assert read(a.astype(">i4"), 6) == list(range(6))
+    assert read([torch.tensor(5), np.int64(6)], 2) == [5, 6]
+    assert T._int32_array(a.reshape(2, 3), 6, table=True)[0] == a.ctypes.data          # in place
+    for x, kw in ((a.reshape(2, 3), dict()), (torch.zeros(2, 2, dtype=torch.int32), dict()),
+                  (np.int32(3).reshape(()), dict(table=True)), (a.reshape(1, 2, 3), dict(table=True)),
+                  (a.reshape(2, 3), dict(n=7, table=True))):
+        with pytest.raises(ValueError):
+            T._int32_array(x, **kw)
+    # two streams' lists as a table: taken, and a bad id in the second row is seen
+    for bad, streams in ((64, [(1, 0, 1, 32), (1, 1, 17, 32)]), (-1, [(1, 0, 1, 32), (1, 1, 1, 32)])):
+        assert build(T, streams, np.array([[0, 1], [2, bad]], np.int32)) == T.TF_EINVAL
+        assert build(T, streams, torch.tensor([[0, 1], [2, bad]])) == T.TF_EINVAL
+    with pytest.raises(ValueError):
+        T.tf_pages_copy([P0], 16, 8, np.array([[0, 1], [2, 3]], np.int32), [4, 5], stream=0)
