@@ -310,3 +310,19 @@ def test_captured_and_replayed(mods):
         torch.cuda.synchronize()
         rp, _, _ = OS.sample_rows(host_bits(x, V), u.cpu().numpy(), temperature=t.cpu().numpy())
         assert np.array_equal(pick.cpu().numpy(), rp)
+
+
+def test_settings_of_more_rows_than_a_launch(mods):
+    """70,000 rows go in two launches: each row has its own settings and results in both."""
+    tf, torch = mods
+    R, V = 70000, 40
+    x = normal(torch, R, V, 3.0, 43)
+    kw, u = settings(R, 44)
+    f32 = lambda a: np.asarray(a, np.float32)
+    kw = {n: v if n == "top_k" else f32(v) for n, v in kw.items()}
+    pick, prob, flag = run(mods, x, V, u, **kw)
+    rows = np.r_[0:200, 65535 - 300:65535 + 300, R - 200:R]
+    rp, rq, rf = OS.sample_rows(host_bits(x, V)[rows], f32(u)[rows], **{n: v[rows] for n, v in kw.items()})
+    assert np.array_equal(flag[rows], rf) and np.array_equal(pick[rows], rp)
+    assert np.all(np.abs(prob[rows] - rq) <= 2.0 ** -23 * rq + 2.0 ** -149)
+    assert not flag.any() and ((pick >= 0) & (pick < V)).all() and ((prob > 0) & (prob <= 1)).all()
