@@ -426,13 +426,17 @@ int tf_prompt_build(int32_t rows, int32_t keys, int32_t kv_capacity,
  * tf_paged_build is tf_segments_build for pages:
  *   streams     as there; kv_capacity is a multiple of page_keys
  *   pages       host array of page ids, stream after stream, kv_capacity /
- *               page_keys entries each, every entry in [0, n_pages) (the
- *               entries past a stream's keys are checked and not used)
+ *               page_keys entries each, every entry in [0, n_pages). Entries
+ *               past a stream's keys are not read by the calls, but they are the
+ *               list's all the same: checked, and uses of their page (below), so
+ *               a filler there has to be a page that holds no window rows, one
+ *               kept for that purpose or the next pages that the stream grows into
  *   page_keys   a power of two, TF_MIN_PAGE_KEYS..TF_MAX_PAGE_KEYS
  *   k_pool, v_pool  host arrays [n_attn] of device pointers
  * A page may stand in several lists, or several times in one, for reading; a
  * page that holds rows of a stream's window (they are appended there) must
- * stand in the lists exactly once: copy a shared last page first
+ * stand in the lists exactly once, spare entries included: copy a shared last
+ * page first
  * (tf_pages_copy). Refuses what tf_segments_build refuses, pools that overlap,
  * a bad page size, an id out of range and a shared page with window rows
  * (TF_EINVAL); n_pages > TF_MAX_PAGES or more than TF_MAX_PAGE_IDS entries
