@@ -293,9 +293,10 @@ int tf_argmax_rows(const void* logits, int R, int V, int64_t row_stride,
  *     prefix of the three;
  *   - the pick is the first token at which the cumulative mass exceeds u times
  *     the mass of the kept tokens.
- * T == 0 picks the first token (the greedy pick). Masses are exact to 64-bit
- * fixed point, so a pick equals the float64 definition's except where u lies
- * within about 1e-12 of a border.
+ * T == 0 picks the first token (the greedy pick). Counts are exact and weights
+ * 64-bit fixed point, scaled to the row's mass, so a pick equals the
+ * definition's in exact arithmetic except where u lies within 1e-12 of a border
+ * (and top_p or min_p likewise).
  *   logits      as in tf_argmax_rows (any 2-byte address and stride); -Inf is a
  *               masked token (never picked)
  *   temperature float [R] or NULL (1); 0 <= T < inf

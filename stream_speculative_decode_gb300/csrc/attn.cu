@@ -33,8 +33,9 @@
 // Paged tables (tf_attn_paged) run the same kernels with kPaged set: where each
 // 16 keys of the chunk lie is worked out into shared memory before the
 // dependency wait (the table is immutable), every 16-byte copy finds its
-// address there, and the output is bf16. A page holds at least 16 keys, so each 2 KB of a head's K or V is
-// still contiguous and the copies stay whole 128-byte lines.
+// address there, and the output is bf16. A page holds at least 16 keys, so each
+// 2 KB of a head's K or V is still contiguous and the copies stay whole 128-byte
+// lines.
 #include "attn_item.cuh"
 
 namespace tf {
@@ -288,8 +289,8 @@ int launch_attn_partials(const SegTable& t, int layer, const uint16_t* q, float*
 template <bool kPaged>
 int launch_attn_merge(const SegTable& t, const float* po, const float2* pml, OutT<kPaged>* out, cudaStream_t stream,
                       bool kernel_mode_only) {
-    return launch_pdl(attn_merge_kernel<OutT<kPaged>>, dim3(t.R * kMergeCtasPerRow), dim3(kMergeThreads), 0, stream, t, po, pml,
-                      out, kernel_mode_only ? 1 : 0);
+    return launch_pdl(attn_merge_kernel<OutT<kPaged>>, dim3(t.R * kMergeCtasPerRow), dim3(kMergeThreads), 0, stream, t,
+                      po, pml, out, kernel_mode_only ? 1 : 0);
 }
 
 // attn_static.cu's

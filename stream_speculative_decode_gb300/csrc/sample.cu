@@ -32,11 +32,12 @@
 // (distributed shared memory), weighs it, and every CTA learns the slices'
 // totals: all of them follow the same steps with the same numbers.
 //
-// Measured on a GB300 (1,024 rows of 128,000 N(0, 3) logits): 99 us, 2.6 TB/s,
-// 39 % of the copy rate; masked rows 94 to 101. A CTA's row takes 52,000 cycles,
-// two CTAs an SM, of which the count is 24,000 (HBM and shared-memory atomics),
-// the weights 9,000, the search 9,000. 16 rows, 4 CTAs each: 15 us, a chain of
-// latencies.
+// Measured on a GB300 (1,024 rows of 128,000 N(0, 3) logits): 102 us, 2.6 TB/s,
+// 38 % of the copy rate; with half of the tokens masked 100. A CTA's row takes
+// 53,000 cycles, two CTAs an SM, of which the count is 24,000 (HBM and
+// shared-memory atomics), the weights 9,000, the search 9,000, the rough mass some
+// 1,200. 16 rows, 4 CTAs each: 15.2 us, 18.1 with top-k, top-p and min-p, a chain
+// of latencies.
 #include <cfloat>
 #include <cmath>
 
@@ -1158,8 +1159,9 @@ extern "C" int tf_sample_rows(const void* logits, int R, int V, int64_t row_stri
     if (!on_this_device(logits)) return TF_EINVAL;
     int rc = prepare();
     if (rc != TF_OK) return rc;
-    // CTAs a row: up to 8 while they have an SM each and 16,384 tokens each (128,000 tokens: 16 rows 16.0 us with
-    // 4 CTAs a row, 22.3 with one; 64 rows 19.3 with 2, 22.2 with 4; 100 rows 24.8 with one, 26.9 with 2)
+    // CTAs a row: up to 8 while they have an SM each and 16,384 tokens each. 128,000 tokens, temperature alone, us
+    // with 1, 2, 4 and 8: one row 18.1, 16.3, 13.8, 13.1; 16 rows 20.7, 17.9, 15.3, 17.4; 38 rows 21.5, 18.3, 19.7,
+    // 30.5; 64 rows 21.6, 18.5, 20.9, 35.5; 100 rows 26.6, 25.5, 36.8, 52.6
     int cl = kMaxCluster;
     while (cl > 1 && (int64_t(R) * cl > sm_count() || V < cl * 16384)) cl /= 2;
     Args a = {static_cast<const uint16_t*>(logits), row_stride, temperature, top_k, top_p, min_p, u,
