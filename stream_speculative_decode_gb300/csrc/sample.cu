@@ -791,14 +791,15 @@ __device__ __forceinline__ int frac_of(float m) {
 // The mass of all of a row's tokens, any values; for all threads of the cluster.
 __device__ __noinline__ float mass_of_all(const Row R) {
     Shared& sh = R.sh;
-    const float per = sh.set.per_f;
-    if (!(per < 1e38f)) return float(R.a.V);   // log2(e) / T may not be a float: the most there can be
-    const float half = 0.5f * float_of(R.top_key);   // halves: the difference may not be a float either
+    // log2(e) / T may not be a float, nor the difference of two values: parts and halves of them
+    const bool tiny = sh.set.per > 0x1p64;
+    const float per = float(tiny ? sh.set.per * 0x1p-64 : sh.set.per), up = tiny ? 0x1p64f : 1.f;
+    const float half = 0.5f * float_of(R.top_key);
     float m = 0.f;
     auto one = [&](uint32_t b) {
         if (b == 0xFF80u) return;
         const float d = half - 0.5f * float_of(key_of(b));
-        m += d > 0.f ? exp2_of(-2.f * (d * per)) : 1.f;
+        m += d > 0.f ? exp2_of(-2.f * (d * up * per)) : 1.f;
     };
     for_tokens(R.p, R.begin, R.end, R.head, [&](uint4 v) {
 #pragma unroll 1

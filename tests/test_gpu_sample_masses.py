@@ -70,10 +70,13 @@ def test_flat_tail(mods, V, T, peak, tail, rows):
     ask(mods, V, T, peak, tail, rows=rows, at=V // 3)
 
 
-@pytest.mark.parametrize("V,T,peak,tail", [(128000, 1.0, 130.0, 118.0), (1 << 19, 50.0, -300.0, -900.0)])
-def test_flat_tail_of_large_values(mods, V, T, peak, tail):
-    """Values of 128 and more are counted in other windows."""
-    ask(mods, V, T, peak, tail)
+@pytest.mark.parametrize("rows", [3, ROWS])
+@pytest.mark.parametrize("V,T,peak,tail", [
+    (128000, 1.0, 130.0, 118.0), (1 << 19, 50.0, -300.0, -900.0), (300001, 3e37, 3e38, -6e37),
+    (1 << 19, 7.65e-42, 2.0 ** -132, 2.0 ** -133), (1 << 19, 4e-21, 2.0 ** -64, 2.0 ** -70)])
+def test_flat_tail_of_other_values(mods, V, T, peak, tail, rows):
+    """Values of 128 and more, and below 2^-33, are counted in other windows."""
+    ask(mods, V, T, peak, tail, rows=rows)
 
 
 @pytest.mark.parametrize("V,keep", [(1 << 19, 200001), (128000, 90000)])
