@@ -3,11 +3,11 @@ plain forms.
 
 Five operators that follow one another in a round whose caches hold 8 bits and
 whose weights hold 4: the residual's addition and norm with its 8-bit rows
-(``tf_norm_rows8``), the products of those rows with 4-bit weights
-(``tf_matvec4``), the queries' and keys' norm and rotation with the append to an
-8-bit paged cache (``tf_qk_rows`` on a table of ``tf_paged8_build``), the
+(``tf_norm_rows``), the products of those rows with 4-bit weights
+(``tf_linear_rows``), the queries' and keys' norm and rotation with the append to an
+8-bit paged cache (``tf_qk_rows`` on a table of ``tf_paged_scaled_build``), the
 attention over it (``tf_attn_paged``), and the copies of its pages behind a fork
-or a compaction (``tf_pages_copy8``). With ``own`` false ``run`` computes them
+or a compaction (``tf_pages_copy_scaled``). With ``own`` false ``run`` computes them
 with elementary torch operations in 32 bits (angles in 64); with ``own`` true it
 makes the library's calls.
 
@@ -206,10 +206,11 @@ def prepare(case, seed):
             table = [(r, o, k, -(-k // P) * P) for r, o, k in streams]
             if case.get("prompt"):
                 r, _, k, cap = table[0]
-                st["seg"] = tf.tf_paged8_prompt_build(r, k, cap, None, lists[0], P, n_pages, [K], [V], [ks], [vs], 0, 1)
+                st["seg"] = tf.tf_paged_scaled_prompt_build(r, k, cap, None, lists[0], P, n_pages, [K], [V], [ks], [vs],
+                                                            0, 1)
             else:
-                st["seg"] = tf.tf_paged8_build(table, None, None, np.concatenate(lists), P, n_pages, [K], [V], [ks],
-                                               [vs], 0, 1)
+                st["seg"] = tf.tf_paged_scaled_build(table, None, None, np.concatenate(lists), P, n_pages, [K], [V],
+                                                     [ks], [vs], 0, 1)
             st["out"] = torch.empty((R, NQ, D), dtype=BF16, device="cuda")
             if op == "attn":
                 st["partials"] = torch.empty(max(16, st["seg"].partials_bytes), dtype=torch.uint8, device="cuda")
@@ -271,14 +272,14 @@ def _run_own(st, case):
         tf.tf_attn_paged(st["seg"], 0, st["q"], st["partials"], st["out"])
         return dict(out=st["out"])
     if op == "copy":
-        tf.tf_pages_copy8(st["pools"], st["scales"], case["page"], case["n_pages"], st["src"], st["dst"], st["keys"])
+        tf.tf_pages_copy_scaled(st["pools"], st["scales"], case["page"], case["n_pages"], st["src"], st["dst"], st["keys"])
         return dict(pools=[p.view(E4M3) for p in st["pools"]], scales=[s.view(E8M0) for s in st["scales"]])
     if op == "norm":
         W = case["width"]
-        tf.tf_norm_rows8(st["x"], W, st["res"], W, st["w"], EPS, case["rows"], W, st["sum"], W, st["codes"],
+        tf.tf_norm_rows(st["x"], W, st["res"], W, st["w"], EPS, case["rows"], W, st["sum"], W, st["codes"],
                          st["scales"])
         return dict(sum=st["sum"], codes=st["codes"].view(E4M3), scales=st["scales"].view(E8M0))
-    tf.tf_matvec4(st["x"], case["k"], st["xs"], case["rows"], case["k"], st["w"], st["g"], st["s"], case["n"], st["y"],
+    tf.tf_linear_rows(st["x"], case["k"], st["xs"], case["rows"], case["k"], st["w"], st["g"], st["s"], case["n"], st["y"],
                   case["n"])
     return dict(y=st["y"])
 
