@@ -245,6 +245,8 @@ def prepare(case, seed):
                   s=(0.5 + torch.rand(N, generator=g, device="cuda")) / math.sqrt(21.5 * K))
         if own:
             st["y"] = torch.empty((R, N), dtype=BF16, device="cuda")
+    if own:
+        st["outputs"] = _outputs(st, case)
     return st
 
 
@@ -261,27 +263,39 @@ def _cache(st):
     return dict(K=st["K"].view(E4M3), V=st["V"].view(E4M3), ks=st["ks"].view(E8M0), vs=st["vs"].view(E8M0))
 
 
+def _outputs(st, case):
+    """What ``_run_own`` returns: the buffers that its call writes, as the values they stand for."""
+    op = case["op"]
+    if op == "qk":
+        return dict(q=st["out"], **_cache(st))
+    if op == "attn":
+        return dict(out=st["out"])
+    if op == "copy":
+        return dict(pools=[p.view(E4M3) for p in st["pools"]], scales=[s.view(E8M0) for s in st["scales"]])
+    if op == "norm":
+        return dict(sum=st["sum"], codes=st["codes"].view(E4M3), scales=st["scales"].view(E8M0))
+    return dict(y=st["y"])
+
+
 def _run_own(st, case):
     from stream_speculative_decode_gb300 import tf
     op = case["op"]
     if op == "qk":
         tf.tf_qk_rows(st["seg"], 0, st["q"], NQ * D, st["k"], NKV * D, st["v"], NKV * D, st["qw"], st["kw"], EPS, THETA,
                       st["out"])
-        return dict(q=st["out"], **_cache(st))
-    if op == "attn":
+    elif op == "attn":
         tf.tf_attn_paged(st["seg"], 0, st["q"], st["partials"], st["out"])
-        return dict(out=st["out"])
-    if op == "copy":
-        tf.tf_pages_copy_scaled(st["pools"], st["scales"], case["page"], case["n_pages"], st["src"], st["dst"], st["keys"])
-        return dict(pools=[p.view(E4M3) for p in st["pools"]], scales=[s.view(E8M0) for s in st["scales"]])
-    if op == "norm":
+    elif op == "copy":
+        tf.tf_pages_copy_scaled(st["pools"], st["scales"], case["page"], case["n_pages"], st["src"], st["dst"],
+                                st["keys"])
+    elif op == "norm":
         W = case["width"]
         tf.tf_norm_rows(st["x"], W, st["res"], W, st["w"], EPS, case["rows"], W, st["sum"], W, st["codes"],
-                         st["scales"])
-        return dict(sum=st["sum"], codes=st["codes"].view(E4M3), scales=st["scales"].view(E8M0))
-    tf.tf_linear_rows(st["x"], case["k"], st["xs"], case["rows"], case["k"], st["w"], st["g"], st["s"], case["n"], st["y"],
-                  case["n"])
-    return dict(y=st["y"])
+                        st["scales"])
+    else:
+        tf.tf_linear_rows(st["x"], case["k"], st["xs"], case["rows"], case["k"], st["w"], st["g"], st["s"], case["n"],
+                          st["y"], case["n"])
+    return st["outputs"]
 
 
 def _qk(st, case):
