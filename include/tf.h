@@ -66,6 +66,8 @@ extern "C" {
 #define TF_MAX_PAGES (1 << 24)    /* pages of a pool */
 #define TF_MAX_PAGE_IDS (1 << 28) /* entries of a paged table's lists together */
 #define TF_MK       256         /* width of the drafter's Markov head rows (W1, W2) */
+#define TF_SCALE_KEYS 16          /* keys of a head that share a scale in scaled pools */
+#define TF_SCALE_COLUMNS 32       /* columns of a row (inputs of a weight) that share a scale */
 
 typedef enum {
     TF_OK = 0,
@@ -452,7 +454,10 @@ int tf_prompt_build(int32_t rows, int32_t keys, int32_t kv_capacity,
  *
  * Either table serves every call that a dense table of its kind serves, except
  * that its attention is tf_attn_paged: tf_attn, tf_attn_block, their partials
- * forms, tf_attn_merge and tf_attn_static refuse it (TF_EINVAL). */
+ * forms, tf_attn_merge and tf_attn_static refuse it (TF_EINVAL).
+ *
+ * tf_paged_scaled_build and tf_paged_scaled_prompt_build are the two for scaled
+ * pools (below). */
 int tf_paged_build(const tf_stream* streams, int n_streams, const void* const* conv_state,
                    const void* const* conv_hist, const int32_t* pages, int32_t page_keys,
                    int32_t n_pages, const void* const* k_pool, const void* const* v_pool,
@@ -530,6 +535,105 @@ int tf_qk_rows(const tf_segments* seg, int attn_layer, const void* q, int64_t q_
 int tf_pages_copy(void* const* pools, int n_pools, int32_t page_keys, int32_t n_pages,
                   const int32_t* src, const int32_t* dst, const int32_t* keys,
                   int n_copies, tf_cuda_stream stream);
+
+/* ---- scaled pools and rows: 8 bits ------------------------------------------
+ * A value of 8 bits is an e4m3 code under a scale 2^(b - 127) that neighbours
+ * share, held as the byte b (0..254). The library writes the smallest scale, from
+ * 2^-127 on, under which no finite value of its set saturates (the set's largest
+ * magnitude is at most 464 times the scale), and codes to nearest even; a NaN or
+ * an infinity becomes the code NaN and has no say on the scale. Rounding is off by
+ * at most 2^-4 of a value, or 2^-10 of the scale where that is more (then below
+ * 2^-17 of the set's largest).
+ *
+ * Scaled pools hold keys and values that way, half the bytes of a bf16 pool: the
+ * scale of K, and of V, is shared by TF_SCALE_KEYS keys (slots 16 j .. 16 j + 15
+ * of a page) of one head.
+ *   pool    uint8 [n_pages][TF_NKV][page_keys][TF_D], codes
+ *   scales  uint8 [n_pages][TF_NKV][page_keys / TF_SCALE_KEYS], at any address
+ *
+ * tf_paged_scaled_build and tf_paged_scaled_prompt_build are tf_paged_build and
+ * tf_paged_prompt_build with a pool of scales beside each pool of codes (host
+ * arrays [n_attn] of device pointers); no two pools, scales included, overlap.
+ * Their tables serve the calls that a paged table serves:
+ *   tf_qk_rows    codes the rows that it appends. A block of 16 keys takes the
+ *                 scale of the rows before the window that it holds and of the
+ *                 window's rows in it, and rows that it held are coded again where
+ *                 the scale moves (the same values, but for those below 2^-14 of
+ *                 the block's largest); slots past the window keep their bytes and
+ *                 have no say. Pages that are filled in another way keep to the
+ *                 format above.
+ *   tf_attn_paged reads codes and scales (q and out bf16; the window's own rows
+ *                 are read back as coded). P.V runs with fp16 weights (off by
+ *                 2^-12 of each) and exact codes, summed in fp32; keys whose
+ *                 weight times V's scale is below 2^-31 of the largest such
+ *                 product of a chunk do not count in P.V. A NaN reaches the rows
+ *                 that see its key, no other. q, partials and out lie apart. */
+int tf_paged_scaled_build(const tf_stream* streams, int n_streams, const void* const* conv_state,
+                          const void* const* conv_hist, const int32_t* pages, int32_t page_keys,
+                          int32_t n_pages, const void* const* k_pool, const void* const* v_pool,
+                          const void* const* k_scale, const void* const* v_scale,
+                          int n_conv, int n_attn, tf_cuda_stream stream, tf_segments** out);
+int tf_paged_scaled_prompt_build(int32_t rows, int32_t keys, int32_t kv_capacity,
+                                 const void* const* conv_state, const int32_t* pages, int32_t page_keys,
+                                 int32_t n_pages, const void* const* k_pool, const void* const* v_pool,
+                                 const void* const* k_scale, const void* const* v_scale,
+                                 int n_conv, int n_attn, tf_cuda_stream stream, tf_segments** out);
+
+/* tf_pages_copy for scaled pools: the codes of keys [0, keys[i]) and the scales of
+ * the blocks that hold them.
+ *   pools, scales  host arrays [n_pools] of device pointers
+ * The other arguments, rules and errors are tf_pages_copy's. */
+int tf_pages_copy_scaled(void* const* pools, void* const* scales, int n_pools, int32_t page_keys, int32_t n_pages,
+                         const int32_t* src, const int32_t* dst, const int32_t* keys, int n_copies,
+                         tf_cuda_stream stream);
+
+/* The residual's addition, the RMS norm and the 8-bit coding of each row, between
+ * a projection's output and the next projection's input:
+ *   h = bf16(x + res)            (h = x when res is NULL)
+ *   n = h * w / sqrt(mean(h^2) + eps)                      in fp32
+ * coded with a scale for each TF_SCALE_COLUMNS columns.
+ *   x, res  bf16, row r at x + r*x_stride, res + r*res_stride (elements); res may
+ *           be NULL, and sum is then NULL too
+ *   w       bf16 [width]
+ *   sum     bf16, row r at sum + r*sum_stride: h, the residual of the next addition;
+ *           may be x or res itself (at the same stride)
+ *   codes   uint8 [R][width]
+ *   scales  uint8 [R][width / TF_SCALE_COLUMNS], at any address
+ * width is a multiple of TF_SCALE_COLUMNS, strides are multiples of 8; other
+ * overlaps of an output with anything are refused. A NaN or an infinity in a row
+ * makes that row's codes NaN (or, where the root is infinite, 0). Needs no table;
+ * R == 0 is a no-op. Errors: TF_EINVAL (null, one of res and sum alone, misaligned,
+ * overlaps, a bad width or stride, eps not positive and finite, another device's
+ * memory), TF_ERANGE (R > 2^24, width > TF_NORM_MAX_WIDTH, a stride beyond 2^32). */
+#define TF_NORM_MAX_WIDTH (1 << 14)
+int tf_norm_rows(const void* x, int64_t x_stride, const void* res, int64_t res_stride, const void* w, float eps,
+                 int R, int width, void* sum, int64_t sum_stride, void* codes, void* scales,
+                 tf_cuda_stream stream);
+
+/* Rows times a matrix of 4-bit weights (a projection, or the logits):
+ *   y[r][n] = s[n] * sum_k x[r][k] * g[n][k / 32] * (c[n][k] - 8)
+ * summed in fp32 over exact products and rounded once to bf16.
+ *   x         x_scales NULL: bf16, row r at x + r*x_stride (elements, a multiple
+ *             of 8). Otherwise codes, row r at x + r*x_stride (a multiple of 16),
+ *             with x_scales uint8 [R][K / TF_SCALE_COLUMNS] (at any address): what
+ *             tf_norm_rows writes
+ *   w         uint8 [N][K / 2]: codes c in 0..15, the even k in the low four bits
+ *   w_scales  uint8 [N][K / TF_SCALE_COLUMNS] (at any address): g, e4m3
+ *   s         float [N]
+ *   y         bf16, row r at y + r*y_stride (any 2-byte address and stride >= N);
+ *             overlaps nothing else
+ * K is a multiple of TF_SCALE_COLUMNS. The weights are read once for up to 32 rows.
+ * Sums run in a fixed order. A NaN or an infinity in a row of x reaches that row of
+ * y only. Needs no table; R == 0 is a no-op. Errors: TF_EINVAL (null, misaligned,
+ * overlaps, a bad K or stride, N < 1, another device's memory), TF_ERANGE
+ * (R > TF_LINEAR_MAX_ROWS, K > TF_LINEAR_MAX_INPUTS, N > TF_LINEAR_MAX_OUTPUTS, a
+ * stride beyond 2^32). */
+#define TF_LINEAR_MAX_ROWS (1 << 20)
+#define TF_LINEAR_MAX_INPUTS (1 << 20)
+#define TF_LINEAR_MAX_OUTPUTS (1 << 24)
+int tf_linear_rows(const void* x, int64_t x_stride, const void* x_scales, int R, int K, const void* w,
+                   const void* w_scales, const float* s, int N, void* y, int64_t y_stride,
+                   tf_cuda_stream stream);
 
 /* ---- failures on the device ------------------------------------------------
  * The tensor-core attention kernel (tf_attn*, streams of 9 rows or more and

@@ -37,6 +37,7 @@
 // 2 KB of a head's K or V is still contiguous and the copies stay whole 128-byte
 // lines.
 #include "attn_item.cuh"
+#include "scaled.cuh"
 
 namespace tf {
 namespace {
@@ -379,8 +380,9 @@ extern "C" int tf_attn_paged(const tf_segments* seg, int attn_layer, const void*
     float* po = static_cast<float*>(partials);
     float2* pml = reinterpret_cast<float2*>(po + t.n_partials * TF_D);
     uint16_t* o = static_cast<uint16_t*>(out);
-    int rc = launch_attn_partials<true>(t, attn_layer, static_cast<const uint16_t*>(q), po, pml, stream, o,
-                                        full ? 1 : 0);
+    const uint16_t* queries = static_cast<const uint16_t*>(q);
+    int rc = seg->scaled ? launch_attn_scaled(t, attn_layer, queries, po, pml, stream, o, full ? 1 : 0)
+                         : launch_attn_partials<true>(t, attn_layer, queries, po, pml, stream, o, full ? 1 : 0);
     if (rc != TF_OK || t.n_merge_rows == 0) return rc;
     return launch_attn_merge<true>(t, po, pml, o, stream, true);
 }

@@ -1,0 +1,473 @@
+// Attention (tf_attn_paged) over scaled pools: keys and values as e4m3 codes
+// with a power-of-two scale for each 16 keys of a head. Items, chunks, partial
+// records and merges are those of attn.cu; a window of more than 8 rows runs as
+// several items over its chunk, next to each other in the grid.
+//
+// With c the codes, ek and ev a block's exponents and x the scores in log2 units:
+//   x_t = (q . ck_t) * 2^ek * log2(e) / 8
+//   o = sum 2^x_t 2^ev cv_t / sum 2^x_t
+// HBM bound: 128 bytes of K and V (and 1/8 of scales) a key and KV head, half of
+// the bf16 caches', so what a key costs in instructions counts twice as much:
+//
+// - The products run transposed on mma.sync m16n8k16: 16 keys (then 16 dimensions
+//   of V) by 8 queries, so that a window of two rows fills a tile; 16 queries a
+//   tile would double the MMAs and softmax work of narrow windows.
+// - A lane's fragments of K are 16 consecutive codes of a key's row, those of V
+//   8 consecutive dimensions of four keys: the order of the summed index is free
+//   as long as both factors have it. Codes become fp16 in registers (exact).
+// - K's scale is a factor of the block's scores. V's enters the weights that go
+//   into P.V, w = 2^(x - m) * 2^(ev - E) with E the chunk's largest exponent, so
+//   the accumulators hold o / 2^E; the sum l takes 2^(x - m) itself. The
+//   reference m moves when a w passes 2^15 (fp16 holds 65,504), to put the
+//   largest at 2^6: the small weights then keep fp16's 11 bits down to 2^-20 of
+//   the largest and vanish below 2^-31. A V block 2^64 below the chunk's largest
+//   counts as if it were 2^64 below (its codes are weighed by 2^-64).
+// - Queries become fp16 under a power of two of their own that puts a head's
+//   largest at 2^14: exact for bf16 values down to 2^-28 of it, off by at most
+//   2^-39 of it below.
+//
+// Four warps share a chunk: warp w takes the stages (32 keys) w, w + 4, ... of
+// it through a ring of its own (cp.async, no CTA barrier in the loop); their
+// results are joined at the end.
+//
+// What no row of the item may see is kept out: scores are masked, and in blocks
+// that reach past the first row's keys a NaN code of V is taken out of the
+// product and put back, as NaN, into the rows that see its key.
+#include "attn_item.cuh"
+#include "scaled.cuh"
+
+namespace tf {
+namespace {
+
+using item::kThreads;
+using item::kWarps;
+using item::ex2;
+using item::pack_h2;
+using item::mma_f16;
+using item::smem_u32;
+
+constexpr int kKeys = TF_SCALE_KEYS;           // a block: the keys that share a scale
+constexpr int kStageKeys = 2 * kKeys;
+constexpr int kBlockB = kKeys * TF_D;          // 1 KB of codes
+constexpr int kStageB = 4 * kBlockB;           // K of two blocks, then V of them
+constexpr int kStages = 4;
+constexpr int kRingB = kStages * kStageB;
+constexpr int kOStride = TF_D + 4;             // floats a query row of the warps' joining
+constexpr int kBlocks = 512 * TF_MAX_ROWS / kKeys;   // blocks of the longest chunk
+constexpr float kLog2e8 = 0.18033688011112042f;      // log2(e) / sqrt(64)
+constexpr float kNoRef = -3e38f;               // the reference of a query without a key so far
+constexpr float kLargest = 32768.f;            // a weight beyond it moves the reference
+constexpr float kHeadroom = 6.f;               // log2 of the largest weight after that
+constexpr int kMaxShift = 64;
+static_assert(kStageKeys * kWarps <= 256, "chunks are whole rounds of the warps");
+static_assert(kKeys == item::kBlockKeys && kBlocks * 4 == item::kBlocksB, "one block index for pools and scales");
+
+// ring (joined through it at the end), block indices, exponents (K low byte, V high), the warps' largest V
+constexpr int kSmem = kWarps * kRingB + kBlocks * 4 + kBlocks * 2 + 16;
+static_assert(kWarps * kRingB >= kWarps * 8 * 4 * (kOStride + 2) * 4, "the joining fits the rings");
+
+__device__ __forceinline__ void movmatrix_t(uint32_t& d, uint32_t a) {
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint2 lds8(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint32_t hmax2(uint32_t a, uint32_t b) {
+    __half2 r = __hmax2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+    return *reinterpret_cast<uint32_t*>(&r);
+}
+
+// Where the 16 bytes `c` (0..3) of key row r lie in a block's 1 KB of shared
+// memory: two rows a 128-byte line, their order such that the lanes of a phase
+// (K: rows i and 4 + i, all of c; V: four consecutive rows, two of c) fall on
+// different banks.
+__device__ __forceinline__ uint32_t k_at(int r, int c) { return (r >> 1) * 128 + ((((r & 1) * 4 + c) ^ (r & 4)) << 4); }
+__device__ __forceinline__ uint32_t v_at(int r, int c) { return (r >> 1) * 128 + ((((r & 1) * 4 + c) ^ (r & 2)) << 4); }
+
+// MMA row i of a K tile is key perm(i) of its block: the keys 2 t4, 2 t4 + 1 (and
+// + 8) that a lane weighs are then the four rows t4, 4 + t4, ... of V.
+__device__ __forceinline__ int perm(int i) { return (i & 8) | ((i & 1) << 2) | ((i & 7) >> 1); }
+
+// Bytes 0xFF where a code is NaN.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu); }
+
+// One item: one key chunk of one stream, query rows [q0, q0 + 8 NT) of KV head
+// g, by 128 threads.
+template <int NT>
+__global__ void __launch_bounds__(kThreads, 3)
+attn_scaled_kernel(SegTable t, int layer, const uint16_t* __restrict__ q, float* __restrict__ part_o,
+                   float2* __restrict__ part_ml, uint16_t* __restrict__ out, int full) {
+    extern __shared__ __align__(128) unsigned char smem[];
+    uint32_t* const blocks = reinterpret_cast<uint32_t*>(smem + kWarps * kRingB);
+    uint16_t* const exps = reinterpret_cast<uint16_t*>(blocks + kBlocks);
+    uint32_t* const top = reinterpret_cast<uint32_t*>(exps + kBlocks);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g8 = lane >> 2, t4 = lane & 3;
+    const int g = blockIdx.x % TF_NKV;
+    const AttnItem it = t.items[blockIdx.x / TF_NKV];
+    const SegStream st = t.streams[it.stream];
+    const int q0 = it.q0;
+    const int nq = min(8 * NT, st.rows * 4 - q0);
+    const int c0 = it.chunk * st.chunk_keys;
+    const int nkeys = min(st.chunk_keys, st.keys - c0);
+    const int nblocks = (nkeys + kKeys - 1) / kKeys;
+    item::load_blocks(t, it, nkeys, g, blocks, tid, kThreads);
+    const size_t slot = size_t(layer) * t.S + it.stream;
+    const uint8_t* const Kp = static_cast<const uint8_t*>(t.k_cache[slot]);
+    const uint8_t* const Vp = static_cast<const uint8_t*>(t.v_cache[slot]);
+    __syncthreads();
+    pdl_wait();   // the table above; queries and caches below
+
+    // ---- the ring
+    const uint32_t ring = smem_u32(smem) + warp * kRingB;
+    const int nst = (nkeys + kStageKeys - 1) / kStageKeys;
+    const int mine = nst > warp ? (nst - warp + kWarps - 1) / kWarps : 0;
+    // this lane's two 16-byte pieces of a block: rows lane / 4 and 8 + lane / 4
+    const uint32_t kd = k_at(lane >> 2, lane & 3), vd = v_at(lane >> 2, lane & 3);
+    auto issue = [&](int i) {
+        const uint32_t buf = ring + (i % kStages) * kStageB;
+        const uint2 b = *reinterpret_cast<const uint2*>(blocks + 2 * (warp + i * kWarps));
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {   // a second block past the chunk is block 0: read, never used
+            const size_t off = size_t(k ? b.y : b.x) * kBlockB + lane * 16;
+            copy16(buf + k * kBlockB + kd, Kp + off);
+            copy16(buf + k * kBlockB + kd + kBlockB / 2, Kp + off + kBlockB / 2);
+            copy16(buf + (2 + k) * kBlockB + vd, Vp + off);
+            copy16(buf + (2 + k) * kBlockB + vd + kBlockB / 2, Vp + off + kBlockB / 2);
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) {
+        if (i < mine) issue(i);
+        item::cp_async_commit();
+    }
+
+    // ---- the chunk's exponents
+    {
+        const uint8_t *ks = t.k_scale[layer], *vs = t.v_scale[layer];
+        uint32_t m = 0;
+        for (int i = tid; i < nblocks; i += kThreads) {
+            const uint32_t b = blocks[i], e = vs[b];
+            exps[i] = uint16_t(ks[b] | e << 8);
+            m = max(m, e);
+        }
+        m = __reduce_max_sync(0xFFFFFFFFu, m);
+        if (lane == 0) top[warp] = m;
+    }
+
+    // ---- queries: column n of a tile is query row q0 + 8 nt + n (window row / 4, head % 4)
+    uint32_t qf[NT][4][2];
+    float cq[NT][2];   // factors of the columns 2 t4, 2 t4 + 1
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int qi = nt * 8 + g8;
+        uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        if (qi < nq) {
+            const uint16_t* src = q + (size_t(st.row_offset + ((q0 + qi) >> 2)) * TF_NQ + 4 * g + (qi & 3)) * TF_D + 16 * t4;
+            const uint4 a = *reinterpret_cast<const uint4*>(src), b = *reinterpret_cast<const uint4*>(src + 8);
+            w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+            w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+        }
+        uint32_t most = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            most = max(most, max(finite_bits(__uint_as_float(w[i] << 16)), finite_bits(__uint_as_float(w[i] & 0xFFFF0000u))));
+        most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
+        most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
+        const int up = min(141 - int(most >> 23), 100);   // the head's largest becomes 2^14..2^15
+        const float mul = __uint_as_float(uint32_t(127 + up) << 23);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            qf[nt][i >> 1][i & 1] = pack_h2(__uint_as_float(w[i] << 16) * mul, __uint_as_float(w[i] & 0xFFFF0000u) * mul);
+        const float back = __uint_as_float(uint32_t(127 - up) << 23) * kLog2e8;
+        cq[nt][0] = __shfl_sync(0xFFFFFFFFu, back, 8 * t4);
+        cq[nt][1] = __shfl_sync(0xFFFFFFFFu, back, 8 * t4 + 4);
+    }
+    __syncthreads();
+    const int E = int(max(max(top[0], top[1]), max(top[2], top[3])));
+
+    // keys that a column's window row sees, chunk-local (a tile's columns 2 t4 and 2 t4 + 1 are of one row)
+    int lim[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int qi = nt * 8 + 2 * t4;
+        const int vis = (full ? st.keys : st.keys - st.rows + ((q0 + qi) >> 2) + 1) - c0;
+        lim[nt] = qi < nq ? max(0, min(vis, nkeys)) : 0;
+    }
+    const int lim_all = min((full ? st.keys : st.keys - st.rows + (q0 >> 2) + 1) - c0, nkeys);
+
+    float o[NT][4][4], m[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[nt][mt][e] = 0.f;
+        m[nt][0] = m[nt][1] = kNoRef;
+        l[nt][0] = l[nt][1] = 0.f;
+    }
+    // this lane's pieces in a block: K rows perm(g8) and 8 + perm(g8), V rows t4, 4 + t4, 8 + t4, 12 + t4
+    const uint32_t ka = k_at(perm(g8), t4);
+    const uint32_t va0 = v_at(t4, g8 >> 1) + (g8 & 1) * 8, va1 = v_at(4 + t4, g8 >> 1) + (g8 & 1) * 8;
+
+    for (int i = 0; i < mine; ++i) {
+        if (i + kStages - 1 < mine) issue(i + kStages - 1);
+        item::cp_async_commit();
+        item::cp_async_wait<kStages - 1>();
+        __syncwarp();
+        const uint32_t buf = ring + (i % kStages) * kStageB;
+#pragma unroll 1
+        for (int k = 0; k < 2; ++k) {
+            const int bi = 2 * (warp + i * kWarps) + k;
+            if (bi >= nblocks) break;
+            const int key0 = bi * kKeys;
+            const bool edge = key0 + kKeys > lim_all;
+            const uint32_t ex = exps[bi];
+            const float kf = __uint_as_float((ex & 0xFFu) << 23);
+            const int dv = max(int(ex >> 8) - E, -kMaxShift);
+            const float vf = __uint_as_float(uint32_t(127 + dv) << 23);
+
+            // scores
+            float s[NT][4];
+            {
+                const uint4 r0 = lds16(buf + k * kBlockB + ka), r1 = lds16(buf + k * kBlockB + ka + kBlockB / 2);
+                const uint32_t w0[4] = {r0.x, r0.y, r0.z, r0.w}, w1[4] = {r1.x, r1.y, r1.z, r1.w};
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks) {
+                    const uint32_t a[4] = {e4m3_low(w0[ks]), e4m3_low(w1[ks]), e4m3_high(w0[ks]), e4m3_high(w1[ks])};
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        if (ks == 0) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+                        mma_f16(s[nt], a, qf[nt][ks][0], qf[nt][ks][1]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const float f0 = cq[nt][0] * kf, f1 = cq[nt][1] * kf;
+                s[nt][0] *= f0;
+                s[nt][1] *= f1;
+                s[nt][2] *= f0;
+                s[nt][3] *= f1;
+            }
+            if (edge) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    if (key0 + perm(g8) >= lim[nt]) s[nt][0] = s[nt][1] = -INFINITY;
+                    if (key0 + 8 + perm(g8) >= lim[nt]) s[nt][2] = s[nt][3] = -INFINITY;
+                }
+            }
+            // weights
+            uint32_t pw[NT][2];
+            float ps[NT][2];
+            auto weigh = [&]() {
+                uint32_t most = 0;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float p[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) p[e] = ex2(s[nt][e] - m[nt][e & 1]);
+                    ps[nt][0] = p[0] + p[2];
+                    ps[nt][1] = p[1] + p[3];
+                    pw[nt][0] = pack_h2(p[0] * vf, p[1] * vf);
+                    pw[nt][1] = pack_h2(p[2] * vf, p[3] * vf);
+                    most = hmax2(most, hmax2(pw[nt][0], pw[nt][1]));
+                }
+                const float2 h = h2_to_f2(most);
+                return fmaxf(h.x, h.y) > kLargest;
+            };
+            if (__any_sync(0xFFFFFFFFu, weigh())) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float y[2] = {fmaxf(s[nt][0], s[nt][2]), fmaxf(s[nt][1], s[nt][3])};
+                    float alpha[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                        for (int d = 4; d < 32; d *= 2) y[e] = fmaxf(y[e], __shfl_xor_sync(0xFFFFFFFFu, y[e], d));
+                        y[e] += float(dv) - kHeadroom;
+                        alpha[e] = 1.f;
+                        if (y[e] > m[nt][e] + (15.f - kHeadroom)) {
+                            alpha[e] = ex2(m[nt][e] - y[e]);
+                            m[nt][e] = y[e];
+                        }
+                        l[nt][e] *= alpha[e];
+                    }
+#pragma unroll
+                    for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[nt][mt][e] *= alpha[e & 1];
+                }
+                weigh();
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                l[nt][0] += ps[nt][0];
+                l[nt][1] += ps[nt][1];
+                movmatrix_t(pw[nt][0], pw[nt][0]);
+                movmatrix_t(pw[nt][1], pw[nt][1]);
+            }
+            // P.V: MMA row g8 of tile mt is dimension 8 g8 + 2 mt, row 8 + g8 the next one
+            const uint32_t bv = buf + (2 + k) * kBlockB;
+            uint2 v[4] = {lds8(bv + va0), lds8(bv + va1), lds8(bv + kBlockB / 2 + va0), lds8(bv + kBlockB / 2 + va1)};
+            auto product = [&](const uint2 (&c)[4], const uint32_t (&p)[NT][2], float (&acc)[NT][4][4]) {
+#pragma unroll
+                for (int mt = 0; mt < 4; ++mt) {
+                    const uint32_t sel = (mt & 1) ? 0x7362u : 0x5140u;   // bytes 2 mt, 2 mt + 1 of both
+                    const uint32_t lo = __byte_perm(mt < 2 ? c[0].x : c[0].y, mt < 2 ? c[1].x : c[1].y, sel);
+                    const uint32_t hi = __byte_perm(mt < 2 ? c[2].x : c[2].y, mt < 2 ? c[3].x : c[3].y, sel);
+                    const uint32_t a[4] = {e4m3_low(lo), e4m3_high(lo), e4m3_low(hi), e4m3_high(hi)};
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma_f16(acc[nt][mt], a, p[nt][0], p[nt][1]);
+                }
+            };
+            if (edge) {
+                uint2 bad[4];
+                uint32_t any = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    bad[j] = make_uint2(nan_bytes(v[j].x), nan_bytes(v[j].y));
+                    any |= bad[j].x | bad[j].y;
+                }
+                if (__any_sync(0xFFFFFFFFu, any != 0)) {
+                    uint32_t sees[NT][2];   // 1 where the column's row sees the key
+                    float hits[NT][4][4];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const uint32_t one = 0x3C003C00u;
+                        movmatrix_t(sees[nt][0], key0 + perm(g8) < lim[nt] ? one : 0u);
+                        movmatrix_t(sees[nt][1], key0 + 8 + perm(g8) < lim[nt] ? one : 0u);
+#pragma unroll
+                        for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) hits[nt][mt][e] = 0.f;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        v[j].x &= ~bad[j].x;
+                        v[j].y &= ~bad[j].y;
+                        bad[j].x &= 0x38383838u;   // 1 as a code
+                        bad[j].y &= 0x38383838u;
+                    }
+                    product(bad, sees, hits);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (hits[nt][mt][e] > 0.f) o[nt][mt][e] = __uint_as_float(0x7FC00000u);
+                }
+            }
+            product(v, pw, o);
+        }
+        __syncwarp();   // the stage is read: its buffer may be filled again
+    }
+    item::cp_async_wait<0>();
+    __syncthreads();
+    pdl_trigger();
+
+    // ---- join the four warps (the ring's memory): the record, or the output
+    float* const sO = reinterpret_cast<float*>(smem);   // [4][8 NT][kOStride]
+    float* const sM = sO + kWarps * 8 * NT * kOStride;  // [4][8 NT]
+    float* const sL = sM + kWarps * 8 * NT;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            float sum = l[nt][e];
+#pragma unroll
+            for (int d = 4; d < 32; d *= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+            const int col = warp * 8 * NT + nt * 8 + 2 * t4 + e;
+            if (g8 == 0) {
+                sM[col] = m[nt][e];
+                sL[col] = sum;
+            }
+            float4* row = reinterpret_cast<float4*>(sO + col * kOStride + 8 * g8);
+            row[0] = make_float4(o[nt][0][e], o[nt][0][2 + e], o[nt][1][e], o[nt][1][2 + e]);
+            row[1] = make_float4(o[nt][2][e], o[nt][2][2 + e], o[nt][3][e], o[nt][3][2 + e]);
+        }
+    __syncthreads();
+    const int mode = out ? st.merge_mode : kMergeKernel;
+    const int64_t rec0 = st.pbase + (int64_t(it.chunk) * TF_NKV + g) * (st.rows * 4) + q0;
+    const int half = (E - kScaleBias) / 2;   // 2^E in two factors, both normal numbers
+    const float up0 = __uint_as_float(uint32_t(127 + half) << 23);
+    const float up1 = __uint_as_float(uint32_t(127 + E - kScaleBias - half) << 23);
+    for (int idx = tid; idx < nq * (TF_D / 4); idx += kThreads) {
+        const int qi = idx >> 4, d4 = (idx & 15) * 4;
+        float M = kNoRef;   // (a weight NaN leaves o NaN as well)
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sM[w * 8 * NT + qi]);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float L = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float f = ex2(sM[w * 8 * NT + qi] - M);   // 0 for a warp without a key of the row; its sums are 0 or NaN
+            const float4 v = *reinterpret_cast<const float4*>(sO + (w * 8 * NT + qi) * kOStride + d4);
+            L += f * sL[w * 8 * NT + qi];
+            acc.x += f * v.x;
+            acc.y += f * v.y;
+            acc.z += f * v.z;
+            acc.w += f * v.w;
+        }
+        if (mode == kMergeDirect) {
+            const float inv = 1.f / L;
+            store_out4(out_row(out, st, g, q0 + qi) + d4,
+                       make_float4(acc.x * inv * up0 * up1, acc.y * inv * up0 * up1, acc.z * inv * up0 * up1,
+                                   acc.w * inv * up0 * up1));
+        } else {
+            *reinterpret_cast<float4*>(part_o + (rec0 + qi) * TF_D + d4) =
+                make_float4(acc.x * up0 * up1, acc.y * up0 * up1, acc.z * up0 * up1, acc.w * up0 * up1);
+            if (d4 == 0) {   // a row without a key; a sum that is no number, which a merge must not take for none
+                const bool lost = !(L <= 3e38f);
+                part_ml[rec0 + qi] = make_float2(M > kNoRef ? M : lost ? 0.f : -INFINITY, lost ? INFINITY : L);
+            }
+        }
+    }
+    if (mode == kMergeLastCta) {
+        __shared__ int last_flag;
+        finish_last_cta<8>(t, layer, it.stream, st, g, part_o, part_ml, out, &last_flag);
+    }
+}
+
+template <int NT>
+int prepare_one() {
+    cudaError_t e = cudaFuncSetAttribute(attn_scaled_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kSmem);
+    return e == cudaSuccess ? TF_OK : cuda_fail(e);
+}
+
+template <int NT>
+int launch_one(const SegTable& t, int layer, const uint16_t* q, float* po, float2* pml, cudaStream_t stream,
+               uint16_t* out, int full) {
+    return launch_pdl(attn_scaled_kernel<NT>, dim3(t.n_items * TF_NKV), dim3(kThreads), kSmem, stream, t, layer,
+                      q, po, pml, out, full);
+}
+
+}  // namespace
+
+int attn_scaled_prepare() {
+    int rc;
+    if ((rc = prepare_one<1>()) != TF_OK || (rc = prepare_one<2>()) != TF_OK || (rc = prepare_one<3>()) != TF_OK) return rc;
+    return prepare_one<4>();
+}
+
+int launch_attn_scaled(const SegTable& t, int layer, const uint16_t* q, float* po, float2* pml, cudaStream_t stream,
+                       uint16_t* out, int full) {
+    const int nt = (t.item_rows + 1) / 2;   // tiles of 8 query rows in the widest item
+    return nt == 1 ? launch_one<1>(t, layer, q, po, pml, stream, out, full)
+         : nt == 2 ? launch_one<2>(t, layer, q, po, pml, stream, out, full)
+         : nt == 3 ? launch_one<3>(t, layer, q, po, pml, stream, out, full)
+                   : launch_one<4>(t, layer, q, po, pml, stream, out, full);
+}
+
+}  // namespace tf

@@ -24,7 +24,7 @@
 // HBM bound: 6,144 bytes in and as many out a row.
 #include <cmath>
 
-#include "tf_internal.cuh"
+#include "scaled.cuh"
 
 namespace tf {
 namespace {
@@ -33,16 +33,7 @@ constexpr int kWarps = (TF_NQ + 2 * TF_NKV) / 8;
 constexpr int kThreads = kWarps * 32;
 static_assert(TF_D == 64 && TF_NKV == 8, "a warp's 8 heads of 4 lanes");
 
-struct Turns {
-    uint64_t f[TF_D / 2];   // f_j as a fraction of a turn, 2^64 = one turn
-};
-
-struct Rows {
-    const uint16_t* q;
-    const uint16_t* k;
-    const uint16_t* v;
-    int64_t q_stride, k_stride, v_stride;
-};
+using Rows = QkvRows;
 
 __device__ __forceinline__ void unpack8(uint4 u, float (&x)[8]) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -244,6 +235,7 @@ extern "C" int tf_qk_rows(const tf_segments* seg, int attn_layer, const void* q,
                      q_stride, k_stride, v_stride};
     const uint16_t *qw = static_cast<const uint16_t*>(q_norm), *kw = static_cast<const uint16_t*>(k_norm);
     uint16_t* out = static_cast<uint16_t*>(q_out);
+    if (seg->scaled) return launch_qk_scaled(t, attn_layer, in, qw, kw, eps, turns, out, stream);
     if (t.R >= kManyRows)
         return launch_pdl(qk_rows_many_kernel, dim3((t.R + kRowWarps - 1) / kRowWarps), dim3(kRowWarps * 32), 0, stream,
                           t, attn_layer, in, qw, kw, eps, turns, out);

@@ -17,7 +17,7 @@
 
 #include <cudaTypedefs.h>   // PFN_cuTensorMapEncodeTiled
 
-#include "tf_internal.cuh"
+#include "scaled.cuh"
 
 namespace tf {
 
@@ -142,7 +142,8 @@ bool encode_w2_map(CUtensorMap* out, const void* w2, int rows) {
 
 // Attention kernel of a stream: tensor cores once its window holds 3 rows (12
 // query rows per KV head); TF_ATTN_PATH=mma|tc forces one (tests compare both).
-int attn_path_of(int rows) {
+int attn_path_of(int rows, bool scaled) {
+    if (scaled) return kAttnMma;
     if (rows > 16) return kAttnTc;   // prompt windows (17-32 rows): the tensor cores, whatever is forced
     const char* e = std::getenv("TF_ATTN_PATH");
     if (e && std::strcmp(e, "mma") == 0) return kAttnMma;
@@ -173,7 +174,7 @@ namespace tf {
 
 // The plan of a set of windows, each of at most `max_window_rows` rows
 // (TF_MAX_ROWS for the verify tables, kPromptTileRows for a prompt call).
-int plan_windows(const tf_stream* streams, int n_streams, tf_plan* out, int max_window_rows) {
+int plan_windows(const tf_stream* streams, int n_streams, tf_plan* out, int max_window_rows, bool scaled = false) {
     if (!out) return TF_EINVAL;
     std::memset(out, 0, sizeof(*out));
     if (n_streams < 0) return TF_EINVAL;
@@ -195,7 +196,7 @@ int plan_windows(const tf_stream* streams, int n_streams, tf_plan* out, int max_
         items += nch;
         tiles += (st.rows + tf::kConvTileRows - 1) / tf::kConvTileRows;
         max_rows = std::max(max_rows, int(st.rows));
-        (tf::attn_path_of(st.rows) == tf::kAttnTc ? any_tc : any_mma) = true;
+        (tf::attn_path_of(st.rows, scaled) == tf::kAttnTc ? any_tc : any_mma) = true;
         if (nch > 1 && 4 * st.rows * nch > tf::kMergeLastCtaMaxRecords) any_merge = true;
     }
     if (R > (1 << 24)) return TF_ERANGE;
@@ -217,10 +218,14 @@ namespace {
 
 // The page side of a paged build: the caller's lists (stream after stream,
 // kv_capacity / page_keys entries each) and pools; k_cache and v_cache hold
-// one pool a layer then.
+// one pool a layer then. Scaled pools hold codes of a byte, with a pool of scale
+// bytes a layer beside each.
 struct Paged {
     const int32_t* pages;
     int32_t page_keys, n_pages;
+    bool scaled = false;
+    const void* const* k_scale = nullptr;
+    const void* const* v_scale = nullptr;
 };
 
 // The checks of a paged build that need no look at the streams' state: page
@@ -230,15 +235,34 @@ int check_pools(const Paged& pg, const void* const* k_pool, const void* const* v
     const int P = pg.page_keys;
     if (P < TF_MIN_PAGE_KEYS || P > TF_MAX_PAGE_KEYS || (P & (P - 1)) || pg.n_pages < 1) return TF_EINVAL;
     if (pg.n_pages > TF_MAX_PAGES) return TF_ERANGE;
+    if (pg.scaled && n_attn > 0 && (!pg.k_scale || !pg.v_scale)) return TF_EINVAL;
     std::vector<Interval> iv;
-    const size_t bytes = size_t(pg.n_pages) * TF_NKV * P * TF_D * 2;
+    const size_t slots = size_t(pg.n_pages) * TF_NKV * P, bytes = slots * TF_D * (pg.scaled ? 1 : 2);
     for (int i = 0; i < 2 * n_attn; ++i) {
         const void* p = i < n_attn ? k_pool[i] : v_pool[i - n_attn];
         if (!p || !aligned16(p)) return TF_EINVAL;
         const uintptr_t a = reinterpret_cast<uintptr_t>(p);
         iv.push_back({a, a + bytes});
+        if (!pg.scaled) continue;
+        const uintptr_t b = reinterpret_cast<uintptr_t>(i < n_attn ? pg.k_scale[i] : pg.v_scale[i - n_attn]);
+        if (!b) return TF_EINVAL;
+        iv.push_back({b, b + slots / TF_SCALE_KEYS});
     }
     return any_overlap(iv) ? TF_EINVAL : TF_OK;
+}
+
+// Scaled pools: the blocks that the rows of a cache's window fall into, appended
+// to `out`. `stream_of(row)` names the table's stream of a window row (one whose
+// page list is the cache's).
+template <typename F>
+void append_items(const tf_stream& cache, F&& stream_of, std::vector<tf::AppendItem>& out) {
+    const int first = cache.keys - cache.rows;
+    for (int key = first; key < cache.keys;) {
+        const int key0 = key / TF_SCALE_KEYS * TF_SCALE_KEYS, row = key - first;
+        const int n = std::min(key0 + TF_SCALE_KEYS, cache.keys) - key;
+        out.push_back({stream_of(row), cache.row_offset + row, key0, int16_t(key - key0), int16_t(n)});
+        key += n;
+    }
 }
 
 // The page lists of `n` caches (their streams' rows, keys and capacity), checked
@@ -281,10 +305,12 @@ int finish_build(std::unique_ptr<tf_segments> owned, std::vector<tf::SegStream>&
                  const void* const* conv_state, const void* const* conv_hist, const void* const* k_cache,
                  const void* const* v_cache, int n_conv, int n_attn, tf_cuda_stream stream, tf_segments** out,
                  const Paged* pg = nullptr, const std::vector<int32_t>* page_ids = nullptr,
-                 const std::vector<int32_t>* page_first = nullptr) {
+                 const std::vector<int32_t>* page_first = nullptr,
+                 const std::vector<tf::AppendItem>* appends = nullptr) {
     using namespace tf;
     tf_segments* const seg = owned.get();
     seg->paged = pg != nullptr;
+    const bool scaled = seg->scaled = pg && pg->scaled;
     cudaGetDevice(&seg->device);
     const int S = int(ss.size());
     const int R = int(row_stream.size());
@@ -298,7 +324,7 @@ int finish_build(std::unique_ptr<tf_segments> owned, std::vector<tf::SegStream>&
         for (SegStream& d : ss) d.n_qg = 1;
         for (const AttnItem& it : items) {
             SegStream& d = ss[it.stream];
-            const int ng = attn_path_of(d.rows) == kAttnMma ? (d.rows + kMmaGroupRows - 1) / kMmaGroupRows : 1;
+            const int ng = attn_path_of(d.rows, scaled) == kAttnMma ? (d.rows + kMmaGroupRows - 1) / kMmaGroupRows : 1;
             d.n_qg = ng;
             for (int gi = 0; gi < ng; ++gi) groups.push_back({it.stream, it.chunk, 4 * kMmaGroupRows * gi, 0});
         }
@@ -310,7 +336,7 @@ int finish_build(std::unique_ptr<tf_segments> owned, std::vector<tf::SegStream>&
     // mma.sync items first, then tensor-core items; within each, largest
     // chunks first so the long work starts early in the grid
     std::stable_sort(items.begin(), items.end(), [&](const AttnItem& a, const AttnItem& b) {
-        const int pa = attn_path_of(ss[a.stream].rows), pb = attn_path_of(ss[b.stream].rows);
+        const int pa = attn_path_of(ss[a.stream].rows, scaled), pb = attn_path_of(ss[b.stream].rows, scaled);
         if (pa != pb) return pa < pb;
         auto len = [&](const AttnItem& it) {
             const SegStream& d = ss[it.stream];
@@ -322,7 +348,7 @@ int finish_build(std::unique_ptr<tf_segments> owned, std::vector<tf::SegStream>&
     });
     int n_items_mma = 0, mma_rows = 1;
     for (const AttnItem& it : items)
-        if (attn_path_of(ss[it.stream].rows) == kAttnMma) {
+        if (attn_path_of(ss[it.stream].rows, scaled) == kAttnMma) {
             ++n_items_mma;
             mma_rows = std::max(mma_rows, std::min(ss[it.stream].rows - it.q0 / 4, kMmaGroupRows));
         }
@@ -343,6 +369,9 @@ int finish_build(std::unique_ptr<tf_segments> owned, std::vector<tf::SegStream>&
     const size_t n_ids = pg ? page_ids->size() : 0;
     const size_t o_pg = off;       off = align_up(off + sizeof(int32_t) * n_ids, 256);
     const size_t o_pf = off;       off = align_up(off + (pg ? sizeof(int32_t) * S : 0), 256);
+    const size_t o_sc = off;       off = align_up(off + (scaled ? sizeof(void*) * 2 * size_t(n_attn) : 0), 256);
+    const size_t n_app = appends ? appends->size() : 0;
+    const size_t o_app = off;      off = align_up(off + sizeof(AppendItem) * n_app, 256);
     const size_t o_ctr = off;      off = align_up(off + sizeof(int32_t) * n_ap * TF_NKV, 256);
     const size_t n_groups = (size_t(S) + 127) / 128;   // Markov step: 128 streams per group
     const size_t o_mkk = off;      off = align_up(off + sizeof(unsigned long long) * S, 256);
@@ -378,6 +407,11 @@ int finish_build(std::unique_ptr<tf_segments> owned, std::vector<tf::SegStream>&
         if (n_ids) std::memcpy(h + o_pg, page_ids->data(), sizeof(int32_t) * n_ids);
         if (S) std::memcpy(h + o_pf, page_first->data(), sizeof(int32_t) * S);
     }
+    if (scaled && S && n_attn) {
+        std::memcpy(h + o_sc, pg->k_scale, sizeof(void*) * n_attn);
+        std::memcpy(h + o_sc + sizeof(void*) * n_attn, pg->v_scale, sizeof(void*) * n_attn);
+    }
+    if (n_app) std::memcpy(h + o_app, appends->data(), sizeof(AppendItem) * n_app);
     for (size_t i = 0; i < n_maps; ++i) {
         CUtensorMap km, vm;   // aligned locals, copied into the image
         bool ok;
@@ -407,6 +441,8 @@ int finish_build(std::unique_ptr<tf_segments> owned, std::vector<tf::SegStream>&
     t.n_partials = plan.n_partials;
     t.n_items_mma = n_items_mma;
     t.mma_mt = (mma_rows + 3) / 4;
+    t.item_rows = mma_rows;
+    t.n_appends = int32_t(n_app);
     t.n_merge_rows = 0;
     for (const SegStream& d : ss)
         if (d.merge_mode == kMergeKernel) t.n_merge_rows += d.rows;
@@ -438,6 +474,11 @@ int finish_build(std::unique_ptr<tf_segments> owned, std::vector<tf::SegStream>&
             t.page_first = reinterpret_cast<const int32_t*>(b + o_pf);
             while ((1 << t.page_shift) < pg->page_keys) ++t.page_shift;
         }
+        if (scaled) {
+            t.k_scale = reinterpret_cast<uint8_t* const*>(b + o_sc);
+            t.v_scale = t.k_scale + n_attn;
+            t.appends = reinterpret_cast<const AppendItem*>(b + o_app);
+        }
         t.counters = reinterpret_cast<int32_t*>(b + o_ctr);   // zero in the image
         t.mk_keys = reinterpret_cast<unsigned long long*>(b + o_mkk);   // zero in the image
         t.mk_flags = reinterpret_cast<uint32_t*>(b + o_mkf);
@@ -448,6 +489,7 @@ int finish_build(std::unique_ptr<tf_segments> owned, std::vector<tf::SegStream>&
         t.status = reinterpret_cast<uint32_t*>(b + o_st);   // zero in the image
         rc = attn_prepare();
         if (rc == TF_OK) rc = attn_tc_prepare();
+        if (rc == TF_OK && scaled) rc = attn_scaled_prepare();
         if (rc == TF_OK && n_items_mma > 0 && size_t(n_items_mma) < items.size()) {
             // a round of both window kinds: the tensor-core launch runs on a side
             // stream with a grid proportional to its share of the keys (the K/V
@@ -455,7 +497,7 @@ int finish_build(std::unique_ptr<tf_segments> owned, std::vector<tf::SegStream>&
             int64_t keys_tc = 0, keys_all = 0;
             for (const SegStream& d : ss) {
                 keys_all += d.keys;
-                if (attn_path_of(d.rows) == kAttnTc) keys_tc += d.keys;
+                if (attn_path_of(d.rows, scaled) == kAttnTc) keys_tc += d.keys;
             }
             const int slots = 2 * sm_count();
             int g = int((int64_t(slots) * keys_tc + keys_all - 1) / (keys_all > 0 ? keys_all : 1));
@@ -506,7 +548,7 @@ int build_verify(const tf_stream* streams, int n_streams, const void* const* con
     *out = nullptr;
     if (n_conv < 0 || n_attn < 0 || n_conv > 4096 || n_attn > 4096) return TF_EINVAL;
     tf_plan plan;
-    int rc = tf_segments_plan(streams, n_streams, &plan);
+    int rc = plan_windows(streams, n_streams, &plan, TF_MAX_ROWS, pg && pg->scaled);
     if (rc != TF_OK) return rc;
     const int S = n_streams;
     if (S > 0 && n_conv > 0 && !conv_state) return TF_EINVAL;
@@ -581,8 +623,11 @@ int build_verify(const tf_stream* streams, int n_streams, const void* const* con
             tiles.push_back({s, r0, std::min(kConvTileRows, st.rows - r0), 0});
         for (int c = 0; c < d.n_chunks; ++c) items.push_back({s, c, 0, 0});
     }
+    std::vector<AppendItem> appends;
+    if (pg && pg->scaled)
+        for (int s = 0; s < S; ++s) append_items(streams[s], [&](int) { return s; }, appends);
     return finish_build(std::move(seg), ss, row_stream, tiles, items, conv_state, conv_hist, k_cache, v_cache, n_conv,
-                        n_attn, stream, out, pg, &page_ids, &page_first);
+                        n_attn, stream, out, pg, &page_ids, &page_first, &appends);
 }
 
 // tf_prompt_build and (pg) tf_paged_prompt_build.
@@ -633,7 +678,7 @@ int build_prompt(int32_t rows, int32_t keys, int32_t kv_capacity, const void* co
         tiles_as_streams.push_back({r, t * kPromptTileRows, keys - rows + t * kPromptTileRows + r, kv_capacity});
     }
     tf_plan plan;
-    int rc = plan_windows(tiles_as_streams.data(), T, &plan, kPromptTileRows);   // the attention work
+    int rc = plan_windows(tiles_as_streams.data(), T, &plan, kPromptTileRows, pg && pg->scaled);   // the attention work
     if (rc != TF_OK) return rc;
     plan.n_streams = 1;
     plan.n_conv_tiles = (rows + kConvTileRows - 1) / kConvTileRows;
@@ -676,9 +721,12 @@ int build_prompt(int32_t rows, int32_t keys, int32_t kv_capacity, const void* co
             kc[size_t(l) * S + s] = k_cache[l];
             vc[size_t(l) * S + s] = v_cache[l];
         }
+    std::vector<AppendItem> appends;
+    if (pg && pg->scaled)
+        append_items({rows, 0, keys, kv_capacity}, [](int row) { return 1 + row / kPromptTileRows; }, appends);
     return finish_build(std::move(seg), ss, row_stream, tiles, items, n_conv ? cs.data() : nullptr, nullptr,
                         pg ? k_cache : n_attn ? kc.data() : nullptr, pg ? v_cache : n_attn ? vc.data() : nullptr,
-                        n_conv, n_attn, stream, out, pg, &page_ids, &page_first);
+                        n_conv, n_attn, stream, out, pg, &page_ids, &page_first, &appends);
 }
 
 // A build runs out of host memory: TF_ENOMEM, no exception past the C entry.
@@ -719,7 +767,7 @@ int tf_paged_build(const tf_stream* streams, int n_streams, const void* const* c
                    const void* const* k_pool, const void* const* v_pool, int n_conv, int n_attn,
                    tf_cuda_stream stream, tf_segments** out) {
     return guarded([&] {
-        const Paged pg = {pages, page_keys, n_pages};
+        const Paged pg = {pages, page_keys, n_pages, false, nullptr, nullptr};
         return build_verify(streams, n_streams, conv_state, conv_hist, k_pool, v_pool, n_conv, n_attn, stream, out,
                             &pg);
     });
@@ -730,7 +778,29 @@ int tf_paged_prompt_build(int32_t rows, int32_t keys, int32_t kv_capacity, const
                           const void* const* v_pool, int n_conv, int n_attn, tf_cuda_stream stream,
                           tf_segments** out) {
     return guarded([&] {
-        const Paged pg = {pages, page_keys, n_pages};
+        const Paged pg = {pages, page_keys, n_pages, false, nullptr, nullptr};
+        return build_prompt(rows, keys, kv_capacity, conv_state, k_pool, v_pool, n_conv, n_attn, stream, out, &pg);
+    });
+}
+
+int tf_paged_scaled_build(const tf_stream* streams, int n_streams, const void* const* conv_state,
+                          const void* const* conv_hist, const int32_t* pages, int32_t page_keys, int32_t n_pages,
+                          const void* const* k_pool, const void* const* v_pool, const void* const* k_scale,
+                          const void* const* v_scale, int n_conv, int n_attn, tf_cuda_stream stream,
+                          tf_segments** out) {
+    return guarded([&] {
+        const Paged pg = {pages, page_keys, n_pages, true, k_scale, v_scale};
+        return build_verify(streams, n_streams, conv_state, conv_hist, k_pool, v_pool, n_conv, n_attn, stream, out,
+                            &pg);
+    });
+}
+
+int tf_paged_scaled_prompt_build(int32_t rows, int32_t keys, int32_t kv_capacity, const void* const* conv_state,
+                                 const int32_t* pages, int32_t page_keys, int32_t n_pages, const void* const* k_pool,
+                                 const void* const* v_pool, const void* const* k_scale, const void* const* v_scale,
+                                 int n_conv, int n_attn, tf_cuda_stream stream, tf_segments** out) {
+    return guarded([&] {
+        const Paged pg = {pages, page_keys, n_pages, true, k_scale, v_scale};
         return build_prompt(rows, keys, kv_capacity, conv_state, k_pool, v_pool, n_conv, n_attn, stream, out, &pg);
     });
 }

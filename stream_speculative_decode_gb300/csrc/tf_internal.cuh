@@ -55,6 +55,14 @@ constexpr int kConvTileRows = 8;
 // of the per-stream kernels, fill half of it).
 constexpr int kPromptTileRows = TF_PROMPT_WINDOW_ROWS;
 
+// Tables of scaled pools: the window rows that fall into one 16-key block of a
+// cache, n_rows rows from row `row0` on at the block's slots slot0, slot0 + 1, ..;
+// the slots below slot0 hold rows that are kept. key0: the block's first key.
+struct AppendItem {
+    int32_t stream, row0, key0;
+    int16_t slot0, n_rows;
+};
+
 // Device view of a segment table, passed to kernels by value.
 struct SegTable {
     const SegStream* streams;
@@ -100,6 +108,13 @@ struct SegTable {
     int32_t page_shift;
     const int32_t* pages;
     const int32_t* page_first;        // [S]
+    // Scaled pools (tf_paged_scaled_build, tf_paged_scaled_prompt_build): the
+    // pools hold e4m3 codes, a scale byte for each 16 keys of a head beside them.
+    uint8_t* const* k_scale;          // [n_attn] pools of scale bytes; null for bf16 pools
+    uint8_t* const* v_scale;
+    const AppendItem* appends;        // [n_appends]
+    int32_t n_appends;
+    int32_t item_rows;                // window rows of the mma.sync kernel's widest item
 };
 
 // The Markov chain's scratch: 64 words of barrier state, then three
@@ -115,7 +130,8 @@ constexpr int kAttnTc = 1;    // tcgen05 + TMA kernel (windows of 9 rows or more
 constexpr int kTcMinRows = 9;
 
 // Kernel of a stream: by its window rows, unless TF_ATTN_PATH forces one.
-int attn_path_of(int rows);
+// Windows over scaled pools all run on an mma.sync kernel (attn_scaled.cu).
+int attn_path_of(int rows, bool scaled = false);
 
 // segments.cu: TMA map of a bf16 [rows][256] matrix (the Markov head's W2),
 // boxes of 128 rows x 64 columns with 128-byte swizzle; rows past `rows` read
@@ -136,7 +152,8 @@ struct tf_segments {
     std::vector<tf::SegStream> streams;
     tf_plan plan{};
     bool prompt = false;               // built by tf_prompt_build (conv + attention only)
-    bool paged = false;                // built by tf_paged_build / tf_paged_prompt_build
+    bool paged = false;                // built by tf_paged_build / tf_paged_prompt_build or their scaled forms
+    bool scaled = false;               // built by tf_paged_scaled_build / tf_paged_scaled_prompt_build
     int device = 0;                    // current device of the build
     size_t scratch_off = 0;            // the blob's cross-CTA scratch and status word:
     size_t scratch_bytes = 0;          // zero in the image, zeroed again by tf_segments_status

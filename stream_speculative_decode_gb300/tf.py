@@ -23,6 +23,9 @@ TF_MAX_STREAMS = 65536
 TF_MAX_PROMPT_ROWS = 65536
 TF_PROMPT_WINDOW_ROWS = 32
 TF_MK = 256
+TF_SCALE_KEYS, TF_SCALE_COLUMNS = 16, 32
+TF_NORM_MAX_WIDTH = 1 << 14
+TF_LINEAR_MAX_ROWS, TF_LINEAR_MAX_INPUTS, TF_LINEAR_MAX_OUTPUTS = 1 << 20, 1 << 20, 1 << 24
 TF_MIN_PAGE_KEYS, TF_MAX_PAGE_KEYS = 16, 256
 TF_MAX_PAGES, TF_MAX_PAGE_IDS = 1 << 24, 1 << 28
 TF_SAMPLE_MAX_VOCAB = 1 << 19
@@ -40,7 +43,8 @@ EXPORTS = ("tf_chunk_keys", "tf_segments_plan", "tf_segments_build", "tf_segment
            "tf_argmax_rows", "tf_accept", "tf_markov_chain", "tf_draft_ids", "tf_prompt_build",
            "tf_strerror", "tf_last_cuda_error", "tf_set_wait_limit_ns", "tf_wait_limit_ns",
            "tf_segments_status", "tf_paged_build", "tf_paged_prompt_build", "tf_attn_paged",
-           "tf_qk_rows", "tf_pages_copy", "tf_sample_rows")
+           "tf_qk_rows", "tf_pages_copy", "tf_sample_rows", "tf_paged_scaled_build",
+           "tf_paged_scaled_prompt_build", "tf_pages_copy_scaled", "tf_norm_rows", "tf_linear_rows")
 TF_STATIC_SCRATCH_BYTES = 16 << 20
 
 
@@ -95,6 +99,14 @@ def _load():
                                  P(vp), P(vp), i32, i32, vp, P(vp)]),
         "tf_paged_prompt_build": (i32, [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, P(vp), vp,
                                         ctypes.c_int32, ctypes.c_int32, P(vp), P(vp), i32, i32, vp, P(vp)]),
+        "tf_paged_scaled_build": (i32, [P(tf_stream), i32, P(vp), P(vp), vp, ctypes.c_int32, ctypes.c_int32,
+                                        P(vp), P(vp), P(vp), P(vp), i32, i32, vp, P(vp)]),
+        "tf_paged_scaled_prompt_build": (i32, [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, P(vp), vp,
+                                               ctypes.c_int32, ctypes.c_int32, P(vp), P(vp), P(vp), P(vp), i32, i32,
+                                               vp, P(vp)]),
+        "tf_pages_copy_scaled": (i32, [P(vp), P(vp), i32, ctypes.c_int32, ctypes.c_int32, vp, vp, vp, i32, vp]),
+        "tf_norm_rows": (i32, [vp, i64, vp, i64, vp, ctypes.c_float, i32, i32, vp, i64, vp, vp, vp]),
+        "tf_linear_rows": (i32, [vp, i64, vp, i32, i32, vp, vp, vp, i32, vp, i64, vp]),
         "tf_attn_paged": (i32, [vp, i32, vp, vp, vp, i32, vp]),
         "tf_qk_rows": (i32, [vp, i32, vp, i64, vp, i64, vp, i64, vp, vp, ctypes.c_float, ctypes.c_double, vp, vp]),
         "tf_pages_copy": (i32, [P(vp), i32, ctypes.c_int32, ctypes.c_int32, vp, vp, vp, i32, vp]),
@@ -321,6 +333,51 @@ def tf_paged_prompt_build(rows, keys, kv_capacity, conv_state, pages, page_keys,
     return Segments(handle)
 
 
+def tf_paged_scaled_build_status(streams, conv_state, conv_hist, pages, page_keys, n_pages, k_pool, v_pool, k_scale,
+                                 v_scale, n_conv, n_attn, stream=None):
+    """Raw status and handle of tf_paged_scaled_build; the arguments are
+    tf_paged_build_status's, ``k_scale``/``v_scale``: a pool of scale bytes a layer."""
+    out = ctypes.c_void_p()
+    n = sum(st[3] // page_keys for st in streams) if page_keys > 0 else 0
+    at, _keep = _int32_array(pages, n, table=True)
+    rc = _lib.tf_paged_scaled_build(_streams_array(streams), len(streams), _ptr_array(conv_state),
+                                    _ptr_array(conv_hist), at, page_keys, n_pages, _ptr_array(k_pool),
+                                    _ptr_array(v_pool), _ptr_array(k_scale), _ptr_array(v_scale), n_conv, n_attn,
+                                    _stream(stream), ctypes.byref(out))
+    return rc, out.value
+
+
+def tf_paged_scaled_build(streams, conv_state, conv_hist, pages, page_keys, n_pages, k_pool, v_pool, k_scale, v_scale,
+                          n_conv, n_attn, stream=None):
+    """A verify table whose streams keep their keys as 8-bit codes in pages of
+    shared pools, with a scale for each TF_SCALE_KEYS keys of a head."""
+    rc, handle = tf_paged_scaled_build_status(streams, conv_state, conv_hist, pages, page_keys, n_pages, k_pool,
+                                              v_pool, k_scale, v_scale, n_conv, n_attn, stream)
+    _check("tf_paged_scaled_build", rc)
+    return Segments(handle)
+
+
+def tf_paged_scaled_prompt_build_status(rows, keys, kv_capacity, conv_state, pages, page_keys, n_pages, k_pool, v_pool,
+                                        k_scale, v_scale, n_conv, n_attn, stream=None):
+    """Raw status and handle of tf_paged_scaled_prompt_build."""
+    out = ctypes.c_void_p()
+    n = kv_capacity // page_keys if page_keys > 0 else 0
+    at, _keep = _int32_array(pages, n, table=True)
+    rc = _lib.tf_paged_scaled_prompt_build(rows, keys, kv_capacity, _ptr_array(conv_state), at, page_keys, n_pages,
+                                           _ptr_array(k_pool), _ptr_array(v_pool), _ptr_array(k_scale),
+                                           _ptr_array(v_scale), n_conv, n_attn, _stream(stream), ctypes.byref(out))
+    return rc, out.value
+
+
+def tf_paged_scaled_prompt_build(rows, keys, kv_capacity, conv_state, pages, page_keys, n_pages, k_pool, v_pool,
+                                 k_scale, v_scale, n_conv, n_attn, stream=None):
+    """A prompt call's table over the scaled pages of one stream."""
+    rc, handle = tf_paged_scaled_prompt_build_status(rows, keys, kv_capacity, conv_state, pages, page_keys, n_pages,
+                                                     k_pool, v_pool, k_scale, v_scale, n_conv, n_attn, stream)
+    _check("tf_paged_scaled_prompt_build", rc)
+    return Segments(handle)
+
+
 def tf_segments_free(seg):
     seg.free()
 
@@ -384,6 +441,16 @@ def tf_pages_copy(pools, page_keys, n_pages, src, dst, keys=None, stream=None):
                                                _stream(stream)))
 
 
+def tf_pages_copy_scaled(pools, scales, page_keys, n_pages, src, dst, keys=None, stream=None):
+    """tf_pages_copy for scaled pools: codes, and the scales of the blocks that hold them."""
+    n = len(src)
+    if len(scales) != len(pools):
+        raise ValueError(f"{len(scales)} pools of scales for {len(pools)} pools")
+    (s, _s), (d, _d), (k, _k) = _int32_array(src, n), _int32_array(dst, n), _int32_array(keys, n)
+    _check("tf_pages_copy_scaled", _lib.tf_pages_copy_scaled(_ptr_array(pools), _ptr_array(scales), len(pools),
+                                                             page_keys, n_pages, s, d, k, n, _stream(stream)))
+
+
 def tf_qk_rows(seg, attn_layer, q, q_stride, k, k_stride, v, v_stride, q_norm, k_norm, eps, theta, q_out, stream=None):
     """Norm and rotation of one layer's queries and keys, and the append of its
     keys and values to the table's caches."""
@@ -415,6 +482,19 @@ def tf_sample_rows(logits, R, V, row_stride, temperature, top_k, top_p, min_p, u
     _check("tf_sample_rows", _lib.tf_sample_rows(_ptr(logits), R, V, row_stride, _ptr(temperature), _ptr(top_k),
                                                  _ptr(top_p), _ptr(min_p), _ptr(u), _ptr(pick), _ptr(prob), _ptr(flag),
                                                  _stream(stream)))
+
+
+def tf_norm_rows(x, x_stride, res, res_stride, w, eps, R, width, sum, sum_stride, codes, scales, stream=None):
+    """Residual addition, RMS norm and 8-bit coding of each row; ``res`` and ``sum``
+    may both be None (a norm alone)."""
+    _check("tf_norm_rows", _lib.tf_norm_rows(_ptr(x), x_stride, _ptr(res), res_stride, _ptr(w), eps, R, width,
+                                             _ptr(sum), sum_stride, _ptr(codes), _ptr(scales), _stream(stream)))
+
+
+def tf_linear_rows(x, x_stride, x_scales, R, K, w, w_scales, s, N, y, y_stride, stream=None):
+    """Rows (bf16, or 8-bit codes with ``x_scales``) times a matrix of 4-bit weights."""
+    _check("tf_linear_rows", _lib.tf_linear_rows(_ptr(x), x_stride, _ptr(x_scales), R, K, _ptr(w), _ptr(w_scales),
+                                                 _ptr(s), N, _ptr(y), y_stride, _stream(stream)))
 
 
 def tf_accept(seg, ids, pick, flag, vocab, accept_len, next_token, new_keys, sflag, rewind_conv=True,

@@ -1,0 +1,210 @@
+"""Attention over scaled pools against float64 on the codes' values; the bounds are
+derived in scaled.check_attention. Slots past a stream's keys and spare pages hold
+NaN codes and the largest scale."""
+
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+PAGES = [16, 32, 64, 128, 256]
+
+
+@pytest.fixture(scope="module")
+def tf():
+    import __graft_entry__
+    __graft_entry__.build()
+    from stream_speculative_decode_gb300 import tf
+    torch.cuda.set_device(0)
+    return tf
+
+
+# rows of every tile width; keys of one, around a block's, a stage's and a page's end, of several chunks
+STREAMS = [(1, 1), (1, 17), (2, 64), (8, 65), (9, 31), (16, 16), (5, 1025), (12, 4700), (16, 8193), (1, 3001),
+           (3, 257), (7, 2049), (6, 32)]
+
+
+def bits(x):
+    return x.view(torch.int16)
+
+
+@pytest.mark.parametrize("page", PAGES)
+@pytest.mark.parametrize("full", [False, True])
+def test_small_rounds(tf, page, full):
+    from scaled import ScaledAttn
+    a = ScaledAttn(tf, STREAMS, page, seed=page)
+    a.run(full)
+    a.check(full)
+    assert tf.tf_segments_status(a.seg) == (tf.TF_OK, 0)
+
+
+@pytest.mark.parametrize("rows", [1, 2, 3, 4, 5, 6, 7, 8, 9, 15, 16])
+def test_rows_of_a_window(tf, rows):
+    """Tables whose widest window has these rows (one kernel variant each)."""
+    from scaled import ScaledAttn
+    a = ScaledAttn(tf, [(rows, max(rows, k)) for k in (rows, 16, 33, 700, 2500)], 32, seed=rows)
+    a.run()
+    a.check(what=rows)
+
+
+@pytest.mark.parametrize("page", PAGES)
+@pytest.mark.parametrize("rows,cached", [(1, 0), (33, 7), (300, 1700), (64, 8200)])
+def test_prompt(tf, page, rows, cached):
+    from scaled import ScaledAttn
+    a = ScaledAttn(tf, [(rows, rows + cached)], page, seed=rows, prompt=True)
+    a.run()
+    a.check()
+
+
+@pytest.mark.parametrize("std", [1e-30, 2e-5, 300.0, 1e30])
+def test_v_of_any_size(tf, std):
+    """Scores and outputs far from 1: K of that size with queries of its inverse, V of that size."""
+    from scaled import ScaledAttn
+    a = ScaledAttn(tf, [(16, 2100), (1, 1500), (4, 40)], 64, seed=3, std=std, spread=6.0)
+    a.q[0] = (a.q[0].float() / std).to(torch.bfloat16)
+    a.run()
+    a.check(what=std)
+
+
+def test_blocks_of_very_different_size(tf):
+    """V blocks up to 2^40 apart; the weights sit on small and on large ones."""
+    from scaled import ScaledAttn
+    a = ScaledAttn(tf, [(1, 900), (8, 1400), (16, 3000)], 16, seed=4, spread=0.0)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    used = a.vs[0] != 0xFE
+    shift = torch.randint(-40, 1, a.vs[0].shape, generator=g, device="cuda", dtype=torch.int32)
+    a.vs[0][:] = torch.where(used, (a.vs[0].int() + shift).clamp(0, 254).to(torch.uint8), a.vs[0])
+    a.q[0] *= 6           # few keys carry a row
+    a.run()
+    a.check()
+
+
+@pytest.mark.parametrize("factor", [0.0, 2.0 ** -120, 2.0 ** 100])
+def test_queries_of_any_size(tf, factor):
+    from scaled import ScaledAttn
+    a = ScaledAttn(tf, [(2, 400), (1, 30)], 16, seed=5)
+    a.q[0] = (a.q[0].double() * factor).to(torch.bfloat16)
+    for s in a.ks:
+        s[:] = torch.where(s == 0xFE, s, (s.int() - (100 if factor > 1 else 0)).clamp(min=0).to(torch.uint8))
+    a.run()
+    a.check(what=factor)
+
+
+def test_nan_stays_with_the_rows_that_see_it(tf):
+    """NaN codes of K and V at the window's own keys, and deep in the cache, over one and several chunks."""
+    from scaled import ScaledAttn
+    for keys in (40, 1500, 9000):
+        clean = ScaledAttn(tf, [(16, keys), (6, keys), (1, keys)], 32, seed=6)
+        clean.run()
+        for pool in ("K", "V"):
+            a = ScaledAttn(tf, [(16, keys), (6, keys), (1, keys)], 32, seed=6)
+            seen = []
+            for (r, o, k), ids, at in zip(a.streams, a.lists, (keys - 11, keys - 2, 3)):
+                getattr(a, pool)[0][int(ids[at // 32]), 2, at % 32, 5] = 0x7F     # head 2, dimension 5
+                seen.append(at)
+            a.run()
+            for (r, o, k), at in zip(a.streams, seen):
+                for i in range(r):
+                    hit = at < k - r + i + 1
+                    got, want = a.out[0][o + i].clone(), clean.out[0][o + i].clone()
+                    if hit:
+                        head = got[8:12] if pool == "K" else got[8:12, 5]
+                        assert torch.isnan(head).all(), (pool, keys, r, i)
+                        head.zero_()
+                        (want[8:12] if pool == "K" else want[8:12, 5]).zero_()
+                    assert torch.equal(bits(got), bits(want)), (pool, keys, r, i)
+
+
+def test_nan_queries(tf):
+    """A NaN or an infinity in a query's head stays in that head's row."""
+    from scaled import ScaledAttn
+    a = ScaledAttn(tf, [(4, 3000), (16, 90)], 64, seed=7)
+    want = a.run()[0].clone()
+    a.q[0][1, 6, 3] = float("nan")
+    a.q[0][9, 31, 63] = float("inf")
+    got = a.run()[0]
+    for r, h in ((1, 6), (9, 31)):
+        assert torch.isnan(got[r, h]).all()
+        got[r, h] = want[r, h]
+    assert torch.equal(bits(got), bits(want))
+
+
+def test_result_is_the_streams_own(tf):
+    """A stream's bits depend neither on its pages nor on the other streams of its width's kernel."""
+    from scaled import ScaledAttn
+    a = ScaledAttn(tf, [(5, 2000), (6, 5000)], 16, seed=8)
+    a.run()
+    g = np.random.default_rng(1)
+    move = torch.as_tensor(g.permutation(a.n_pages), device="cuda")
+    b = ScaledAttn(tf, [(5, 2000), (6, 5000)], 16, seed=8)
+    for x, y in ((a.K, b.K), (a.V, b.V), (a.ks, b.ks), (a.vs, b.vs)):
+        y[0][move] = x[0]
+    b.lists = [move[torch.as_tensor(l.astype(np.int64), device="cuda")].cpu().numpy().astype(np.int32) for l in a.lists]
+    b.build()
+    b.run()
+    assert torch.equal(bits(a.out[0]), bits(b.out[0]))
+
+
+def test_pool_beyond_32_bits(tf):
+    """Pages past 4 GB of codes."""
+    from scaled import ScaledAttn
+    page, n_pages = 256, (1 << 15) + 100           # 128 KB a page
+    ids = [np.arange(n_pages - 3, n_pages, dtype=np.int32), np.array([5, n_pages - 9, n_pages - 20, 16390], np.int32)]
+    small = ScaledAttn(tf, [(1, 600), (16, 900)], page, seed=9)
+    want = small.run()[0]
+    a = small
+    pools = []
+    for x in (a.K, a.V, a.ks, a.vs):
+        big = torch.zeros((n_pages,) + x[0].shape[1:], dtype=torch.uint8, device="cuda")
+        for far, near in zip(ids, a.lists):
+            big[torch.as_tensor(far.astype(np.int64), device="cuda")] = x[0][torch.as_tensor(near.astype(np.int64), device="cuda")]
+        pools.append([big])
+    table = [(r, o, k, len(x) * page) for (r, o, k), x in zip(a.streams, ids)]
+    seg = tf.tf_paged_scaled_build(table, None, None, np.concatenate(ids), page, n_pages, *pools, 0, 1)
+    out = torch.empty_like(want)
+    tf.tf_attn_paged(seg, 0, a.q[0], a.partials, out)
+    assert torch.equal(bits(out), bits(want))
+
+
+def test_captured_and_replayed(tf):
+    """Two layers in a graph on a side stream, replayed on changed queries."""
+    from scaled import ScaledAttn
+    p = ScaledAttn(tf, [(1, 900), (9, 70), (16, 8300), (3, 2050)], 64, seed=10, layers=2)
+    want = [x.clone() for x in p.run()]
+    s, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s), torch.cuda.graph(g, stream=s):
+        p.run(stream=torch.cuda.current_stream())
+    torch.cuda.current_stream().wait_stream(s)
+    for o in p.out:
+        o.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(p.out, want):
+        assert torch.equal(bits(a), bits(b))
+    p.q[0].copy_(p.q[1])
+    g.replay()
+    p.check()
+
+
+def test_refusals(tf):
+    from scaled import ScaledAttn
+    a = ScaledAttn(tf, [(2, 40)], 16, seed=11)
+    out32 = torch.empty((a.R, 32, 64), device="cuda")
+
+    def status(fn, *args):
+        with pytest.raises(tf.TFError) as e:
+            fn(*args)
+        return e.value.status
+
+    for fn in (tf.tf_attn, tf.tf_attn_block):
+        assert status(fn, a.seg, 0, a.q[0], a.partials, out32) == tf.TF_EINVAL
+    assert status(tf.tf_attn_partials, a.seg, 0, a.q[0], a.partials) == tf.TF_EINVAL
+    assert status(tf.tf_attn_merge, a.seg, a.partials, out32) == tf.TF_EINVAL
+    assert status(tf.tf_attn_static, a.seg, 0, a.q[0], out32) == tf.TF_EINVAL
+    for layer in (-1, 1):
+        assert status(tf.tf_attn_paged, a.seg, layer, a.q[0], a.partials, a.out[0]) == tf.TF_EINVAL
+    assert status(tf.tf_attn_paged, a.seg, 0, a.q[0], a.partials, a.q[0]) == tf.TF_EINVAL
+    assert status(tf.tf_attn_paged, a.seg, 0, a.q[0], a.partials, a.out[0].data_ptr() + 2) == tf.TF_EINVAL
+    assert status(tf.tf_attn_paged, a.seg, 0, None, a.partials, a.out[0]) == tf.TF_EINVAL
