@@ -8,10 +8,10 @@
 // times its power of two at most 4: both are exact in bf16, so the products run
 // on bf16 MMAs with fp32 sums and nothing is rounded before the store.
 //
-// HBM bound for few rows: 17/32 bytes a weight, whatever their number. mma.sync
-// m16n8k16 with 16 outputs by 8 rows a tile: the weights are the operand whose
-// fragments come straight from memory, 32 codes of one row and scale (16 bytes)
-// a lane, four lanes a row's 128 inputs; the order of the inputs in an MMA is
+// For few rows 17/32 bytes a weight have to be read, whatever the rows' number.
+// mma.sync m16n8k16 with 16 outputs by 8 rows a tile: the weights are the operand
+// whose fragments come straight from memory, 32 codes of one row and scale (16
+// bytes) a lane, four lanes a row's 128 inputs; the order of the inputs in an MMA is
 // free as long as x has the same. A nibble becomes 128 + c in bf16 by masks
 // (0x4300 | c), and one bf16 FMA (128 + c) * g - 136 * g gives the weight.
 //
@@ -20,6 +20,13 @@
 // chunk side by side), staged once a CTA where it fits. One CTA of 16 warps an
 // SM. For few outputs, S warps share a 16-output tile, each with its part of the
 // inputs, and their sums are added in order through shared memory.
+//
+// Measured, 128,000 outputs by 2,048 inputs (139 MB): 1 row 37.1 us, 16 rows 45.8
+// us (3.8 and 3.1 TB/s; the same loads alone 21.5 us). What bounds it is the
+// ALU: 56 of a chunk's 144 instructions take its codes apart, at half rate.
+// Loads a chunk at a time into a ring in shared memory (47 and 80 us), into the
+// registers just used (48.5 and 56) or with the scales' codes picked apart as they
+// arrive (44 and 51) were slower: a set of registers ahead hides the memory.
 #include <cuda_bf16.h>
 
 #include "scaled.cuh"
@@ -31,8 +38,7 @@ constexpr int kWarps = 16;
 constexpr int kThreads = kWarps * 32;
 constexpr int kChunk = 128;                 // inputs of a chunk: four groups, one a lane of a row
 constexpr int kGroup = TF_SCALE_COLUMNS;
-constexpr int kQuad = 4;                    // chunks whose loads are in flight together
-constexpr int kMaxX = 160 << 10;            // shared memory for x
+constexpr int kPair = 2;                    // chunks whose loads are in flight together (linear_rows_kernel)
 
 struct Linear {
     const uint8_t* x;          // bf16 or codes
@@ -45,7 +51,8 @@ struct Linear {
     int R, K, N;
     int row_tiles;             // CTAs side by side that share the weights' tiles
     int slab;                  // chunks of x in shared memory at a time
-    int words;                 // the scales of a chunk are an aligned word
+    uint32_t nibbles;          // 0x000F000F: as a value that the compiler does not know it stays in a register, and
+                               // masking and setting the exponent are one instruction (two constants make it two)
 };
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -57,6 +64,11 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
 __device__ __forceinline__ uint32_t fma_bf2(uint32_t a, uint32_t b, uint32_t c) {
     uint32_t d;
     asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+__device__ __forceinline__ uint32_t mul_bf2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
 }
 __device__ __forceinline__ uint32_t pack_bf2(float a, float b) {
@@ -105,140 +117,279 @@ __device__ __forceinline__ void stage(const Linear& a, int r0, int c0, int n, un
     }
 }
 
-// A lane's weights of up to four chunks of its two outputs, and their scales' bytes.
+// A lane's weights of one chunk of its two outputs, and the scales (kWords: the
+// chunk's four codes of an output as a word; otherwise the lane's own code).
 struct Piece {
-    uint4 w[kQuad][2];
-    uint32_t g[kQuad];   // the code of output g8 in the low byte, of 8 + g8 in the next
+    uint4 w[2];
+    uint32_t g[2];
 };
 
-__device__ __forceinline__ void load_piece(const Linear& a, int64_t n0, int64_t n1, int c, int end, int t4, Piece& p) {
-    const int groups = a.K / kGroup;
+// Where a warp's lanes read: the rows of its tile's outputs.
+struct Rows2 {
+    const uint8_t* w[2];   // + 64 bytes a chunk
+    const uint8_t* g[2];   // + 4 codes a chunk
+};
+__device__ __forceinline__ Rows2 rows_of(const Linear& a, int tile, int g8, int t4) {
+    Rows2 r;
 #pragma unroll
-    for (int j = 0; j < kQuad; ++j) {
-        const int grp = (c + j) * 4 + t4;
-        p.w[j][0] = p.w[j][1] = make_uint4(0u, 0u, 0u, 0u);
-        p.g[j] = 0;   // scale 0: no weight
-        if (c + j < end && grp < groups) {
-            p.w[j][0] = load_once(a.w + n0 * (a.K / 2) + grp * 16);
-            p.w[j][1] = load_once(a.w + n1 * (a.K / 2) + grp * 16);
-            if (a.words) {
-                const uint32_t u = __ldg(reinterpret_cast<const uint32_t*>(a.g + n0 * groups) + c + j);
-                const uint32_t v = __ldg(reinterpret_cast<const uint32_t*>(a.g + n1 * groups) + c + j);
-                p.g[j] = __byte_perm(u, v, uint32_t(t4 | (4 + t4) << 4));
-            } else {
-                p.g[j] = uint32_t(__ldg(a.g + n0 * groups + grp)) | uint32_t(__ldg(a.g + n1 * groups + grp)) << 8;
-            }
+    for (int i = 0; i < 2; ++i) {   // outputs past N read the last one's weights and are not stored
+        const int64_t n = min(tile * 16 + 8 * i + g8, a.N - 1);
+        r.w[i] = a.w + n * (a.K / 2) + t4 * 16;
+        r.g[i] = a.g + n * (a.K / kGroup);
+    }
+    return r;
+}
+template <bool kWords>
+__device__ __forceinline__ void load_piece(const Linear& a, const Rows2& r, int c, int t4, Piece& p) {
+    if (!kWords && c * 4 + t4 >= a.K / kGroup) {   // the last chunk's missing groups: scale 0
+        p.w[0] = p.w[1] = make_uint4(0u, 0u, 0u, 0u);
+        p.g[0] = p.g[1] = 0u;
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        p.w[i] = load_once(r.w[i] + int64_t(c) * 64);
+        // (volatile: the compiler would move a plain load to its use)
+        if constexpr (kWords)
+            asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(p.g[i]) : "l"(r.g[i] + c * 4));
+        else
+            asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(p.g[i]) : "l"(r.g[i] + c * 4 + t4));
+    }
+}
+
+// One chunk's products: a lane's codes and scales of two outputs times x's fragments
+// at xr (+ nt * 8 rows). Even and odd MMAs have accumulators of their own, so that
+// they need not wait for one another.
+template <int NT, bool kWords>
+__device__ __forceinline__ void multiply(const Piece& p, const unsigned char* xr, int rowb, uint32_t sel, uint32_t nibbles,
+                                         float (&acc)[NT][2][4]) {
+    const float2 g = h2_to_f2(e4m3_low(__byte_perm(p.g[0], p.g[1], sel)));
+    const uint32_t s0 = pack_bf2(g.x, g.x), s1 = pack_bf2(g.y, g.y);
+    const uint32_t z0 = mul_bf2(s0, 0xC308C308u), z1 = mul_bf2(s1, 0xC308C308u);   // -136
+    const uint32_t w0[4] = {p.w[0].x, p.w[0].y, p.w[0].z, p.w[0].w};
+    const uint32_t w1[4] = {p.w[1].x, p.w[1].y, p.w[1].z, p.w[1].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        uint4 b[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) b[nt] = *reinterpret_cast<const uint4*>(xr + nt * 8 * rowb + k * 64);
+        auto weights = [&](uint32_t w, int i, uint32_t s, uint32_t z) {
+            return fma_bf2(((w >> (4 * i)) & nibbles) | 0x43004300u, s, z);
+        };
+        const uint32_t lo[4] = {weights(w0[k], 0, s0, z0), weights(w1[k], 0, s1, z1), weights(w0[k], 1, s0, z0),
+                                weights(w1[k], 1, s1, z1)};
+        const uint32_t hi[4] = {weights(w0[k], 2, s0, z0), weights(w1[k], 2, s1, z1), weights(w0[k], 3, s0, z0),
+                                weights(w1[k], 3, s1, z1)};
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            mma_bf16(acc[nt][0], lo, b[nt].x, b[nt].y);
+            mma_bf16(acc[nt][1], hi, b[nt].z, b[nt].w);
         }
     }
 }
 
-// Row tiles of 8 NT rows; S warps share an output tile.
+// The S warps of a group (named barriers 1..) meet.
+__device__ __forceinline__ void group_sync(int group, int S) {
+    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(S * 32) : "memory");
+}
+
+// A tile's end: the parts' sums added in order, scaled and stored.
 template <int NT>
-__global__ void __launch_bounds__(kThreads, 1)
-linear_rows_kernel(const __grid_constant__ Linear a, int S) {
-    extern __shared__ __align__(128) unsigned char smem[];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g8 = lane >> 2, t4 = lane & 3;
-    const int r0 = (blockIdx.x % a.row_tiles) * 8 * NT;
-    const int cta = blockIdx.x / a.row_tiles, ctas = gridDim.x / a.row_tiles;
-    const int chunks = (a.K + kChunk - 1) / kChunk, rowb = row_bytes(min(a.slab, chunks));
-    unsigned char* const sx = smem;
-    float4* const sums = reinterpret_cast<float4*>(smem + 8 * NT * rowb);   // [warp][NT][lane], when S > 1
-    const int per_cta = kWarps / S, part = warp % S, tiles = (a.N + 15) / 16;
-    const bool one_slab = a.slab >= chunks;
-    pdl_wait();
-    if (one_slab) {
-        stage<NT>(a, r0, 0, chunks, sx, rowb);
-        __syncthreads();
-    }
-    for (int first = cta * per_cta; first < tiles; first += ctas * per_cta) {
-        const int tile = first + warp / S;
-        // outputs past N read the last one's weights and are not stored
-        const int64_t n0 = min(tile * 16 + g8, a.N - 1), n1 = min(tile * 16 + 8 + g8, a.N - 1);
-        float acc[NT][4];
+__device__ __forceinline__ void finish_tile(const Linear& a, int S, int tile, int tiles, int r0, int group, int part,
+                                            const float (&acc)[NT][2][4], float4* sums) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g8 = lane >> 2, t4 = lane & 3;
+    auto total = [](const float (&v)[2][4]) {
+        return make_float4(v[0][0] + v[1][0], v[0][1] + v[1][1], v[0][2] + v[1][2], v[0][3] + v[1][3]);
+    };
+    auto store = [&](int nt, const float4& v) {
+        const int n = tile * 16 + g8, r = r0 + nt * 8 + 2 * t4;
+        const float d[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
-        for (int c0 = 0; c0 < chunks; c0 += a.slab) {
-            const int n = min(a.slab, chunks - c0);
-            if (!one_slab) {
-                __syncthreads();
-                stage<NT>(a, r0, c0, n, sx, rowb);
-                __syncthreads();
-            }
-            const int begin = c0 + n * part / S, end = c0 + n * (part + 1) / S;
-            if (tile >= tiles) continue;
-            Piece now, next;
-            load_piece(a, n0, n1, begin, end, t4, now);
-            for (int c = begin; c < end; c += kQuad) {
-                load_piece(a, n0, n1, c + kQuad, end, t4, next);
-#pragma unroll
-                for (int j = 0; j < kQuad; ++j) {
-                    if (c + j >= end) break;
-                    const float2 g = h2_to_f2(e4m3_low(now.g[j]));
-                    const uint32_t s0 = pack_bf2(g.x, g.x), s1 = pack_bf2(g.y, g.y);
-                    const uint32_t z0 = pack_bf2(-136.f * g.x, -136.f * g.x), z1 = pack_bf2(-136.f * g.y, -136.f * g.y);
-                    const uint32_t w0[4] = {now.w[j][0].x, now.w[j][0].y, now.w[j][0].z, now.w[j][0].w};
-                    const uint32_t w1[4] = {now.w[j][1].x, now.w[j][1].y, now.w[j][1].z, now.w[j][1].w};
-                    const unsigned char* xr = sx + g8 * rowb + (c + j - c0) * 256 + t4 * 16;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        uint4 b[NT];
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            b[nt] = *reinterpret_cast<const uint4*>(xr + nt * 8 * rowb + k * 64);
-                        auto weights = [&](uint32_t w, int i, uint32_t s, uint32_t z) {
-                            return fma_bf2(((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u, s, z);
-                        };
-                        const uint32_t lo[4] = {weights(w0[k], 0, s0, z0), weights(w1[k], 0, s1, z1),
-                                                weights(w0[k], 1, s0, z0), weights(w1[k], 1, s1, z1)};
-                        const uint32_t hi[4] = {weights(w0[k], 2, s0, z0), weights(w1[k], 2, s1, z1),
-                                                weights(w0[k], 3, s0, z0), weights(w1[k], 3, s1, z1)};
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            mma_bf16(acc[nt], lo, b[nt].x, b[nt].y);
-                            mma_bf16(acc[nt], hi, b[nt].z, b[nt].w);
-                        }
-                    }
-                }
-                now = next;
+        for (int e = 0; e < 4; ++e) {
+            const int nn = n + 8 * (e >> 1), rr = r + (e & 1);
+            if (nn < a.N && rr < a.R) {
+                const __nv_bfloat16 b = __float2bfloat16_rn(d[e] * __ldg(a.s + nn));
+                a.y[int64_t(rr) * a.y_stride + nn] = *reinterpret_cast<const uint16_t*>(&b);
             }
         }
-        auto store = [&](int tl, int nt, int ln, const float4& v) {
-            const int n = tl * 16 + (ln >> 2), r = r0 + nt * 8 + 2 * (ln & 3);
-            const float d[4] = {v.x, v.y, v.z, v.w};
+    };
+    if (S == 1) {
+        if (tile < tiles)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int nn = n + 8 * (e >> 1), rr = r + (e & 1);
-                if (nn < a.N && rr < a.R) {
-                    const __nv_bfloat16 b = __float2bfloat16_rn(d[e] * __ldg(a.s + nn));
-                    a.y[int64_t(rr) * a.y_stride + nn] = *reinterpret_cast<const uint16_t*>(&b);
-                }
-            }
-        };
-        if (S == 1) {
-            if (tile < tiles)
+            for (int nt = 0; nt < NT; ++nt) store(nt, total(acc[nt]));
+    } else {
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    store(tile, nt, lane, make_float4(acc[nt][0], acc[nt][1], acc[nt][2], acc[nt][3]));
-        } else {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-                sums[(warp * NT + nt) * 32 + lane] = make_float4(acc[nt][0], acc[nt][1], acc[nt][2], acc[nt][3]);
-            __syncthreads();
-            for (int i = tid; i < per_cta * NT * 32; i += kThreads) {
-                const int tl = i / (NT * 32), at = i % (NT * 32);
-                if (first + tl >= tiles) continue;
-                float4 v = sums[tl * S * NT * 32 + at];
+        for (int nt = 0; nt < NT; ++nt)
+            sums[(warp * NT + nt) * 32 + lane] = total(acc[nt]);
+        group_sync(group, S);
+        if (tile < tiles)
+            for (int nt = part; nt < NT; nt += S) {   // the parts' sums in order
+                float4 v = sums[(group * S * NT + nt) * 32 + lane];
                 for (int p = 1; p < S; ++p) {
-                    const float4 u = sums[(tl * S + p) * NT * 32 + at];
+                    const float4 u = sums[((group * S + p) * NT + nt) * 32 + lane];
                     v.x += u.x;
                     v.y += u.y;
                     v.z += u.z;
                     v.w += u.w;
                 }
-                store(first + tl, at / 32, at % 32, v);
+                store(nt, v);
             }
-            __syncthreads();
+        group_sync(group, S);
+    }
+}
+
+// The same for whole steps: a warp's part of a tile is a number of steps of U chunks
+// (kWords, x in one slab). Two sets of registers take turns, one being multiplied
+// while the other's loads, up to the next tile's first, are on their way.
+template <int NT, int U>
+__global__ void __launch_bounds__(kThreads, 1)
+linear_steps_kernel(const __grid_constant__ Linear a, int S) {
+    extern __shared__ __align__(128) unsigned char smem[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g8 = lane >> 2, t4 = lane & 3;
+    const int r0 = (blockIdx.x % a.row_tiles) * 8 * NT;
+    const int per_cta = kWarps / S, group = warp / S, part = warp % S;
+    const int first = (blockIdx.x / a.row_tiles) * per_cta + group, step = gridDim.x / a.row_tiles * per_cta;
+    const int tiles = (a.N + 15) / 16, chunks = a.K / kChunk, mine = chunks / S, rowb = row_bytes(chunks);
+    float4* const sums = reinterpret_cast<float4*>(smem + 8 * NT * rowb);
+    const unsigned char* const x0 = smem + g8 * rowb + t4 * 16 + part * mine * 256;
+    const uint32_t sel = uint32_t(t4 | (4 + t4) << 4);
+    struct Set {
+        Piece p[U];
+    };
+    int ahead = first, left = mine;   // the tile that is being loaded, its chunks left
+    Rows2 rows = rows_of(a, min(first, tiles - 1), g8, t4);
+    auto skip_to_part = [&]() {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            rows.w[i] += int64_t(part) * mine * 64;
+            rows.g[i] += part * mine * 4;
         }
+    };
+    skip_to_part();
+    auto load = [&](Set& set) {
+        if (ahead >= tiles) return;
+#pragma unroll
+        for (int j = 0; j < U; ++j) load_piece<true>(a, rows, j, t4, set.p[j]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            rows.w[i] += U * 64;
+            rows.g[i] += U * 4;
+        }
+        if ((left -= U) == 0) {
+            ahead += step;
+            left = mine;
+            rows = rows_of(a, min(ahead, tiles - 1), g8, t4);
+            skip_to_part();
+        }
+    };
+    pdl_wait();
+    Set one, two;
+    load(one);
+    stage<NT>(a, r0, 0, chunks, smem, rowb);
+    __syncthreads();
+    int tile = first, done = 0;
+    float acc[NT][2][4] = {};
+    auto take = [&](const Set& set) {
+#pragma unroll
+        for (int j = 0; j < U; ++j) multiply<NT, true>(set.p[j], x0 + (done + j) * 256, rowb, sel, a.nibbles, acc);
+        if ((done += U) == mine) {
+            finish_tile<NT>(a, S, tile, tiles, r0, group, part, acc, sums);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) acc[nt][e >> 2][e & 3] = 0.f;
+            done = 0;
+            tile += step;
+        }
+    };
+    while (tile < tiles) {
+        load(two);
+        take(one);
+        if (tile >= tiles) break;
+        load(one);
+        take(two);
+    }
+    pdl_trigger();
+}
+
+// Row tiles of 8 NT rows; S warps share an output tile. Every warp goes through its
+// tiles, the slabs of x and its part of a slab's chunks, two chunks at a time, with
+// the next two's loads (those of its next tile among them) in flight.
+template <int NT, bool kWords>
+__global__ void __launch_bounds__(kThreads, 1)
+linear_rows_kernel(const __grid_constant__ Linear a, int S) {
+    extern __shared__ __align__(128) unsigned char smem[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g8 = lane >> 2, t4 = lane & 3;
+    const int r0 = (blockIdx.x % a.row_tiles) * 8 * NT;
+    const int per_cta = kWarps / S, group = warp / S, part = warp % S;
+    const int first = (blockIdx.x / a.row_tiles) * per_cta, step = gridDim.x / a.row_tiles * per_cta;
+    const int tiles = (a.N + 15) / 16, chunks = (a.K + kChunk - 1) / kChunk;
+    const int rowb = row_bytes(min(a.slab, chunks));
+    unsigned char* const sx = smem;
+    float4* const sums = reinterpret_cast<float4*>(smem + 8 * NT * rowb);   // [warp][NT][lane], when S > 1
+    const bool one_slab = a.slab >= chunks;
+
+    // this warp's chunks [c, end) of the slab at c0
+    struct Place {
+        int tile, c0, c, end;
+    };
+    auto enter = [&](int tile, int c0) {
+        const int n = min(a.slab, chunks - c0);
+        return Place{tile, c0, c0 + n * part / S, c0 + n * (part + 1) / S};
+    };
+    // the next chunks after p that are this warp's, tile >= tiles at the end
+    auto after = [&](Place p) {
+        p.c += kPair;
+        while (p.c >= p.end && p.tile < tiles) {
+            const int c0 = p.c0 + a.slab;
+            p = c0 < chunks ? enter(p.tile, c0) : enter(p.tile + step, 0);
+        }
+        return p;
+    };
+    pdl_wait();
+    Place at = enter(first + group, 0);
+    if (at.c >= at.end) at = after(at);
+    Rows2 rows = rows_of(a, at.tile, g8, t4);
+    Piece now[kPair], next[kPair];
+    auto load = [&](const Place& p, Piece (&piece)[kPair]) {
+        const int n = p.tile < tiles ? p.end - p.c : 0;
+#pragma unroll
+        for (int j = 0; j < kPair; ++j)
+            if (j < n) load_piece<kWords>(a, rows, p.c + j, t4, piece[j]);
+    };
+    load(at, now);
+    if (one_slab) {
+        stage<NT>(a, r0, 0, chunks, sx, rowb);
+        __syncthreads();
+    }
+    const uint32_t sel = kWords ? uint32_t(t4 | (4 + t4) << 4) : 0x40u;   // the lane's scale codes of two outputs
+    for (int base = first; base < tiles; base += step) {
+        const int tile = base + group;
+        float acc[NT][2][4] = {};
+        for (int c0 = 0; c0 < chunks; c0 += a.slab) {
+            if (!one_slab) {
+                __syncthreads();
+                stage<NT>(a, r0, c0, min(a.slab, chunks - c0), sx, rowb);
+                __syncthreads();
+            }
+            while (at.tile == tile && at.c0 == c0 && tile < tiles) {
+                const Place then = after(at);
+                if (then.tile != at.tile) rows = rows_of(a, then.tile, g8, t4);
+                load(then, next);
+                const int left = at.end - at.c;
+                const unsigned char* const xq = sx + g8 * rowb + (at.c - c0) * 256 + t4 * 16;
+#pragma unroll
+                for (int j = 0; j < kPair; ++j) {
+                    if (j < left) {
+                        multiply<NT, kWords>(now[j], xq + j * 256, rowb, sel, a.nibbles, acc);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < kPair; ++j) now[j] = next[j];
+                at = then;
+            }
+        }
+        finish_tile<NT>(a, S, tile, tiles, r0, group, part, acc, sums);
     }
     pdl_trigger();
 }
@@ -259,27 +410,41 @@ int split_of(int tiles, int chunks, int ctas) {
     return best;
 }
 
+constexpr int kMaxSmem = 227 << 10;
+constexpr int sum_bytes(int NT, int S) { return S > 1 ? kWarps * NT * 512 : 0; }
+
+// A launch of one of the kernels; `ready` remembers its shared memory's attribute by device.
+int launch_one(void (*kernel)(Linear, int), bool (&ready)[64], const Linear& a, int ctas, int S, int smem,
+               cudaStream_t stream) {
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= 64 || !ready[dev]) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+        if (e != cudaSuccess) return cuda_fail(e);
+        if (dev >= 0 && dev < 64) ready[dev] = true;
+    }
+    return launch_pdl(kernel, dim3(ctas * a.row_tiles), dim3(kThreads), smem, stream, a, S);
+}
+
 template <int NT>
 int launch(Linear a, cudaStream_t stream) {
+    constexpr int U = NT <= 2 ? 4 : 2;   // registers: two sets of 10 U, 8 NT sums
+    static bool ready[3][64] = {};
     const int chunks = (a.K + kChunk - 1) / kChunk, tiles = (a.N + 15) / 16, sms = sm_count();
     a.row_tiles = (a.R + 8 * NT - 1) / (8 * NT);
-    a.slab = (kMaxX / (8 * NT) - 64) / (kChunk * 2);
-    if (a.slab > chunks) a.slab = chunks;
     int ctas = sms / a.row_tiles;
     if (ctas < 1) ctas = 1;
     const int S = split_of(tiles, chunks, ctas), need = (tiles + kWarps / S - 1) / (kWarps / S);
     if (ctas > need) ctas = need;
-    const int smem = 8 * NT * row_bytes(a.slab) + (S > 1 ? kWarps * NT * 32 * 16 : 0);
-    static bool ready[64] = {};
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (dev < 0 || dev >= 64 || !ready[dev]) {
-        const cudaError_t e = cudaFuncSetAttribute(linear_rows_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   kMaxX + kWarps * NT * 32 * 16);
-        if (e != cudaSuccess) return cuda_fail(e);
-        if (dev >= 0 && dev < 64) ready[dev] = true;
-    }
-    return launch_pdl(linear_rows_kernel<NT>, dim3(ctas * a.row_tiles), dim3(kThreads), smem, stream, a, S);
+    a.slab = ((kMaxSmem - sum_bytes(NT, S)) / (8 * NT) - 64) / (kChunk * 2);
+    if (a.slab > chunks) a.slab = chunks;
+    a.nibbles = 0x000F000Fu;
+    const int smem = 8 * NT * row_bytes(a.slab) + sum_bytes(NT, S);
+    const bool words = a.K % kChunk == 0 && (reinterpret_cast<uintptr_t>(a.g) & 3u) == 0;
+    if (words && a.slab == chunks && chunks % (U * S) == 0)
+        return launch_one(linear_steps_kernel<NT, U>, ready[0], a, ctas, S, smem, stream);
+    return words ? launch_one(linear_rows_kernel<NT, true>, ready[1], a, ctas, S, smem, stream)
+                 : launch_one(linear_rows_kernel<NT, false>, ready[2], a, ctas, S, smem, stream);
 }
 
 bool overlap(const void* p, size_t np, const void* q, size_t nq) {
@@ -319,6 +484,5 @@ extern "C" int tf_linear_rows(const void* x, int64_t x_stride, const void* x_sca
     a.R = R;
     a.K = K;
     a.N = N;
-    a.words = K % kChunk == 0 && (reinterpret_cast<uintptr_t>(w_scales) & 3u) == 0;
     return R <= 8 ? launch<1>(a, stream) : R <= 16 ? launch<2>(a, stream) : launch<4>(a, stream);
 }
