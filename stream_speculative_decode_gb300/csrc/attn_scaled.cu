@@ -50,20 +50,20 @@ constexpr int kKeys = TF_SCALE_KEYS;           // a block: the keys that share a
 constexpr int kStageKeys = 2 * kKeys;
 constexpr int kBlockB = kKeys * TF_D;          // 1 KB of codes
 constexpr int kStageB = 4 * kBlockB;           // K of two blocks, then V of them
-constexpr int kStages = 4;
+constexpr int kStages = 3;
 constexpr int kRingB = kStages * kStageB;
 constexpr int kOStride = TF_D + 4;             // floats a query row of the warps' joining
 constexpr int kBlocks = 512 * TF_MAX_ROWS / kKeys;   // blocks of the longest chunk
 constexpr float kLog2e8 = 0.18033688011112042f;      // log2(e) / sqrt(64)
 constexpr float kNoRef = -3e38f;               // the reference of a query without a key so far
-constexpr float kLargest = 32768.f;            // a weight beyond it moves the reference
+constexpr float kLargest = 32768.f;            // 2^15: a weight beyond it moves the row's reference
 constexpr float kHeadroom = 6.f;               // log2 of the largest weight after that
 constexpr int kMaxShift = 64;
 static_assert(kStageKeys * kWarps <= 256, "chunks are whole rounds of the warps");
 static_assert(kKeys == item::kBlockKeys && kBlocks * 4 == item::kBlocksB, "one block index for pools and scales");
 
-// ring (joined through it at the end), block indices, exponents (K low byte, V high), the warps' largest V
-constexpr int kSmem = kWarps * kRingB + kBlocks * 4 + kBlocks * 2 + 16;
+// ring (joined through it at the end), block indices, scales (K's, and V's exponent), the warps' largest V
+constexpr int kSmem = kWarps * kRingB + kBlocks * 4 + kBlocks * 8 + 16;
 static_assert(kWarps * kRingB >= kWarps * 8 * 4 * (kOStride + 2) * 4, "the joining fits the rings");
 
 __device__ __forceinline__ void movmatrix_t(uint32_t& d, uint32_t a) {
@@ -82,9 +82,31 @@ __device__ __forceinline__ uint2 lds8(uint32_t a) {
     asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
     return v;
 }
-__device__ __forceinline__ uint32_t hmax2(uint32_t a, uint32_t b) {
-    __half2 r = __hmax2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
-    return *reinterpret_cast<uint32_t*>(&r);
+// Pairs of fp32, an instruction for both.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 both(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
 }
 
 // Where the 16 bytes `c` (0..3) of key row r lie in a block's 1 KB of shared
@@ -104,13 +126,13 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return __vcmpeq4(w &
 // One item: one key chunk of one stream, query rows [q0, q0 + 8 NT) of KV head
 // g, by 128 threads.
 template <int NT>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, NT <= 2 ? 4 : 3)
 attn_scaled_kernel(SegTable t, int layer, const uint16_t* __restrict__ q, float* __restrict__ part_o,
                    float2* __restrict__ part_ml, uint16_t* __restrict__ out, int full) {
     extern __shared__ __align__(128) unsigned char smem[];
     uint32_t* const blocks = reinterpret_cast<uint32_t*>(smem + kWarps * kRingB);
-    uint16_t* const exps = reinterpret_cast<uint16_t*>(blocks + kBlocks);
-    uint32_t* const top = reinterpret_cast<uint32_t*>(exps + kBlocks);
+    float2* const scales = reinterpret_cast<float2*>(blocks + kBlocks);   // K's scale, V's exponent
+    uint32_t* const top = reinterpret_cast<uint32_t*>(scales + kBlocks);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g8 = lane >> 2, t4 = lane & 3;
     const int g = blockIdx.x % TF_NKV;
     const AttnItem it = t.items[blockIdx.x / TF_NKV];
@@ -151,13 +173,13 @@ attn_scaled_kernel(SegTable t, int layer, const uint16_t* __restrict__ q, float*
         item::cp_async_commit();
     }
 
-    // ---- the chunk's exponents
+    // ---- the chunk's scales
     {
         const uint8_t *ks = t.k_scale[layer], *vs = t.v_scale[layer];
         uint32_t m = 0;
         for (int i = tid; i < nblocks; i += kThreads) {
             const uint32_t b = blocks[i], e = vs[b];
-            exps[i] = uint16_t(ks[b] | e << 8);
+            scales[i] = make_float2(__uint_as_float(uint32_t(ks[b]) << 23), float(e));
             m = max(m, e);
         }
         m = __reduce_max_sync(0xFFFFFFFFu, m);
@@ -166,7 +188,7 @@ attn_scaled_kernel(SegTable t, int layer, const uint16_t* __restrict__ q, float*
 
     // ---- queries: column n of a tile is query row q0 + 8 nt + n (window row / 4, head % 4)
     uint32_t qf[NT][4][2];
-    float cq[NT][2];   // factors of the columns 2 t4, 2 t4 + 1
+    uint64_t cq[NT];   // factors of the columns 2 t4, 2 t4 + 1
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         const int qi = nt * 8 + g8;
@@ -189,8 +211,7 @@ attn_scaled_kernel(SegTable t, int layer, const uint16_t* __restrict__ q, float*
         for (int i = 0; i < 8; ++i)
             qf[nt][i >> 1][i & 1] = pack_h2(__uint_as_float(w[i] << 16) * mul, __uint_as_float(w[i] & 0xFFFF0000u) * mul);
         const float back = __uint_as_float(uint32_t(127 - up) << 23) * kLog2e8;
-        cq[nt][0] = __shfl_sync(0xFFFFFFFFu, back, 8 * t4);
-        cq[nt][1] = __shfl_sync(0xFFFFFFFFu, back, 8 * t4 + 4);
+        cq[nt] = pair(__shfl_sync(0xFFFFFFFFu, back, 8 * t4), __shfl_sync(0xFFFFFFFFu, back, 8 * t4 + 4));
     }
     __syncthreads();
     const int E = int(max(max(top[0], top[1]), max(top[2], top[3])));
@@ -205,15 +226,16 @@ attn_scaled_kernel(SegTable t, int layer, const uint16_t* __restrict__ q, float*
     }
     const int lim_all = min((full ? st.keys : st.keys - st.rows + (q0 >> 2) + 1) - c0, nkeys);
 
-    float o[NT][4][4], m[NT][2], l[NT][2];
+    float o[NT][4][4];
+    uint64_t nm[NT], l[NT];   // of both columns: minus the reference, this lane's sum of 2^(x - m)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[nt][mt][e] = 0.f;
-        m[nt][0] = m[nt][1] = kNoRef;
-        l[nt][0] = l[nt][1] = 0.f;
+        nm[nt] = pair(-kNoRef, -kNoRef);
+        l[nt] = pair(0.f, 0.f);
     }
     // this lane's pieces in a block: K rows perm(g8) and 8 + perm(g8), V rows t4, 4 + t4, 8 + t4, 12 + t4
     const uint32_t ka = k_at(perm(g8), t4);
@@ -231,10 +253,12 @@ attn_scaled_kernel(SegTable t, int layer, const uint16_t* __restrict__ q, float*
             if (bi >= nblocks) break;
             const int key0 = bi * kKeys;
             const bool edge = key0 + kKeys > lim_all;
-            const uint32_t ex = exps[bi];
-            const float kf = __uint_as_float((ex & 0xFFu) << 23);
-            const int dv = max(int(ex >> 8) - E, -kMaxShift);
-            const float vf = __uint_as_float(uint32_t(127 + dv) << 23);
+            const float2 sc = scales[bi];
+            const float dv = fmaxf(sc.y - float(E), float(-kMaxShift));
+            const uint64_t dv2 = pair(dv, dv);
+            const float down = ex2(-dv);
+            const uint64_t kf2 = pair(sc.x, sc.x), down2 = pair(down, down);
+            const uint64_t tiny2 = pair(0x1p-149f, 0x1p-149f);   // keeps a factor above 0, which a masked score (-inf) needs
 
             // scores
             float s[NT][4];
@@ -251,14 +275,6 @@ attn_scaled_kernel(SegTable t, int layer, const uint16_t* __restrict__ q, float*
                     }
                 }
             }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const float f0 = cq[nt][0] * kf, f1 = cq[nt][1] * kf;
-                s[nt][0] *= f0;
-                s[nt][1] *= f1;
-                s[nt][2] *= f0;
-                s[nt][3] *= f1;
-            }
             if (edge) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
@@ -266,42 +282,43 @@ attn_scaled_kernel(SegTable t, int layer, const uint16_t* __restrict__ q, float*
                     if (key0 + 8 + perm(g8) >= lim[nt]) s[nt][2] = s[nt][3] = -INFINITY;
                 }
             }
-            // weights
+            // weights, in fp32 and (pw) as fp16 pairs; a weight is at most the sum of all
             uint32_t pw[NT][2];
-            float ps[NT][2];
+            uint64_t ps[NT];
             auto weigh = [&]() {
-                uint32_t most = 0;
+                uint64_t all = pair(0.f, 0.f);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    float p[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) p[e] = ex2(s[nt][e] - m[nt][e & 1]);
-                    ps[nt][0] = p[0] + p[2];
-                    ps[nt][1] = p[1] + p[3];
-                    pw[nt][0] = pack_h2(p[0] * vf, p[1] * vf);
-                    pw[nt][1] = pack_h2(p[2] * vf, p[3] * vf);
-                    most = hmax2(most, hmax2(pw[nt][0], pw[nt][1]));
+                    const uint64_t f = fma2(cq[nt], kf2, tiny2), c = add2(nm[nt], dv2);
+                    const float2 x = both(fma2(pair(s[nt][0], s[nt][1]), f, c)), y = both(fma2(pair(s[nt][2], s[nt][3]), f, c));
+                    const float w0 = ex2(x.x), w1 = ex2(x.y), w2 = ex2(y.x), w3 = ex2(y.y);
+                    ps[nt] = add2(pair(w0, w1), pair(w2, w3));
+                    all = add2(all, ps[nt]);
+                    pw[nt][0] = pack_h2(w0, w1);
+                    pw[nt][1] = pack_h2(w2, w3);
                 }
-                const float2 h = h2_to_f2(most);
-                return fmaxf(h.x, h.y) > kLargest;
+                const float2 a = both(all);
+                return !(a.x + a.y <= kLargest);
             };
             if (__any_sync(0xFFFFFFFFu, weigh())) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    float y[2] = {fmaxf(s[nt][0], s[nt][2]), fmaxf(s[nt][1], s[nt][3])};
-                    float alpha[2];
+                    const float2 f = both(fma2(cq[nt], kf2, tiny2)), old = both(nm[nt]);
+                    float y[2] = {fmaxf(s[nt][0] * f.x, s[nt][2] * f.x), fmaxf(s[nt][1] * f.y, s[nt][3] * f.y)};
+                    float to[2] = {-old.x, -old.y}, alpha[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
 #pragma unroll
                         for (int d = 4; d < 32; d *= 2) y[e] = fmaxf(y[e], __shfl_xor_sync(0xFFFFFFFFu, y[e], d));
-                        y[e] += float(dv) - kHeadroom;
+                        y[e] += dv - kHeadroom;
                         alpha[e] = 1.f;
-                        if (y[e] > m[nt][e] + (15.f - kHeadroom)) {
-                            alpha[e] = ex2(m[nt][e] - y[e]);
-                            m[nt][e] = y[e];
+                        if (y[e] > to[e] + (15.f - kHeadroom)) {   // this row's own: others do not move it
+                            alpha[e] = ex2(to[e] - y[e]);
+                            to[e] = y[e];
                         }
-                        l[nt][e] *= alpha[e];
                     }
+                    nm[nt] = pair(-to[0], -to[1]);
+                    l[nt] = mul2(l[nt], pair(alpha[0], alpha[1]));
 #pragma unroll
                     for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
@@ -311,8 +328,7 @@ attn_scaled_kernel(SegTable t, int layer, const uint16_t* __restrict__ q, float*
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                l[nt][0] += ps[nt][0];
-                l[nt][1] += ps[nt][1];
+                l[nt] = fma2(ps[nt], down2, l[nt]);
                 movmatrix_t(pw[nt][0], pw[nt][0]);
                 movmatrix_t(pw[nt][1], pw[nt][1]);
             }
@@ -381,21 +397,23 @@ attn_scaled_kernel(SegTable t, int layer, const uint16_t* __restrict__ q, float*
     float* const sM = sO + kWarps * 8 * NT * kOStride;  // [4][8 NT]
     float* const sL = sM + kWarps * 8 * NT;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt) {
+        const float2 sums = both(l[nt]), refs = both(nm[nt]);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            float sum = l[nt][e];
+            float sum = e ? sums.y : sums.x;
 #pragma unroll
             for (int d = 4; d < 32; d *= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
             const int col = warp * 8 * NT + nt * 8 + 2 * t4 + e;
             if (g8 == 0) {
-                sM[col] = m[nt][e];
+                sM[col] = e ? -refs.y : -refs.x;
                 sL[col] = sum;
             }
             float4* row = reinterpret_cast<float4*>(sO + col * kOStride + 8 * g8);
             row[0] = make_float4(o[nt][0][e], o[nt][0][2 + e], o[nt][1][e], o[nt][1][2 + e]);
             row[1] = make_float4(o[nt][2][e], o[nt][2][2 + e], o[nt][3][e], o[nt][3][2 + e]);
         }
+    }
     __syncthreads();
     const int mode = out ? st.merge_mode : kMergeKernel;
     const int64_t rec0 = st.pbase + (int64_t(it.chunk) * TF_NKV + g) * (st.rows * 4) + q0;

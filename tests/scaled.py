@@ -121,8 +121,8 @@ def check_attention(q, k, v, vs, keys, out, full=False, what=""):
                 partial sums, which are at most S = sum |q k| / 8, each time), three
                 factors, log2 units: off by e = 70 * 2^-23 * S * log2(e); a weight by
                 e * ln 2 + 2^-21 (ex2 and its argument's rounding, 2^-23 |x|)
-      weights   fp16: 2^-11 of each, or 2^-31 of the chunk's largest product of
-                weight and V scale where that is more, times a code of up to 448
+      weights   fp16: 2^-11 of each, or 2^-31 of the chunk's largest weight where that
+                is more, times a value of up to 448 of the chunk's largest V scale
       sums      P.V over n keys: (n / 64 + 64) roundings of 2^-23 of A, and as many
                 for the sum of the weights; merging a few more
       store     bf16: 2^-8 of the value.
@@ -138,7 +138,7 @@ def check_attention(q, k, v, vs, keys, out, full=False, what=""):
         s = torch.where(sees[:, None], s, -torch.inf)
         p = torch.softmax(s, -1)
         ref, A = p @ v[g], p @ v[g].abs()
-        top = (p * torch.ldexp(torch.ones((), dtype=torch.float64, device="cuda"), vs[g].int() - 127)).amax(-1)
+        top = p.amax(-1) * 2.0 ** (int(vs[g].max()) - 127)
         x = torch.where(sees[:, None], s - s.amax(-1, keepdim=True), 0.0).abs().clamp(max=40).amax(-1)
         e = 70 * 2.0 ** -23 * torch.where(sees[:, None], size, 0.0).amax(-1) + 2.0 ** -21 + 2.0 ** -22 * x
         bound = (2 * e + 2.0 ** -11 + 2 * (keys / 64 + 64) * 2.0 ** -23)[..., None] * A \

@@ -67,6 +67,23 @@ def test_v_of_any_size(tf, std):
     a.check(what=std)
 
 
+def test_zeros(tf):
+    """Caches and queries of zeros (scale bytes 0), at window edges too: the mean of V, and zeros."""
+    from scaled import ScaledAttn
+    for keys in (9, 40, 3000):
+        a = ScaledAttn(tf, [(6, keys), (1, keys), (8, keys)], 16, seed=13)
+        a.K[0].zero_()
+        a.ks[0].zero_()
+        a.run()
+        a.check(what=("K", keys))
+        a.q[0].zero_()
+        a.run()
+        a.check(what=("q", keys))
+        a.V[0].zero_()
+        a.vs[0].zero_()
+        assert (a.run()[0] == 0).all()
+
+
 def test_blocks_of_very_different_size(tf):
     """V blocks up to 2^40 apart; the weights sit on small and on large ones."""
     from scaled import ScaledAttn
