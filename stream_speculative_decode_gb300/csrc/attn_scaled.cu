@@ -467,8 +467,17 @@ int prepare_one() {
 template <int NT>
 int launch_one(const SegTable& t, int layer, const uint16_t* q, float* po, float2* pml, cudaStream_t stream,
                uint16_t* out, int full) {
-    return launch_pdl(attn_scaled_kernel<NT>, dim3(t.n_items * TF_NKV), dim3(kThreads), kSmem, stream, t, layer,
-                      q, po, pml, out, full);
+    return launch_pdl(attn_scaled_kernel<NT>, dim3(t.n_items_mma * TF_NKV), dim3(kThreads), kSmem, stream, t, layer, q, po,
+                      pml, out, full);
+}
+
+int launch_mma(const SegTable& t, int layer, const uint16_t* q, float* po, float2* pml, cudaStream_t stream,
+               uint16_t* out, int full) {
+    const int nt = (t.item_rows + 1) / 2;   // tiles of 8 query rows in the widest item
+    return nt == 1 ? launch_one<1>(t, layer, q, po, pml, stream, out, full)
+         : nt == 2 ? launch_one<2>(t, layer, q, po, pml, stream, out, full)
+         : nt == 3 ? launch_one<3>(t, layer, q, po, pml, stream, out, full)
+                   : launch_one<4>(t, layer, q, po, pml, stream, out, full);
 }
 
 }  // namespace
@@ -476,16 +485,29 @@ int launch_one(const SegTable& t, int layer, const uint16_t* q, float* po, float
 int attn_scaled_prepare() {
     int rc;
     if ((rc = prepare_one<1>()) != TF_OK || (rc = prepare_one<2>()) != TF_OK || (rc = prepare_one<3>()) != TF_OK) return rc;
-    return prepare_one<4>();
+    if ((rc = prepare_one<4>()) != TF_OK) return rc;
+    return attn_scaled_tc_prepare();
 }
 
 int launch_attn_scaled(const SegTable& t, int layer, const uint16_t* q, float* po, float2* pml, cudaStream_t stream,
                        uint16_t* out, int full) {
-    const int nt = (t.item_rows + 1) / 2;   // tiles of 8 query rows in the widest item
-    return nt == 1 ? launch_one<1>(t, layer, q, po, pml, stream, out, full)
-         : nt == 2 ? launch_one<2>(t, layer, q, po, pml, stream, out, full)
-         : nt == 3 ? launch_one<3>(t, layer, q, po, pml, stream, out, full)
-                   : launch_one<4>(t, layer, q, po, pml, stream, out, full);
+    if (t.n_items_mma == t.n_items) return launch_mma(t, layer, q, po, pml, stream, out, full);
+    if (t.n_items_mma > 0 && t.side) {   // both kinds of windows side by side, as over bf16 caches (attn.cu)
+        cudaError_t e = cudaEventRecord(t.ev_fork, stream);
+        if (e == cudaSuccess) e = cudaStreamWaitEvent(t.side, t.ev_fork, 0);
+        if (e != cudaSuccess) return cuda_fail(e);
+        int rc = launch_attn_scaled_tc(t, layer, q, po, pml, stream, out, full, t.tc_grid_mixed);
+        if (rc == TF_OK) rc = launch_mma(t, layer, q, po, pml, t.side, out, full);
+        if (rc != TF_OK) return rc;
+        e = cudaEventRecord(t.ev_join, t.side);
+        if (e == cudaSuccess) e = cudaStreamWaitEvent(stream, t.ev_join, 0);
+        return e == cudaSuccess ? TF_OK : cuda_fail(e);
+    }
+    if (t.n_items_mma > 0) {
+        const int rc = launch_mma(t, layer, q, po, pml, stream, out, full);
+        if (rc != TF_OK) return rc;
+    }
+    return launch_attn_scaled_tc(t, layer, q, po, pml, stream, out, full);
 }
 
 }  // namespace tf

@@ -1,0 +1,772 @@
+// Attention over scaled pools on the 5th-generation tensor cores: windows of 9 rows
+// or more and prompt windows (attn_scaled.cu takes the narrower ones). Units,
+// records and merges are those of attn_tc.cu, and so is the softmax with a thread a
+// query row; what differs is what the codes ask for.
+//
+// With c the codes, ek and ev a block's exponents, E the chunk's largest ev and x the
+// scores in log2 units:
+//   x_t = (q . ck_t) * 2^ek * log2(e) / 8
+//   o = 2^E * sum 2^(x_t - m) (2^(ev - E) cv_t) / sum 2^(x_t - m)
+// K's codes go into the MMA as they are (kind::f8f6f4): a query, under a power of two
+// of its own that puts its largest at 2^7..2^8, is split into two e4m3 parts, its
+// rounding and the rounding of the remainder. A bf16 value has 8 significant bits and
+// the two parts 4 each, so together they are exact down to 2^-9 of the largest, and
+// off by at most 2^-10 (2^-17 of the largest) below. K's scale is a factor of the
+// softmax's 16 scores of a block, which costs it nothing but the factor.
+// V's codes become fp16 tiles in shared memory (exact) times 2^(ev - E + 7), at most
+// 448 * 2^7; that is exact too down to 2^-28 below the chunk's largest block.
+//
+// Persistent, two CTAs an SM, 9 warps:
+//   warp 8      TMA loads of the codes (64 keys: 4 KB of K, 64-byte swizzle, and 4 KB
+//               of V) into a ring of 6 stages, each with its blocks' K scales and V
+//               factors beside it; at a unit's start its V scales, for E;
+//   warps 5, 6  the conversion of the V tiles, half a tile each, ring of 3;
+//   warp 4      lane 0: the q.K MMAs, and the queries' TMA loads;
+//   warp 7      lane 0: the P.V MMAs;
+//   warps 0-3   softmax and records; at a unit's start the queries' two parts, each
+//               row by the thread that owns it.
+// Tensor memory: S/P of tile j at columns 64 * (j % 3), O at 192.
+//
+// What bounds it: a 64-key tile is 8 KB from HBM, 350 cycles of an SM's share. Of
+// that the tensor cores take some 270 (M = 128 whatever the window's rows), the
+// softmax warps' chain of a tile 780 of a CTA and half that with two. Both conversions
+// by a warp each (K to fp16 too, the load warp's work) took 2,600 cycles a tile:
+// 212 us for 64 windows of 16 rows, where the K tiles stood in wait for their warp.
+//
+// A weight is at most 2^15 (fp16), the largest of a row at 2^6 when its reference
+// moves: weights below 2^-31 of it vanish. A block of V whose scale is 2^31 below the
+// chunk's largest counts as zero.
+//
+// A NaN code of V must not reach the rows that do not see its key (0 * NaN): in tiles
+// that reach past the first row's keys the converters write 0 for it and note, for
+// each dimension, the first such key; a row that sees it gets the NaN when it is
+// stored. Slots past the chunk's keys are zeroed.
+//
+// Waits are bounded as in attn_tc.cu.
+#include "tc_ptx.cuh"
+#include "scaled.cuh"
+
+namespace tf {
+namespace {
+
+constexpr int kStages = 6;
+constexpr int kRawB = kKT * TF_D;           // 4 KB: the codes of a K or V tile
+constexpr int kStageB = 2 * kRawB;          // K then V
+constexpr int kTileB = kKT * TF_D * 2;      // 8 KB: a tile in fp16
+constexpr int kBuf = 3;                     // S/P and V buffers: tile j uses buffer j % 3
+constexpr int kQ8B = kQRows * TF_D;         // 8 KB: one of the queries' two parts
+constexpr int kThreads = 288;
+constexpr uint32_t kCols = 256;
+constexpr uint32_t kColS = 0;
+constexpr uint32_t kColO = 192;
+constexpr float kLog2e8 = 0.18033688011112042f;
+constexpr float kSumMax = 32768.f;          // a thread's weights of a tile adding up to more move the row's reference
+constexpr float kHeadroom = 6.f;            // log2 of the largest weight after that
+constexpr int kVShift = 7;
+constexpr int kBlocks = 512 * TF_MAX_ROWS / TF_SCALE_KEYS;   // blocks of the longest chunk
+constexpr int kScaleRing = 16;              // tiles whose scales are kept
+constexpr int kUnits = 8;                   // units whose notes are kept (no role is that far ahead of another)
+constexpr int kUQConsumers = 8;             // the two MMA threads, 2 V converter warps, 4 softmax warps
+
+struct Bars {
+    uint64_t raw_full[kStages];
+    uint64_t v_read[kStages];    // both V converters have read the stage
+    uint64_t k_free[kStages];    // its q.K completed
+    uint64_t v_ready[kBuf];
+    uint64_t s_full[kBuf];
+    uint64_t p_full[kBuf];
+    uint64_t o_done[kBuf];       // P.V completed
+    uint64_t q_full;             // the unit's queries landed (one phase a unit)
+    uint64_t q_ready;            // and are in their two parts
+    uint64_t uq_full[kUQ];
+    uint64_t uq_empty[kUQ];
+    int32_t uq[kUQ];
+    uint64_t grp;
+    uint64_t drain;
+    uint64_t drain_pv;
+    uint32_t tmem_base;
+    WaitCtl wc;
+    int32_t last;
+    int32_t top[kUnits];                     // a unit's E, as a scale byte
+    int32_t any_nan[kUnits];
+    int32_t nan_key[kUnits][TF_D];           // first key (of the chunk) with a NaN code taken out, by dimension
+    alignas(16) float k_scale[kScaleRing][4];    // by running tile, a block each
+    alignas(16) uint32_t v_scale[kScaleRing][4]; // 2^(ev - E + 7) as fp16 pairs
+    alignas(16) uint8_t k_byte[kBlocks];     // warp 8: the unit's scale bytes
+    alignas(16) uint8_t v_byte[kBlocks];
+};
+constexpr int kQ8Off = kQB, kVOff = kQ8Off + 2 * kQ8B, kRawOff = kVOff + kBuf * kTileB;
+constexpr int kBarsOff = kRawOff + kStages * kStageB;
+constexpr int kSmemBytes = 1024 + kBarsOff + int(sizeof(Bars));
+static_assert(kSmemBytes <= 113 * 1024, "two CTAs an SM");
+
+// Instruction descriptors (attn_tc.cu): fp32 sums, M = 128, N = 64; format 0 is e4m3 for
+// kind::f8f6f4 (q.K) and fp16 for kind::f16 (P.V, V MN-major).
+constexpr uint32_t kIdescQK = (1u << 4) | (uint32_t(64 >> 3) << 17) | (uint32_t(128 >> 4) << 24);
+constexpr uint32_t kIdescPV = kIdescQK | (1u << 16);
+
+// sdesc's descriptor for K-major tiles of 64-byte rows under the 64-byte swizzle (layout
+// 4): groups of 8 rows 512 bytes apart.
+__device__ __forceinline__ uint64_t sdesc64(uint32_t addr) {
+    uint64_t d = uint64_t((addr >> 4) & 0x3FFFu);
+    d |= uint64_t(1) << 16;
+    d |= uint64_t(512 >> 4) << 32;
+    d |= uint64_t(1) << 46;
+    d |= uint64_t(4) << 61;
+    return d;
+}
+__device__ __forceinline__ void tc_mma_ss_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}"
+                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+}
+
+__device__ __forceinline__ uint32_t pack_h2(float a, float b) {
+    __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t mul_h2(uint32_t a, uint32_t b) {
+    __half2 r = __hmul2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+    return *reinterpret_cast<uint32_t*>(&r);
+}
+// 2^(7 - d) as an fp16 pair, d >= 0: subnormal from d = 22 on, 0 from 32 on.
+__device__ __forceinline__ uint32_t v_factor(int d) {
+    const uint32_t h = d <= 21 ? uint32_t(22 - d) << 10 : d <= 31 ? 0x400u >> (d - 21) : 0u;
+    return h | h << 16;
+}
+
+// Weights 2^(v * f - mu) of a thread's scores, f one factor for 16 of them, packed to
+// fp16 pairs; returns their sum. mu = 0 stands for a reference of -inf.
+template <int NV>
+__device__ __forceinline__ float weigh(const float (&v)[NV], const float (&f)[NV / 16], float mref,
+                                       uint32_t (&own)[NV / 2]) {
+    const float mu = (mref == -INFINITY) ? 0.f : mref;
+    const uint64_t nmu2 = f2pack(-mu, -mu);
+    uint64_t sum2[2] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f)};
+#pragma unroll
+    for (int b = 0; b < NV / 16; ++b) {
+        const uint64_t f2 = f2pack(f[b], f[b]);
+#pragma unroll
+        for (int c = 8 * b; c < 8 * b + 8; ++c) {
+            float x0, x1;
+            f2unpack(ffma2(f2pack(v[2 * c], v[2 * c + 1]), f2, nmu2), x0, x1);
+            const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+            sum2[c & 1] = fadd2(sum2[c & 1], f2pack(p0, p1));
+            own[c] = pack_h2(p0, p1);
+        }
+    }
+    float s4[4];
+    f2unpack(sum2[0], s4[0], s4[1]);
+    f2unpack(sum2[1], s4[2], s4[3]);
+    return (s4[0] + s4[1]) + (s4[2] + s4[3]);
+}
+
+// State of one softmax thread for one unit; rows and lanes as in attn_tc.cu (windows
+// of at most 16 rows run dual: lanes L and L + 16 of a quadrant share a query, each
+// with its half of a tile's keys).
+struct SoftState {
+    Bars* bars;
+    volatile WaitCtl* abortp;
+    uint32_t trow;
+    int g0, T, lim, lim_all;
+    bool wact;
+    float cq;     // factor of the row's scores, but for K's scales
+    float mref;
+    float l;
+};
+
+template <bool DUAL>
+__device__ __forceinline__ void softmax_tiles(SoftState& st) {
+    const int lane = threadIdx.x & 31;
+    const int half = DUAL ? (lane >> 4) : 0;
+    constexpr int NB = DUAL ? 2 : 4;   // blocks, and halves of a tile, that a thread scores
+    constexpr int NH = NB / 2;
+    Bars* bars = st.bars;
+    for (int j = 0; j < st.T; ++j) {
+        const int gj = st.g0 + j;
+        const int b = gj % kBuf;
+        const uint32_t colS = kColS + 64 * b;
+        if (!mbar_wait_warp(su32(&bars->s_full[b]), (gj / kBuf) & 1, st.abortp)) break;
+        tc_fence_after();
+        if (st.wact) {
+            float f[NB];
+            {
+                const float* ks = bars->k_scale[gj % kScaleRing] + half * NB;
+#pragma unroll
+                for (int i = 0; i < NB; ++i) f[i] = fmaf(st.cq, ks[i], 0x1p-149f);   // never 0 (masked scores are -inf)
+            }
+            const bool edge = j * kKT + kKT > st.lim_all;
+            // 32 of the thread's scores, -inf past the row's last key
+            auto load_scores = [&](int h, float (&v)[32]) {
+                uint32_t r[32];
+                if constexpr (DUAL)
+                    tc_ld16x2_32<kKT / 2>(st.trow + colS, r);
+                else
+                    tc_ld_n<32>(st.trow + colS + 32 * h, r);
+                tc_wait_ld();
+#pragma unroll
+                for (int c = 0; c < 32; ++c) v[c] = __uint_as_float(r[c]);
+                if (edge) {
+                    const int k0 = j * kKT + half * 32 + 32 * h;
+#pragma unroll
+                    for (int c = 0; c < 32; ++c)
+                        if (k0 + c >= st.lim) v[c] = -INFINITY;
+                }
+            };
+            // the tile's weights, kept in registers until all are there (P lies over S)
+            uint32_t own[NH][16];
+            auto weigh_tile = [&]() {
+                float sum = 0.f;
+#pragma unroll
+                for (int h = 0; h < NH; ++h) {
+                    float v[32];
+                    load_scores(h, v);
+                    const float f2[2] = {f[2 * h], f[2 * h + 1]};
+                    sum += weigh<32>(v, f2, st.mref, own[h]);
+                }
+                return sum;
+            };
+            float psum = weigh_tile();
+            // a weight is at most its tile's sum; a row that has no reference yet, or too
+            // large a sum (or a NaN), takes the warp through the maxima, and moves its own
+            // reference (which other rows have no say in)
+            const bool slow = (st.mref == -INFINITY && st.lim > 0) || !(psum <= kSumMax);
+            if (__any_sync(0xFFFFFFFFu, slow)) {
+                float mx = -INFINITY;
+#pragma unroll
+                for (int h = 0; h < NH; ++h) {
+                    float v[32];
+                    load_scores(h, v);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float m2[2] = {v[16 * i], v[16 * i + 1]};
+#pragma unroll
+                        for (int c = 2; c < 14; c += 4) {
+                            m2[0] = max3f(m2[0], v[16 * i + c], v[16 * i + c + 2]);
+                            m2[1] = max3f(m2[1], v[16 * i + c + 1], v[16 * i + c + 3]);
+                        }
+                        m2[0] = fmaxf(m2[0], v[16 * i + 14]);
+                        m2[1] = fmaxf(m2[1], v[16 * i + 15]);
+                        mx = fmaxf(mx, fmaxf(m2[0], m2[1]) * f[2 * h + i]);
+                    }
+                }
+                bool row_slow = slow;
+                if (DUAL) {
+                    mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));
+                    row_slow |= __shfl_xor_sync(0xFFFFFFFFu, int(slow), 16) != 0;
+                }
+                const float to = mx - kHeadroom;
+                const bool resc = row_slow && to > st.mref;
+                if (__any_sync(0xFFFFFFFFu, resc)) {
+                    if (j >= 1 && !mbar_wait_warp(su32(&bars->o_done[(gj - 1) % kBuf]), ((gj - 1) / kBuf) & 1, st.abortp))
+                        break;
+                    tc_fence_after();
+                    const float alpha = resc ? ex2_approx(st.mref - to) : 1.f;
+                    if (resc) {
+                        st.mref = to;
+                        st.l *= alpha;
+                    }
+                    if (j >= 1) {
+#pragma unroll 1
+                        for (int h = 0; h < (DUAL ? 2 : 4); ++h) {
+                            uint32_t o16[16];
+                            if constexpr (DUAL)
+                                tc_ld16x2_16<32>(st.trow + kColO + 16 * h, o16);
+                            else
+                                tc_ld16(st.trow + kColO + 16 * h, o16);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int c = 0; c < 16; ++c) o16[c] = __float_as_uint(__uint_as_float(o16[c]) * alpha);
+                            if constexpr (DUAL)
+                                tc_st16x2_16<32>(st.trow + kColO + 16 * h, o16);
+                            else
+                                tc_st_n<16>(st.trow + kColO + 16 * h, o16);
+                        }
+                        tc_wait_st();
+                    }
+                }
+                psum = weigh_tile();
+            }
+            if constexpr (DUAL) {
+                tc_st16x2_16<kKT / 4>(st.trow + colS, own[0]);
+            } else {
+                tc_st_n<16>(st.trow + colS, own[0]);
+                tc_st_n<16>(st.trow + colS + 16, own[NH - 1]);
+            }
+            st.l += psum;
+            tc_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(su32(&bars->p_full[b]));
+    }
+}
+
+// The thread's query row (TMEM lane 32 * warp + row of the tile) from bf16 to its two
+// e4m3 parts, under the power of two that puts its largest at 2^7..2^8; returns the
+// factor of its scores. Dual: two threads a row, half of its dimensions each.
+template <bool DUAL>
+__device__ __forceinline__ float convert_query(uint32_t sQ, uint32_t sQ8, int warp, int lane) {
+    const int r = 32 * warp + (DUAL ? (lane & 15) : lane);
+    constexpr int NP = DUAL ? 2 : 4;   // pieces of 16 dimensions
+    const int p0 = DUAL ? (lane >> 4) * 2 : 0;
+    uint32_t most = 0;
+#pragma unroll
+    for (int i = 0; i < 2 * NP; ++i) {
+        const uint4 v = lds128(sQ + r * 128 + (((2 * p0 + i) ^ (r & 7)) << 4));
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            most = max(most, max(finite_bits(__uint_as_float(w[k] << 16)), finite_bits(__uint_as_float(w[k] & 0xFFFF0000u))));
+    }
+    if (DUAL) most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 16));
+    const int up = min(134 - int(most >> 23), 126);
+    const float mul = __uint_as_float(uint32_t(127 + up) << 23);
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const uint4 v = lds128(sQ + r * 128 + (((2 * (p0 + i) + k) ^ (r & 7)) << 4));
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const float y[4] = {__uint_as_float(w[2 * c] << 16) * mul, __uint_as_float(w[2 * c] & 0xFFFF0000u) * mul,
+                                    __uint_as_float(w[2 * c + 1] << 16) * mul,
+                                    __uint_as_float(w[2 * c + 1] & 0xFFFF0000u) * mul};
+                const uint32_t h = e4m3_quad(y[0], y[1], y[2], y[3]);
+                const float2 a = h2_to_f2(e4m3_low(h)), b = h2_to_f2(e4m3_high(h));
+                hi[2 * k + c] = h;
+                lo[2 * k + c] = e4m3_quad(y[0] - a.x, y[1] - a.y, y[2] - b.x, y[3] - b.y);
+            }
+        }
+        const uint32_t at = sQ8 + r * 64 + (((p0 + i) ^ ((r >> 1) & 3)) << 4);   // the 64-byte swizzle
+        sts128(at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+        sts128(at + kQ8B, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+    }
+    return __uint_as_float(uint32_t(127 - up) << 23) * kLog2e8;
+}
+
+// The index of block i of a unit's chunk in the layer's pools (and scales).
+__device__ __forceinline__ uint32_t block_of(const SegTable& t, const Unit& U, int i, int32_t page) {
+    const int bs = t.page_shift - 4;
+    return ((uint32_t(page) * TF_NKV + U.g) << bs) + (i & ((1 << bs) - 1));
+}
+__device__ __forceinline__ int32_t page_of(const SegTable& t, const Unit& U, int i) {
+    return __ldg(t.pages + U.pages + (i >> (t.page_shift - 4)));
+}
+
+// Where the 16 codes `p` (0..3) of key row r go in a fp16 tile (128-byte rows, 128-byte
+// swizzle): two 16-byte pieces.
+__device__ __forceinline__ void store_codes(uint32_t tile, int r, int p, const uint32_t (&h)[8]) {
+    const uint32_t row = tile + r * 128;
+    sts128(row + (((2 * p) ^ (r & 7)) << 4), make_uint4(h[0], h[1], h[2], h[3]));
+    sts128(row + (((2 * p + 1) ^ (r & 7)) << 4), make_uint4(h[4], h[5], h[6], h[7]));
+}
+
+__global__ void __launch_bounds__(kThreads, 2)
+attn_scaled_tc_kernel(SegTable t, int layer, float* __restrict__ part_o, float2* __restrict__ part_ml,
+                      uint16_t* __restrict__ out, int full, int n_units, const __grid_constant__ CUtensorMap qmap) {
+    extern __shared__ unsigned char smem_raw[];
+    const uint32_t raw = su32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    unsigned char* gbase = smem_raw + (base - raw);
+    const uint32_t sQ = base, sQ8 = base + kQ8Off, sV = base + kVOff, sRaw = base + kRawOff;
+    Bars* bars = reinterpret_cast<Bars*>(gbase + kBarsOff);
+    volatile WaitCtl* abortp = &bars->wc;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (tid == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(su32(&bars->raw_full[s]), 1);
+            mbar_init(su32(&bars->v_read[s]), 2);
+            mbar_init(su32(&bars->k_free[s]), 1);
+        }
+        for (int b = 0; b < kBuf; ++b) {
+            mbar_init(su32(&bars->v_ready[b]), 2);
+            mbar_init(su32(&bars->s_full[b]), 1);
+            mbar_init(su32(&bars->p_full[b]), 4);
+            mbar_init(su32(&bars->o_done[b]), 1);
+        }
+        mbar_init(su32(&bars->q_full), 1);
+        mbar_init(su32(&bars->q_ready), 4);
+        for (int k = 0; k < kUQ; ++k) {
+            mbar_init(su32(&bars->uq_full[k]), 1);
+            mbar_init(su32(&bars->uq_empty[k]), kUQConsumers);
+        }
+        mbar_init(su32(&bars->grp), 128);
+        mbar_init(su32(&bars->drain), 1);
+        mbar_init(su32(&bars->drain_pv), 1);
+        bars->wc.flag = 0;
+        bars->wc.limit_ns = t.wait_ns;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    for (int i = tid; i < kUnits * TF_D; i += kThreads) (&bars->nan_key[0][0])[i] = INT32_MAX;
+    if (tid < kUnits) bars->any_nan[tid] = 0;
+    pdl_wait();   // the table above; queries and caches below
+    if (warp == 4) tc_alloc(su32(&bars->tmem_base), kCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars->tmem_base;
+
+    if (warp == 4) {
+        // ------------------------------------------------------------ q.K MMAs
+        if (lane == 0) {
+            const uint64_t dq = sdesc64(sQ8);
+            bool ok = true;
+            int gt = 0, n = 0, q_issued = 0;
+            if (int(blockIdx.x) < n_units) {
+                issue_q(sQ, &qmap, unit_of<true>(t, layer, blockIdx.x), su32(&bars->q_full));
+                q_issued = 1;
+            }
+            for (int u = blockIdx.x; u >= 0 && ok; ++n) {
+                const int T = unit_of<true>(t, layer, u).T;
+                ok = mbar_wait(su32(&bars->q_ready), n & 1, abortp);
+                if (!ok) break;
+                tc_fence_after();
+                for (int j = 0; j < T && ok; ++j) {
+                    const int g1 = gt + j, s = g1 % kStages, b = g1 % kBuf;
+                    ok = mbar_wait(su32(&bars->raw_full[s]), (g1 / kStages) & 1, abortp);
+                    if (!ok) break;
+                    if (g1 >= kBuf) {   // P.V(g1-3) has released S buffer b
+                        ok = mbar_wait(su32(&bars->o_done[b]), ((g1 - kBuf) / kBuf) & 1, abortp);
+                        if (!ok) break;
+                    }
+                    tc_fence_after();
+                    const uint64_t dk = sdesc64(sRaw + s * kStageB);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)   // both parts, K = 64 in 2 steps of 32 bytes each
+                        tc_mma_ss_f8(tmem + kColS + 64 * b, dq + (k >> 1) * (kQ8B >> 4) + 2 * (k & 1), dk + 2 * (k & 1),
+                                     kIdescQK, k > 0 ? 1u : 0u);
+                    tc_commit(su32(&bars->s_full[b]));
+                    tc_commit(su32(&bars->k_free[s]));
+                }
+                gt += T;
+                if (!ok) break;
+                // the next unit's queries: their bf16 tile has been free since q_ready
+                u = next_unit_thread(bars, n, abortp);
+                if (u >= 0) {
+                    issue_q(sQ, &qmap, unit_of<true>(t, layer, u), su32(&bars->q_full));
+                    ++q_issued;
+                }
+            }
+            tc_commit(su32(&bars->drain));
+            mbar_drain(su32(&bars->drain), 0);
+            if (q_issued > 0) mbar_drain(su32(&bars->q_full), (q_issued - 1) & 1);   // the last query load has landed
+        }
+        __syncwarp();
+    } else if (warp == 7) {
+        // ------------------------------------------------------------ P.V MMAs
+        if (lane == 0) {
+            bool ok = true;
+            int gt = 0, n = 0;
+            for (int u = blockIdx.x; u >= 0 && ok; ++n) {
+                const int T = unit_of<true>(t, layer, u).T;
+                for (int j = 0; j < T && ok; ++j) {
+                    const int g2 = gt + j, b = g2 % kBuf;
+                    ok = mbar_wait(su32(&bars->p_full[b]), (g2 / kBuf) & 1, abortp);
+                    if (!ok) break;
+                    ok = mbar_wait(su32(&bars->v_ready[b]), (g2 / kBuf) & 1, abortp);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t dv = sdesc(sV + b * kTileB, kTileB, 1024);
+#pragma unroll
+                    for (int k = 0; k < kKT / 16; ++k)
+                        tc_mma_ts(tmem + kColO, tmem + kColS + 64 * b + 8 * k, dv + 128 * k, kIdescPV,
+                                  (j > 0 || k > 0) ? 1u : 0u);
+                    tc_commit(su32(&bars->o_done[b]));
+                }
+                gt += T;
+                if (ok) u = next_unit_thread(bars, n, abortp);
+            }
+            tc_commit(su32(&bars->drain_pv));
+            mbar_drain(su32(&bars->drain_pv), 0);
+        }
+        __syncwarp();
+    } else if (warp == 8) {
+        // ------------------------------------------------------------ loads, scales
+        const uint64_t once = l2_evict_first();
+        const uint8_t *const ks = t.k_scale[layer], *const vs = t.v_scale[layer];
+        int gt = 0;
+        bool ok = true;
+        for (int u = blockIdx.x, m = 0; u >= 0 && ok; ++m) {
+            const Unit U = unit_of<true>(t, layer, u);
+            const int nblocks = (min(U.st.chunk_keys, U.st.keys - U.c0) + TF_SCALE_KEYS - 1) / TF_SCALE_KEYS;
+            int4 pid = tile_pages(t, U, 0);
+            uint32_t top = 0;
+            for (int i = lane; i < 4 * U.T; i += 32) {   // slots past the chunk: any K scale, no V
+                const uint32_t at = block_of(t, U, i, page_of(t, U, i));
+                const uint32_t e = i < nblocks ? uint32_t(__ldg(vs + at)) : 0u;
+                bars->k_byte[i] = __ldg(ks + at);
+                bars->v_byte[i] = uint8_t(e);
+                top = max(top, e);
+            }
+            top = __reduce_max_sync(0xFFFFFFFFu, top);
+            if (lane == 0) bars->top[m % kUnits] = int32_t(top);
+            __syncwarp();
+            for (int j = 0; j < U.T; ++j, ++gt) {
+                const int s = gt % kStages;
+                if (gt >= kStages &&
+                    (!mbar_wait_warp(su32(&bars->v_read[s]), ((gt - kStages) / kStages) & 1, abortp) ||
+                     !mbar_wait_warp(su32(&bars->k_free[s]), ((gt - kStages) / kStages) & 1, abortp))) {
+                    ok = false;
+                    break;
+                }
+                if (lane < 4) {
+                    bars->k_scale[gt % kScaleRing][lane] = scale_value(bars->k_byte[4 * j + lane]);
+                    bars->v_scale[gt % kScaleRing][lane] = v_factor(int(top) - int(bars->v_byte[4 * j + lane]));
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    const uint32_t bar = su32(&bars->raw_full[s]);
+                    mbar_expect_tx(bar, kStageB);
+                    tile_boxes(t, U, j, pid, [&](uint32_t off, int slot, int page) {   // off: of 128-byte rows
+                        const int head = page * TF_NKV + U.g;
+                        tma_load_3d_hint(sRaw + s * kStageB + off / 2, U.kmap, 0, slot, head, bar, once);
+                        tma_load_3d_hint(sRaw + s * kStageB + kRawB + off / 2, U.vmap, 0, slot, head, bar, once);
+                    });
+                }
+                if (j + 1 < U.T) pid = tile_pages(t, U, j + 1);
+            }
+            if (!ok) break;
+            // the next unit of the launch, for this CTA's roles
+            int un = 0;
+            if (lane == 0) un = int(gridDim.x) + atomicAdd(&t.tc_work[2 * layer], 1);
+            un = __shfl_sync(0xFFFFFFFFu, un, 0);
+            if (un >= n_units) un = -1;
+            const int slot = m % kUQ;
+            if (m >= kUQ && !mbar_wait_warp(su32(&bars->uq_empty[slot]), ((m / kUQ) - 1) & 1, abortp)) break;
+            if (lane == 0) {
+                bars->uq[slot] = un;
+                mbar_arrive(su32(&bars->uq_full[slot]));
+            }
+            __syncwarp();
+            u = un;
+        }
+        if (abortp->flag && lane == 0)   // let the copies in flight land before the CTA exits
+            for (int k = gt > kStages ? gt - kStages : 0; k < gt; ++k)
+                mbar_drain(su32(&bars->raw_full[k % kStages]), (k / kStages) & 1);
+        __syncwarp();
+    } else if (warp == 5 || warp == 6) {
+        // ------------------------------------------------------------ V tiles, rows 32 * (warp - 5) ..
+        const int r0 = 32 * (warp - 5);
+        int gt = 0;
+        bool ok = true;
+        for (int u = blockIdx.x, m = 0; u >= 0 && ok; ++m) {
+            const Unit U = unit_of<true>(t, layer, u);
+            const int nkeys = min(U.st.chunk_keys, U.st.keys - U.c0);
+            const int lim_all = min((full ? U.st.keys : U.st.keys - U.st.rows + 1) - U.c0, nkeys);
+            for (int j = 0; j < U.T; ++j, ++gt) {
+                const int s = gt % kStages, b = gt % kBuf;
+                if (!mbar_wait_warp(su32(&bars->raw_full[s]), (gt / kStages) & 1, abortp)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t src = sRaw + s * kStageB + kRawB + r0 * TF_D + uint32_t(lane) * 16u;
+                const uint2 f = *reinterpret_cast<const uint2*>(bars->v_scale[gt % kScaleRing] + (r0 >> 4));
+                uint4 v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = lds128(src + i * 512);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(su32(&bars->v_read[s]));
+                if (j * kKT + r0 + 32 > lim_all) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int key = j * kKT + r0 + 8 * i + (lane >> 2);
+                        uint32_t* w = &v[i].x;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            if (key >= nkeys) w[k] = 0u;
+                            const uint32_t bad = __vcmpeq4(w[k] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+                            if (bad) {
+                                for (int c = 0; c < 4; ++c)
+                                    if (bad >> (8 * c) & 1) atomicMin(&bars->nan_key[m % kUnits][16 * (lane & 3) + 4 * k + c], key);
+                                bars->any_nan[m % kUnits] = 1;
+                                w[k] &= ~bad;
+                            }
+                        }
+                    }
+                }
+                if (gt >= kBuf && !mbar_wait_warp(su32(&bars->o_done[b]), ((gt - kBuf) / kBuf) & 1, abortp)) {
+                    ok = false;
+                    break;
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {   // rows 8 i .. 8 i + 7 of the half are of its block i / 2
+                    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                    uint32_t o[8];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        o[2 * k] = mul_h2(e4m3_low(w[k]), i < 2 ? f.x : f.y);
+                        o[2 * k + 1] = mul_h2(e4m3_high(w[k]), i < 2 ? f.x : f.y);
+                    }
+                    store_codes(sV + b * kTileB, r0 + 8 * i + (lane >> 2), lane & 3, o);
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(su32(&bars->v_ready[b]));
+            }
+            if (ok) u = next_unit_warp(bars, m, abortp);
+        }
+    } else {
+        // ------------------------------------------------------------ softmax + records
+        int gt = 0, gph = 0;
+        const uint32_t trow = tmem + (uint32_t(warp * 32) << 16);
+        for (int u = blockIdx.x, m = 0; u >= 0; ++m) {
+            const Unit U = unit_of<true>(t, layer, u);
+            const SegStream& st = U.st;
+            const int nq = st.rows * 4, per = q_per(st.rows);
+            const bool dual = per == 16;
+            const int ql = dual ? (lane & 15) : lane;
+            const int qi = per * warp + ql;
+            const bool qvalid = qi < nq;
+            const bool wact = per * warp < nq;
+            const int mode = out ? st.merge_mode : kMergeKernel;
+            SoftState ss;
+            ss.bars = bars;
+            ss.abortp = abortp;
+            ss.trow = trow;
+            ss.g0 = gt;
+            ss.T = U.T;
+            ss.lim = qvalid ? (full ? st.keys : st.keys - st.rows + (qi >> 2) + 1) - U.c0 : 0;
+            ss.lim_all = (full ? st.keys : st.keys - st.rows + 1) - U.c0;
+            ss.wact = wact;
+            ss.cq = 0.f;
+            ss.mref = -INFINITY;
+            ss.l = 0.f;
+            if (mbar_wait_warp(su32(&bars->q_full), m & 1, abortp))
+                ss.cq = dual ? convert_query<true>(sQ, sQ8, warp, lane) : convert_query<false>(sQ, sQ8, warp, lane);
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(su32(&bars->q_ready));
+            if (dual)
+                softmax_tiles<true>(ss);
+            else
+                softmax_tiles<false>(ss);
+            gt += U.T;
+            const int un = next_unit_warp(bars, m, abortp);
+            if (!abortp->flag) mbar_wait_warp(su32(&bars->o_done[(gt - 1) % kBuf]), ((gt - 1) / kBuf) & 1, abortp);
+            tc_fence_after();
+            const bool aborted = abortp->flag != 0;
+            const volatile int32_t* const nan_key = bars->nan_key[m % kUnits];
+            const bool any_nan = reinterpret_cast<volatile int32_t*>(bars->any_nan)[m % kUnits] != 0;
+            if (wact) {
+                // (m, l, O) relative to the row's reference -> the chunk's record, O in units of 2^(E - 7)
+                const int e = reinterpret_cast<volatile int32_t*>(bars->top)[m % kUnits] - kScaleBias - kVShift;
+                const float up0 = __uint_as_float(uint32_t(127 + e / 2) << 23);
+                const float up1 = __uint_as_float(uint32_t(127 + e - e / 2) << 23);
+                auto finish = [&](auto& ro) {
+                    constexpr int ND = int(sizeof(ro) / sizeof(ro[0]));
+                    const int d0 = ND == 32 ? 32 * (lane >> 4) : 0;
+                    float lsum = ss.l;
+                    if (ND == 32) lsum += __shfl_xor_sync(0xFFFFFFFFu, lsum, 16);
+                    if (any_nan) {
+#pragma unroll
+                        for (int c = 0; c < ND; ++c)
+                            if (nan_key[d0 + c] < ss.lim) ro[c] = 0x7FC00000u;
+                    }
+                    if (qvalid && mode == kMergeDirect) {
+                        const float inv = aborted ? NAN : 1.f / lsum;
+                        auto* dst = out_row(out, st, U.g, qi) + d0;
+#pragma unroll
+                        for (int c = 0; c < ND / 4; ++c)
+                            store_out4(dst + 4 * c, make_float4(__uint_as_float(ro[4 * c]) * inv * up0 * up1,
+                                                                __uint_as_float(ro[4 * c + 1]) * inv * up0 * up1,
+                                                                __uint_as_float(ro[4 * c + 2]) * inv * up0 * up1,
+                                                                __uint_as_float(ro[4 * c + 3]) * inv * up0 * up1));
+                    } else if (qvalid) {
+                        const int64_t rec = st.pbase + (int64_t(U.chunk) * TF_NKV + U.g) * nq + qi;
+                        const bool empty = ss.mref == -INFINITY && !(lsum != lsum);
+                        float4* dst = reinterpret_cast<float4*>(part_o + rec * TF_D + d0);
+#pragma unroll
+                        for (int c = 0; c < ND / 4; ++c) {
+                            float4 v = make_float4(__uint_as_float(ro[4 * c]) * up0 * up1,
+                                                   __uint_as_float(ro[4 * c + 1]) * up0 * up1,
+                                                   __uint_as_float(ro[4 * c + 2]) * up0 * up1,
+                                                   __uint_as_float(ro[4 * c + 3]) * up0 * up1);
+                            if (aborted) v = make_float4(NAN, NAN, NAN, NAN);
+                            else if (empty) v = make_float4(0.f, 0.f, 0.f, 0.f);
+                            dst[c] = v;
+                        }
+                        if (d0 == 0) {   // a sum that is no number must not pass for none in a merge
+                            const bool lost = aborted || !(lsum <= 3e38f);
+                            part_ml[rec] = make_float2(aborted ? NAN : ss.mref > -INFINITY ? ss.mref : lost ? 0.f : -INFINITY,
+                                                       lost ? INFINITY : empty ? 0.f : lsum);
+                        }
+                    }
+                };
+                if (dual) {
+                    uint32_t r32[32];
+                    tc_ld16x2_32<32>(trow + kColO, r32);
+                    tc_wait_ld();
+                    finish(r32);
+                } else {
+                    uint32_t r64[64];
+                    tc_ld64(trow + kColO, r64);
+                    tc_wait_ld();
+                    finish(r64);
+                }
+            }
+            tc_fence_before();
+            if (any_nan && group_sync(bars, gph, abortp)) {   // every warp has read the unit's notes
+                if (warp == 0) {
+                    bars->nan_key[m % kUnits][lane] = INT32_MAX;
+                    bars->nan_key[m % kUnits][32 + lane] = INT32_MAX;
+                    if (lane == 0) bars->any_nan[m % kUnits] = 0;
+                }
+            }
+            if (mode == kMergeLastCta) {
+                __threadfence();
+                if (group_sync(bars, gph, abortp)) {
+                    int* ctr = t.counters + (size_t(layer) * t.S + U.stream) * TF_NKV + U.g;
+                    if (tid == 0) bars->last = atomicAdd(ctr, 1) == st.n_chunks - 1;
+                    if (group_sync(bars, gph, abortp) && bars->last) {
+                        __threadfence();
+                        merge_stream_head<2, 4>(st, U.g, part_o, part_ml, out, tid, 128);
+                        if (tid == 0) atomicExch(ctr, 0);
+                    }
+                }
+            }
+            u = un;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();   // every role is done
+    tc_fence_after();
+    if (tid == 0) {
+        if (abortp->flag) atomicOr(t.status, uint32_t(TF_STATUS_ATTN_TIMEOUT));
+        __threadfence();
+        if (atomicAdd(&t.tc_work[2 * layer + 1], 1) == int(gridDim.x) - 1) {   // the last CTA resets the work counters
+            atomicExch(&t.tc_work[2 * layer], 0);
+            atomicExch(&t.tc_work[2 * layer + 1], 0);
+        }
+    }
+    pdl_trigger();
+    if (warp == 4) {
+        tc_fence_after();
+        tc_dealloc(tmem, kCols);
+    }
+}
+
+}  // namespace
+
+int attn_scaled_tc_prepare() {
+    const cudaError_t e = cudaFuncSetAttribute(attn_scaled_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    return e == cudaSuccess ? TF_OK : cuda_fail(e);
+}
+
+int launch_attn_scaled_tc(const SegTable& t0, int layer, const uint16_t* q, float* po, float2* pml, cudaStream_t stream,
+                          uint16_t* out, int full, int grid_cap) {
+    if (!t0.k_maps || !t0.v_maps) return TF_EINVAL;
+    SegTable t = t0;
+    t.wait_ns = wait_limit_ns();
+    const int n_units = (t.n_items - t.n_items_mma) * TF_NKV;
+    const int slots = grid_cap > 0 ? grid_cap : 2 * sm_count();
+    const int grid = n_units < slots ? n_units : slots;
+    CUtensorMap qmap;
+    if (!encode_q_map(&qmap, q, t.R)) return cuda_fail(cudaErrorInvalidValue);
+    return launch_pdl(attn_scaled_tc_kernel, dim3(grid), dim3(kThreads), kSmemBytes, stream, t, layer, po, pml, out, full,
+                      n_units, qmap);
+}
+
+}  // namespace tf

@@ -67,6 +67,11 @@ __device__ __forceinline__ float2 h2_to_f2(uint32_t h) { return __half22float2(*
 int launch_attn_scaled(const SegTable& t, int layer, const uint16_t* q, float* po, float2* pml, cudaStream_t stream,
                        uint16_t* out, int full);
 int attn_scaled_prepare();
+// attn_scaled_tc.cu: the tensor-core part of them, items [n_items_mma, n_items);
+// grid_cap 0: two CTAs an SM.
+int launch_attn_scaled_tc(const SegTable& t, int layer, const uint16_t* q, float* po, float2* pml, cudaStream_t stream,
+                          uint16_t* out, int full, int grid_cap = 0);
+int attn_scaled_tc_prepare();
 
 // qk_scaled.cu: the append with the queries' norm and rotation (tf_qk_rows).
 struct Turns {

@@ -97,16 +97,19 @@ bool encode_kv_map(CUtensorMap* out, const void* base, int keys, int cap) {
 // TMA map of one layer's pool of K or V pages, bf16 [n_pages][8][page_keys][64],
 // as a 3-D tensor (d, slot, page * 8 + head); a box is one head's 64 slots (or
 // the whole of a smaller page).
-bool encode_pool_map(CUtensorMap* out, const void* base, int page_keys, int n_pages) {
+// Scaled pools: a byte an element, the box's 64-byte rows under `swizzle`.
+bool encode_pool_map(CUtensorMap* out, const void* base, int page_keys, int n_pages, bool scaled,
+                     CUtensorMapSwizzle swizzle) {
     auto enc = tensor_map_encoder();
     if (!enc) return false;
+    const cuuint64_t size = scaled ? 1 : 2;
     const cuuint64_t dims[3] = {cuuint64_t(TF_D), cuuint64_t(page_keys), cuuint64_t(n_pages) * TF_NKV};
-    const cuuint64_t strides[2] = {cuuint64_t(TF_D) * 2, cuuint64_t(page_keys) * TF_D * 2};
+    const cuuint64_t strides[2] = {TF_D * size, page_keys * TF_D * size};
     const cuuint32_t box[3] = {cuuint32_t(TF_D), cuuint32_t(std::min(page_keys, 64)), 1u};
     const cuuint32_t estr[3] = {1u, 1u, 1u};
-    CUresult r = enc(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    CUresult r = enc(out, scaled ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                     const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
 }
 
@@ -142,8 +145,7 @@ bool encode_w2_map(CUtensorMap* out, const void* w2, int rows) {
 
 // Attention kernel of a stream: tensor cores once its window holds 3 rows (12
 // query rows per KV head); TF_ATTN_PATH=mma|tc forces one (tests compare both).
-int attn_path_of(int rows, bool scaled) {
-    if (scaled) return kAttnMma;
+int attn_path_of(int rows) {
     if (rows > 16) return kAttnTc;   // prompt windows (17-32 rows): the tensor cores, whatever is forced
     const char* e = std::getenv("TF_ATTN_PATH");
     if (e && std::strcmp(e, "mma") == 0) return kAttnMma;
@@ -174,7 +176,7 @@ namespace tf {
 
 // The plan of a set of windows, each of at most `max_window_rows` rows
 // (TF_MAX_ROWS for the verify tables, kPromptTileRows for a prompt call).
-int plan_windows(const tf_stream* streams, int n_streams, tf_plan* out, int max_window_rows, bool scaled = false) {
+int plan_windows(const tf_stream* streams, int n_streams, tf_plan* out, int max_window_rows) {
     if (!out) return TF_EINVAL;
     std::memset(out, 0, sizeof(*out));
     if (n_streams < 0) return TF_EINVAL;
@@ -196,7 +198,7 @@ int plan_windows(const tf_stream* streams, int n_streams, tf_plan* out, int max_
         items += nch;
         tiles += (st.rows + tf::kConvTileRows - 1) / tf::kConvTileRows;
         max_rows = std::max(max_rows, int(st.rows));
-        (tf::attn_path_of(st.rows, scaled) == tf::kAttnTc ? any_tc : any_mma) = true;
+        (tf::attn_path_of(st.rows) == tf::kAttnTc ? any_tc : any_mma) = true;
         if (nch > 1 && 4 * st.rows * nch > tf::kMergeLastCtaMaxRecords) any_merge = true;
     }
     if (R > (1 << 24)) return TF_ERANGE;
@@ -324,7 +326,7 @@ int finish_build(std::unique_ptr<tf_segments> owned, std::vector<tf::SegStream>&
         for (SegStream& d : ss) d.n_qg = 1;
         for (const AttnItem& it : items) {
             SegStream& d = ss[it.stream];
-            const int ng = attn_path_of(d.rows, scaled) == kAttnMma ? (d.rows + kMmaGroupRows - 1) / kMmaGroupRows : 1;
+            const int ng = attn_path_of(d.rows) == kAttnMma ? (d.rows + kMmaGroupRows - 1) / kMmaGroupRows : 1;
             d.n_qg = ng;
             for (int gi = 0; gi < ng; ++gi) groups.push_back({it.stream, it.chunk, 4 * kMmaGroupRows * gi, 0});
         }
@@ -336,7 +338,7 @@ int finish_build(std::unique_ptr<tf_segments> owned, std::vector<tf::SegStream>&
     // mma.sync items first, then tensor-core items; within each, largest
     // chunks first so the long work starts early in the grid
     std::stable_sort(items.begin(), items.end(), [&](const AttnItem& a, const AttnItem& b) {
-        const int pa = attn_path_of(ss[a.stream].rows, scaled), pb = attn_path_of(ss[b.stream].rows, scaled);
+        const int pa = attn_path_of(ss[a.stream].rows), pb = attn_path_of(ss[b.stream].rows);
         if (pa != pb) return pa < pb;
         auto len = [&](const AttnItem& it) {
             const SegStream& d = ss[it.stream];
@@ -348,7 +350,7 @@ int finish_build(std::unique_ptr<tf_segments> owned, std::vector<tf::SegStream>&
     });
     int n_items_mma = 0, mma_rows = 1;
     for (const AttnItem& it : items)
-        if (attn_path_of(ss[it.stream].rows, scaled) == kAttnMma) {
+        if (attn_path_of(ss[it.stream].rows) == kAttnMma) {
             ++n_items_mma;
             mma_rows = std::max(mma_rows, std::min(ss[it.stream].rows - it.q0 / 4, kMmaGroupRows));
         }
@@ -416,8 +418,11 @@ int finish_build(std::unique_ptr<tf_segments> owned, std::vector<tf::SegStream>&
         CUtensorMap km, vm;   // aligned locals, copied into the image
         bool ok;
         if (pg) {
-            ok = encode_pool_map(&km, k_cache[i], pg->page_keys, pg->n_pages) &&
-                 encode_pool_map(&vm, v_cache[i], pg->page_keys, pg->n_pages);
+            // scaled: K's codes are an MMA's operand as they land, V's are converted
+            const auto ksw = scaled ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+            const auto vsw = scaled ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B;
+            ok = encode_pool_map(&km, k_cache[i], pg->page_keys, pg->n_pages, scaled, ksw) &&
+                 encode_pool_map(&vm, v_cache[i], pg->page_keys, pg->n_pages, scaled, vsw);
         } else {
             const SegStream& st = ss[i % S];
             ok = encode_kv_map(&km, k_cache[i], st.keys, st.cap) && encode_kv_map(&vm, v_cache[i], st.keys, st.cap);
@@ -497,7 +502,7 @@ int finish_build(std::unique_ptr<tf_segments> owned, std::vector<tf::SegStream>&
             int64_t keys_tc = 0, keys_all = 0;
             for (const SegStream& d : ss) {
                 keys_all += d.keys;
-                if (attn_path_of(d.rows, scaled) == kAttnTc) keys_tc += d.keys;
+                if (attn_path_of(d.rows) == kAttnTc) keys_tc += d.keys;
             }
             const int slots = 2 * sm_count();
             int g = int((int64_t(slots) * keys_tc + keys_all - 1) / (keys_all > 0 ? keys_all : 1));
@@ -548,7 +553,7 @@ int build_verify(const tf_stream* streams, int n_streams, const void* const* con
     *out = nullptr;
     if (n_conv < 0 || n_attn < 0 || n_conv > 4096 || n_attn > 4096) return TF_EINVAL;
     tf_plan plan;
-    int rc = plan_windows(streams, n_streams, &plan, TF_MAX_ROWS, pg && pg->scaled);
+    int rc = plan_windows(streams, n_streams, &plan, TF_MAX_ROWS);
     if (rc != TF_OK) return rc;
     const int S = n_streams;
     if (S > 0 && n_conv > 0 && !conv_state) return TF_EINVAL;
@@ -678,7 +683,7 @@ int build_prompt(int32_t rows, int32_t keys, int32_t kv_capacity, const void* co
         tiles_as_streams.push_back({r, t * kPromptTileRows, keys - rows + t * kPromptTileRows + r, kv_capacity});
     }
     tf_plan plan;
-    int rc = plan_windows(tiles_as_streams.data(), T, &plan, kPromptTileRows, pg && pg->scaled);   // the attention work
+    int rc = plan_windows(tiles_as_streams.data(), T, &plan, kPromptTileRows);   // the attention work
     if (rc != TF_OK) return rc;
     plan.n_streams = 1;
     plan.n_conv_tiles = (rows + kConvTileRows - 1) / kConvTileRows;

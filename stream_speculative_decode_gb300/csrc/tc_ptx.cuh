@@ -284,5 +284,152 @@ __device__ __forceinline__ void tc_dealloc(uint32_t taddr, uint32_t cols) {
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(cols) : "memory");
 }
 
+// ---- what the tensor-core attention kernels share ----------------------------
+// (attn_tc.cu over bf16 caches and pools, attn_scaled_tc.cu over scaled pools):
+// units of work and their tiles, the queue that hands a persistent CTA its units,
+// the queries' tile, Blackwell's paired fp32 instructions. B: a kernel's barriers,
+// with uq, uq_full, uq_empty and grp.
+
+constexpr int kKT = 64;                     // keys per tile
+constexpr int kQRows = 128;                 // MMA M
+constexpr int kQB = kQRows * TF_D * 2;      // 16 KB
+constexpr int kUQ = 4;                      // queue of the CTA's next units
+
+// One unit of work: one key chunk of one stream (an attention item) for one
+// KV head. A CTA takes the units blockIdx.x, blockIdx.x + gridDim.x, ... of the
+// tensor-core items (largest first); every role walks the same list.
+struct Unit {
+    SegStream st;
+    const CUtensorMap* kmap;
+    const CUtensorMap* vmap;
+    int stream, chunk, g, c0, T;
+    int pages;   // paged: the list entry of the chunk's first key
+};
+template <bool kPaged>
+__device__ __forceinline__ Unit unit_of(const SegTable& t, int layer, int u) {
+    Unit U;
+    const AttnItem it = t.items[t.n_items_mma + u / TF_NKV];   // tensor-core items follow the mma.sync ones
+    U.g = u % TF_NKV;
+    U.stream = it.stream;
+    U.chunk = it.chunk;
+    U.st = t.streams[it.stream];
+    U.pages = it.pages;
+    U.c0 = it.chunk * U.st.chunk_keys;
+    U.T = (min(U.st.chunk_keys, U.st.keys - U.c0) + kKT - 1) / kKT;
+    const size_t slot = kPaged ? size_t(layer) : size_t(layer) * t.S + it.stream;
+    U.kmap = t.k_maps + slot;
+    U.vmap = t.v_maps + slot;
+    return U;
+}
+
+// The page ids of tile j of a unit (x only for pages of 64 keys or more, x and
+// y for 32-key pages, all four for 16-key pages).
+__device__ __forceinline__ int4 tile_pages(const SegTable& t, const Unit& U, int j) {
+    const int32_t* ids = t.pages + U.pages + ((j * kKT) >> t.page_shift);   // c0 starts a page
+    if (t.page_shift == 4) return __ldg(reinterpret_cast<const int4*>(ids));
+    if (t.page_shift == 5) {
+        const int2 p = __ldg(reinterpret_cast<const int2*>(ids));
+        return make_int4(p.x, p.y, 0, 0);
+    }
+    return make_int4(__ldg(ids), 0, 0, 0);
+}
+// Tile j of a paged unit: f(offset in the tile, slot in the page, page) for each of its boxes.
+template <typename F>
+__device__ __forceinline__ void tile_boxes(const SegTable& t, const Unit& U, int j, int4 id, F&& f) {
+    const int ps = t.page_shift;
+    f(0u, ps >= 6 ? (U.c0 + j * kKT) & ((1 << ps) - 1) : 0, id.x);
+    if (ps == 5) f(32u * 128u, 0, id.y);
+    if (ps == 4) {
+        f(16u * 128u, 0, id.y);
+        f(32u * 128u, 0, id.z);
+        f(48u * 128u, 0, id.w);
+    }
+}
+
+// Blackwell's three-input max and paired fp32 FMA / add: each of these does
+// the work of two instructions with the same per-element rounding.
+__device__ __forceinline__ float max3f(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t f2pack(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void f2unpack(uint64_t v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t ffma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t fadd2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// The m-th unit the producer handed this CTA after its first (blockIdx.x), or
+// -1: no more (or the CTA gave up). Single-thread consumer (the MMA thread).
+template <typename B>
+__device__ __forceinline__ int next_unit_thread(B* bars, int m, volatile WaitCtl* abortp) {
+    const int slot = m % kUQ;
+    if (!mbar_wait(su32(&bars->uq_full[slot]), (m / kUQ) & 1, abortp)) return -1;
+    const int u = reinterpret_cast<volatile int32_t*>(bars->uq)[slot];
+    mbar_arrive(su32(&bars->uq_empty[slot]));
+    return u;
+}
+// The same for a whole warp: every lane reads, then lane 0 releases the slot.
+template <typename B>
+__device__ __forceinline__ int next_unit_warp(B* bars, int m, volatile WaitCtl* abortp) {
+    const int slot = m % kUQ;
+    int u = -1;
+    if (mbar_wait_warp(su32(&bars->uq_full[slot]), (m / kUQ) & 1, abortp))
+        u = reinterpret_cast<volatile int32_t*>(bars->uq)[slot];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(su32(&bars->uq_empty[slot]));
+    return u;
+}
+
+// The four softmax warps (128 threads) meet; bounded like every wait here.
+template <typename B>
+__device__ __forceinline__ bool group_sync(B* bars, int& ph, volatile WaitCtl* abortp) {
+    mbar_arrive(su32(&bars->grp));
+    const bool ok = mbar_wait(su32(&bars->grp), ph & 1, abortp);
+    ++ph;
+    return ok;
+}
+
+// Query rows of a unit per TMEM lane quadrant: 16 for windows of at most 16
+// rows (dual softmax: lanes L and L + 16 of a quadrant hold the same query),
+// 32 for the prompt's wider windows. Quadrant w holds the unit's queries
+// [per*w, per*w + per), i.e. window rows per/4*w .. +per/4 - 1 with their four
+// heads of the KV head.
+__device__ __forceinline__ int q_per(int rows) { return rows <= 16 ? 16 : 32; }
+
+// The unit's queries into shared memory by TMA (one thread), K-major with the
+// 128-byte swizzle, lane L of the Q tile holding query per*(L/32) + L%per
+// (dual: lanes L%32 < 16 only): boxes of 16 query rows (4 window rows x 4
+// heads), completing `bar` with 16 KB. Rows past the window belong to no query
+// of the unit (other streams' rows, or zeros past the last row): their lanes
+// are not valid rows and their results are never written.
+__device__ __forceinline__ void issue_q(uint32_t sQ, const CUtensorMap* qmap, const Unit& U, uint32_t bar) {
+    const bool dual = U.st.rows <= 16;
+    mbar_expect_tx(bar, dual ? kQB / 2 : kQB);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const int w = k >> 1, h = k & 1;
+        // dual: lanes 0-15 of quadrant w hold window rows 4w..4w+3 (lanes 16-31
+        // hold no query: their S rows are never read); else the halves hold
+        // rows 8w..8w+3 and 8w+4..8w+7
+        if (dual && h) continue;
+        const int row = U.st.row_offset + (dual ? 4 * w : 8 * w + 4 * h);
+        tma_load_3d(sQ + uint32_t(32 * w + 16 * h) * 128u, qmap, 0, 4 * U.g, row, bar);
+    }
+}
+
 }  // namespace
 }  // namespace tf

@@ -130,8 +130,7 @@ constexpr int kAttnTc = 1;    // tcgen05 + TMA kernel (windows of 9 rows or more
 constexpr int kTcMinRows = 9;
 
 // Kernel of a stream: by its window rows, unless TF_ATTN_PATH forces one.
-// Windows over scaled pools all run on an mma.sync kernel (attn_scaled.cu).
-int attn_path_of(int rows, bool scaled = false);
+int attn_path_of(int rows);
 
 // segments.cu: TMA map of a bf16 [rows][256] matrix (the Markov head's W2),
 // boxes of 128 rows x 64 columns with 128-byte swizzle; rows past `rows` read

@@ -120,7 +120,9 @@ def check_attention(q, k, v, vs, keys, out, full=False, what=""):
       scores    a sum of 64 exact products in fp32 (a rounding of up to 2^-23 of the
                 partial sums, which are at most S = sum |q k| / 8, each time), three
                 factors, log2 units: off by e = 70 * 2^-23 * S * log2(e); a weight by
-                e * ln 2 + 2^-21 (ex2 and its argument's rounding, 2^-23 |x|)
+                e * ln 2 + 2^-21 (ex2 and its argument's rounding, 2^-23 |x|). Wide windows
+                split a query into two e4m3 parts, which hold 8 bits down to 2^-9 of its
+                largest: an element below 2^-8 of it is off by at most 2^-17 of the largest
       weights   fp16: 2^-11 of each, or 2^-31 of the chunk's largest weight where that
                 is more, times a value of up to 448 of the chunk's largest V scale
       sums      P.V over n keys: (n / 64 + 64) roundings of 2^-23 of A, and as many
@@ -138,6 +140,9 @@ def check_attention(q, k, v, vs, keys, out, full=False, what=""):
         s = torch.where(sees[:, None], s, -torch.inf)
         p = torch.softmax(s, -1)
         ref, A = p @ v[g], p @ v[g].abs()
+        most = qd[:, g].abs().amax(-1, keepdim=True)
+        low = torch.where(qd[:, g].abs() < 2.0 ** -8 * most, 2.0 ** -17 * most, 0.0)
+        size = size + torch.einsum("rhd,kd->rhk", low, k[g].abs()) / 8 / (70 * 2.0 ** -23)
         top = p.amax(-1) * 2.0 ** (int(vs[g].max()) - 127)
         x = torch.where(sees[:, None], s - s.amax(-1, keepdim=True), 0.0).abs().clamp(max=40).amax(-1)
         e = 70 * 2.0 ** -23 * torch.where(sees[:, None], size, 0.0).amax(-1) + 2.0 ** -21 + 2.0 ** -22 * x

@@ -57,6 +57,31 @@ def test_prompt(tf, page, rows, cached):
     a.check()
 
 
+@pytest.mark.parametrize("path", ["mma", "tc"])
+@pytest.mark.parametrize("page", [16, 128])
+def test_forced_kernel(tf, path, page, monkeypatch):
+    """Every window on either kernel, causal and FULL."""
+    from scaled import ScaledAttn
+    monkeypatch.setenv("TF_ATTN_PATH", path)
+    a = ScaledAttn(tf, [(16, 9000), (1, 70), (10, 33), (4, 5000), (1, 1), (2, 16), (13, 8192), (7, 64)], page, seed=14)
+    for full in (False, True):
+        a.run(full)
+        a.check(full, what=(path, full))
+    assert tf.tf_segments_status(a.seg) == (tf.TF_OK, 0)
+
+
+def test_many_short_units(tf):
+    """Units of a tile or two, more of them than CTAs, run after one another in a CTA."""
+    from scaled import ScaledAttn
+    g = np.random.default_rng(5)
+    a = ScaledAttn(tf, [(int(r), int(r + k)) for r, k in zip(g.integers(9, 17, 150), g.integers(0, 200, 150))], 16, seed=15)
+    for _ in range(3):
+        a.out[0].fill_(float("nan"))
+        a.run()
+        a.check()
+    assert tf.tf_segments_status(a.seg) == (tf.TF_OK, 0)
+
+
 @pytest.mark.parametrize("std", [1e-30, 2e-5, 300.0, 1e30])
 def test_v_of_any_size(tf, std):
     """Scores and outputs far from 1: K of that size with queries of its inverse, V of that size."""
@@ -108,9 +133,11 @@ def test_queries_of_any_size(tf, factor):
     a.check(what=factor)
 
 
-def test_nan_stays_with_the_rows_that_see_it(tf):
+@pytest.mark.parametrize("path", ["mma", "tc"])
+def test_nan_stays_with_the_rows_that_see_it(tf, path, monkeypatch):
     """NaN codes of K and V at the window's own keys, and deep in the cache, over one and several chunks."""
     from scaled import ScaledAttn
+    monkeypatch.setenv("TF_ATTN_PATH", path)
     for keys in (40, 1500, 9000):
         clean = ScaledAttn(tf, [(16, keys), (6, keys), (1, keys)], 32, seed=6)
         clean.run()
@@ -203,6 +230,24 @@ def test_captured_and_replayed(tf):
     p.q[0].copy_(p.q[1])
     g.replay()
     p.check()
+
+
+def test_a_wait_that_runs_out(tf):
+    """With a wait limit of 0 the tensor-core kernel gives up, reports it, and works again afterwards."""
+    from scaled import ScaledAttn
+    a = ScaledAttn(tf, [(16, 9000), (12, 300)], 64, seed=16)
+    want = a.run()[0].clone()
+    torch.cuda.synchronize()
+    try:
+        tf.tf_set_wait_limit_ns(0)
+        a.run()
+        rc, bits_ = tf.tf_segments_status(a.seg)
+        assert rc == tf.TF_ETIMEOUT and bits_ == tf.TF_STATUS_ATTN_TIMEOUT
+    finally:
+        tf.tf_set_wait_limit_ns(tf.TF_WAIT_LIMIT_DEFAULT_NS)
+    assert tf.tf_segments_status(a.seg) == (tf.TF_OK, 0)
+    a.run()
+    assert torch.equal(bits(a.out[0]), bits(want)) and tf.tf_segments_status(a.seg) == (tf.TF_OK, 0)
 
 
 def test_refusals(tf):
