@@ -16,16 +16,17 @@
 // V's codes become fp16 tiles in shared memory (exact) times 2^(ev - E + 7), at most
 // 448 * 2^7; that is exact too down to 2^-28 below the chunk's largest block.
 //
-// Persistent, two CTAs an SM, 9 warps:
-//   warp 8      TMA loads of the codes (64 keys: 4 KB of K, 64-byte swizzle, and 4 KB
+// Persistent, two CTAs an SM, 8 warps:
+//   warp 7      TMA loads of the codes (64 keys: 4 KB of K, 64-byte swizzle, and 4 KB
 //               of V) into a ring of 6 stages, each with its blocks' K scales and V
 //               factors beside it; at a unit's start its V scales, for E;
 //   warps 5, 6  the conversion of the V tiles, half a tile each, ring of 3;
-//   warp 4      lane 0: the q.K MMAs, and the queries' TMA loads;
-//   warp 7      lane 0: the P.V MMAs;
+//   warp 4      lane 0: both products' MMAs, and the queries' TMA loads;
 //   warps 0-3   softmax and records; at a unit's start the queries' two parts, each
 //               row by the thread that owns it.
-// Tensor memory: S/P of tile j at columns 64 * (j % 3), O at 192.
+// Tensor memory: S/P of tile j at columns 64 * (j % 2), O at 128, the queries' parts at
+// 192. (An MMA of 64 keys that reads its 128 query rows from shared memory is bound by
+// that: 4 KB of queries beside 2 KB of keys.)
 //
 // What bounds it: a 64-key tile is 8 KB from HBM, 350 cycles of an SM's share. Of
 // that the tensor cores take some 270 (M = 128 whatever the window's rows), the
@@ -53,12 +54,13 @@ constexpr int kStages = 6;
 constexpr int kRawB = kKT * TF_D;           // 4 KB: the codes of a K or V tile
 constexpr int kStageB = 2 * kRawB;          // K then V
 constexpr int kTileB = kKT * TF_D * 2;      // 8 KB: a tile in fp16
-constexpr int kBuf = 3;                     // S/P and V buffers: tile j uses buffer j % 3
-constexpr int kQ8B = kQRows * TF_D;         // 8 KB: one of the queries' two parts
-constexpr int kThreads = 288;
+constexpr int kBuf = 2;                     // S/P buffers: tile j uses buffer j % 2
+constexpr int kVBuf = 3;                    // V buffers
+constexpr int kThreads = 256;
 constexpr uint32_t kCols = 256;
-constexpr uint32_t kColS = 0;
-constexpr uint32_t kColO = 192;
+constexpr uint32_t kColS = 0;               // + 64 * (tile % 2)
+constexpr uint32_t kColO = 128;             // 64 columns
+constexpr uint32_t kColQ = 192;             // 32 columns: dimensions 0-31 (8 columns a part), then 32-63
 constexpr float kLog2e8 = 0.18033688011112042f;
 constexpr float kSumMax = 32768.f;          // a thread's weights of a tile adding up to more move the row's reference
 constexpr float kHeadroom = 6.f;            // log2 of the largest weight after that
@@ -66,13 +68,14 @@ constexpr int kVShift = 7;
 constexpr int kBlocks = 512 * TF_MAX_ROWS / TF_SCALE_KEYS;   // blocks of the longest chunk
 constexpr int kScaleRing = 16;              // tiles whose scales are kept
 constexpr int kUnits = 8;                   // units whose notes are kept (no role is that far ahead of another)
-constexpr int kUQConsumers = 8;             // the two MMA threads, 2 V converter warps, 4 softmax warps
+constexpr int kUQConsumers = 7;             // the MMA thread, 2 V converter warps, 4 softmax warps
 
 struct Bars {
     uint64_t raw_full[kStages];
     uint64_t v_read[kStages];    // both V converters have read the stage
     uint64_t k_free[kStages];    // its q.K completed
-    uint64_t v_ready[kBuf];
+    uint64_t v_ready[kVBuf];
+    uint64_t v_free[kVBuf];      // its P.V completed
     uint64_t s_full[kBuf];
     uint64_t p_full[kBuf];
     uint64_t o_done[kBuf];       // P.V completed
@@ -82,8 +85,7 @@ struct Bars {
     uint64_t uq_empty[kUQ];
     int32_t uq[kUQ];
     uint64_t grp;
-    uint64_t drain;
-    uint64_t drain_pv;
+    uint64_t drain;              // the MMAs in flight (drained at the end)
     uint32_t tmem_base;
     WaitCtl wc;
     int32_t last;
@@ -92,10 +94,11 @@ struct Bars {
     int32_t nan_key[kUnits][TF_D];           // first key (of the chunk) with a NaN code taken out, by dimension
     alignas(16) float k_scale[kScaleRing][4];    // by running tile, a block each
     alignas(16) uint32_t v_scale[kScaleRing][4]; // 2^(ev - E + 7) as fp16 pairs
-    alignas(16) uint8_t k_byte[kBlocks];     // warp 8: the unit's scale bytes
+    alignas(16) uint32_t block[kBlocks];     // warp 7: where the unit's blocks lie in the pools, and their scale bytes
+    alignas(16) uint8_t k_byte[kBlocks];
     alignas(16) uint8_t v_byte[kBlocks];
 };
-constexpr int kQ8Off = kQB, kVOff = kQ8Off + 2 * kQ8B, kRawOff = kVOff + kBuf * kTileB;
+constexpr int kVOff = kQB, kRawOff = kVOff + kVBuf * kTileB;
 constexpr int kBarsOff = kRawOff + kStages * kStageB;
 constexpr int kSmemBytes = 1024 + kBarsOff + int(sizeof(Bars));
 static_assert(kSmemBytes <= 113 * 1024, "two CTAs an SM");
@@ -115,9 +118,50 @@ __device__ __forceinline__ uint64_t sdesc64(uint32_t addr) {
     d |= uint64_t(4) << 61;
     return d;
 }
-__device__ __forceinline__ void tc_mma_ss_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}"
-                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+// mbar_wait that looks at the clock every kTests tests only: reading %globaltimer takes
+// longer than most waits here, and a chain of waits is what a tile's time is.
+constexpr int kTests = 32;
+__device__ __noinline__ bool wait_long(uint32_t a, uint32_t parity, volatile WaitCtl* wc) {
+    unsigned long long t0 = 0;
+    for (;;) {
+#pragma unroll 1
+        for (int i = 0; i < kTests; ++i)
+            if (mbar_test(a, parity)) return true;
+        if (wc->flag) return false;
+        const unsigned long long now = gtime();
+        if (t0 == 0) t0 = now;
+        if (now - t0 > wc->limit_ns) wc->flag = 1;
+    }
+}
+__device__ __forceinline__ bool wait_thread(uint32_t a, uint32_t parity, volatile WaitCtl* wc) {
+    return mbar_test(a, parity) || wait_long(a, parity, wc);
+}
+// The same by a whole warp, with one outcome for its lanes.
+__device__ __forceinline__ bool wait_warp(uint32_t a, uint32_t parity, volatile WaitCtl* wc) {
+    return __all_sync(0xFFFFFFFFu, wait_thread(a, parity, wc));
+}
+// One lane of a converged warp, the same every time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+    return p != 0;
+}
+// A place in a ring of N barriers and the parity of its current use. A wait for the
+// use before it (parity ^ 1) passes at once in the first round.
+template <int N>
+struct Ring {
+    int i = 0;
+    uint32_t parity = 0;
+    __device__ __forceinline__ void next() {
+        if (++i == N) {
+            i = 0;
+            parity ^= 1u;
+        }
+    }
+};
+__device__ __forceinline__ void tc_mma_ts_f8(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n}"
+                 ::"r"(d), "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc) : "memory");
 }
 
 __device__ __forceinline__ uint32_t pack_h2(float a, float b) {
@@ -185,7 +229,7 @@ __device__ __forceinline__ void softmax_tiles(SoftState& st) {
         const int gj = st.g0 + j;
         const int b = gj % kBuf;
         const uint32_t colS = kColS + 64 * b;
-        if (!mbar_wait_warp(su32(&bars->s_full[b]), (gj / kBuf) & 1, st.abortp)) break;
+        if (!wait_warp(su32(&bars->s_full[b]), (gj / kBuf) & 1, st.abortp)) break;
         tc_fence_after();
         if (st.wact) {
             float f[NB];
@@ -257,7 +301,7 @@ __device__ __forceinline__ void softmax_tiles(SoftState& st) {
                 const float to = mx - kHeadroom;
                 const bool resc = row_slow && to > st.mref;
                 if (__any_sync(0xFFFFFFFFu, resc)) {
-                    if (j >= 1 && !mbar_wait_warp(su32(&bars->o_done[(gj - 1) % kBuf]), ((gj - 1) / kBuf) & 1, st.abortp))
+                    if (j >= 1 && !wait_warp(su32(&bars->o_done[(gj - 1) % kBuf]), ((gj - 1) / kBuf) & 1, st.abortp))
                         break;
                     tc_fence_after();
                     const float alpha = resc ? ex2_approx(st.mref - to) : 1.f;
@@ -301,19 +345,21 @@ __device__ __forceinline__ void softmax_tiles(SoftState& st) {
     }
 }
 
-// The thread's query row (TMEM lane 32 * warp + row of the tile) from bf16 to its two
-// e4m3 parts, under the power of two that puts its largest at 2^7..2^8; returns the
-// factor of its scores. Dual: two threads a row, half of its dimensions each.
+// The thread's query row (tensor memory lane 32 * warp + row of the tile) from bf16 to
+// its two e4m3 parts in tensor memory, under the power of two that puts its largest at
+// 2^7..2^8; returns the factor of its scores. Dual: two threads a row, 32 dimensions
+// each. 8 columns hold 32 dimensions (an MMA's K) of a part.
 template <bool DUAL>
-__device__ __forceinline__ float convert_query(uint32_t sQ, uint32_t sQ8, int warp, int lane) {
+__device__ __forceinline__ float convert_query(uint32_t sQ, uint32_t trow, int warp, int lane) {
     const int r = 32 * warp + (DUAL ? (lane & 15) : lane);
-    constexpr int NP = DUAL ? 2 : 4;   // pieces of 16 dimensions
-    const int p0 = DUAL ? (lane >> 4) * 2 : 0;
+    constexpr int NP = DUAL ? 4 : 8;   // pieces of 8 dimensions
+    const int p0 = DUAL ? (lane >> 4) * 4 : 0;
+    uint4 v[NP];
     uint32_t most = 0;
 #pragma unroll
-    for (int i = 0; i < 2 * NP; ++i) {
-        const uint4 v = lds128(sQ + r * 128 + (((2 * p0 + i) ^ (r & 7)) << 4));
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    for (int i = 0; i < NP; ++i) {
+        v[i] = lds128(sQ + r * 128 + (((p0 + i) ^ (r & 7)) << 4));
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
         for (int k = 0; k < 4; ++k)
             most = max(most, max(finite_bits(__uint_as_float(w[k] << 16)), finite_bits(__uint_as_float(w[k] & 0xFFFF0000u))));
@@ -321,38 +367,28 @@ __device__ __forceinline__ float convert_query(uint32_t sQ, uint32_t sQ8, int wa
     if (DUAL) most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 16));
     const int up = min(134 - int(most >> 23), 126);
     const float mul = __uint_as_float(uint32_t(127 + up) << 23);
+    uint32_t q8[NP * 4];   // for each 32 dimensions: 8 words of the first part, 8 of the second
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-        uint32_t hi[4], lo[4];
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const uint4 v = lds128(sQ + r * 128 + (((2 * (p0 + i) + k) ^ (r & 7)) << 4));
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const float y[4] = {__uint_as_float(w[2 * c] << 16) * mul, __uint_as_float(w[2 * c] & 0xFFFF0000u) * mul,
-                                    __uint_as_float(w[2 * c + 1] << 16) * mul,
-                                    __uint_as_float(w[2 * c + 1] & 0xFFFF0000u) * mul};
-                const uint32_t h = e4m3_quad(y[0], y[1], y[2], y[3]);
-                const float2 a = h2_to_f2(e4m3_low(h)), b = h2_to_f2(e4m3_high(h));
-                hi[2 * k + c] = h;
-                lo[2 * k + c] = e4m3_quad(y[0] - a.x, y[1] - a.y, y[2] - b.x, y[3] - b.y);
-            }
+        for (int c = 0; c < 2; ++c) {
+            const float y[4] = {__uint_as_float(w[2 * c] << 16) * mul, __uint_as_float(w[2 * c] & 0xFFFF0000u) * mul,
+                                __uint_as_float(w[2 * c + 1] << 16) * mul,
+                                __uint_as_float(w[2 * c + 1] & 0xFFFF0000u) * mul};
+            const uint32_t h = e4m3_quad(y[0], y[1], y[2], y[3]);
+            const float2 a = h2_to_f2(e4m3_low(h)), b = h2_to_f2(e4m3_high(h));
+            const int at = (i >> 2) * 16 + (i & 3) * 2 + c;
+            q8[at] = h;
+            q8[at + 8] = e4m3_quad(y[0] - a.x, y[1] - a.y, y[2] - b.x, y[3] - b.y);
         }
-        const uint32_t at = sQ8 + r * 64 + (((p0 + i) ^ ((r >> 1) & 3)) << 4);   // the 64-byte swizzle
-        sts128(at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-        sts128(at + kQ8B, make_uint4(lo[0], lo[1], lo[2], lo[3]));
     }
+    if constexpr (DUAL)
+        tc_st16x2_16<16>(trow + kColQ, q8);
+    else
+        tc_st32(trow + kColQ, q8);
+    tc_wait_st();
     return __uint_as_float(uint32_t(127 - up) << 23) * kLog2e8;
-}
-
-// The index of block i of a unit's chunk in the layer's pools (and scales).
-__device__ __forceinline__ uint32_t block_of(const SegTable& t, const Unit& U, int i, int32_t page) {
-    const int bs = t.page_shift - 4;
-    return ((uint32_t(page) * TF_NKV + U.g) << bs) + (i & ((1 << bs) - 1));
-}
-__device__ __forceinline__ int32_t page_of(const SegTable& t, const Unit& U, int i) {
-    return __ldg(t.pages + U.pages + (i >> (t.page_shift - 4)));
 }
 
 // Where the 16 codes `p` (0..3) of key row r go in a fp16 tile (128-byte rows, 128-byte
@@ -370,7 +406,7 @@ attn_scaled_tc_kernel(SegTable t, int layer, float* __restrict__ part_o, float2*
     const uint32_t raw = su32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     unsigned char* gbase = smem_raw + (base - raw);
-    const uint32_t sQ = base, sQ8 = base + kQ8Off, sV = base + kVOff, sRaw = base + kRawOff;
+    const uint32_t sQ = base, sV = base + kVOff, sRaw = base + kRawOff;
     Bars* bars = reinterpret_cast<Bars*>(gbase + kBarsOff);
     volatile WaitCtl* abortp = &bars->wc;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -382,10 +418,13 @@ attn_scaled_tc_kernel(SegTable t, int layer, float* __restrict__ part_o, float2*
             mbar_init(su32(&bars->k_free[s]), 1);
         }
         for (int b = 0; b < kBuf; ++b) {
-            mbar_init(su32(&bars->v_ready[b]), 2);
             mbar_init(su32(&bars->s_full[b]), 1);
             mbar_init(su32(&bars->p_full[b]), 4);
             mbar_init(su32(&bars->o_done[b]), 1);
+        }
+        for (int b = 0; b < kVBuf; ++b) {
+            mbar_init(su32(&bars->v_ready[b]), 2);
+            mbar_init(su32(&bars->v_free[b]), 1);
         }
         mbar_init(su32(&bars->q_full), 1);
         mbar_init(su32(&bars->q_ready), 4);
@@ -395,8 +434,7 @@ attn_scaled_tc_kernel(SegTable t, int layer, float* __restrict__ part_o, float2*
         }
         mbar_init(su32(&bars->grp), 128);
         mbar_init(su32(&bars->drain), 1);
-        mbar_init(su32(&bars->drain_pv), 1);
-        bars->wc.flag = 0;
+        bars->wc.flag = t.wait_ns == 0;   // a limit of 0: what does not complete at once is given up
         bars->wc.limit_ns = t.wait_ns;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -410,92 +448,110 @@ attn_scaled_tc_kernel(SegTable t, int layer, float* __restrict__ part_o, float2*
     const uint32_t tmem = bars->tmem_base;
 
     if (warp == 4) {
-        // ------------------------------------------------------------ q.K MMAs
-        if (lane == 0) {
-            const uint64_t dq = sdesc64(sQ8);
-            bool ok = true;
-            int gt = 0, n = 0, q_issued = 0;
-            if (int(blockIdx.x) < n_units) {
-                issue_q(sQ, &qmap, unit_of<true>(t, layer, blockIdx.x), su32(&bars->q_full));
-                q_issued = 1;
-            }
-            for (int u = blockIdx.x; u >= 0 && ok; ++n) {
-                const int T = unit_of<true>(t, layer, u).T;
-                ok = mbar_wait(su32(&bars->q_ready), n & 1, abortp);
-                if (!ok) break;
+        // ------------------------------------------------------------ MMAs
+        // P.V of tile j, then the q.K of tile j + 2, which takes over its S buffer. The whole
+        // warp walks the loop and one lane of it issues: with the control flow the warp's,
+        // addresses and descriptors stay in uniform registers (in a lone thread's code an
+        // MMA took some 70 cycles to issue, and everything else stands behind it).
+        Ring<kStages> kr;   // the stage of the next q.K
+        Ring<kVBuf> vr;     // the V buffer of the next P.V
+        Ring<kUQ> ur;
+        uint32_t qs = 0, ps = 0;   // their S buffers' uses so far: buffer & 1, parity >> 1
+        const uint64_t dk0 = sdesc64(sRaw), dv0 = sdesc(sV, kTileB, 1024);
+        bool ok = true;
+        if (elect_one()) issue_q(sQ, &qmap, unit_of<true>(t, layer, blockIdx.x), su32(&bars->q_full));
+        int q_issued = 1;
+        for (int u = blockIdx.x, n = 0; u >= 0 && ok; ++n) {
+            const int T = unit_of<true>(t, layer, u).T;
+            auto qk = [&]() {
+                const uint32_t b = qs & 1;
+                if (!wait_warp(su32(&bars->raw_full[kr.i]), kr.parity, abortp) ||
+                    !wait_warp(su32(&bars->o_done[b]), (qs >> 1 & 1) ^ 1, abortp))
+                    return false;
                 tc_fence_after();
-                for (int j = 0; j < T && ok; ++j) {
-                    const int g1 = gt + j, s = g1 % kStages, b = g1 % kBuf;
-                    ok = mbar_wait(su32(&bars->raw_full[s]), (g1 / kStages) & 1, abortp);
-                    if (!ok) break;
-                    if (g1 >= kBuf) {   // P.V(g1-3) has released S buffer b
-                        ok = mbar_wait(su32(&bars->o_done[b]), ((g1 - kBuf) / kBuf) & 1, abortp);
-                        if (!ok) break;
-                    }
-                    tc_fence_after();
-                    const uint64_t dk = sdesc64(sRaw + s * kStageB);
+                if (elect_one()) {
+                    const uint64_t dk = dk0 + uint32_t(kr.i) * (kStageB >> 4);
 #pragma unroll
                     for (int k = 0; k < 4; ++k)   // both parts, K = 64 in 2 steps of 32 bytes each
-                        tc_mma_ss_f8(tmem + kColS + 64 * b, dq + (k >> 1) * (kQ8B >> 4) + 2 * (k & 1), dk + 2 * (k & 1),
-                                     kIdescQK, k > 0 ? 1u : 0u);
+                        tc_mma_ts_f8(tmem + kColS + 64 * b, tmem + kColQ + 8 * k, dk + 2 * (k >> 1), kIdescQK,
+                                     k > 0 ? 1u : 0u);
                     tc_commit(su32(&bars->s_full[b]));
-                    tc_commit(su32(&bars->k_free[s]));
+                    tc_commit(su32(&bars->k_free[kr.i]));
                 }
-                gt += T;
+                __syncwarp();
+                kr.next();
+                ++qs;
+                return true;
+            };
+            ok = wait_warp(su32(&bars->q_ready), n & 1, abortp);
+            if (!ok) break;
+            tc_fence_after();
+            ok = qk() && (T < 2 || qk());
+            int next = -2;   // the next unit, not known yet
+            auto enter_next = [&]() {
+                next = reinterpret_cast<volatile int32_t*>(bars->uq)[ur.i];
+                __syncwarp();
+                if (elect_one()) {
+                    mbar_arrive(su32(&bars->uq_empty[ur.i]));
+                    // the bf16 tile of the queries has been free since q_ready
+                    if (next >= 0) issue_q(sQ, &qmap, unit_of<true>(t, layer, next), su32(&bars->q_full));
+                }
+                __syncwarp();
+                ur.next();
+                if (next >= 0) ++q_issued;
+            };
+            for (int j = 0; j < T && ok; ++j) {
+                const uint32_t b = ps & 1;
+                ok = wait_warp(su32(&bars->p_full[b]), ps >> 1 & 1, abortp) &&
+                     wait_warp(su32(&bars->v_ready[vr.i]), vr.parity, abortp);
                 if (!ok) break;
-                // the next unit's queries: their bf16 tile has been free since q_ready
-                u = next_unit_thread(bars, n, abortp);
-                if (u >= 0) {
-                    issue_q(sQ, &qmap, unit_of<true>(t, layer, u), su32(&bars->q_full));
-                    ++q_issued;
-                }
-            }
-            tc_commit(su32(&bars->drain));
-            mbar_drain(su32(&bars->drain), 0);
-            if (q_issued > 0) mbar_drain(su32(&bars->q_full), (q_issued - 1) & 1);   // the last query load has landed
-        }
-        __syncwarp();
-    } else if (warp == 7) {
-        // ------------------------------------------------------------ P.V MMAs
-        if (lane == 0) {
-            bool ok = true;
-            int gt = 0, n = 0;
-            for (int u = blockIdx.x; u >= 0 && ok; ++n) {
-                const int T = unit_of<true>(t, layer, u).T;
-                for (int j = 0; j < T && ok; ++j) {
-                    const int g2 = gt + j, b = g2 % kBuf;
-                    ok = mbar_wait(su32(&bars->p_full[b]), (g2 / kBuf) & 1, abortp);
-                    if (!ok) break;
-                    ok = mbar_wait(su32(&bars->v_ready[b]), (g2 / kBuf) & 1, abortp);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint64_t dv = sdesc(sV + b * kTileB, kTileB, 1024);
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint64_t dv = dv0 + uint32_t(vr.i) * (kTileB >> 4);
 #pragma unroll
                     for (int k = 0; k < kKT / 16; ++k)
                         tc_mma_ts(tmem + kColO, tmem + kColS + 64 * b + 8 * k, dv + 128 * k, kIdescPV,
                                   (j > 0 || k > 0) ? 1u : 0u);
                     tc_commit(su32(&bars->o_done[b]));
+                    tc_commit(su32(&bars->v_free[vr.i]));
                 }
-                gt += T;
-                if (ok) u = next_unit_thread(bars, n, abortp);
+                __syncwarp();
+                vr.next();
+                ++ps;
+                if (j + 2 < T)
+                    ok = qk();
+                else if (next == -2 && __all_sync(0xFFFFFFFFu, mbar_test(su32(&bars->uq_full[ur.i]), ur.parity)))
+                    enter_next();
             }
-            tc_commit(su32(&bars->drain_pv));
-            mbar_drain(su32(&bars->drain_pv), 0);
+            if (ok && next == -2) {
+                ok = wait_warp(su32(&bars->uq_full[ur.i]), ur.parity, abortp);
+                if (ok) enter_next();
+            }
+            u = next;
+        }
+        if (elect_one()) {
+            tc_commit(su32(&bars->drain));
+            mbar_drain(su32(&bars->drain), 0);
+            mbar_drain(su32(&bars->q_full), (q_issued - 1) & 1);   // the last query load has landed
         }
         __syncwarp();
-    } else if (warp == 8) {
+    } else if (warp == 7) {
         // ------------------------------------------------------------ loads, scales
         const uint64_t once = l2_evict_first();
         const uint8_t *const ks = t.k_scale[layer], *const vs = t.v_scale[layer];
+        Ring<kStages> r;
+        Ring<kUQ> ur;
         int gt = 0;
         bool ok = true;
         for (int u = blockIdx.x, m = 0; u >= 0 && ok; ++m) {
             const Unit U = unit_of<true>(t, layer, u);
             const int nblocks = (min(U.st.chunk_keys, U.st.keys - U.c0) + TF_SCALE_KEYS - 1) / TF_SCALE_KEYS;
-            int4 pid = tile_pages(t, U, 0);
+            const int bs = t.page_shift - 4;
             uint32_t top = 0;
             for (int i = lane; i < 4 * U.T; i += 32) {   // slots past the chunk: any K scale, no V
-                const uint32_t at = block_of(t, U, i, page_of(t, U, i));
+                const uint32_t at = ((uint32_t(__ldg(t.pages + U.pages + (i >> bs))) * TF_NKV + U.g) << bs) +
+                                    (i & ((1 << bs) - 1));
+                bars->block[i] = at;
                 const uint32_t e = i < nblocks ? uint32_t(__ldg(vs + at)) : 0u;
                 bars->k_byte[i] = __ldg(ks + at);
                 bars->v_byte[i] = uint8_t(e);
@@ -505,13 +561,13 @@ attn_scaled_tc_kernel(SegTable t, int layer, float* __restrict__ part_o, float2*
             if (lane == 0) bars->top[m % kUnits] = int32_t(top);
             __syncwarp();
             for (int j = 0; j < U.T; ++j, ++gt) {
-                const int s = gt % kStages;
-                if (gt >= kStages &&
-                    (!mbar_wait_warp(su32(&bars->v_read[s]), ((gt - kStages) / kStages) & 1, abortp) ||
-                     !mbar_wait_warp(su32(&bars->k_free[s]), ((gt - kStages) / kStages) & 1, abortp))) {
+                const int s = r.i;
+                if (!wait_warp(su32(&bars->v_read[s]), r.parity ^ 1u, abortp) ||
+                    !wait_warp(su32(&bars->k_free[s]), r.parity ^ 1u, abortp)) {
                     ok = false;
                     break;
                 }
+                r.next();
                 if (lane < 4) {
                     bars->k_scale[gt % kScaleRing][lane] = scale_value(bars->k_byte[4 * j + lane]);
                     bars->v_scale[gt % kScaleRing][lane] = v_factor(int(top) - int(bars->v_byte[4 * j + lane]));
@@ -520,13 +576,15 @@ attn_scaled_tc_kernel(SegTable t, int layer, float* __restrict__ part_o, float2*
                 if (lane == 0) {
                     const uint32_t bar = su32(&bars->raw_full[s]);
                     mbar_expect_tx(bar, kStageB);
-                    tile_boxes(t, U, j, pid, [&](uint32_t off, int slot, int page) {   // off: of 128-byte rows
-                        const int head = page * TF_NKV + U.g;
-                        tma_load_3d_hint(sRaw + s * kStageB + off / 2, U.kmap, 0, slot, head, bar, once);
-                        tma_load_3d_hint(sRaw + s * kStageB + kRawB + off / 2, U.vmap, 0, slot, head, bar, once);
-                    });
+                    // a box is 64 keys of a head, or the whole of a smaller page
+                    for (int i = 0; i < 4; i += bs >= 2 ? 4 : 1 << bs) {
+                        const uint32_t at = bars->block[4 * j + i];
+                        const int head = int(at >> bs), row = int(at & ((1u << bs) - 1u)) * TF_SCALE_KEYS;
+                        const uint32_t dst = sRaw + s * kStageB + i * (TF_SCALE_KEYS * TF_D);
+                        tma_load_3d_hint(dst, U.kmap, 0, row, head, bar, once);
+                        tma_load_3d_hint(dst + kRawB, U.vmap, 0, row, head, bar, once);
+                    }
                 }
-                if (j + 1 < U.T) pid = tile_pages(t, U, j + 1);
             }
             if (!ok) break;
             // the next unit of the launch, for this CTA's roles
@@ -534,12 +592,12 @@ attn_scaled_tc_kernel(SegTable t, int layer, float* __restrict__ part_o, float2*
             if (lane == 0) un = int(gridDim.x) + atomicAdd(&t.tc_work[2 * layer], 1);
             un = __shfl_sync(0xFFFFFFFFu, un, 0);
             if (un >= n_units) un = -1;
-            const int slot = m % kUQ;
-            if (m >= kUQ && !mbar_wait_warp(su32(&bars->uq_empty[slot]), ((m / kUQ) - 1) & 1, abortp)) break;
+            if (!wait_warp(su32(&bars->uq_empty[ur.i]), ur.parity ^ 1u, abortp)) break;
             if (lane == 0) {
-                bars->uq[slot] = un;
-                mbar_arrive(su32(&bars->uq_full[slot]));
+                bars->uq[ur.i] = un;
+                mbar_arrive(su32(&bars->uq_full[ur.i]));
             }
+            ur.next();
             __syncwarp();
             u = un;
         }
@@ -550,6 +608,8 @@ attn_scaled_tc_kernel(SegTable t, int layer, float* __restrict__ part_o, float2*
     } else if (warp == 5 || warp == 6) {
         // ------------------------------------------------------------ V tiles, rows 32 * (warp - 5) ..
         const int r0 = 32 * (warp - 5);
+        Ring<kStages> r;
+        Ring<kVBuf> vr;
         int gt = 0;
         bool ok = true;
         for (int u = blockIdx.x, m = 0; u >= 0 && ok; ++m) {
@@ -557,11 +617,12 @@ attn_scaled_tc_kernel(SegTable t, int layer, float* __restrict__ part_o, float2*
             const int nkeys = min(U.st.chunk_keys, U.st.keys - U.c0);
             const int lim_all = min((full ? U.st.keys : U.st.keys - U.st.rows + 1) - U.c0, nkeys);
             for (int j = 0; j < U.T; ++j, ++gt) {
-                const int s = gt % kStages, b = gt % kBuf;
-                if (!mbar_wait_warp(su32(&bars->raw_full[s]), (gt / kStages) & 1, abortp)) {
+                const int s = r.i, b = vr.i;
+                if (!wait_warp(su32(&bars->raw_full[s]), r.parity, abortp)) {
                     ok = false;
                     break;
                 }
+                r.next();
                 const uint32_t src = sRaw + s * kStageB + kRawB + r0 * TF_D + uint32_t(lane) * 16u;
                 const uint2 f = *reinterpret_cast<const uint2*>(bars->v_scale[gt % kScaleRing] + (r0 >> 4));
                 uint4 v[4];
@@ -587,10 +648,11 @@ attn_scaled_tc_kernel(SegTable t, int layer, float* __restrict__ part_o, float2*
                         }
                     }
                 }
-                if (gt >= kBuf && !mbar_wait_warp(su32(&bars->o_done[b]), ((gt - kBuf) / kBuf) & 1, abortp)) {
+                if (!wait_warp(su32(&bars->v_free[b]), vr.parity ^ 1u, abortp)) {
                     ok = false;
                     break;
                 }
+                vr.next();
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {   // rows 8 i .. 8 i + 7 of the half are of its block i / 2
                     const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
@@ -634,9 +696,9 @@ attn_scaled_tc_kernel(SegTable t, int layer, float* __restrict__ part_o, float2*
             ss.cq = 0.f;
             ss.mref = -INFINITY;
             ss.l = 0.f;
-            if (mbar_wait_warp(su32(&bars->q_full), m & 1, abortp))
-                ss.cq = dual ? convert_query<true>(sQ, sQ8, warp, lane) : convert_query<false>(sQ, sQ8, warp, lane);
-            fence_async_smem();
+            if (wait_warp(su32(&bars->q_full), m & 1, abortp))
+                ss.cq = dual ? convert_query<true>(sQ, trow, warp, lane) : convert_query<false>(sQ, trow, warp, lane);
+            tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(su32(&bars->q_ready));
             if (dual)
@@ -645,7 +707,7 @@ attn_scaled_tc_kernel(SegTable t, int layer, float* __restrict__ part_o, float2*
                 softmax_tiles<false>(ss);
             gt += U.T;
             const int un = next_unit_warp(bars, m, abortp);
-            if (!abortp->flag) mbar_wait_warp(su32(&bars->o_done[(gt - 1) % kBuf]), ((gt - 1) / kBuf) & 1, abortp);
+            if (!abortp->flag) wait_warp(su32(&bars->o_done[(gt - 1) % kBuf]), ((gt - 1) / kBuf) & 1, abortp);
             tc_fence_after();
             const bool aborted = abortp->flag != 0;
             const volatile int32_t* const nan_key = bars->nan_key[m % kUnits];
