@@ -10,7 +10,8 @@
 // stream that the next addition reads. A row is read once and stays in registers
 // between its sum of squares and its codes: a CTA a row, 8 columns a thread (and
 // pass of the width), 4 neighbouring lanes a scale. HBM bound: 7 bytes a value
-// with a residual (3 without).
+// with a residual (3 without). 16,381 rows of 2,048 with a residual: 36.8 us, 6.4
+// TB/s, 96 % of the measured copy rate.
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -168,8 +169,11 @@ extern "C" int tf_norm_rows(const void* x, int64_t x_stride, const void* res, in
     const NormRows a = {static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(res), static_cast<const uint16_t*>(w),
                         static_cast<uint16_t*>(sum), static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales),
                         x_stride, res_stride, sum_stride, eps, width};
-    const int vecs = width / kVec;
-    const int threads = vecs < kMaxThreads ? (vecs + 31) / 32 * 32 : kMaxThreads;
+    // Up to 128 threads a row: the more rows an SM has under way, the better its loads cover one another's latency
+    // (16,381 rows of 2,048: 64 or 128 threads 36.8 us, 256 or 512 threads 44.0 us). More than four vectors a thread
+    // would cost more in registers than that gains.
+    const int vecs = width / kVec, most = vecs <= 4 * 128 ? 128 : kMaxThreads;
+    const int threads = vecs < most ? (vecs + 31) / 32 * 32 : most;
     const int iters = (vecs + threads - 1) / threads;
     const dim3 grid(R), block(threads);
     if (iters == 1) return launch_pdl(norm_rows_kernel<1>, grid, block, 0, stream, a);
