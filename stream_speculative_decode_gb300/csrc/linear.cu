@@ -18,15 +18,15 @@
 // x lies in shared memory in the order in which the fragments want it (a row's 8
 // inputs 8 w .. 8 w + 7 of a group as 0 4 1 5 2 6 3 7, the groups of a 128-input
 // chunk side by side), staged once a CTA where it fits. One CTA of 16 warps an
-// SM. For few outputs, S warps share a 16-output tile, each with its part of the
-// inputs, and their sums are added in order through shared memory.
+// SM with a run of 16-output tiles, whose inputs the warps share out evenly.
 //
-// Measured, 128,000 outputs by 2,048 inputs (139 MB): 1 row 37.1 us, 16 rows 45.8
-// us (3.8 and 3.1 TB/s; the same loads alone 21.5 us). What bounds it is the
-// ALU: 56 of a chunk's 144 instructions take its codes apart, at half rate.
-// Loads a chunk at a time into a ring in shared memory (47 and 80 us), into the
-// registers just used (48.5 and 56) or with the scales' codes picked apart as they
-// arrive (44 and 51) were slower: a set of registers ahead hides the memory.
+// Measured, 128,000 outputs by 2,048 inputs (139 MB): 1 row 27.7 us, 16 rows 34.9
+// us (5.0 and 4.1 TB/s; the same loads alone 21.5 us). What bounds it is issue:
+// of a chunk's 144 instructions 56 take its codes apart at half rate, and 16 warps
+// wait for one another's turn, not for memory. Warps that share tiles and meet at
+// each one's end (37.1 and 45.8), loads a chunk at a time into a ring in shared
+// memory (47 and 80), into the registers just used (48.5 and 56) or with the scales'
+// codes picked apart as they arrive (44 and 51) were slower.
 #include <cuda_bf16.h>
 
 #include "scaled.cuh"
@@ -86,35 +86,60 @@ __device__ __forceinline__ uint4 load_once(const uint8_t* p) {
 // rows' pieces fall on different banks.
 __host__ __device__ constexpr int row_bytes(int chunks) { return chunks * kChunk * 2 + 64; }
 
-// Rows [r0, r0 + 8 NT) and chunks [c0, c0 + n) of x into shared memory.
-template <int NT>
-__device__ __forceinline__ void stage(const Linear& a, int r0, int c0, int n, unsigned char* sx, int rowb) {
-    const int units = n * kChunk / 8;   // 8 inputs each
-    for (int i = threadIdx.x; i < 8 * NT * units; i += kThreads) {
-        const int r = i / units, u = i % units, k = (c0 * kChunk) + u * 8;
-        uint32_t v[4] = {0u, 0u, 0u, 0u};   // inputs (0, 4), (1, 5), (2, 6), (3, 7)
-        if (r0 + r < a.R && k < a.K) {
-            const int64_t at = int64_t(r0 + r) * a.x_stride + k;
-            if (a.xs) {
-                const uint2 c = *reinterpret_cast<const uint2*>(a.x + at);
-                const float e = scale_value(a.xs[int64_t(r0 + r) * (a.K / kGroup) + k / kGroup]);
-                const float2 p = h2_to_f2(e4m3_low(c.x)), q = h2_to_f2(e4m3_high(c.x));
-                const float2 s = h2_to_f2(e4m3_low(c.y)), t = h2_to_f2(e4m3_high(c.y));
-                v[0] = pack_bf2(p.x * e, s.x * e);
-                v[1] = pack_bf2(p.y * e, s.y * e);
-                v[2] = pack_bf2(q.x * e, t.x * e);
-                v[3] = pack_bf2(q.y * e, t.y * e);
-            } else {
-                const uint4 c = *reinterpret_cast<const uint4*>(a.x + 2 * at);
-                v[0] = __byte_perm(c.x, c.z, 0x5410);
-                v[1] = __byte_perm(c.x, c.z, 0x7632);
-                v[2] = __byte_perm(c.y, c.w, 0x5410);
-                v[3] = __byte_perm(c.y, c.w, 0x7632);
+// Rows [r0, r0 + 8 NT) and chunks [c0, c0 + n) of x into shared memory, in units of 8
+// inputs: four a thread in flight together (16 rows of 2,048: 5.8 us a call of few
+// outputs, one by one 6.8), one for up to 8 rows, where most units may be of rows that
+// are not there (1 row of 128,000 outputs: 27.7 us, four together 28.1).
+template <int NT, bool kCodes>
+__device__ __forceinline__ void stage_as(const Linear& a, int r0, int c0, int n, unsigned char* sx, int rowb) {
+    constexpr int kFly = NT == 1 ? 1 : 4;
+    const int units = n * kChunk / 8, total = 8 * NT * units;
+    for (int i0 = threadIdx.x; i0 < total; i0 += kFly * kThreads) {
+        uint4 v[kFly];
+        uint8_t e[kFly];
+#pragma unroll
+        for (int j = 0; j < kFly; ++j) {
+            const int i = i0 + j * kThreads, r = r0 + i / units, k = c0 * kChunk + i % units * 8;
+            v[j] = make_uint4(0u, 0u, 0u, 0u);
+            e[j] = 127;
+            if (i < total && r < a.R && k < a.K) {
+                const int64_t at = int64_t(r) * a.x_stride + k;
+                if constexpr (kCodes) {
+                    const uint2 c = *reinterpret_cast<const uint2*>(a.x + at);
+                    v[j].x = c.x;
+                    v[j].y = c.y;
+                    e[j] = a.xs[int64_t(r) * (a.K / kGroup) + k / kGroup];
+                } else {
+                    v[j] = *reinterpret_cast<const uint4*>(a.x + 2 * at);
+                }
             }
         }
-        const int chunk = u >> 4, lane = (u >> 2) & 3, w = u & 3;
-        *reinterpret_cast<uint4*>(sx + r * rowb + chunk * 256 + w * 64 + lane * 16) = make_uint4(v[0], v[1], v[2], v[3]);
+#pragma unroll
+        for (int j = 0; j < kFly; ++j) {
+            const int i = i0 + j * kThreads, r = i / units, u = i % units;
+            if (i >= total) break;
+            const uint4 c = v[j];
+            uint4 o;   // inputs (0, 4), (1, 5), (2, 6), (3, 7)
+            if constexpr (kCodes) {
+                const float f = scale_value(e[j]);
+                const float2 p = h2_to_f2(e4m3_low(c.x)), q = h2_to_f2(e4m3_high(c.x));
+                const float2 s = h2_to_f2(e4m3_low(c.y)), t = h2_to_f2(e4m3_high(c.y));
+                o = make_uint4(pack_bf2(p.x * f, s.x * f), pack_bf2(p.y * f, s.y * f), pack_bf2(q.x * f, t.x * f),
+                               pack_bf2(q.y * f, t.y * f));
+            } else {
+                o = make_uint4(__byte_perm(c.x, c.z, 0x5410), __byte_perm(c.x, c.z, 0x7632), __byte_perm(c.y, c.w, 0x5410),
+                               __byte_perm(c.y, c.w, 0x7632));
+            }
+            *reinterpret_cast<uint4*>(sx + r * rowb + (u >> 4) * 256 + (u & 3) * 64 + ((u >> 2) & 3) * 16) = o;
+        }
     }
+}
+template <int NT>
+__device__ __forceinline__ void stage(const Linear& a, int r0, int c0, int n, unsigned char* sx, int rowb) {
+    if (a.xs)
+        stage_as<NT, true>(a, r0, c0, n, sx, rowb);
+    else
+        stage_as<NT, false>(a, r0, c0, n, sx, rowb);
 }
 
 // A lane's weights of one chunk of its two outputs, and the scales (kWords: the
@@ -193,81 +218,87 @@ __device__ __forceinline__ void group_sync(int group, int S) {
     asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(S * 32) : "memory");
 }
 
+template <int NT>
+__device__ __forceinline__ float4 tile_sum(const float (&acc)[NT][2][4], int nt) {
+    const float (&v)[2][4] = acc[nt];
+    return make_float4(v[0][0] + v[1][0], v[0][1] + v[1][1], v[0][2] + v[1][2], v[0][3] + v[1][3]);
+}
+__device__ __forceinline__ void add4(float4& v, const float4& u) {
+    v.x += u.x;
+    v.y += u.y;
+    v.z += u.z;
+    v.w += u.w;
+}
+// A lane's sums of rows r, r + 1 and outputs n, n + 8, scaled and stored.
+__device__ __forceinline__ void store_sums(const Linear& a, int n, int r, const float4& v) {
+    const float d[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int nn = n + 8 * (e >> 1), rr = r + (e & 1);
+        if (nn < a.N && rr < a.R) {
+            const __nv_bfloat16 b = __float2bfloat16_rn(d[e] * __ldg(a.s + nn));
+            a.y[int64_t(rr) * a.y_stride + nn] = *reinterpret_cast<const uint16_t*>(&b);
+        }
+    }
+}
+
 // A tile's end: the parts' sums added in order, scaled and stored.
 template <int NT>
 __device__ __forceinline__ void finish_tile(const Linear& a, int S, int tile, int tiles, int r0, int group, int part,
                                             const float (&acc)[NT][2][4], float4* sums) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g8 = lane >> 2, t4 = lane & 3;
-    auto total = [](const float (&v)[2][4]) {
-        return make_float4(v[0][0] + v[1][0], v[0][1] + v[1][1], v[0][2] + v[1][2], v[0][3] + v[1][3]);
-    };
-    auto store = [&](int nt, const float4& v) {
-        const int n = tile * 16 + g8, r = r0 + nt * 8 + 2 * t4;
-        const float d[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int nn = n + 8 * (e >> 1), rr = r + (e & 1);
-            if (nn < a.N && rr < a.R) {
-                const __nv_bfloat16 b = __float2bfloat16_rn(d[e] * __ldg(a.s + nn));
-                a.y[int64_t(rr) * a.y_stride + nn] = *reinterpret_cast<const uint16_t*>(&b);
-            }
-        }
-    };
+    const int n = tile * 16 + g8, r = r0 + 2 * t4;
     if (S == 1) {
         if (tile < tiles)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) store(nt, total(acc[nt]));
+            for (int nt = 0; nt < NT; ++nt) store_sums(a, n, r + nt * 8, tile_sum<NT>(acc, nt));
     } else {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
-            sums[(warp * NT + nt) * 32 + lane] = total(acc[nt]);
+            sums[(warp * NT + nt) * 32 + lane] = tile_sum<NT>(acc, nt);
         group_sync(group, S);
         if (tile < tiles)
             for (int nt = part; nt < NT; nt += S) {   // the parts' sums in order
                 float4 v = sums[(group * S * NT + nt) * 32 + lane];
-                for (int p = 1; p < S; ++p) {
-                    const float4 u = sums[((group * S + p) * NT + nt) * 32 + lane];
-                    v.x += u.x;
-                    v.y += u.y;
-                    v.z += u.z;
-                    v.w += u.w;
-                }
-                store(nt, v);
+                for (int p = 1; p < S; ++p) add4(v, sums[((group * S + p) * NT + nt) * 32 + lane]);
+                store_sums(a, n, r + nt * 8, v);
             }
         group_sync(group, S);
     }
 }
 
-// The same for whole steps: a warp's part of a tile is a number of steps of U chunks
-// (kWords, x in one slab). Two sets of registers take turns, one being multiplied
-// while the other's loads, up to the next tile's first, are on their way.
+// The same for whole steps of U chunks (kWords, x in one slab). A CTA takes a run of
+// tiles, its warps even parts of the run's steps, so that no warp waits for another
+// before the end: a warp that begins inside a tile leaves its sums of it in shared
+// memory, and the one that has the tile's beginning adds them in order. Two sets of
+// registers take turns, one being multiplied while the other's loads are on their way.
 template <int NT, int U>
 __global__ void __launch_bounds__(kThreads, 1)
-linear_steps_kernel(const __grid_constant__ Linear a, int S) {
+linear_steps_kernel(const __grid_constant__ Linear a, int) {
     extern __shared__ __align__(128) unsigned char smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g8 = lane >> 2, t4 = lane & 3;
     const int r0 = (blockIdx.x % a.row_tiles) * 8 * NT;
-    const int per_cta = kWarps / S, group = warp / S, part = warp % S;
-    const int first = (blockIdx.x / a.row_tiles) * per_cta + group, step = gridDim.x / a.row_tiles * per_cta;
-    const int tiles = (a.N + 15) / 16, chunks = a.K / kChunk, mine = chunks / S, rowb = row_bytes(chunks);
-    float4* const sums = reinterpret_cast<float4*>(smem + 8 * NT * rowb);
-    const unsigned char* const x0 = smem + g8 * rowb + t4 * 16 + part * mine * 256;
+    const int cta = blockIdx.x / a.row_tiles, ctas = gridDim.x / a.row_tiles;
+    const int tiles = (a.N + 15) / 16, chunks = a.K / kChunk, steps = chunks / U, rowb = row_bytes(chunks);
+    const int tile0 = int(int64_t(tiles) * cta / ctas), run = (int(int64_t(tiles) * (cta + 1) / ctas) - tile0) * steps;
+    auto begin = [&](int w) { return int(int64_t(run) * w / kWarps); };
+    float4* const sums = reinterpret_cast<float4*>(smem + 8 * NT * rowb);   // [warp][NT][lane]
+    const unsigned char* const x0 = smem + g8 * rowb + t4 * 16;
     const uint32_t sel = uint32_t(t4 | (4 + t4) << 4);
     struct Set {
         Piece p[U];
     };
-    int ahead = first, left = mine;   // the tile that is being loaded, its chunks left
-    Rows2 rows = rows_of(a, min(first, tiles - 1), g8, t4);
-    auto skip_to_part = [&]() {
+    int left = begin(warp + 1) - begin(warp), tile = tile0 + begin(warp) / steps, at = begin(warp) % steps;
+    int l_left = left, l_tile = tile, l_at = at;   // what has not been asked for yet
+    Rows2 rows = rows_of(a, min(tile, tiles - 1), g8, t4);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            rows.w[i] += int64_t(part) * mine * 64;
-            rows.g[i] += part * mine * 4;
-        }
-    };
-    skip_to_part();
+    for (int i = 0; i < 2; ++i) {
+        rows.w[i] += at * (U * 64);
+        rows.g[i] += at * (U * 4);
+    }
     auto load = [&](Set& set) {
-        if (ahead >= tiles) return;
+        if (l_left == 0) return;
+        --l_left;
 #pragma unroll
         for (int j = 0; j < U; ++j) load_piece<true>(a, rows, j, t4, set.p[j]);
 #pragma unroll
@@ -275,11 +306,9 @@ linear_steps_kernel(const __grid_constant__ Linear a, int S) {
             rows.w[i] += U * 64;
             rows.g[i] += U * 4;
         }
-        if ((left -= U) == 0) {
-            ahead += step;
-            left = mine;
-            rows = rows_of(a, min(ahead, tiles - 1), g8, t4);
-            skip_to_part();
+        if (++l_at == steps) {
+            l_at = 0;
+            rows = rows_of(a, min(++l_tile, tiles - 1), g8, t4);
         }
     };
     pdl_wait();
@@ -287,27 +316,55 @@ linear_steps_kernel(const __grid_constant__ Linear a, int S) {
     load(one);
     stage<NT>(a, r0, 0, chunks, smem, rowb);
     __syncthreads();
-    int tile = first, done = 0;
+    bool joined = at != 0;   // the tile was begun by a warp before this one
     float acc[NT][2][4] = {};
+    auto leave = [&]() {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) sums[(warp * NT + nt) * 32 + lane] = tile_sum<NT>(acc, nt);
+    };
     auto take = [&](const Set& set) {
 #pragma unroll
-        for (int j = 0; j < U; ++j) multiply<NT, true>(set.p[j], x0 + (done + j) * 256, rowb, sel, a.nibbles, acc);
-        if ((done += U) == mine) {
-            finish_tile<NT>(a, S, tile, tiles, r0, group, part, acc, sums);
+        for (int j = 0; j < U; ++j) multiply<NT, true>(set.p[j], x0 + (at * U + j) * 256, rowb, sel, a.nibbles, acc);
+        --left;
+        if (++at == steps) {
+            if (joined)
+                leave();
+            else
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                    store_sums(a, tile * 16 + g8, r0 + nt * 8 + 2 * t4, tile_sum<NT>(acc, nt));
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) acc[nt][e >> 2][e & 3] = 0.f;
-            done = 0;
-            tile += step;
+            joined = false;
+            at = 0;
+            ++tile;
         }
     };
-    while (tile < tiles) {
+    while (left) {
         load(two);
         take(one);
-        if (tile >= tiles) break;
+        if (!left) break;
         load(one);
         take(two);
+    }
+    if (at != 0 && joined) leave();
+    __syncthreads();
+    if (at != 0 && !joined) {
+        int need = steps - at;
+        float4 v[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) v[nt] = tile_sum<NT>(acc, nt);
+        for (int w = warp + 1; need > 0; ++w) {
+            const int n = begin(w + 1) - begin(w);
+            if (n == 0) continue;
+            need -= n;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) add4(v[nt], sums[(w * NT + nt) * 32 + lane]);
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) store_sums(a, tile * 16 + g8, r0 + nt * 8 + 2 * t4, v[nt]);
     }
     pdl_trigger();
 }
@@ -428,23 +485,33 @@ int launch_one(void (*kernel)(Linear, int), bool (&ready)[64], const Linear& a, 
 
 template <int NT>
 int launch(Linear a, cudaStream_t stream) {
-    constexpr int U = NT <= 2 ? 4 : 2;   // registers: two sets of 10 U, 8 NT sums
-    static bool ready[3][64] = {};
+    constexpr int U = 2, kSums = kWarps * NT * 512;
+    static bool ready[4][64] = {};
     const int chunks = (a.K + kChunk - 1) / kChunk, tiles = (a.N + 15) / 16, sms = sm_count();
     a.row_tiles = (a.R + 8 * NT - 1) / (8 * NT);
     int ctas = sms / a.row_tiles;
     if (ctas < 1) ctas = 1;
+    a.nibbles = 0x000F000Fu;
+    const bool words = a.K % kChunk == 0 && (reinterpret_cast<uintptr_t>(a.g) & 3u) == 0;
+    const int whole = 8 * NT * row_bytes(chunks);
+    if (words && whole + kSums <= kMaxSmem) {
+        if (ctas > tiles) ctas = tiles;
+        a.slab = chunks;
+        // Steps of two chunks where every warp has several of them: with four in flight, or with more warps and
+        // fewer registers, a lane's weights leave no room to work ahead (128,000 outputs, 1 and 16 rows: 27.7 and
+        // 34.9 us; four chunks 31.6 and 42.7; 24 warps 32.8 and 45.9, one chunk 29.3 and 41.5).
+        const int steps = (tiles + ctas - 1) / ctas * (chunks / U);
+        if (chunks % U == 0 && steps >= 2 * kWarps)
+            return launch_one(linear_steps_kernel<NT, U>, ready[0], a, ctas, 1, whole + kSums, stream);
+        return launch_one(linear_steps_kernel<NT, 1>, ready[1], a, ctas, 1, whole + kSums, stream);
+    }
     const int S = split_of(tiles, chunks, ctas), need = (tiles + kWarps / S - 1) / (kWarps / S);
     if (ctas > need) ctas = need;
     a.slab = ((kMaxSmem - sum_bytes(NT, S)) / (8 * NT) - 64) / (kChunk * 2);
     if (a.slab > chunks) a.slab = chunks;
-    a.nibbles = 0x000F000Fu;
     const int smem = 8 * NT * row_bytes(a.slab) + sum_bytes(NT, S);
-    const bool words = a.K % kChunk == 0 && (reinterpret_cast<uintptr_t>(a.g) & 3u) == 0;
-    if (words && a.slab == chunks && chunks % (U * S) == 0)
-        return launch_one(linear_steps_kernel<NT, U>, ready[0], a, ctas, S, smem, stream);
-    return words ? launch_one(linear_rows_kernel<NT, true>, ready[1], a, ctas, S, smem, stream)
-                 : launch_one(linear_rows_kernel<NT, false>, ready[2], a, ctas, S, smem, stream);
+    return words ? launch_one(linear_rows_kernel<NT, true>, ready[2], a, ctas, S, smem, stream)
+                 : launch_one(linear_rows_kernel<NT, false>, ready[3], a, ctas, S, smem, stream);
 }
 
 bool overlap(const void* p, size_t np, const void* q, size_t nq) {
