@@ -63,7 +63,7 @@ static_assert(kStageKeys * kWarps <= 256, "chunks are whole rounds of the warps"
 static_assert(kKeys == item::kBlockKeys && kBlocks * 4 == item::kBlocksB, "one block index for pools and scales");
 
 // ring (joined through it at the end), block indices, scales (K's, and V's exponent), the warps' largest V
-constexpr int kSmem = kWarps * kRingB + kBlocks * 4 + kBlocks * 8 + 16;
+constexpr int smem_bytes(int NT) { return kWarps * kRingB + kBlocks * 4 + kBlocks * 8 + 16 + (NT >= 3 ? NT * 1024 : 0); }
 static_assert(kWarps * kRingB >= kWarps * 8 * 4 * (kOStride + 2) * 4, "the joining fits the rings");
 
 __device__ __forceinline__ void movmatrix_t(uint32_t& d, uint32_t a) {
@@ -133,6 +133,9 @@ attn_scaled_kernel(SegTable t, int layer, const uint16_t* __restrict__ q, float*
     uint32_t* const blocks = reinterpret_cast<uint32_t*>(smem + kWarps * kRingB);
     float2* const scales = reinterpret_cast<float2*>(blocks + kBlocks);   // K's scale, V's exponent
     uint32_t* const top = reinterpret_cast<uint32_t*>(scales + kBlocks);
+    uint2* const sq = reinterpret_cast<uint2*>(top + kWarps) + (threadIdx.x & 31);   // [nt][ks][lane], kSharedQ
+    constexpr bool kSharedQ = NT >= 3;   // query fragments in shared memory
+    constexpr int B = NT <= 3 ? 2 : 1;   // blocks at a time
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g8 = lane >> 2, t4 = lane & 3;
     const int g = blockIdx.x % TF_NKV;
     const AttnItem it = t.items[blockIdx.x / TF_NKV];
@@ -182,12 +185,13 @@ attn_scaled_kernel(SegTable t, int layer, const uint16_t* __restrict__ q, float*
             scales[i] = make_float2(__uint_as_float(uint32_t(ks[b]) << 23), float(e));
             m = max(m, e);
         }
+        if (tid == 0 && (nblocks & 1)) scales[nblocks] = make_float2(1.f, 0.f);   // a last pair's missing block, masked
         m = __reduce_max_sync(0xFFFFFFFFu, m);
         if (lane == 0) top[warp] = m;
     }
 
     // ---- queries: column n of a tile is query row q0 + 8 nt + n (window row / 4, head % 4)
-    uint32_t qf[NT][4][2];
+    uint2 qf[kSharedQ ? 1 : NT][4];
     uint64_t cq[NT];   // factors of the columns 2 t4, 2 t4 + 1
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -208,8 +212,14 @@ attn_scaled_kernel(SegTable t, int layer, const uint16_t* __restrict__ q, float*
         const int up = min(141 - int(most >> 23), 100);   // the head's largest becomes 2^14..2^15
         const float mul = __uint_as_float(uint32_t(127 + up) << 23);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            qf[nt][i >> 1][i & 1] = pack_h2(__uint_as_float(w[i] << 16) * mul, __uint_as_float(w[i] & 0xFFFF0000u) * mul);
+        for (int ks = 0; ks < 4; ++ks) {
+            auto half2 = [&](uint32_t v) { return pack_h2(__uint_as_float(v << 16) * mul, __uint_as_float(v & 0xFFFF0000u) * mul); };
+            const uint2 f = make_uint2(half2(w[2 * ks]), half2(w[2 * ks + 1]));
+            if constexpr (!kSharedQ)
+                qf[nt][ks] = f;
+            else if (warp == nt)
+                sq[(nt * 4 + ks) * 32] = f;
+        }
         const float back = __uint_as_float(uint32_t(127 - up) << 23) * kLog2e8;
         cq[nt] = pair(__shfl_sync(0xFFFFFFFFu, back, 8 * t4), __shfl_sync(0xFFFFFFFFu, back, 8 * t4 + 4));
     }
@@ -248,54 +258,78 @@ attn_scaled_kernel(SegTable t, int layer, const uint16_t* __restrict__ q, float*
         __syncwarp();
         const uint32_t buf = ring + (i % kStages) * kStageB;
 #pragma unroll 1
-        for (int k = 0; k < 2; ++k) {
+        for (int k = 0; k < 2; k += B) {
             const int bi = 2 * (warp + i * kWarps) + k;
             if (bi >= nblocks) break;
             const int key0 = bi * kKeys;
-            const bool edge = key0 + kKeys > lim_all;
-            const float2 sc = scales[bi];
-            const float dv = fmaxf(sc.y - float(E), float(-kMaxShift));
-            const uint64_t dv2 = pair(dv, dv);
-            const float down = ex2(-dv);
-            const uint64_t kf2 = pair(sc.x, sc.x), down2 = pair(down, down);
+            const bool edge = key0 + B * kKeys > lim_all;
             const uint64_t tiny2 = pair(0x1p-149f, 0x1p-149f);   // keeps a factor above 0, which a masked score (-inf) needs
+            float dv[B], kf[B];
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                const float2 sc = scales[bi + b];
+                kf[b] = sc.x;
+                dv[b] = fmaxf(sc.y - float(E), float(-kMaxShift));
+            }
 
             // scores
-            float s[NT][4];
+            float s[B][NT][4];
             {
-                const uint4 r0 = lds16(buf + k * kBlockB + ka), r1 = lds16(buf + k * kBlockB + ka + kBlockB / 2);
-                const uint32_t w0[4] = {r0.x, r0.y, r0.z, r0.w}, w1[4] = {r1.x, r1.y, r1.z, r1.w};
+                uint4 w[B][2];
+#pragma unroll
+                for (int b = 0; b < B; ++b) {
+                    w[b][0] = lds16(buf + (k + b) * kBlockB + ka);
+                    w[b][1] = lds16(buf + (k + b) * kBlockB + ka + kBlockB / 2);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) s[b][nt][0] = s[b][nt][1] = s[b][nt][2] = s[b][nt][3] = 0.f;
+                }
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks) {
-                    const uint32_t a[4] = {e4m3_low(w0[ks]), e4m3_low(w1[ks]), e4m3_high(w0[ks]), e4m3_high(w1[ks])};
+                    uint2 qs[NT];
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        if (ks == 0) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
-                        mma_f16(s[nt], a, qf[nt][ks][0], qf[nt][ks][1]);
+                    for (int nt = 0; nt < NT; ++nt) qs[nt] = kSharedQ ? sq[(nt * 4 + ks) * 32] : qf[kSharedQ ? 0 : nt][ks];
+#pragma unroll
+                    for (int b = 0; b < B; ++b) {
+                        const uint32_t r0 = (&w[b][0].x)[ks], r1 = (&w[b][1].x)[ks];
+                        const uint32_t a[4] = {e4m3_low(r0), e4m3_low(r1), e4m3_high(r0), e4m3_high(r1)};
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) mma_f16(s[b][nt], a, qs[nt].x, qs[nt].y);
                     }
                 }
             }
             if (edge) {
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    if (key0 + perm(g8) >= lim[nt]) s[nt][0] = s[nt][1] = -INFINITY;
-                    if (key0 + 8 + perm(g8) >= lim[nt]) s[nt][2] = s[nt][3] = -INFINITY;
-                }
+                for (int b = 0; b < B; ++b)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const int key = key0 + b * kKeys + perm(g8);
+                        if (key >= lim[nt]) s[b][nt][0] = s[b][nt][1] = -INFINITY;
+                        if (key + 8 >= lim[nt]) s[b][nt][2] = s[b][nt][3] = -INFINITY;
+                    }
             }
             // weights, in fp32 and (pw) as fp16 pairs; a weight is at most the sum of all
-            uint32_t pw[NT][2];
-            uint64_t ps[NT];
+            uint32_t pw[B][NT][2];
+            uint64_t ln[NT];   // l with these blocks'
             auto weigh = [&]() {
                 uint64_t all = pair(0.f, 0.f);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const uint64_t f = fma2(cq[nt], kf2, tiny2), c = add2(nm[nt], dv2);
-                    const float2 x = both(fma2(pair(s[nt][0], s[nt][1]), f, c)), y = both(fma2(pair(s[nt][2], s[nt][3]), f, c));
-                    const float w0 = ex2(x.x), w1 = ex2(x.y), w2 = ex2(y.x), w3 = ex2(y.y);
-                    ps[nt] = add2(pair(w0, w1), pair(w2, w3));
-                    all = add2(all, ps[nt]);
-                    pw[nt][0] = pack_h2(w0, w1);
-                    pw[nt][1] = pack_h2(w2, w3);
+                for (int nt = 0; nt < NT; ++nt) ln[nt] = l[nt];
+#pragma unroll
+                for (int b = 0; b < B; ++b) {
+                    const float down = ex2(-dv[b]);
+                    const uint64_t kf2 = pair(kf[b], kf[b]), dv2 = pair(dv[b], dv[b]), down2 = pair(down, down);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const uint64_t f = fma2(cq[nt], kf2, tiny2), c = add2(nm[nt], dv2);
+                        const float2 x = both(fma2(pair(s[b][nt][0], s[b][nt][1]), f, c));
+                        const float2 y = both(fma2(pair(s[b][nt][2], s[b][nt][3]), f, c));
+                        const float w0 = ex2(x.x), w1 = ex2(x.y), w2 = ex2(y.x), w3 = ex2(y.y);
+                        const uint64_t ps = add2(pair(w0, w1), pair(w2, w3));
+                        all = add2(all, ps);
+                        ln[nt] = fma2(ps, down2, ln[nt]);
+                        pw[b][nt][0] = pack_h2(w0, w1);
+                        pw[b][nt][1] = pack_h2(w2, w3);
+                    }
                 }
                 const float2 a = both(all);
                 return !(a.x + a.y <= kLargest);
@@ -303,14 +337,20 @@ attn_scaled_kernel(SegTable t, int layer, const uint16_t* __restrict__ q, float*
             if (__any_sync(0xFFFFFFFFu, weigh())) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    const float2 f = both(fma2(cq[nt], kf2, tiny2)), old = both(nm[nt]);
-                    float y[2] = {fmaxf(s[nt][0] * f.x, s[nt][2] * f.x), fmaxf(s[nt][1] * f.y, s[nt][3] * f.y)};
+                    const float2 old = both(nm[nt]);
+                    float y[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                    for (int b = 0; b < B; ++b) {
+                        const float2 f = both(fma2(cq[nt], pair(kf[b], kf[b]), tiny2));
+                        y[0] = fmaxf(y[0], fmaxf(s[b][nt][0] * f.x, s[b][nt][2] * f.x) + dv[b]);
+                        y[1] = fmaxf(y[1], fmaxf(s[b][nt][1] * f.y, s[b][nt][3] * f.y) + dv[b]);
+                    }
                     float to[2] = {-old.x, -old.y}, alpha[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
 #pragma unroll
                         for (int d = 4; d < 32; d *= 2) y[e] = fmaxf(y[e], __shfl_xor_sync(0xFFFFFFFFu, y[e], d));
-                        y[e] += dv - kHeadroom;
+                        y[e] -= kHeadroom;
                         alpha[e] = 1.f;
                         if (y[e] > to[e] + (15.f - kHeadroom)) {   // this row's own: others do not move it
                             alpha[e] = ex2(to[e] - y[e]);
@@ -328,13 +368,14 @@ attn_scaled_kernel(SegTable t, int layer, const uint16_t* __restrict__ q, float*
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                l[nt] = fma2(ps[nt], down2, l[nt]);
-                movmatrix_t(pw[nt][0], pw[nt][0]);
-                movmatrix_t(pw[nt][1], pw[nt][1]);
+                l[nt] = ln[nt];
+#pragma unroll
+                for (int b = 0; b < B; ++b) {
+                    movmatrix_t(pw[b][nt][0], pw[b][nt][0]);
+                    movmatrix_t(pw[b][nt][1], pw[b][nt][1]);
+                }
             }
             // P.V: MMA row g8 of tile mt is dimension 8 g8 + 2 mt, row 8 + g8 the next one
-            const uint32_t bv = buf + (2 + k) * kBlockB;
-            uint2 v[4] = {lds8(bv + va0), lds8(bv + va1), lds8(bv + kBlockB / 2 + va0), lds8(bv + kBlockB / 2 + va1)};
             auto product = [&](const uint2 (&c)[4], const uint32_t (&p)[NT][2], float (&acc)[NT][4][4]) {
 #pragma unroll
                 for (int mt = 0; mt < 4; ++mt) {
@@ -346,45 +387,51 @@ attn_scaled_kernel(SegTable t, int layer, const uint16_t* __restrict__ q, float*
                     for (int nt = 0; nt < NT; ++nt) mma_f16(acc[nt][mt], a, p[nt][0], p[nt][1]);
                 }
             };
-            if (edge) {
-                uint2 bad[4];
-                uint32_t any = 0;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    bad[j] = make_uint2(nan_bytes(v[j].x), nan_bytes(v[j].y));
-                    any |= bad[j].x | bad[j].y;
-                }
-                if (__any_sync(0xFFFFFFFFu, any != 0)) {
-                    uint32_t sees[NT][2];   // 1 where the column's row sees the key
-                    float hits[NT][4][4];
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        const uint32_t one = 0x3C003C00u;
-                        movmatrix_t(sees[nt][0], key0 + perm(g8) < lim[nt] ? one : 0u);
-                        movmatrix_t(sees[nt][1], key0 + 8 + perm(g8) < lim[nt] ? one : 0u);
-#pragma unroll
-                        for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) hits[nt][mt][e] = 0.f;
-                    }
+            for (int b = 0; b < B; ++b) {
+                const uint32_t bv = buf + (2 + k + b) * kBlockB;
+                uint2 v[4] = {lds8(bv + va0), lds8(bv + va1), lds8(bv + kBlockB / 2 + va0), lds8(bv + kBlockB / 2 + va1)};
+                if (edge) {
+                    uint2 bad[4];
+                    uint32_t any = 0;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        v[j].x &= ~bad[j].x;
-                        v[j].y &= ~bad[j].y;
-                        bad[j].x &= 0x38383838u;   // 1 as a code
-                        bad[j].y &= 0x38383838u;
+                        bad[j] = make_uint2(nan_bytes(v[j].x), nan_bytes(v[j].y));
+                        any |= bad[j].x | bad[j].y;
                     }
-                    product(bad, sees, hits);
+                    if (__any_sync(0xFFFFFFFFu, any != 0)) {
+                        const int key = key0 + b * kKeys + perm(g8);
+                        uint32_t sees[NT][2];   // 1 where the column's row sees the key
+                        float hits[NT][4][4];
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                        for (int nt = 0; nt < NT; ++nt) {
+                            const uint32_t one = 0x3C003C00u;
+                            movmatrix_t(sees[nt][0], key < lim[nt] ? one : 0u);
+                            movmatrix_t(sees[nt][1], key + 8 < lim[nt] ? one : 0u);
 #pragma unroll
-                        for (int mt = 0; mt < 4; ++mt)
+                            for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                if (hits[nt][mt][e] > 0.f) o[nt][mt][e] = __uint_as_float(0x7FC00000u);
+                                for (int e = 0; e < 4; ++e) hits[nt][mt][e] = 0.f;
+                        }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            v[j].x &= ~bad[j].x;
+                            v[j].y &= ~bad[j].y;
+                            bad[j].x &= 0x38383838u;   // 1 as a code
+                            bad[j].y &= 0x38383838u;
+                        }
+                        product(bad, sees, hits);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    if (hits[nt][mt][e] > 0.f) o[nt][mt][e] = __uint_as_float(0x7FC00000u);
+                    }
                 }
+                product(v, pw[b], o);
             }
-            product(v, pw, o);
         }
         __syncwarp();   // the stage is read: its buffer may be filled again
     }
@@ -460,14 +507,14 @@ attn_scaled_kernel(SegTable t, int layer, const uint16_t* __restrict__ q, float*
 template <int NT>
 int prepare_one() {
     cudaError_t e = cudaFuncSetAttribute(attn_scaled_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kSmem);
+                                         smem_bytes(NT));
     return e == cudaSuccess ? TF_OK : cuda_fail(e);
 }
 
 template <int NT>
 int launch_one(const SegTable& t, int layer, const uint16_t* q, float* po, float2* pml, cudaStream_t stream,
                uint16_t* out, int full) {
-    return launch_pdl(attn_scaled_kernel<NT>, dim3(t.n_items_mma * TF_NKV), dim3(kThreads), kSmem, stream, t, layer, q, po,
+    return launch_pdl(attn_scaled_kernel<NT>, dim3(t.n_items_mma * TF_NKV), dim3(kThreads), smem_bytes(NT), stream, t, layer, q, po,
                       pml, out, full);
 }
 
