@@ -28,7 +28,16 @@
 //
 // Four warps share a chunk: warp w takes the stages (32 keys) w, w + 4, ... of
 // it through a ring of its own (cp.async, no CTA barrier in the loop); their
-// results are joined at the end.
+// results are joined at the end. A stage's two blocks go through the products and
+// the softmax together: a warp's instructions wait mostly for one another, with
+// three or four warps a scheduler, and a test of the reference serves both.
+//
+// Measured: 4 windows of 6 rows at 65,536 to 130,816 keys 90.8 us (4.6 TB/s; a
+// block at a time 97.1), of 2 rows 72.8 us (5.7 TB/s, 85 % of the measured copy
+// rate); 16 single rows at 256 to 4,096 keys 9.4 us. What bounds it is issue: some
+// 245 instructions a block of 24 queries, half of the issue slots used. The queries
+// of 3 or 4 tiles lie in shared memory, which leaves three CTAs an SM their
+// registers; four CTAs a block at a time with 24 queries 97.7 us.
 //
 // What no row of the item may see is kept out: scores are masked, and in blocks
 // that reach past the first row's keys a NaN code of V is taken out of the
@@ -63,7 +72,9 @@ static_assert(kStageKeys * kWarps <= 256, "chunks are whole rounds of the warps"
 static_assert(kKeys == item::kBlockKeys && kBlocks * 4 == item::kBlocksB, "one block index for pools and scales");
 
 // ring (joined through it at the end), block indices, scales (K's, and V's exponent), the warps' largest V
-constexpr int smem_bytes(int NT) { return kWarps * kRingB + kBlocks * 4 + kBlocks * 8 + 16 + (NT >= 3 ? NT * 1024 : 0); }
+constexpr int smem_bytes(int NT) {
+    return kWarps * kRingB + kBlocks * 4 + kBlocks * 8 + 16 + (NT >= 3 ? NT * 1024 : 0);
+}
 static_assert(kWarps * kRingB >= kWarps * 8 * 4 * (kOStride + 2) * 4, "the joining fits the rings");
 
 __device__ __forceinline__ void movmatrix_t(uint32_t& d, uint32_t a) {
@@ -135,7 +146,7 @@ attn_scaled_kernel(SegTable t, int layer, const uint16_t* __restrict__ q, float*
     uint32_t* const top = reinterpret_cast<uint32_t*>(scales + kBlocks);
     uint2* const sq = reinterpret_cast<uint2*>(top + kWarps) + (threadIdx.x & 31);   // [nt][ks][lane], kSharedQ
     constexpr bool kSharedQ = NT >= 3;   // query fragments in shared memory
-    constexpr int B = NT <= 3 ? 2 : 1;   // blocks at a time
+    constexpr int B = kStageKeys / kKeys;   // blocks at a time (for every NT: a stream's bits are its own)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g8 = lane >> 2, t4 = lane & 3;
     const int g = blockIdx.x % TF_NKV;
     const AttnItem it = t.items[blockIdx.x / TF_NKV];
@@ -198,7 +209,8 @@ attn_scaled_kernel(SegTable t, int layer, const uint16_t* __restrict__ q, float*
         const int qi = nt * 8 + g8;
         uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
         if (qi < nq) {
-            const uint16_t* src = q + (size_t(st.row_offset + ((q0 + qi) >> 2)) * TF_NQ + 4 * g + (qi & 3)) * TF_D + 16 * t4;
+            const size_t row = st.row_offset + ((q0 + qi) >> 2);
+            const uint16_t* src = q + (row * TF_NQ + 4 * g + (qi & 3)) * TF_D + 16 * t4;
             const uint4 a = *reinterpret_cast<const uint4*>(src), b = *reinterpret_cast<const uint4*>(src + 8);
             w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
             w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
@@ -206,14 +218,17 @@ attn_scaled_kernel(SegTable t, int layer, const uint16_t* __restrict__ q, float*
         uint32_t most = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            most = max(most, max(finite_bits(__uint_as_float(w[i] << 16)), finite_bits(__uint_as_float(w[i] & 0xFFFF0000u))));
+            most = max(most, max(finite_bits(__uint_as_float(w[i] << 16)),
+                                 finite_bits(__uint_as_float(w[i] & 0xFFFF0000u))));
         most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
         most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
         const int up = min(141 - int(most >> 23), 100);   // the head's largest becomes 2^14..2^15
         const float mul = __uint_as_float(uint32_t(127 + up) << 23);
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
-            auto half2 = [&](uint32_t v) { return pack_h2(__uint_as_float(v << 16) * mul, __uint_as_float(v & 0xFFFF0000u) * mul); };
+            auto half2 = [&](uint32_t v) {
+                return pack_h2(__uint_as_float(v << 16) * mul, __uint_as_float(v & 0xFFFF0000u) * mul);
+            };
             const uint2 f = make_uint2(half2(w[2 * ks]), half2(w[2 * ks + 1]));
             if constexpr (!kSharedQ)
                 qf[nt][ks] = f;
@@ -257,181 +272,177 @@ attn_scaled_kernel(SegTable t, int layer, const uint16_t* __restrict__ q, float*
         item::cp_async_wait<kStages - 1>();
         __syncwarp();
         const uint32_t buf = ring + (i % kStages) * kStageB;
-#pragma unroll 1
-        for (int k = 0; k < 2; k += B) {
-            const int bi = 2 * (warp + i * kWarps) + k;
-            if (bi >= nblocks) break;
-            const int key0 = bi * kKeys;
-            const bool edge = key0 + B * kKeys > lim_all;
-            const uint64_t tiny2 = pair(0x1p-149f, 0x1p-149f);   // keeps a factor above 0, which a masked score (-inf) needs
-            float dv[B], kf[B];
+        const int bi = 2 * (warp + i * kWarps);
+        const int key0 = bi * kKeys;
+        const bool edge = key0 + B * kKeys > lim_all;
+        const uint64_t tiny2 = pair(0x1p-149f, 0x1p-149f);   // keeps a factor above 0: a masked score is -inf
+        float dv[B], kf[B];
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            const float2 sc = scales[bi + b];
+            kf[b] = sc.x;
+            dv[b] = fmaxf(sc.y - float(E), float(-kMaxShift));
+        }
+
+        // scores
+        float s[B][NT][4];
+        {
+            uint4 w[B][2];
 #pragma unroll
             for (int b = 0; b < B; ++b) {
-                const float2 sc = scales[bi + b];
-                kf[b] = sc.x;
-                dv[b] = fmaxf(sc.y - float(E), float(-kMaxShift));
+                w[b][0] = lds16(buf + b * kBlockB + ka);
+                w[b][1] = lds16(buf + b * kBlockB + ka + kBlockB / 2);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) s[b][nt][0] = s[b][nt][1] = s[b][nt][2] = s[b][nt][3] = 0.f;
             }
-
-            // scores
-            float s[B][NT][4];
-            {
-                uint4 w[B][2];
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) {
+                uint2 qs[NT];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) qs[nt] = kSharedQ ? sq[(nt * 4 + ks) * 32] : qf[kSharedQ ? 0 : nt][ks];
 #pragma unroll
                 for (int b = 0; b < B; ++b) {
-                    w[b][0] = lds16(buf + (k + b) * kBlockB + ka);
-                    w[b][1] = lds16(buf + (k + b) * kBlockB + ka + kBlockB / 2);
+                    const uint32_t r0 = (&w[b][0].x)[ks], r1 = (&w[b][1].x)[ks];
+                    const uint32_t a[4] = {e4m3_low(r0), e4m3_low(r1), e4m3_high(r0), e4m3_high(r1)};
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) s[b][nt][0] = s[b][nt][1] = s[b][nt][2] = s[b][nt][3] = 0.f;
-                }
-#pragma unroll
-                for (int ks = 0; ks < 4; ++ks) {
-                    uint2 qs[NT];
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) qs[nt] = kSharedQ ? sq[(nt * 4 + ks) * 32] : qf[kSharedQ ? 0 : nt][ks];
-#pragma unroll
-                    for (int b = 0; b < B; ++b) {
-                        const uint32_t r0 = (&w[b][0].x)[ks], r1 = (&w[b][1].x)[ks];
-                        const uint32_t a[4] = {e4m3_low(r0), e4m3_low(r1), e4m3_high(r0), e4m3_high(r1)};
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) mma_f16(s[b][nt], a, qs[nt].x, qs[nt].y);
-                    }
+                    for (int nt = 0; nt < NT; ++nt) mma_f16(s[b][nt], a, qs[nt].x, qs[nt].y);
                 }
             }
-            if (edge) {
+        }
+        if (edge) {
 #pragma unroll
-                for (int b = 0; b < B; ++b)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        const int key = key0 + b * kKeys + perm(g8);
-                        if (key >= lim[nt]) s[b][nt][0] = s[b][nt][1] = -INFINITY;
-                        if (key + 8 >= lim[nt]) s[b][nt][2] = s[b][nt][3] = -INFINITY;
-                    }
-            }
-            // weights, in fp32 and (pw) as fp16 pairs; a weight is at most the sum of all
-            uint32_t pw[B][NT][2];
-            uint64_t ln[NT];   // l with these blocks'
-            auto weigh = [&]() {
-                uint64_t all = pair(0.f, 0.f);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) ln[nt] = l[nt];
-#pragma unroll
-                for (int b = 0; b < B; ++b) {
-                    const float down = ex2(-dv[b]);
-                    const uint64_t kf2 = pair(kf[b], kf[b]), dv2 = pair(dv[b], dv[b]), down2 = pair(down, down);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        const uint64_t f = fma2(cq[nt], kf2, tiny2), c = add2(nm[nt], dv2);
-                        const float2 x = both(fma2(pair(s[b][nt][0], s[b][nt][1]), f, c));
-                        const float2 y = both(fma2(pair(s[b][nt][2], s[b][nt][3]), f, c));
-                        const float w0 = ex2(x.x), w1 = ex2(x.y), w2 = ex2(y.x), w3 = ex2(y.y);
-                        const uint64_t ps = add2(pair(w0, w1), pair(w2, w3));
-                        all = add2(all, ps);
-                        ln[nt] = fma2(ps, down2, ln[nt]);
-                        pw[b][nt][0] = pack_h2(w0, w1);
-                        pw[b][nt][1] = pack_h2(w2, w3);
-                    }
-                }
-                const float2 a = both(all);
-                return !(a.x + a.y <= kLargest);
-            };
-            if (__any_sync(0xFFFFFFFFu, weigh())) {
+            for (int b = 0; b < B; ++b)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    const float2 old = both(nm[nt]);
-                    float y[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-                    for (int b = 0; b < B; ++b) {
-                        const float2 f = both(fma2(cq[nt], pair(kf[b], kf[b]), tiny2));
-                        y[0] = fmaxf(y[0], fmaxf(s[b][nt][0] * f.x, s[b][nt][2] * f.x) + dv[b]);
-                        y[1] = fmaxf(y[1], fmaxf(s[b][nt][1] * f.y, s[b][nt][3] * f.y) + dv[b]);
-                    }
-                    float to[2] = {-old.x, -old.y}, alpha[2];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-#pragma unroll
-                        for (int d = 4; d < 32; d *= 2) y[e] = fmaxf(y[e], __shfl_xor_sync(0xFFFFFFFFu, y[e], d));
-                        y[e] -= kHeadroom;
-                        alpha[e] = 1.f;
-                        if (y[e] > to[e] + (15.f - kHeadroom)) {   // this row's own: others do not move it
-                            alpha[e] = ex2(to[e] - y[e]);
-                            to[e] = y[e];
-                        }
-                    }
-                    nm[nt] = pair(-to[0], -to[1]);
-                    l[nt] = mul2(l[nt], pair(alpha[0], alpha[1]));
-#pragma unroll
-                    for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) o[nt][mt][e] *= alpha[e & 1];
+                    const int key = key0 + b * kKeys + perm(g8);
+                    if (key >= lim[nt]) s[b][nt][0] = s[b][nt][1] = -INFINITY;
+                    if (key + 8 >= lim[nt]) s[b][nt][2] = s[b][nt][3] = -INFINITY;
                 }
-                weigh();
-            }
+        }
+        // weights, in fp32 and (pw) as fp16 pairs; a weight is at most the sum of all
+        uint32_t pw[B][NT][2];
+        uint64_t ln[NT];   // l with these blocks'
+        auto weigh = [&]() {
+            uint64_t all = pair(0.f, 0.f);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                l[nt] = ln[nt];
-#pragma unroll
-                for (int b = 0; b < B; ++b) {
-                    movmatrix_t(pw[b][nt][0], pw[b][nt][0]);
-                    movmatrix_t(pw[b][nt][1], pw[b][nt][1]);
-                }
-            }
-            // P.V: MMA row g8 of tile mt is dimension 8 g8 + 2 mt, row 8 + g8 the next one
-            auto product = [&](const uint2 (&c)[4], const uint32_t (&p)[NT][2], float (&acc)[NT][4][4]) {
-#pragma unroll
-                for (int mt = 0; mt < 4; ++mt) {
-                    const uint32_t sel = (mt & 1) ? 0x7362u : 0x5140u;   // bytes 2 mt, 2 mt + 1 of both
-                    const uint32_t lo = __byte_perm(mt < 2 ? c[0].x : c[0].y, mt < 2 ? c[1].x : c[1].y, sel);
-                    const uint32_t hi = __byte_perm(mt < 2 ? c[2].x : c[2].y, mt < 2 ? c[3].x : c[3].y, sel);
-                    const uint32_t a[4] = {e4m3_low(lo), e4m3_high(lo), e4m3_low(hi), e4m3_high(hi)};
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma_f16(acc[nt][mt], a, p[nt][0], p[nt][1]);
-                }
-            };
+            for (int nt = 0; nt < NT; ++nt) ln[nt] = l[nt];
 #pragma unroll
             for (int b = 0; b < B; ++b) {
-                const uint32_t bv = buf + (2 + k + b) * kBlockB;
-                uint2 v[4] = {lds8(bv + va0), lds8(bv + va1), lds8(bv + kBlockB / 2 + va0), lds8(bv + kBlockB / 2 + va1)};
-                if (edge) {
-                    uint2 bad[4];
-                    uint32_t any = 0;
+                const float down = ex2(-dv[b]);
+                const uint64_t kf2 = pair(kf[b], kf[b]), dv2 = pair(dv[b], dv[b]), down2 = pair(down, down);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        bad[j] = make_uint2(nan_bytes(v[j].x), nan_bytes(v[j].y));
-                        any |= bad[j].x | bad[j].y;
-                    }
-                    if (__any_sync(0xFFFFFFFFu, any != 0)) {
-                        const int key = key0 + b * kKeys + perm(g8);
-                        uint32_t sees[NT][2];   // 1 where the column's row sees the key
-                        float hits[NT][4][4];
+                for (int nt = 0; nt < NT; ++nt) {
+                    const uint64_t f = fma2(cq[nt], kf2, tiny2), c = add2(nm[nt], dv2);
+                    const float2 x = both(fma2(pair(s[b][nt][0], s[b][nt][1]), f, c));
+                    const float2 y = both(fma2(pair(s[b][nt][2], s[b][nt][3]), f, c));
+                    const float w0 = ex2(x.x), w1 = ex2(x.y), w2 = ex2(y.x), w3 = ex2(y.y);
+                    const uint64_t ps = add2(pair(w0, w1), pair(w2, w3));
+                    all = add2(all, ps);
+                    ln[nt] = fma2(ps, down2, ln[nt]);
+                    pw[b][nt][0] = pack_h2(w0, w1);
+                    pw[b][nt][1] = pack_h2(w2, w3);
+                }
+            }
+            const float2 a = both(all);
+            return !(a.x + a.y <= kLargest);
+        };
+        if (__any_sync(0xFFFFFFFFu, weigh())) {
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            const uint32_t one = 0x3C003C00u;
-                            movmatrix_t(sees[nt][0], key < lim[nt] ? one : 0u);
-                            movmatrix_t(sees[nt][1], key + 8 < lim[nt] ? one : 0u);
+            for (int nt = 0; nt < NT; ++nt) {
+                const float2 old = both(nm[nt]);
+                float y[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                            for (int mt = 0; mt < 4; ++mt)
+                for (int b = 0; b < B; ++b) {
+                    const float2 f = both(fma2(cq[nt], pair(kf[b], kf[b]), tiny2));
+                    y[0] = fmaxf(y[0], fmaxf(s[b][nt][0] * f.x, s[b][nt][2] * f.x) + dv[b]);
+                    y[1] = fmaxf(y[1], fmaxf(s[b][nt][1] * f.y, s[b][nt][3] * f.y) + dv[b]);
+                }
+                float to[2] = {-old.x, -old.y}, alpha[2];
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) hits[nt][mt][e] = 0.f;
-                        }
+                for (int e = 0; e < 2; ++e) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            v[j].x &= ~bad[j].x;
-                            v[j].y &= ~bad[j].y;
-                            bad[j].x &= 0x38383838u;   // 1 as a code
-                            bad[j].y &= 0x38383838u;
-                        }
-                        product(bad, sees, hits);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    if (hits[nt][mt][e] > 0.f) o[nt][mt][e] = __uint_as_float(0x7FC00000u);
+                    for (int d = 4; d < 32; d *= 2) y[e] = fmaxf(y[e], __shfl_xor_sync(0xFFFFFFFFu, y[e], d));
+                    y[e] -= kHeadroom;
+                    alpha[e] = 1.f;
+                    if (y[e] > to[e] + (15.f - kHeadroom)) {   // this row's own: others do not move it
+                        alpha[e] = ex2(to[e] - y[e]);
+                        to[e] = y[e];
                     }
                 }
-                product(v, pw[b], o);
+                nm[nt] = pair(-to[0], -to[1]);
+                l[nt] = mul2(l[nt], pair(alpha[0], alpha[1]));
+#pragma unroll
+                for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[nt][mt][e] *= alpha[e & 1];
             }
+            weigh();
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            l[nt] = ln[nt];
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                movmatrix_t(pw[b][nt][0], pw[b][nt][0]);
+                movmatrix_t(pw[b][nt][1], pw[b][nt][1]);
+            }
+        }
+        // P.V: MMA row g8 of tile mt is dimension 8 g8 + 2 mt, row 8 + g8 the next one
+        auto product = [&](const uint2 (&c)[4], const uint32_t (&p)[NT][2], float (&acc)[NT][4][4]) {
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt) {
+                const uint32_t sel = (mt & 1) ? 0x7362u : 0x5140u;   // bytes 2 mt, 2 mt + 1 of both
+                const uint32_t lo = __byte_perm(mt < 2 ? c[0].x : c[0].y, mt < 2 ? c[1].x : c[1].y, sel);
+                const uint32_t hi = __byte_perm(mt < 2 ? c[2].x : c[2].y, mt < 2 ? c[3].x : c[3].y, sel);
+                const uint32_t a[4] = {e4m3_low(lo), e4m3_high(lo), e4m3_low(hi), e4m3_high(hi)};
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) mma_f16(acc[nt][mt], a, p[nt][0], p[nt][1]);
+            }
+        };
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            const uint32_t bv = buf + (2 + b) * kBlockB;
+            uint2 v[4] = {lds8(bv + va0), lds8(bv + va1), lds8(bv + kBlockB / 2 + va0), lds8(bv + kBlockB / 2 + va1)};
+            if (edge) {
+                uint2 bad[4];
+                uint32_t any = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    bad[j] = make_uint2(nan_bytes(v[j].x), nan_bytes(v[j].y));
+                    any |= bad[j].x | bad[j].y;
+                }
+                if (__any_sync(0xFFFFFFFFu, any != 0)) {
+                    const int key = key0 + b * kKeys + perm(g8);
+                    uint32_t sees[NT][2];   // 1 where the column's row sees the key
+                    float hits[NT][4][4];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const uint32_t one = 0x3C003C00u;
+                        movmatrix_t(sees[nt][0], key < lim[nt] ? one : 0u);
+                        movmatrix_t(sees[nt][1], key + 8 < lim[nt] ? one : 0u);
+#pragma unroll
+                        for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) hits[nt][mt][e] = 0.f;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        v[j].x &= ~bad[j].x;
+                        v[j].y &= ~bad[j].y;
+                        bad[j].x &= 0x38383838u;   // 1 as a code
+                        bad[j].y &= 0x38383838u;
+                    }
+                    product(bad, sees, hits);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (hits[nt][mt][e] > 0.f) o[nt][mt][e] = __uint_as_float(0x7FC00000u);
+                }
+            }
+            product(v, pw[b], o);
         }
         __syncwarp();   // the stage is read: its buffer may be filled again
     }
@@ -476,7 +487,8 @@ attn_scaled_kernel(SegTable t, int layer, const uint16_t* __restrict__ q, float*
         float L = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            const float f = ex2(sM[w * 8 * NT + qi] - M);   // 0 for a warp without a key of the row; its sums are 0 or NaN
+            // 0 for a warp without a key of the row, whose sums are 0 or NaN
+            const float f = ex2(sM[w * 8 * NT + qi] - M);
             const float4 v = *reinterpret_cast<const float4*>(sO + (w * 8 * NT + qi) * kOStride + d4);
             L += f * sL[w * 8 * NT + qi];
             acc.x += f * v.x;
@@ -514,8 +526,8 @@ int prepare_one() {
 template <int NT>
 int launch_one(const SegTable& t, int layer, const uint16_t* q, float* po, float2* pml, cudaStream_t stream,
                uint16_t* out, int full) {
-    return launch_pdl(attn_scaled_kernel<NT>, dim3(t.n_items_mma * TF_NKV), dim3(kThreads), smem_bytes(NT), stream, t, layer, q, po,
-                      pml, out, full);
+    return launch_pdl(attn_scaled_kernel<NT>, dim3(t.n_items_mma * TF_NKV), dim3(kThreads), smem_bytes(NT), stream, t,
+                      layer, q, po, pml, out, full);
 }
 
 int launch_mma(const SegTable& t, int layer, const uint16_t* q, float* po, float2* pml, cudaStream_t stream,
@@ -531,8 +543,8 @@ int launch_mma(const SegTable& t, int layer, const uint16_t* q, float* po, float
 
 int attn_scaled_prepare() {
     int rc;
-    if ((rc = prepare_one<1>()) != TF_OK || (rc = prepare_one<2>()) != TF_OK || (rc = prepare_one<3>()) != TF_OK) return rc;
-    if ((rc = prepare_one<4>()) != TF_OK) return rc;
+    if ((rc = prepare_one<1>()) != TF_OK || (rc = prepare_one<2>()) != TF_OK) return rc;
+    if ((rc = prepare_one<3>()) != TF_OK || (rc = prepare_one<4>()) != TF_OK) return rc;
     return attn_scaled_tc_prepare();
 }
 

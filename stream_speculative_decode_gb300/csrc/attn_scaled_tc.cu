@@ -14,7 +14,8 @@
 // off by at most 2^-10 (2^-17 of the largest) below. K's scale is a factor of the
 // softmax's 16 scores of a block, which costs it nothing but the factor.
 // V's codes become fp16 tiles in shared memory (exact) times 2^(ev - E + 7), at most
-// 448 * 2^7; that is exact too down to 2^-28 below the chunk's largest block.
+// 448 * 2^7; that is exact too for blocks down to 2^-22 of the chunk's largest, and off
+// by at most 2^-25 (2^-32 of the largest block's scale) below.
 //
 // Persistent, two CTAs an SM, 8 warps:
 //   warp 7      TMA loads of the codes (64 keys: 4 KB of K, 64-byte swizzle, and 4 KB
@@ -28,11 +29,17 @@
 // 192. (An MMA of 64 keys that reads its 128 query rows from shared memory is bound by
 // that: 4 KB of queries beside 2 KB of keys.)
 //
-// What bounds it: a 64-key tile is 8 KB from HBM, 350 cycles of an SM's share. Of
-// that the tensor cores take some 270 (M = 128 whatever the window's rows), the
-// softmax warps' chain of a tile 780 of a CTA and half that with two. Both conversions
-// by a warp each (K to fp16 too, the load warp's work) took 2,600 cycles a tile:
-// 212 us for 64 windows of 16 rows, where the K tiles stood in wait for their warp.
+// Measured: 64 windows of 16 rows at 16 to 32,768 keys 122.8 us (3.1 TB/s, 47 % of
+// the measured copy rate); a 2,048-row prompt chunk at 8,179 keys 181 us (662
+// TFLOP/s). What bounds it is the chain of a tile, no unit by itself: a 64-key tile
+// is 8 KB from HBM, 350 cycles of an SM's share, the tensor cores take some 270 (M =
+// 128 whatever the window's rows), the softmax warps' chain 780 of a CTA and half that
+// with two. Of the 181 us the exponentials cost 29 (copies of the kernel without
+// them), V's conversion 12, K's second product 2; of the 123 us 8, 7 and 4, and the
+// units' tail 15 % (760 of up to 128 tiles on 304 CTAs; chunks half as long 125 us).
+// Both conversions by a warp each (K to fp16 too, the load warp's work) took 2,600
+// cycles a tile (212 us), the queries in shared memory and the MMAs issued by a lone
+// thread 147 and 209 us; a third S buffer in place of the queries 130 and 193.
 //
 // A weight is at most 2^15 (fp16), the largest of a row at 2^6 when its reference
 // moves: weights below 2^-31 of it vanish. A block of V whose scale is 2^31 below the
@@ -362,7 +369,8 @@ __device__ __forceinline__ float convert_query(uint32_t sQ, uint32_t trow, int w
         const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-            most = max(most, max(finite_bits(__uint_as_float(w[k] << 16)), finite_bits(__uint_as_float(w[k] & 0xFFFF0000u))));
+            most = max(most, max(finite_bits(__uint_as_float(w[k] << 16)),
+                                 finite_bits(__uint_as_float(w[k] & 0xFFFF0000u))));
     }
     if (DUAL) most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 16));
     const int up = min(134 - int(most >> 23), 126);
@@ -641,7 +649,8 @@ attn_scaled_tc_kernel(SegTable t, int layer, float* __restrict__ part_o, float2*
                             const uint32_t bad = __vcmpeq4(w[k] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
                             if (bad) {
                                 for (int c = 0; c < 4; ++c)
-                                    if (bad >> (8 * c) & 1) atomicMin(&bars->nan_key[m % kUnits][16 * (lane & 3) + 4 * k + c], key);
+                                    if (bad >> (8 * c) & 1)
+                                        atomicMin(&bars->nan_key[m % kUnits][16 * (lane & 3) + 4 * k + c], key);
                                 bars->any_nan[m % kUnits] = 1;
                                 w[k] &= ~bad;
                             }
@@ -813,7 +822,8 @@ attn_scaled_tc_kernel(SegTable t, int layer, float* __restrict__ part_o, float2*
 }  // namespace
 
 int attn_scaled_tc_prepare() {
-    const cudaError_t e = cudaFuncSetAttribute(attn_scaled_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    const cudaError_t e =
+        cudaFuncSetAttribute(attn_scaled_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     return e == cudaSuccess ? TF_OK : cuda_fail(e);
 }
 

@@ -190,6 +190,43 @@ def test_result_is_the_streams_own(tf):
     assert torch.equal(bits(a.out[0]), bits(b.out[0]))
 
 
+def test_bits_alone_and_in_company(tf):
+    """A stream alone and among wider windows, narrower ones and those of the other kernel: the same bits. Large
+    queries move the references often."""
+    from scaled import ScaledAttn
+    a = ScaledAttn(tf, [(5, 2000), (1, 3001), (8, 1200), (3, 900), (2, 40), (16, 2100), (6, 1555), (12, 9000)], 32,
+                   seed=18)
+    a.q[0] *= 5
+    a.run()
+    a.check()
+    for (r, o, k), ids in zip(a.streams, a.lists):
+        seg = tf.tf_paged_scaled_build([(r, 0, k, len(ids) * 32)], None, None, ids, 32, a.n_pages, a.K, a.V, a.ks, a.vs,
+                                       0, 1)
+        partials = torch.empty(max(seg.partials_bytes // 4, 4), device="cuda")
+        out = torch.empty_like(a.out[0][o:o + r])
+        tf.tf_attn_paged(seg, 0, a.q[0][o:o + r].contiguous(), partials, out)
+        assert torch.equal(bits(out), bits(a.out[0][o:o + r])), (r, k)
+
+
+def test_layers_side_by_side(tf):
+    """Two layers of one table on two streams at once, each with partials of its own."""
+    from scaled import ScaledAttn
+    a = ScaledAttn(tf, [(16, 8300), (2, 5000), (9, 70), (1, 900), (16, 20000)], 64, seed=19, layers=2)
+    want = [x.clone() for x in a.run()]
+    partials = [torch.full_like(a.partials, float("nan")) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        for o in a.out:
+            o.zero_()
+        torch.cuda.synchronize()
+        for l in (0, 1):
+            tf.tf_attn_paged(a.seg, l, a.q[l], partials[l], a.out[l], False, streams[l])
+        torch.cuda.synchronize()
+        for l in (0, 1):
+            assert torch.equal(bits(a.out[l]), bits(want[l])), l
+    assert tf.tf_segments_status(a.seg) == (tf.TF_OK, 0)
+
+
 def test_pool_beyond_32_bits(tf):
     """Pages past 4 GB of codes."""
     from scaled import ScaledAttn
