@@ -563,11 +563,18 @@ int tf_pages_copy(void* const* pools, int n_pools, int32_t page_keys, int32_t n_
  *                 have no say. Pages that are filled in another way keep to the
  *                 format above.
  *   tf_attn_paged reads codes and scales (q and out bf16; the window's own rows
- *                 are read back as coded). P.V runs with fp16 weights (off by
- *                 2^-12 of each) and exact codes, summed in fp32; keys whose
- *                 weight times V's scale is below 2^-31 of the largest such
- *                 product of a chunk do not count in P.V. A NaN reaches the rows
- *                 that see its key, no other. q, partials and out lie apart. */
+ *                 are read back as coded); a stream's bits depend on that stream
+ *                 alone. P.V runs with fp16 weights (off by 2^-12 of each) and
+ *                 exact codes, summed in fp32; keys whose weight times V's scale
+ *                 is below 2^-31 of a row's largest such product do not count in
+ *                 P.V. The tensor-core kernel (windows of 9 rows or more,
+ *                 prompts; TF_ATTN_PATH as for tf_attn) takes a query as the sum of
+ *                 two e4m3 parts: exact for elements down to 2^-9 of a head's
+ *                 largest, smaller ones off by at most 2^-17 of it; there a block
+ *                 of V whose scale is 2^31 or more below its chunk's largest counts
+ *                 as zeros (on the other kernel one 2^64 below, as if 2^64 below).
+ *                 A NaN reaches the rows that see its key, no other. q, partials
+ *                 and out lie apart. */
 int tf_paged_scaled_build(const tf_stream* streams, int n_streams, const void* const* conv_state,
                           const void* const* conv_hist, const int32_t* pages, int32_t page_keys,
                           int32_t n_pages, const void* const* k_pool, const void* const* v_pool,
@@ -612,7 +619,7 @@ int tf_norm_rows(const void* x, int64_t x_stride, const void* res, int64_t res_s
 
 /* Rows times a matrix of 4-bit weights (a projection, or the logits):
  *   y[r][n] = s[n] * sum_k x[r][k] * g[n][k / 32] * (c[n][k] - 8)
- * summed in fp32 over exact products and rounded once to bf16.
+ * summed in fp32 and rounded once to bf16.
  *   x         x_scales NULL: bf16, row r at x + r*x_stride (elements, a multiple
  *             of 8). Otherwise codes, row r at x + r*x_stride (a multiple of 16),
  *             with x_scales uint8 [R][K / TF_SCALE_COLUMNS] (at any address): what
@@ -623,7 +630,8 @@ int tf_norm_rows(const void* x, int64_t x_stride, const void* res, int64_t res_s
  *   y         bf16, row r at y + r*y_stride (any 2-byte address and stride >= N);
  *             overlaps nothing else
  * K is a multiple of TF_SCALE_COLUMNS. The weights are read once for up to 32 rows.
- * Sums run in a fixed order. A NaN or an infinity in a row of x reaches that row of
+ * Values of x below bf16's smallest, 2^-133, are rounded to multiples of it; the
+ * other products are exact. Sums run in an order that R, K and N fix. A NaN or an infinity in a row of x reaches that row of
  * y only. Needs no table; R == 0 is a no-op. Errors: TF_EINVAL (null, misaligned,
  * overlaps, a bad K or stride, N < 1, another device's memory), TF_ERANGE
  * (R > TF_LINEAR_MAX_ROWS, K > TF_LINEAR_MAX_INPUTS, N > TF_LINEAR_MAX_OUTPUTS, a

@@ -18,8 +18,8 @@ OUT_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libtf.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["segments.cu", "conv.cu", "attn.cu", "attn_tc.cu", "attn_static.cu", "argmax.cu", "accept.cu",
-           "draft.cu", "markov.cu", "qk.cu", "qk_scaled.cu", "attn_scaled.cu", "attn_scaled_tc.cu", "pages.cu", "sample.cu", "norm.cu",
-           "linear.cu"]
+           "draft.cu", "markov.cu", "qk.cu", "qk_scaled.cu", "attn_scaled.cu", "attn_scaled_tc.cu", "pages.cu",
+           "sample.cu", "norm.cu", "linear.cu"]
 
 
 def nvcc_path():

@@ -29,6 +29,8 @@
 // codes picked apart as they arrive (44 and 51) were slower.
 #include <cuda_bf16.h>
 
+#include <atomic>
+
 #include "scaled.cuh"
 
 namespace tf {
@@ -127,8 +129,8 @@ __device__ __forceinline__ void stage_as(const Linear& a, int r0, int c0, int n,
                 o = make_uint4(pack_bf2(p.x * f, s.x * f), pack_bf2(p.y * f, s.y * f), pack_bf2(q.x * f, t.x * f),
                                pack_bf2(q.y * f, t.y * f));
             } else {
-                o = make_uint4(__byte_perm(c.x, c.z, 0x5410), __byte_perm(c.x, c.z, 0x7632), __byte_perm(c.y, c.w, 0x5410),
-                               __byte_perm(c.y, c.w, 0x7632));
+                o = make_uint4(__byte_perm(c.x, c.z, 0x5410), __byte_perm(c.x, c.z, 0x7632),
+                               __byte_perm(c.y, c.w, 0x5410), __byte_perm(c.y, c.w, 0x7632));
             }
             *reinterpret_cast<uint4*>(sx + r * rowb + (u >> 4) * 256 + (u & 3) * 64 + ((u >> 2) & 3) * 16) = o;
         }
@@ -186,8 +188,8 @@ __device__ __forceinline__ void load_piece(const Linear& a, const Rows2& r, int 
 // at xr (+ nt * 8 rows). Even and odd MMAs have accumulators of their own, so that
 // they need not wait for one another.
 template <int NT, bool kWords>
-__device__ __forceinline__ void multiply(const Piece& p, const unsigned char* xr, int rowb, uint32_t sel, uint32_t nibbles,
-                                         float (&acc)[NT][2][4]) {
+__device__ __forceinline__ void multiply(const Piece& p, const unsigned char* xr, int rowb, uint32_t sel,
+                                         uint32_t nibbles, float (&acc)[NT][2][4]) {
     const float2 g = h2_to_f2(e4m3_low(__byte_perm(p.g[0], p.g[1], sel)));
     const uint32_t s0 = pack_bf2(g.x, g.x), s1 = pack_bf2(g.y, g.y);
     const uint32_t z0 = mul_bf2(s0, 0xC308C308u), z1 = mul_bf2(s1, 0xC308C308u);   // -136
@@ -471,7 +473,7 @@ constexpr int kMaxSmem = 227 << 10;
 constexpr int sum_bytes(int NT, int S) { return S > 1 ? kWarps * NT * 512 : 0; }
 
 // A launch of one of the kernels; `ready` remembers its shared memory's attribute by device.
-int launch_one(void (*kernel)(Linear, int), bool (&ready)[64], const Linear& a, int ctas, int S, int smem,
+int launch_one(void (*kernel)(Linear, int), std::atomic<bool> (&ready)[64], const Linear& a, int ctas, int S, int smem,
                cudaStream_t stream) {
     int dev = 0;
     cudaGetDevice(&dev);
@@ -486,7 +488,7 @@ int launch_one(void (*kernel)(Linear, int), bool (&ready)[64], const Linear& a, 
 template <int NT>
 int launch(Linear a, cudaStream_t stream) {
     constexpr int U = 2, kSums = kWarps * NT * 512;
-    static bool ready[4][64] = {};
+    static std::atomic<bool> ready[4][64] = {};
     const int chunks = (a.K + kChunk - 1) / kChunk, tiles = (a.N + 15) / 16, sms = sm_count();
     a.row_tiles = (a.R + 8 * NT - 1) / (8 * NT);
     int ctas = sms / a.row_tiles;
@@ -535,8 +537,9 @@ extern "C" int tf_linear_rows(const void* x, int64_t x_stride, const void* x_sca
     constexpr int64_t kMaxStride = int64_t(1) << 32;
     if (x_stride > kMaxStride || y_stride > kMaxStride) return TF_ERANGE;
     const size_t xb = size_t((R - 1) * x_stride + K) * (x_scales ? 1 : 2), yb = size_t((R - 1) * y_stride + N) * 2;
-    if (overlap(x, xb, y, yb) || overlap(w, size_t(N) * K / 2, y, yb) || overlap(w_scales, size_t(N) * (K / kGroup), y, yb) ||
-        overlap(s, size_t(N) * 4, y, yb) || (x_scales && overlap(x_scales, size_t(R) * (K / kGroup), y, yb)))
+    if (overlap(x, xb, y, yb) || overlap(w, size_t(N) * K / 2, y, yb) ||
+        overlap(w_scales, size_t(N) * (K / kGroup), y, yb) || overlap(s, size_t(N) * 4, y, yb) ||
+        (x_scales && overlap(x_scales, size_t(R) * (K / kGroup), y, yb)))
         return TF_EINVAL;
     if (!on_this_device(x) || !on_this_device(w) || !on_this_device(y)) return TF_EINVAL;
     Linear a = {};

@@ -158,7 +158,8 @@ extern "C" int tf_norm_rows(const void* x, int64_t x_stride, const void* res, in
     };
     const Span sx = span(x, 2 * x_stride, R, 2 * width), sr = span(res, 2 * res_stride, R, 2 * width),
                sw = span(w, 2 * width, 1, 2 * width), ss = span(sum, 2 * sum_stride, R, 2 * width),
-               sc = span(codes, width, R, width), sb = span(scales, width / TF_SCALE_COLUMNS, R, width / TF_SCALE_COLUMNS);
+               sc = span(codes, width, R, width),
+               sb = span(scales, width / TF_SCALE_COLUMNS, R, width / TF_SCALE_COLUMNS);
     // the sum may lie where an addend lay: a value is read and written by one thread
     if ((sum != x || sum_stride != x_stride) && !apart(ss, sx)) return TF_EINVAL;
     if ((sum != res || sum_stride != res_stride) && !apart(ss, sr)) return TF_EINVAL;
@@ -166,9 +167,9 @@ extern "C" int tf_norm_rows(const void* x, int64_t x_stride, const void* res, in
         if (!apart(in, sc) || !apart(in, sb)) return TF_EINVAL;
     if (!apart(ss, sw) || !apart(sc, sb)) return TF_EINVAL;
     if (!on_this_device(x) || !on_this_device(codes)) return TF_EINVAL;
-    const NormRows a = {static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(res), static_cast<const uint16_t*>(w),
-                        static_cast<uint16_t*>(sum), static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales),
-                        x_stride, res_stride, sum_stride, eps, width};
+    const NormRows a = {static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(res),
+                        static_cast<const uint16_t*>(w), static_cast<uint16_t*>(sum), static_cast<uint8_t*>(codes),
+                        static_cast<uint8_t*>(scales), x_stride, res_stride, sum_stride, eps, width};
     // Up to 128 threads a row: the more rows an SM has under way, the better its loads cover one another's latency
     // (16,381 rows of 2,048: 64 or 128 threads 36.8 us, 256 or 512 threads 44.0 us). More than four vectors a thread
     // would cost more in registers than that gains.

@@ -11,10 +11,12 @@
 // Scaled pools (tf_pages_copy_scaled) hold a byte a value, and the scale bytes
 // of the 16-key blocks that the copied keys fall in go with them.
 //
-// HBM bound: 1,024 bytes (8 heads x 128) a key, read and written (scaled: 512.5). One CTA a
-// (copy, pool); a whole page is one contiguous run, a part of it 8 runs of
-// keys x 128 bytes. Measured: 1,000 whole 64-key pages in 8 pools 152 us (1.05
-// GB, the measured copy rate); 64 forks of 16-key pages in 20 pools 5.2 us.
+// HBM bound: 1,024 bytes (8 heads x 128) a key, read and written (scaled: 512.5).
+// One CTA a (copy, pool); a whole page is one contiguous run, a part of it 8 runs
+// of keys x 128 bytes. Measured: 1,000 whole 64-key pages in 8 pools 152 us (1.05
+// GB, the measured copy rate); 64 forks of 16-key pages in 20 pools 5.2 us. Scaled,
+// 1,000 whole 128-key pages in 8 pools 154 us; 64 forks of 64-key pages, partly
+// filled, in 20 pools 9.6 us.
 #include <algorithm>
 #include <memory>
 #include <utility>
@@ -76,8 +78,8 @@ pages_copy_kernel(const __grid_constant__ Batch<kN> b, int page_keys) {
 }
 
 template <int kN, bool kScaled>
-int launch_batches(void* const* pools, void* const* scales, int n_pools, int page_keys, const int32_t* src, const int32_t* dst,
-                   const int32_t* keys, int n, cudaStream_t stream) {
+int launch_batches(void* const* pools, void* const* scales, int n_pools, int page_keys, const int32_t* src,
+                   const int32_t* dst, const int32_t* keys, int n, cudaStream_t stream) {
     auto b = std::make_unique<Batch<kN>>();
     for (int p0 = 0; p0 < n_pools; p0 += kPools) {
         const int np = std::min(kPools, n_pools - p0);
@@ -99,8 +101,8 @@ int launch_batches(void* const* pools, void* const* scales, int n_pools, int pag
 }
 
 template <bool kScaled>
-int copy_pages(void* const* pools, void* const* scales, int n_pools, int page_keys, int n_pages, const int32_t* src, const int32_t* dst,
-               const int32_t* keys, int n, cudaStream_t stream) {
+int copy_pages(void* const* pools, void* const* scales, int n_pools, int page_keys, int n_pages, const int32_t* src,
+               const int32_t* dst, const int32_t* keys, int n, cudaStream_t stream) {
     if (n_pools < 0 || n < 0 || n_pages < 1) return TF_EINVAL;
     if (page_keys < TF_MIN_PAGE_KEYS || page_keys > TF_MAX_PAGE_KEYS || (page_keys & (page_keys - 1))) return TF_EINVAL;
     if (n_pages > TF_MAX_PAGES || n_pools > 2 * 4096) return TF_ERANGE;

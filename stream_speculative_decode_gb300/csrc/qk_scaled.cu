@@ -188,7 +188,8 @@ qk_scaled_kernel(SegTable t, int layer, QkvRows in, const uint16_t* __restrict__
         const int part = blockIdx.x % kBlockCtas, g = (part & 1) * kWarps + warp;
         if (part < 2) {
             const uint64_t f = turns.f[lane];
-            for (int r = it.slot0 + warp; r < it.slot0 + it.n_rows; r += kWarps) angle[r][lane] = angle_of(it.key0 + r, f);
+            for (int r = it.slot0 + warp; r < it.slot0 + it.n_rows; r += kWarps)
+                angle[r][lane] = angle_of(it.key0 + r, f);
             __syncthreads();
         }
         pdl_wait();
@@ -238,10 +239,10 @@ int launch_qk_scaled(const SegTable& t, int layer, const QkvRows& in, const uint
                      float eps, const Turns& turns, uint16_t* q_out, cudaStream_t stream) {
     const int appends = kBlockCtas * t.n_appends;
     if (t.R >= kManyRows)
-        return launch_pdl(qk_scaled_kernel<true>, dim3(appends + (t.R + kWarps - 1) / kWarps), dim3(kThreads), 0, stream, t,
-                          layer, in, q_norm, k_norm, eps, turns, q_out);
-    return launch_pdl(qk_scaled_kernel<false>, dim3(appends + t.R), dim3(kThreads), 0, stream, t, layer, in, q_norm, k_norm,
-                      eps, turns, q_out);
+        return launch_pdl(qk_scaled_kernel<true>, dim3(appends + (t.R + kWarps - 1) / kWarps), dim3(kThreads), 0,
+                          stream, t, layer, in, q_norm, k_norm, eps, turns, q_out);
+    return launch_pdl(qk_scaled_kernel<false>, dim3(appends + t.R), dim3(kThreads), 0, stream, t, layer, in, q_norm,
+                      k_norm, eps, turns, q_out);
 }
 
 }  // namespace tf

@@ -108,6 +108,43 @@ def test_vocabulary(tf):
     check(call(tf, x, xs, *w), v, *w)
 
 
+@pytest.mark.parametrize("N,K", [(20011, 1024), (31000, 768), (9001, 256)])
+@pytest.mark.parametrize("x8", [False, True])
+def test_runs_of_tiles(tf, N, K, x8):
+    """Runs of several tiles a CTA, whose warps begin and end inside tiles, for each tile of rows."""
+    w = weights(N, K, 15, whole=True)
+    for R in (1, 12, 20, 40):
+        x, xs, v = rows(R, K, R + 16, x8, whole=True)
+        want = (v @ matrix(*w[:2]).T).float().to(torch.bfloat16)
+        assert torch.equal(call(tf, x, xs, *w), want), R
+
+
+def test_scales_far_from_one(tf):
+    """Row scales from 2^-100 to 2^90: exact sums under a power of two are its multiples."""
+    w = weights(300, 256, 17, whole=True)
+    x, xs, v = rows(9, 256, 18, True, whole=True)
+    want = v @ matrix(*w[:2]).T
+    for e in (-100, 90):
+        got = call(tf, x, (xs.int() + e).to(torch.uint8), *w)
+        assert torch.equal(got, torch.ldexp(want, torch.tensor(e, device="cuda")).float().to(torch.bfloat16)), e
+
+
+def test_two_streams_at_once(tf):
+    w = [weights(5000, 2048, 19 + i) for i in range(2)]
+    x = [rows(R, 2048, 21 + i, bool(i)) for i, R in enumerate((7, 16))]
+    want = [call(tf, x[i][0], x[i][1], *w[i]) for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        got = []
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got.append(call(tf, x[i][0], x[i][1], *w[i]))
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+
+
 @pytest.mark.parametrize("x8", [False, True])
 def test_many_rows(tf, x8):
     w = weights(200, 320, 5)
