@@ -63,6 +63,7 @@ constexpr int kStageB = 2 * kRawB;          // K then V
 constexpr int kTileB = kKT * TF_D * 2;      // 8 KB: a tile in fp16
 constexpr int kBuf = 2;                     // S/P buffers: tile j uses buffer j % 2
 constexpr int kVBuf = 3;                    // V buffers
+constexpr int kDone = kVBuf + 1;            // the P.Vs' barriers: none comes round while its V buffer is waited for
 constexpr int kThreads = 256;
 constexpr uint32_t kCols = 256;
 constexpr uint32_t kColS = 0;               // + 64 * (tile % 2)
@@ -80,12 +81,11 @@ constexpr int kUQConsumers = 7;             // the MMA thread, 2 V converter war
 struct Bars {
     uint64_t raw_full[kStages];
     uint64_t v_read[kStages];    // both V converters have read the stage
-    uint64_t k_free[kStages];    // its q.K completed
+    uint64_t k_free[kStages];    // its q.K completed (softmax warp 0 has seen the scores)
     uint64_t v_ready[kVBuf];
-    uint64_t v_free[kVBuf];      // its P.V completed
     uint64_t s_full[kBuf];
-    uint64_t p_full[kBuf];
-    uint64_t o_done[kBuf];       // P.V completed
+    uint64_t p_full[kBuf];       // by tile % 2, though the weights have one place
+    uint64_t o_done[kDone];      // P.V completed, by tile % kDone
     uint64_t q_full;             // the unit's queries landed (one phase a unit)
     uint64_t q_ready;            // and are in their two parts
     uint64_t uq_full[kUQ];
@@ -125,27 +125,29 @@ __device__ __forceinline__ uint64_t sdesc64(uint32_t addr) {
     d |= uint64_t(4) << 61;
     return d;
 }
-// mbar_wait that looks at the clock every kTests tests only: reading %globaltimer takes
-// longer than most waits here, and a chain of waits is what a tile's time is.
+// Bounded waits by a whole warp, with one outcome for its lanes. The clock is looked at
+// every kTests tests only: reading %globaltimer takes longer than most waits here, and a
+// chain of waits is what a tile's time is.
 constexpr int kTests = 32;
 __device__ __noinline__ bool wait_long(uint32_t a, uint32_t parity, volatile WaitCtl* wc) {
     unsigned long long t0 = 0;
     for (;;) {
 #pragma unroll 1
         for (int i = 0; i < kTests; ++i)
-            if (mbar_test(a, parity)) return true;
-        if (wc->flag) return false;
+            if (__all_sync(0xFFFFFFFFu, mbar_test(a, parity))) return true;
+        if (__any_sync(0xFFFFFFFFu, wc->flag != 0)) return false;
         const unsigned long long now = gtime();
         if (t0 == 0) t0 = now;
         if (now - t0 > wc->limit_ns) wc->flag = 1;
     }
 }
-__device__ __forceinline__ bool wait_thread(uint32_t a, uint32_t parity, volatile WaitCtl* wc) {
-    return mbar_test(a, parity) || wait_long(a, parity, wc);
-}
-// The same by a whole warp, with one outcome for its lanes.
 __device__ __forceinline__ bool wait_warp(uint32_t a, uint32_t parity, volatile WaitCtl* wc) {
-    return __all_sync(0xFFFFFFFFu, wait_thread(a, parity, wc));
+    return __all_sync(0xFFFFFFFFu, mbar_test(a, parity)) || wait_long(a, parity, wc);
+}
+// Two barriers at once: every lane tests one of them.
+__device__ __forceinline__ bool wait_both(uint32_t a, uint32_t pa, uint32_t b, uint32_t pb, volatile WaitCtl* wc) {
+    const bool odd = threadIdx.x & 1;
+    return wait_warp(odd ? b : a, odd ? pb : pa, wc);
 }
 // One lane of a converged warp, the same every time.
 __device__ __forceinline__ bool elect_one() {
@@ -237,6 +239,7 @@ __device__ __forceinline__ void softmax_tiles(SoftState& st) {
         const int b = gj % kBuf;
         const uint32_t colS = kColS + 64 * b;
         if (!wait_warp(su32(&bars->s_full[b]), (gj / kBuf) & 1, st.abortp)) break;
+        if (threadIdx.x == 0) mbar_arrive(su32(&bars->k_free[gj % kStages]));
         tc_fence_after();
         if (st.wact) {
             float f[NB];
@@ -308,7 +311,7 @@ __device__ __forceinline__ void softmax_tiles(SoftState& st) {
                 const float to = mx - kHeadroom;
                 const bool resc = row_slow && to > st.mref;
                 if (__any_sync(0xFFFFFFFFu, resc)) {
-                    if (j >= 1 && !wait_warp(su32(&bars->o_done[(gj - 1) % kBuf]), ((gj - 1) / kBuf) & 1, st.abortp))
+                    if (j >= 1 && !wait_warp(su32(&bars->o_done[(gj - 1) % kDone]), ((gj - 1) / kDone) & 1, st.abortp))
                         break;
                     tc_fence_after();
                     const float alpha = resc ? ex2_approx(st.mref - to) : 1.f;
@@ -428,11 +431,10 @@ attn_scaled_tc_kernel(SegTable t, int layer, float* __restrict__ part_o, float2*
         for (int b = 0; b < kBuf; ++b) {
             mbar_init(su32(&bars->s_full[b]), 1);
             mbar_init(su32(&bars->p_full[b]), 4);
-            mbar_init(su32(&bars->o_done[b]), 1);
         }
+        for (int b = 0; b < kDone; ++b) mbar_init(su32(&bars->o_done[b]), 1);
         for (int b = 0; b < kVBuf; ++b) {
             mbar_init(su32(&bars->v_ready[b]), 2);
-            mbar_init(su32(&bars->v_free[b]), 1);
         }
         mbar_init(su32(&bars->q_full), 1);
         mbar_init(su32(&bars->q_ready), 4);
@@ -460,7 +462,9 @@ attn_scaled_tc_kernel(SegTable t, int layer, float* __restrict__ part_o, float2*
         // P.V of tile j, then the q.K of tile j + 2, which takes over its S buffer. The whole
         // warp walks the loop and one lane of it issues: with the control flow the warp's,
         // addresses and descriptors stay in uniform registers (in a lone thread's code an
-        // MMA took some 70 cycles to issue, and everything else stands behind it).
+        // MMA took some 70 cycles to issue, and everything else stands behind it). Even so an MMA
+        // or a commit is 45 to 50 cycles and a wait that is already over some 100, so a product
+        // has one commit, and two barriers are waited for at once.
         Ring<kStages> kr;   // the stage of the next q.K
         Ring<kVBuf> vr;     // the V buffer of the next P.V
         Ring<kUQ> ur;
@@ -473,8 +477,10 @@ attn_scaled_tc_kernel(SegTable t, int layer, float* __restrict__ part_o, float2*
             const int T = unit_of<true>(t, layer, u).T;
             auto qk = [&]() {
                 const uint32_t b = qs & 1;
-                if (!wait_warp(su32(&bars->raw_full[kr.i]), kr.parity, abortp) ||
-                    !wait_warp(su32(&bars->o_done[b]), (qs >> 1 & 1) ^ 1, abortp))
+                const uint32_t raw = su32(&bars->raw_full[kr.i]), last = qs - kBuf;   // the S buffer's last tile
+                if (!(qs < kBuf ? wait_warp(raw, kr.parity, abortp)
+                                : wait_both(raw, kr.parity, su32(&bars->o_done[last % kDone]), last / kDone & 1,
+                                            abortp)))
                     return false;
                 tc_fence_after();
                 if (elect_one()) {
@@ -484,7 +490,6 @@ attn_scaled_tc_kernel(SegTable t, int layer, float* __restrict__ part_o, float2*
                         tc_mma_ts_f8(tmem + kColS + 64 * b, tmem + kColQ + 8 * k, dk + 2 * (k >> 1), kIdescQK,
                                      k > 0 ? 1u : 0u);
                     tc_commit(su32(&bars->s_full[b]));
-                    tc_commit(su32(&bars->k_free[kr.i]));
                 }
                 __syncwarp();
                 kr.next();
@@ -510,8 +515,7 @@ attn_scaled_tc_kernel(SegTable t, int layer, float* __restrict__ part_o, float2*
             };
             for (int j = 0; j < T && ok; ++j) {
                 const uint32_t b = ps & 1;
-                ok = wait_warp(su32(&bars->p_full[b]), ps >> 1 & 1, abortp) &&
-                     wait_warp(su32(&bars->v_ready[vr.i]), vr.parity, abortp);
+                ok = wait_both(su32(&bars->p_full[b]), ps >> 1 & 1, su32(&bars->v_ready[vr.i]), vr.parity, abortp);
                 if (!ok) break;
                 tc_fence_after();
                 if (elect_one()) {
@@ -520,8 +524,7 @@ attn_scaled_tc_kernel(SegTable t, int layer, float* __restrict__ part_o, float2*
                     for (int k = 0; k < kKT / 16; ++k)
                         tc_mma_ts(tmem + kColO, tmem + kColS + 64 * b + 8 * k, dv + 128 * k, kIdescPV,
                                   (j > 0 || k > 0) ? 1u : 0u);
-                    tc_commit(su32(&bars->o_done[b]));
-                    tc_commit(su32(&bars->v_free[vr.i]));
+                    tc_commit(su32(&bars->o_done[ps % kDone]));
                 }
                 __syncwarp();
                 vr.next();
@@ -570,8 +573,8 @@ attn_scaled_tc_kernel(SegTable t, int layer, float* __restrict__ part_o, float2*
             __syncwarp();
             for (int j = 0; j < U.T; ++j, ++gt) {
                 const int s = r.i;
-                if (!wait_warp(su32(&bars->v_read[s]), r.parity ^ 1u, abortp) ||
-                    !wait_warp(su32(&bars->k_free[s]), r.parity ^ 1u, abortp)) {
+                if (!wait_both(su32(&bars->v_read[s]), r.parity ^ 1u, su32(&bars->k_free[s]), r.parity ^ 1u,
+                               abortp)) {
                     ok = false;
                     break;
                 }
@@ -657,7 +660,8 @@ attn_scaled_tc_kernel(SegTable t, int layer, float* __restrict__ part_o, float2*
                         }
                     }
                 }
-                if (!wait_warp(su32(&bars->v_free[b]), vr.parity ^ 1u, abortp)) {
+                const int last = gt - kVBuf;   // the V buffer's last tile
+                if (last >= 0 && !wait_warp(su32(&bars->o_done[last % kDone]), (last / kDone) & 1, abortp)) {
                     ok = false;
                     break;
                 }
@@ -716,7 +720,7 @@ attn_scaled_tc_kernel(SegTable t, int layer, float* __restrict__ part_o, float2*
                 softmax_tiles<false>(ss);
             gt += U.T;
             const int un = next_unit_warp(bars, m, abortp);
-            if (!abortp->flag) wait_warp(su32(&bars->o_done[(gt - 1) % kBuf]), ((gt - 1) / kBuf) & 1, abortp);
+            if (!abortp->flag) wait_warp(su32(&bars->o_done[(gt - 1) % kDone]), ((gt - 1) / kDone) & 1, abortp);
             tc_fence_after();
             const bool aborted = abortp->flag != 0;
             const volatile int32_t* const nan_key = bars->nan_key[m % kUnits];
@@ -761,8 +765,8 @@ attn_scaled_tc_kernel(SegTable t, int layer, float* __restrict__ part_o, float2*
                         }
                         if (d0 == 0) {   // a sum that is no number must not pass for none in a merge
                             const bool lost = aborted || !(lsum <= 3e38f);
-                            part_ml[rec] = make_float2(aborted ? NAN : ss.mref > -INFINITY ? ss.mref : lost ? 0.f : -INFINITY,
-                                                       lost ? INFINITY : empty ? 0.f : lsum);
+                            const float m = ss.mref > -INFINITY ? ss.mref : lost ? 0.f : -INFINITY;
+                            part_ml[rec] = make_float2(aborted ? NAN : m, lost ? INFINITY : empty ? 0.f : lsum);
                         }
                     }
                 };
