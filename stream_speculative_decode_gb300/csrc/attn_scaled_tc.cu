@@ -22,24 +22,30 @@
 //               of V) into a ring of 6 stages, each with its blocks' K scales and V
 //               factors beside it; at a unit's start its V scales, for E;
 //   warps 5, 6  the conversion of the V tiles, half a tile each, ring of 3;
-//   warp 4      lane 0: both products' MMAs, and the queries' TMA loads;
+//   warp 4      both products' MMAs, and the queries' TMA loads;
 //   warps 0-3   softmax and records; at a unit's start the queries' two parts, each
 //               row by the thread that owns it.
 // Tensor memory: S/P of tile j at columns 64 * (j % 2), O at 128, the queries' parts at
 // 192. (An MMA of 64 keys that reads its 128 query rows from shared memory is bound by
 // that: 4 KB of queries beside 2 KB of keys.)
 //
-// Measured: 64 windows of 16 rows at 16 to 32,768 keys 122.8 us (3.1 TB/s, 47 % of
-// the measured copy rate); a 2,048-row prompt chunk at 8,179 keys 181 us (662
-// TFLOP/s). What bounds it is the chain of a tile, no unit by itself: a 64-key tile
-// is 8 KB from HBM, 350 cycles of an SM's share, the tensor cores take some 270 (M =
-// 128 whatever the window's rows), the softmax warps' chain 780 of a CTA and half that
-// with two. Of the 181 us the exponentials cost 29 (copies of the kernel without
-// them), V's conversion 12, K's second product 2; of the 123 us 8, 7 and 4, and the
-// units' tail 15 % (760 of up to 128 tiles on 304 CTAs; chunks half as long 125 us).
-// Both conversions by a warp each (K to fp16 too, the load warp's work) took 2,600
-// cycles a tile (212 us), the queries in shared memory and the MMAs issued by a lone
-// thread 147 and 209 us; a third S buffer in place of the queries 130 and 193.
+// Measured: 64 windows of 16 rows at 16 to 32,768 keys 112 us (3.4 TB/s, 51 % of the
+// measured copy rate); a 2,048-row prompt chunk at 8,179 keys 181 us (662 TFLOP/s).
+// What bounds it is the chain of a tile, no unit by itself: a 64-key tile is 8 KB
+// from HBM, 350 cycles of an SM's share, and the tensor cores take some 270 (M = 128
+// whatever the window's rows), but from weights to weights two tiles on it is P.V's
+// issue (265), its completion (400), q.K's issue (240), the scores (250) and the
+// softmax (750, with 32 query rows a warp 1,050), for each of two CTAs. A unit's
+// beginning and end are 8,500 cycles, and the tail of 760 units of up to 128 tiles on
+// 304 CTAs is 15 % (chunks of half the keys: 125 against 123 us). Copies of the
+// kernel without the exponentials: 104 and 137 us; without V's conversion 104 and 172.
+//
+// Tried and slower: K converted to fp16 as well, by the load warp (212 us for the 64
+// windows); queries in shared memory with a third S buffer in their place (117 and
+// 185); weights in columns of their own, so that q.K need not wait for P.V (120 and
+// 196; with P.V in a warp of its own, which leaves 96 registers a thread, 144 and
+// 211); a quarter of the exponentials as polynomials (125 and 213); the second half
+// of a tile's scores loaded ahead (111 and 189 against 111 and 184).
 //
 // A weight is at most 2^15 (fp16), the largest of a row at 2^6 when its reference
 // moves: weights below 2^-31 of it vanish. A block of V whose scale is 2^31 below the
@@ -91,6 +97,7 @@ struct Bars {
     uint64_t uq_full[kUQ];
     uint64_t uq_empty[kUQ];
     int32_t uq[kUQ];
+    Unit next[kUQ];              // the unit uq[], when there is one
     uint64_t grp;
     uint64_t drain;              // the MMAs in flight (drained at the end)
     uint32_t tmem_base;
@@ -355,21 +362,30 @@ __device__ __forceinline__ void softmax_tiles(SoftState& st) {
     }
 }
 
+// Two columns of the thread's lane; dual: threads 16-31 write those 16 columns on.
+template <bool DUAL>
+__device__ __forceinline__ void st_two(uint32_t taddr, uint32_t a, uint32_t b) {
+    if constexpr (DUAL)
+        asm volatile("tcgen05.st.sync.aligned.16x32bx2.x2.b32 [%0], 16, {%1,%2};" ::"r"(taddr), "r"(a), "r"(b) : "memory");
+    else
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1,%2};" ::"r"(taddr), "r"(a), "r"(b) : "memory");
+}
 // The thread's query row (tensor memory lane 32 * warp + row of the tile) from bf16 to
 // its two e4m3 parts in tensor memory, under the power of two that puts its largest at
 // 2^7..2^8; returns the factor of its scores. Dual: two threads a row, 32 dimensions
 // each. 8 columns hold 32 dimensions (an MMA's K) of a part.
+// (Loops and not straight code, here and where a unit ends: what runs once a unit is
+// fetched anew each time.)
 template <bool DUAL>
 __device__ __forceinline__ float convert_query(uint32_t sQ, uint32_t trow, int warp, int lane) {
     const int r = 32 * warp + (DUAL ? (lane & 15) : lane);
     constexpr int NP = DUAL ? 4 : 8;   // pieces of 8 dimensions
     const int p0 = DUAL ? (lane >> 4) * 4 : 0;
-    uint4 v[NP];
     uint32_t most = 0;
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < NP; ++i) {
-        v[i] = lds128(sQ + r * 128 + (((p0 + i) ^ (r & 7)) << 4));
-        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        const uint4 v = lds128(sQ + r * 128 + (((p0 + i) ^ (r & 7)) << 4));
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int k = 0; k < 4; ++k)
             most = max(most, max(finite_bits(__uint_as_float(w[k] << 16)),
@@ -378,26 +394,25 @@ __device__ __forceinline__ float convert_query(uint32_t sQ, uint32_t trow, int w
     if (DUAL) most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 16));
     const int up = min(134 - int(most >> 23), 126);
     const float mul = __uint_as_float(uint32_t(127 + up) << 23);
-    uint32_t q8[NP * 4];   // for each 32 dimensions: 8 words of the first part, 8 of the second
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < NP; ++i) {
-        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        const uint4 v = lds128(sQ + r * 128 + (((p0 + i) ^ (r & 7)) << 4));
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        uint32_t hi[2], lo[2];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
             const float y[4] = {__uint_as_float(w[2 * c] << 16) * mul, __uint_as_float(w[2 * c] & 0xFFFF0000u) * mul,
                                 __uint_as_float(w[2 * c + 1] << 16) * mul,
                                 __uint_as_float(w[2 * c + 1] & 0xFFFF0000u) * mul};
-            const uint32_t h = e4m3_quad(y[0], y[1], y[2], y[3]);
-            const float2 a = h2_to_f2(e4m3_low(h)), b = h2_to_f2(e4m3_high(h));
-            const int at = (i >> 2) * 16 + (i & 3) * 2 + c;
-            q8[at] = h;
-            q8[at + 8] = e4m3_quad(y[0] - a.x, y[1] - a.y, y[2] - b.x, y[3] - b.y);
+            hi[c] = e4m3_quad(y[0], y[1], y[2], y[3]);
+            const float2 a = h2_to_f2(e4m3_low(hi[c])), b = h2_to_f2(e4m3_high(hi[c]));
+            lo[c] = e4m3_quad(y[0] - a.x, y[1] - a.y, y[2] - b.x, y[3] - b.y);
         }
+        // 32 dimensions: 8 columns of the first part, 8 of the second
+        const uint32_t at = trow + kColQ + (i >> 2) * 16 + (i & 3) * 2;
+        st_two<DUAL>(at, hi[0], hi[1]);
+        st_two<DUAL>(at + 8, lo[0], lo[1]);
     }
-    if constexpr (DUAL)
-        tc_st16x2_16<16>(trow + kColQ, q8);
-    else
-        tc_st32(trow + kColQ, q8);
     tc_wait_st();
     return __uint_as_float(uint32_t(127 - up) << 23) * kLog2e8;
 }
@@ -408,6 +423,19 @@ __device__ __forceinline__ void store_codes(uint32_t tile, int r, int p, const u
     const uint32_t row = tile + r * 128;
     sts128(row + (((2 * p) ^ (r & 7)) << 4), make_uint4(h[0], h[1], h[2], h[3]));
     sts128(row + (((2 * p + 1) ^ (r & 7)) << 4), make_uint4(h[4], h[5], h[6], h[7]));
+}
+
+// The m-th unit that the load warp handed this CTA after its first (unit blockIdx.x); false
+// where there is none, or the CTA gave up. Units travel through shared memory: looking one
+// up in the table is two trips to L2, which every role would stand still for.
+__device__ __forceinline__ bool next_unit(Bars* bars, int m, volatile WaitCtl* abortp, Unit& U) {
+    const int slot = m % kUQ;
+    const bool more = wait_warp(su32(&bars->uq_full[slot]), (m / kUQ) & 1, abortp) &&
+                      reinterpret_cast<volatile int32_t*>(bars->uq)[slot] >= 0;
+    if (more) U = bars->next[slot];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(su32(&bars->uq_empty[slot]));
+    return more;
 }
 
 __global__ void __launch_bounds__(kThreads, 2)
@@ -467,14 +495,15 @@ attn_scaled_tc_kernel(SegTable t, int layer, float* __restrict__ part_o, float2*
         // has one commit, and two barriers are waited for at once.
         Ring<kStages> kr;   // the stage of the next q.K
         Ring<kVBuf> vr;     // the V buffer of the next P.V
-        Ring<kUQ> ur;
         uint32_t qs = 0, ps = 0;   // their S buffers' uses so far: buffer & 1, parity >> 1
         const uint64_t dk0 = sdesc64(sRaw), dv0 = sdesc(sV, kTileB, 1024);
         bool ok = true;
-        if (elect_one()) issue_q(sQ, &qmap, unit_of<true>(t, layer, blockIdx.x), su32(&bars->q_full));
+        Unit U = unit_of<true>(t, layer, blockIdx.x);
+        if (elect_one()) issue_q(sQ, &qmap, U, su32(&bars->q_full));
         int q_issued = 1;
-        for (int u = blockIdx.x, n = 0; u >= 0 && ok; ++n) {
-            const int T = unit_of<true>(t, layer, u).T;
+        bool more = true;
+        for (int n = 0; more && ok; ++n) {
+            const int T = U.T;
             auto qk = [&]() {
                 const uint32_t b = qs & 1;
                 const uint32_t raw = su32(&bars->raw_full[kr.i]), last = qs - kBuf;   // the S buffer's last tile
@@ -500,18 +529,14 @@ attn_scaled_tc_kernel(SegTable t, int layer, float* __restrict__ part_o, float2*
             if (!ok) break;
             tc_fence_after();
             ok = qk() && (T < 2 || qk());
-            int next = -2;   // the next unit, not known yet
+            bool entered = false;   // the next unit is known, its queries on their way
             auto enter_next = [&]() {
-                next = reinterpret_cast<volatile int32_t*>(bars->uq)[ur.i];
+                entered = true;
+                more = next_unit(bars, n, abortp, U);
+                // the bf16 tile of the queries has been free since q_ready
+                if (more && elect_one()) issue_q(sQ, &qmap, U, su32(&bars->q_full));
                 __syncwarp();
-                if (elect_one()) {
-                    mbar_arrive(su32(&bars->uq_empty[ur.i]));
-                    // the bf16 tile of the queries has been free since q_ready
-                    if (next >= 0) issue_q(sQ, &qmap, unit_of<true>(t, layer, next), su32(&bars->q_full));
-                }
-                __syncwarp();
-                ur.next();
-                if (next >= 0) ++q_issued;
+                q_issued += more;
             };
             for (int j = 0; j < T && ok; ++j) {
                 const uint32_t b = ps & 1;
@@ -531,14 +556,10 @@ attn_scaled_tc_kernel(SegTable t, int layer, float* __restrict__ part_o, float2*
                 ++ps;
                 if (j + 2 < T)
                     ok = qk();
-                else if (next == -2 && __all_sync(0xFFFFFFFFu, mbar_test(su32(&bars->uq_full[ur.i]), ur.parity)))
+                else if (!entered && __all_sync(0xFFFFFFFFu, mbar_test(su32(&bars->uq_full[n % kUQ]), n / kUQ & 1)))
                     enter_next();
             }
-            if (ok && next == -2) {
-                ok = wait_warp(su32(&bars->uq_full[ur.i]), ur.parity, abortp);
-                if (ok) enter_next();
-            }
-            u = next;
+            if (ok && !entered) enter_next();
         }
         if (elect_one()) {
             tc_commit(su32(&bars->drain));
@@ -554,8 +575,8 @@ attn_scaled_tc_kernel(SegTable t, int layer, float* __restrict__ part_o, float2*
         Ring<kUQ> ur;
         int gt = 0;
         bool ok = true;
+        Unit U = unit_of<true>(t, layer, blockIdx.x);
         for (int u = blockIdx.x, m = 0; u >= 0 && ok; ++m) {
-            const Unit U = unit_of<true>(t, layer, u);
             const int nblocks = (min(U.st.chunk_keys, U.st.keys - U.c0) + TF_SCALE_KEYS - 1) / TF_SCALE_KEYS;
             const int bs = t.page_shift - 4;
             uint32_t top = 0;
@@ -603,9 +624,11 @@ attn_scaled_tc_kernel(SegTable t, int layer, float* __restrict__ part_o, float2*
             if (lane == 0) un = int(gridDim.x) + atomicAdd(&t.tc_work[2 * layer], 1);
             un = __shfl_sync(0xFFFFFFFFu, un, 0);
             if (un >= n_units) un = -1;
+            if (un >= 0) U = unit_of<true>(t, layer, un);
             if (!wait_warp(su32(&bars->uq_empty[ur.i]), ur.parity ^ 1u, abortp)) break;
             if (lane == 0) {
                 bars->uq[ur.i] = un;
+                bars->next[ur.i] = U;
                 mbar_arrive(su32(&bars->uq_full[ur.i]));
             }
             ur.next();
@@ -622,9 +645,9 @@ attn_scaled_tc_kernel(SegTable t, int layer, float* __restrict__ part_o, float2*
         Ring<kStages> r;
         Ring<kVBuf> vr;
         int gt = 0;
-        bool ok = true;
-        for (int u = blockIdx.x, m = 0; u >= 0 && ok; ++m) {
-            const Unit U = unit_of<true>(t, layer, u);
+        bool ok = true, more = true;
+        Unit U = unit_of<true>(t, layer, blockIdx.x);
+        for (int m = 0; more && ok; ++m) {
             const int nkeys = min(U.st.chunk_keys, U.st.keys - U.c0);
             const int lim_all = min((full ? U.st.keys : U.st.keys - U.st.rows + 1) - U.c0, nkeys);
             for (int j = 0; j < U.T; ++j, ++gt) {
@@ -681,14 +704,15 @@ attn_scaled_tc_kernel(SegTable t, int layer, float* __restrict__ part_o, float2*
                 __syncwarp();
                 if (lane == 0) mbar_arrive(su32(&bars->v_ready[b]));
             }
-            if (ok) u = next_unit_warp(bars, m, abortp);
+            if (ok) more = next_unit(bars, m, abortp, U);
         }
     } else {
         // ------------------------------------------------------------ softmax + records
         int gt = 0, gph = 0;
         const uint32_t trow = tmem + (uint32_t(warp * 32) << 16);
-        for (int u = blockIdx.x, m = 0; u >= 0; ++m) {
-            const Unit U = unit_of<true>(t, layer, u);
+        bool more = true;
+        Unit U = unit_of<true>(t, layer, blockIdx.x);
+        for (int m = 0; more; ++m) {
             const SegStream& st = U.st;
             const int nq = st.rows * 4, per = q_per(st.rows);
             const bool dual = per == 16;
@@ -719,7 +743,6 @@ attn_scaled_tc_kernel(SegTable t, int layer, float* __restrict__ part_o, float2*
             else
                 softmax_tiles<false>(ss);
             gt += U.T;
-            const int un = next_unit_warp(bars, m, abortp);
             if (!abortp->flag) wait_warp(su32(&bars->o_done[(gt - 1) % kDone]), ((gt - 1) / kDone) & 1, abortp);
             tc_fence_after();
             const bool aborted = abortp->flag != 0;
@@ -730,56 +753,47 @@ attn_scaled_tc_kernel(SegTable t, int layer, float* __restrict__ part_o, float2*
                 const int e = reinterpret_cast<volatile int32_t*>(bars->top)[m % kUnits] - kScaleBias - kVShift;
                 const float up0 = __uint_as_float(uint32_t(127 + e / 2) << 23);
                 const float up1 = __uint_as_float(uint32_t(127 + e - e / 2) << 23);
-                auto finish = [&](auto& ro) {
-                    constexpr int ND = int(sizeof(ro) / sizeof(ro[0]));
-                    const int d0 = ND == 32 ? 32 * (lane >> 4) : 0;
-                    float lsum = ss.l;
-                    if (ND == 32) lsum += __shfl_xor_sync(0xFFFFFFFFu, lsum, 16);
+                float lsum = ss.l;
+                if (dual) lsum += __shfl_xor_sync(0xFFFFFFFFu, lsum, 16);
+                const int d0 = dual ? 32 * (lane >> 4) : 0, n16 = dual ? 2 : 4;
+                const bool direct = mode == kMergeDirect, empty = ss.mref == -INFINITY && !(lsum != lsum);
+                const int64_t rec = st.pbase + (int64_t(U.chunk) * TF_NKV + U.g) * nq + qi;
+                float up = up0;   // of an output: / l
+                if (direct) up *= 1.f / lsum;
+                if (aborted) up = NAN;
+                if (!direct && empty) up = 0.f;
+#pragma unroll 1
+                for (int i = 0; i < n16; ++i) {
+                    uint32_t ro[16];
+                    if (dual)
+                        tc_ld16x2_16<32>(trow + kColO + 16 * i, ro);
+                    else
+                        tc_ld16(trow + kColO + 16 * i, ro);
+                    tc_wait_ld();
+                    const int d = d0 + 16 * i;
                     if (any_nan) {
 #pragma unroll
-                        for (int c = 0; c < ND; ++c)
-                            if (nan_key[d0 + c] < ss.lim) ro[c] = 0x7FC00000u;
+                        for (int c = 0; c < 16; ++c)
+                            if (nan_key[d + c] < ss.lim) ro[c] = 0x7FC00000u;
                     }
-                    if (qvalid && mode == kMergeDirect) {
-                        const float inv = aborted ? NAN : 1.f / lsum;
-                        auto* dst = out_row(out, st, U.g, qi) + d0;
+                    if (qvalid) {
 #pragma unroll
-                        for (int c = 0; c < ND / 4; ++c)
-                            store_out4(dst + 4 * c, make_float4(__uint_as_float(ro[4 * c]) * inv * up0 * up1,
-                                                                __uint_as_float(ro[4 * c + 1]) * inv * up0 * up1,
-                                                                __uint_as_float(ro[4 * c + 2]) * inv * up0 * up1,
-                                                                __uint_as_float(ro[4 * c + 3]) * inv * up0 * up1));
-                    } else if (qvalid) {
-                        const int64_t rec = st.pbase + (int64_t(U.chunk) * TF_NKV + U.g) * nq + qi;
-                        const bool empty = ss.mref == -INFINITY && !(lsum != lsum);
-                        float4* dst = reinterpret_cast<float4*>(part_o + rec * TF_D + d0);
-#pragma unroll
-                        for (int c = 0; c < ND / 4; ++c) {
-                            float4 v = make_float4(__uint_as_float(ro[4 * c]) * up0 * up1,
-                                                   __uint_as_float(ro[4 * c + 1]) * up0 * up1,
-                                                   __uint_as_float(ro[4 * c + 2]) * up0 * up1,
-                                                   __uint_as_float(ro[4 * c + 3]) * up0 * up1);
-                            if (aborted) v = make_float4(NAN, NAN, NAN, NAN);
-                            else if (empty) v = make_float4(0.f, 0.f, 0.f, 0.f);
-                            dst[c] = v;
-                        }
-                        if (d0 == 0) {   // a sum that is no number must not pass for none in a merge
-                            const bool lost = aborted || !(lsum <= 3e38f);
-                            const float m = ss.mref > -INFINITY ? ss.mref : lost ? 0.f : -INFINITY;
-                            part_ml[rec] = make_float2(aborted ? NAN : m, lost ? INFINITY : empty ? 0.f : lsum);
+                        for (int c = 0; c < 4; ++c) {
+                            const float4 v = make_float4(
+                                __uint_as_float(ro[4 * c]) * up * up1, __uint_as_float(ro[4 * c + 1]) * up * up1,
+                                __uint_as_float(ro[4 * c + 2]) * up * up1, __uint_as_float(ro[4 * c + 3]) * up * up1);
+                            if (direct)
+                                store_out4(out_row(out, st, U.g, qi) + d + 4 * c, v);
+                            else
+                                *reinterpret_cast<float4*>(part_o + rec * TF_D + d + 4 * c) = v;
                         }
                     }
-                };
-                if (dual) {
-                    uint32_t r32[32];
-                    tc_ld16x2_32<32>(trow + kColO, r32);
-                    tc_wait_ld();
-                    finish(r32);
-                } else {
-                    uint32_t r64[64];
-                    tc_ld64(trow + kColO, r64);
-                    tc_wait_ld();
-                    finish(r64);
+                    __syncwarp();
+                }
+                if (qvalid && !direct && d0 == 0) {   // a sum that is no number must not pass for none in a merge
+                    const bool lost = aborted || !(lsum <= 3e38f);
+                    const float m = ss.mref > -INFINITY ? ss.mref : lost ? 0.f : -INFINITY;
+                    part_ml[rec] = make_float2(aborted ? NAN : m, lost ? INFINITY : empty ? 0.f : lsum);
                 }
             }
             tc_fence_before();
@@ -802,7 +816,7 @@ attn_scaled_tc_kernel(SegTable t, int layer, float* __restrict__ part_o, float2*
                     }
                 }
             }
-            u = un;
+            more = next_unit(bars, m, abortp, U);
         }
     }
     tc_fence_before();
