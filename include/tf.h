@@ -564,7 +564,10 @@ int tf_pages_copy(void* const* pools, int n_pools, int32_t page_keys, int32_t n_
  *                 format above.
  *   tf_attn_paged reads codes and scales (q and out bf16; the window's own rows
  *                 are read back as coded); a stream's bits depend on that stream
- *                 alone. P.V runs with fp16 weights (off by 2^-12 of each) and
+ *                 alone. Windows of 9 rows or more take a quarter of the keys a
+ *                 chunk (2,048 at least, tf_chunk_keys at most), prompts of few
+ *                 windows less than tf_chunk_keys too (tf_partials_bytes and
+ *                 tf_segments_query tell the table's own sizes). P.V runs with fp16 weights (off by 2^-12 of each) and
  *                 exact codes, summed in fp32; keys whose weight times V's scale
  *                 is below 2^-31 of a row's largest such product do not count in
  *                 P.V. The tensor-core kernel (windows of 9 rows or more,

@@ -1,6 +1,6 @@
 // Attention (tf_attn_paged) over scaled pools: keys and values as e4m3 codes
-// with a power-of-two scale for each 16 keys of a head. Items, chunks, partial
-// records and merges are those of attn.cu; a window of more than 8 rows runs as
+// with a power-of-two scale for each 16 keys of a head. Items, partial records
+// and merges are those of attn.cu, and so are the chunks; a window of more than 8 rows runs as
 // several items over its chunk, next to each other in the grid.
 //
 // With c the codes, ek and ev a block's exponents and x the scores in log2 units:

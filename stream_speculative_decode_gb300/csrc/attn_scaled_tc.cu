@@ -29,15 +29,15 @@
 // 192. (An MMA of 64 keys that reads its 128 query rows from shared memory is bound by
 // that: 4 KB of queries beside 2 KB of keys.)
 //
-// Measured: 64 windows of 16 rows at 16 to 32,768 keys 112 us (3.4 TB/s, 51 % of the
+// Measured: 64 windows of 16 rows at 16 to 32,768 keys 114 us (3.4 TB/s, 50 % of the
 // measured copy rate); a 2,048-row prompt chunk at 8,179 keys 181 us (662 TFLOP/s).
 // What bounds it is the chain of a tile, no unit by itself: a 64-key tile is 8 KB
 // from HBM, 350 cycles of an SM's share, and the tensor cores take some 270 (M = 128
 // whatever the window's rows), but from weights to weights two tiles on it is P.V's
 // issue (265), its completion (400), q.K's issue (240), the scores (250) and the
 // softmax (750, with 32 query rows a warp 1,050), for each of two CTAs. A unit's
-// beginning and end are 8,500 cycles, and the tail of 760 units of up to 128 tiles on
-// 304 CTAs is 15 % (chunks of half the keys: 125 against 123 us). Copies of the
+// beginning and end are 8,500 cycles, and the tail of some 900 units of up to 128 tiles
+// on 304 CTAs is 15 % (chunks of half the keys: 125 against 123 us). Copies of the
 // kernel without the exponentials: 104 and 137 us; without V's conversion 104 and 172.
 //
 // Tried and slower: K converted to fp16 as well, by the load warp (212 us for the 64

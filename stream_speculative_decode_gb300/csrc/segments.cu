@@ -174,9 +174,28 @@ size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 namespace tf {
 
+// The keys of a chunk of a window over scaled pools, `prompt_windows` those of its prompt
+// call (0: a verify window). A tile of such keys is half of a bf16 one's bytes and no less
+// work, so a round of few wide windows has to be split further to reach every SM: a verify
+// window of the tensor-core kernel into four chunks (what it is split into must not depend
+// on the other streams), a prompt into about two units an SM. Measured, us with and
+// without: 16 windows of 16 rows at 256 to 4,096 keys 25.3 and 31.6, 6 at 2,000 to 16,000
+// 38 and 68, 1 at 8,000 26 and 63, against 48 at 3,000 to 4,096 69.5 and 65.0 (chunks of
+// 1,024 keys: 87), 64 of 12 at 16 to 32,768 73 and 67.5; prompts of 300 rows at 6,000 keys
+// 44 and 64, of 20 at 4,000 16 and 44, of 2,048 at 8,179 never split 181 (in four 219).
+// Narrow windows gain nothing (16 of 1 to 8 rows: within 10 % either way).
+int32_t scaled_chunk_keys(int32_t rows, int32_t keys, int prompt_windows) {
+    const int32_t most = tf_chunk_keys(rows);
+    if (rows < kTcMinRows && prompt_windows == 0) return most;
+    constexpr int kSlots = 304;   // CTAs of the tensor-core kernel on 152 SMs
+    const int n = prompt_windows ? std::clamp(kSlots / (TF_NKV * prompt_windows), 1, 8) : 4;
+    const int32_t share = ((keys + n - 1) / n + TF_MAX_PAGE_KEYS - 1) / TF_MAX_PAGE_KEYS * TF_MAX_PAGE_KEYS;
+    return std::min(most, std::max(share, prompt_windows ? 512 : 2048));
+}
+
 // The plan of a set of windows, each of at most `max_window_rows` rows
 // (TF_MAX_ROWS for the verify tables, kPromptTileRows for a prompt call).
-int plan_windows(const tf_stream* streams, int n_streams, tf_plan* out, int max_window_rows) {
+int plan_windows(const tf_stream* streams, int n_streams, tf_plan* out, int max_window_rows, bool scaled) {
     if (!out) return TF_EINVAL;
     std::memset(out, 0, sizeof(*out));
     if (n_streams < 0) return TF_EINVAL;
@@ -191,7 +210,8 @@ int plan_windows(const tf_stream* streams, int n_streams, tf_plan* out, int max_
         if (st.rows > max_window_rows || st.kv_capacity > TF_MAX_KEYS) return TF_ERANGE;
         if (st.row_offset != R) return TF_EINVAL;          // packed, in order
         if (st.keys < st.rows || st.keys > st.kv_capacity) return TF_EINVAL;
-        int64_t chunk = tf_chunk_keys(st.rows);
+        int64_t chunk = scaled ? scaled_chunk_keys(st.rows, st.keys, max_window_rows > TF_MAX_ROWS ? n_streams : 0)
+                               : tf_chunk_keys(st.rows);
         int64_t nch = (st.keys + chunk - 1) / chunk;
         R += st.rows;
         parts += int64_t(st.rows) * TF_NQ * nch;
@@ -537,7 +557,7 @@ int32_t tf_chunk_keys(int32_t rows) {
 }
 
 int tf_segments_plan(const tf_stream* streams, int n_streams, tf_plan* out) {
-    return tf::plan_windows(streams, n_streams, out, TF_MAX_ROWS);
+    return tf::plan_windows(streams, n_streams, out, TF_MAX_ROWS, false);
 }
 
 }  // extern "C"
@@ -553,7 +573,7 @@ int build_verify(const tf_stream* streams, int n_streams, const void* const* con
     *out = nullptr;
     if (n_conv < 0 || n_attn < 0 || n_conv > 4096 || n_attn > 4096) return TF_EINVAL;
     tf_plan plan;
-    int rc = plan_windows(streams, n_streams, &plan, TF_MAX_ROWS);
+    int rc = plan_windows(streams, n_streams, &plan, TF_MAX_ROWS, pg && pg->scaled);
     if (rc != TF_OK) return rc;
     const int S = n_streams;
     if (S > 0 && n_conv > 0 && !conv_state) return TF_EINVAL;
@@ -616,7 +636,7 @@ int build_verify(const tf_stream* streams, int n_streams, const void* const* con
         d.row_offset = st.row_offset;
         d.keys = st.keys;
         d.cap = st.kv_capacity;
-        d.chunk_keys = tf_chunk_keys(st.rows);
+        d.chunk_keys = pg && pg->scaled ? scaled_chunk_keys(st.rows, st.keys, 0) : tf_chunk_keys(st.rows);
         d.n_chunks = (st.keys + d.chunk_keys - 1) / d.chunk_keys;
         d.pbase = pbase;
         pbase += int64_t(st.rows) * TF_NQ * d.n_chunks;
@@ -683,7 +703,7 @@ int build_prompt(int32_t rows, int32_t keys, int32_t kv_capacity, const void* co
         tiles_as_streams.push_back({r, t * kPromptTileRows, keys - rows + t * kPromptTileRows + r, kv_capacity});
     }
     tf_plan plan;
-    int rc = plan_windows(tiles_as_streams.data(), T, &plan, kPromptTileRows);   // the attention work
+    int rc = plan_windows(tiles_as_streams.data(), T, &plan, kPromptTileRows, pg && pg->scaled);   // the attention work
     if (rc != TF_OK) return rc;
     plan.n_streams = 1;
     plan.n_conv_tiles = (rows + kConvTileRows - 1) / kConvTileRows;
@@ -706,7 +726,7 @@ int build_prompt(int32_t rows, int32_t keys, int32_t kv_capacity, const void* co
         d.row_offset = st.row_offset;
         d.keys = st.keys;
         d.cap = st.kv_capacity;
-        d.chunk_keys = tf_chunk_keys(st.rows);
+        d.chunk_keys = pg && pg->scaled ? scaled_chunk_keys(st.rows, st.keys, T) : tf_chunk_keys(st.rows);
         d.n_chunks = (st.keys + d.chunk_keys - 1) / d.chunk_keys;
         d.pbase = pbase;
         pbase += int64_t(st.rows) * TF_NQ * d.n_chunks;

@@ -227,6 +227,20 @@ def test_layers_side_by_side(tf):
     assert tf.tf_segments_status(a.seg) == (tf.TF_OK, 0)
 
 
+@pytest.mark.parametrize("streams,prompt", [([(16, 2049), (9, 8192), (12, 8193), (16, 33000), (8, 4096)], False),
+                                            ([(20, 4100)], True), ([(65, 2600)], True), ([(300, 5001)], True)])
+def test_chunks_and_their_scratch(tf, streams, prompt):
+    """Windows of as many chunks as their table gives them, and nothing behind the table's scratch is written."""
+    from scaled import ScaledAttn
+    a = ScaledAttn(tf, streams, 256, seed=20, prompt=prompt)
+    n = a.seg.partials_bytes // 4
+    a.partials = torch.full((n + 4096,), 7.0, device="cuda")
+    for full in (False,) if prompt else (False, True):   # (a prompt's windows end at their own last row)
+        a.run(full)
+        a.check(full, what=full)
+    assert (a.partials[n:] == 7).all()
+
+
 def test_pool_beyond_32_bits(tf):
     """Pages past 4 GB of codes."""
     from scaled import ScaledAttn
