@@ -231,14 +231,18 @@ __device__ __forceinline__ void add4(float4& v, const float4& u) {
     v.z += u.z;
     v.w += u.w;
 }
+// The scales of a lane's outputs n and n + 8.
+__device__ __forceinline__ float2 load_scales(const Linear& a, int n) {
+    return make_float2(__ldg(a.s + min(n, a.N - 1)), __ldg(a.s + min(n + 8, a.N - 1)));
+}
 // A lane's sums of rows r, r + 1 and outputs n, n + 8, scaled and stored.
-__device__ __forceinline__ void store_sums(const Linear& a, int n, int r, const float4& v) {
-    const float d[4] = {v.x, v.y, v.z, v.w};
+__device__ __forceinline__ void store_sums(const Linear& a, int n, int r, const float2& sc, const float4& v) {
+    const float d[4] = {v.x * sc.x, v.y * sc.x, v.z * sc.y, v.w * sc.y};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         const int nn = n + 8 * (e >> 1), rr = r + (e & 1);
         if (nn < a.N && rr < a.R) {
-            const __nv_bfloat16 b = __float2bfloat16_rn(d[e] * __ldg(a.s + nn));
+            const __nv_bfloat16 b = __float2bfloat16_rn(d[e]);
             a.y[int64_t(rr) * a.y_stride + nn] = *reinterpret_cast<const uint16_t*>(&b);
         }
     }
@@ -250,10 +254,11 @@ __device__ __forceinline__ void finish_tile(const Linear& a, int S, int tile, in
                                             const float (&acc)[NT][2][4], float4* sums) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g8 = lane >> 2, t4 = lane & 3;
     const int n = tile * 16 + g8, r = r0 + 2 * t4;
+    const float2 sc = load_scales(a, n);
     if (S == 1) {
         if (tile < tiles)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) store_sums(a, n, r + nt * 8, tile_sum<NT>(acc, nt));
+            for (int nt = 0; nt < NT; ++nt) store_sums(a, n, r + nt * 8, sc, tile_sum<NT>(acc, nt));
     } else {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -263,7 +268,7 @@ __device__ __forceinline__ void finish_tile(const Linear& a, int S, int tile, in
             for (int nt = part; nt < NT; nt += S) {   // the parts' sums in order
                 float4 v = sums[(group * S * NT + nt) * 32 + lane];
                 for (int p = 1; p < S; ++p) add4(v, sums[((group * S + p) * NT + nt) * 32 + lane]);
-                store_sums(a, n, r + nt * 8, v);
+                store_sums(a, n, r + nt * 8, sc, v);
             }
         group_sync(group, S);
     }
@@ -319,6 +324,7 @@ linear_steps_kernel(const __grid_constant__ Linear a, int) {
     stage<NT>(a, r0, 0, chunks, smem, rowb);
     __syncthreads();
     bool joined = at != 0;   // the tile was begun by a warp before this one
+    float2 sc = load_scales(a, tile * 16 + g8);   // (long before they are needed)
     float acc[NT][2][4] = {};
     auto leave = [&]() {
 #pragma unroll
@@ -334,7 +340,7 @@ linear_steps_kernel(const __grid_constant__ Linear a, int) {
             else
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
-                    store_sums(a, tile * 16 + g8, r0 + nt * 8 + 2 * t4, tile_sum<NT>(acc, nt));
+                    store_sums(a, tile * 16 + g8, r0 + nt * 8 + 2 * t4, sc, tile_sum<NT>(acc, nt));
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -342,6 +348,7 @@ linear_steps_kernel(const __grid_constant__ Linear a, int) {
             joined = false;
             at = 0;
             ++tile;
+            sc = load_scales(a, tile * 16 + g8);
         }
     };
     while (left) {
@@ -366,7 +373,7 @@ linear_steps_kernel(const __grid_constant__ Linear a, int) {
             for (int nt = 0; nt < NT; ++nt) add4(v[nt], sums[(w * NT + nt) * 32 + lane]);
         }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) store_sums(a, tile * 16 + g8, r0 + nt * 8 + 2 * t4, v[nt]);
+        for (int nt = 0; nt < NT; ++nt) store_sums(a, tile * 16 + g8, r0 + nt * 8 + 2 * t4, sc, v[nt]);
     }
     pdl_trigger();
 }
