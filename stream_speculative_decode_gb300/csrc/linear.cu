@@ -20,8 +20,8 @@
 // chunk side by side), staged once a CTA where it fits. One CTA of 16 warps an
 // SM with a run of 16-output tiles, whose inputs the warps share out evenly.
 //
-// Measured, 128,000 outputs by 2,048 inputs (139 MB): 1 row 27.7 us, 16 rows 34.9
-// us (5.0 and 4.1 TB/s; the same loads alone 21.5 us). What bounds it is issue:
+// Measured, 128,000 outputs by 2,048 inputs (139 MB): 1 row 27.3 us, 16 rows 34.1
+// us (5.1 and 4.2 TB/s; the same loads alone 21.5 us). What bounds it is issue:
 // of a chunk's 144 instructions 56 take its codes apart at half rate, and 16 warps
 // wait for one another's turn, not for memory. Warps that share tiles and meet at
 // each one's end (37.1 and 45.8), loads a chunk at a time into a ring in shared
@@ -88,29 +88,46 @@ __device__ __forceinline__ uint4 load_once(const uint8_t* p) {
 // rows' pieces fall on different banks.
 __host__ __device__ constexpr int row_bytes(int chunks) { return chunks * kChunk * 2 + 64; }
 
+// 8 inputs as (0, 4), (1, 5), (2, 6), (3, 7): of codes with their scale, or of bf16.
+__device__ __forceinline__ uint4 pairs_of(uint2 c, float e) {
+    const float2 p = h2_to_f2(e4m3_low(c.x)), q = h2_to_f2(e4m3_high(c.x));
+    const float2 s = h2_to_f2(e4m3_low(c.y)), t = h2_to_f2(e4m3_high(c.y));
+    return make_uint4(pack_bf2(p.x * e, s.x * e), pack_bf2(p.y * e, s.y * e), pack_bf2(q.x * e, t.x * e),
+                      pack_bf2(q.y * e, t.y * e));
+}
+__device__ __forceinline__ uint4 pairs_of(const uint4& c) {
+    return make_uint4(__byte_perm(c.x, c.z, 0x5410), __byte_perm(c.x, c.z, 0x7632), __byte_perm(c.y, c.w, 0x5410),
+                      __byte_perm(c.y, c.w, 0x7632));
+}
+
 // Rows [r0, r0 + 8 NT) and chunks [c0, c0 + n) of x into shared memory, in units of 8
-// inputs: four a thread in flight together (16 rows of 2,048: 5.8 us a call of few
-// outputs, one by one 6.8), one for up to 8 rows, where most units may be of rows that
-// are not there (1 row of 128,000 outputs: 27.7 us, four together 28.1).
+// inputs, kFly of them a thread in flight together.
 template <int NT, bool kCodes>
 __device__ __forceinline__ void stage_as(const Linear& a, int r0, int c0, int n, unsigned char* sx, int rowb) {
-    constexpr int kFly = NT == 1 ? 1 : 4;
+    // (bf16 units one by one, which the compiler unrolls; a code's scale would be waited for before the next one's is
+    // asked for: 16 rows of 2,048 to few outputs, 4.8 us, four together 5.2; codes 5.5, one by one 6.2)
+    constexpr int kFly = kCodes ? 4 : 1;
     const int units = n * kChunk / 8, total = 8 * NT * units;
+    // i / units as a product: (i / 16) / n, exact for i / 16 up to 32 n and n up to 180
+    const uint32_t inverse = ((1u << 20) + n - 1) / n;
     for (int i0 = threadIdx.x; i0 < total; i0 += kFly * kThreads) {
         uint4 v[kFly];
         uint8_t e[kFly];
+        int to[kFly];
 #pragma unroll
         for (int j = 0; j < kFly; ++j) {
-            const int i = i0 + j * kThreads, r = r0 + i / units, k = c0 * kChunk + i % units * 8;
+            const int i = i0 + j * kThreads, r = int((uint32_t(i >> 4) * inverse) >> 20), u = i - r * units;
+            const int k = c0 * kChunk + u * 8;
             v[j] = make_uint4(0u, 0u, 0u, 0u);
             e[j] = 127;
-            if (i < total && r < a.R && k < a.K) {
-                const int64_t at = int64_t(r) * a.x_stride + k;
+            to[j] = r * rowb + (u >> 4) * 256 + (u & 3) * 64 + ((u >> 2) & 3) * 16;
+            if (i < total && r0 + r < a.R && k < a.K) {
+                const int64_t at = int64_t(r0 + r) * a.x_stride + k;
                 if constexpr (kCodes) {
                     const uint2 c = *reinterpret_cast<const uint2*>(a.x + at);
                     v[j].x = c.x;
                     v[j].y = c.y;
-                    e[j] = a.xs[int64_t(r) * (a.K / kGroup) + k / kGroup];
+                    e[j] = a.xs[int64_t(r0 + r) * (a.K / kGroup) + k / kGroup];
                 } else {
                     v[j] = *reinterpret_cast<const uint4*>(a.x + 2 * at);
                 }
@@ -118,21 +135,13 @@ __device__ __forceinline__ void stage_as(const Linear& a, int r0, int c0, int n,
         }
 #pragma unroll
         for (int j = 0; j < kFly; ++j) {
-            const int i = i0 + j * kThreads, r = i / units, u = i % units;
-            if (i >= total) break;
-            const uint4 c = v[j];
-            uint4 o;   // inputs (0, 4), (1, 5), (2, 6), (3, 7)
-            if constexpr (kCodes) {
-                const float f = scale_value(e[j]);
-                const float2 p = h2_to_f2(e4m3_low(c.x)), q = h2_to_f2(e4m3_high(c.x));
-                const float2 s = h2_to_f2(e4m3_low(c.y)), t = h2_to_f2(e4m3_high(c.y));
-                o = make_uint4(pack_bf2(p.x * f, s.x * f), pack_bf2(p.y * f, s.y * f), pack_bf2(q.x * f, t.x * f),
-                               pack_bf2(q.y * f, t.y * f));
-            } else {
-                o = make_uint4(__byte_perm(c.x, c.z, 0x5410), __byte_perm(c.x, c.z, 0x7632),
-                               __byte_perm(c.y, c.w, 0x5410), __byte_perm(c.y, c.w, 0x7632));
-            }
-            *reinterpret_cast<uint4*>(sx + r * rowb + (u >> 4) * 256 + (u & 3) * 64 + ((u >> 2) & 3) * 16) = o;
+            if (i0 + j * kThreads >= total) break;
+            uint4 o;
+            if constexpr (kCodes)
+                o = pairs_of(make_uint2(v[j].x, v[j].y), scale_value(e[j]));
+            else
+                o = pairs_of(v[j]);
+            *reinterpret_cast<uint4*>(sx + to[j]) = o;
         }
     }
 }
@@ -525,13 +534,18 @@ int launch(Linear a, cudaStream_t stream) {
 
 // Tiles of 8 rows that a CTA takes: as many as there are, up to four, if their inputs lie
 // in shared memory as a whole; fewer (the weights then come from L2 more than once)
-// before they are staged a slab at a time. 5,000 to 10,000 outputs: 16 rows of 8,192
-// inputs 25.6 us in two tiles of 8 rows, 44.6 in slabs; 32 rows of 4,096 23.7 and 49.2.
-int row_tiles_of(int R, int K) {
+// before they are staged a slab at a time; and fewer while SMs would stand idle, since
+// most of a small call's time is the staging. 16 rows of 8,192 inputs to 4,992 outputs
+// 15.0 us in two tiles of 8 rows, 44.6 in slabs; 32 rows of 4,096 to 10,000 22.9 and
+// 49.2; 32 rows of 2,048 to 512 outputs 4.1 us in four tiles on 128 SMs, 7.6 on 32.
+int row_tiles_of(int R, int K, int N) {
     const int chunks = (K + kChunk - 1) / kChunk, most = R < 25 ? (R + 7) / 8 : 4;
-    for (int nt = most; nt > 0; --nt)
-        if (8 * nt * row_bytes(chunks) + sum_bytes(nt, 2) <= kMaxSmem) return nt;
-    return most;
+    int nt = most;
+    while (nt > 0 && 8 * nt * row_bytes(chunks) + sum_bytes(nt, 2) > kMaxSmem) --nt;
+    if (nt == 0) return most;
+    auto ctas = [&](int tiles) { return int64_t((N + 15) / 16) * ((R + 8 * tiles - 1) / (8 * tiles)); };
+    while (nt > 1 && ctas(nt - 1) <= sm_count()) --nt;
+    return nt;
 }
 
 bool overlap(const void* p, size_t np, const void* q, size_t nq) {
@@ -572,7 +586,7 @@ extern "C" int tf_linear_rows(const void* x, int64_t x_stride, const void* x_sca
     a.R = R;
     a.K = K;
     a.N = N;
-    switch (row_tiles_of(R, K)) {
+    switch (row_tiles_of(R, K, N)) {
         case 1: return launch<1>(a, stream);
         case 2: return launch<2>(a, stream);
         case 3: return launch<3>(a, stream);
