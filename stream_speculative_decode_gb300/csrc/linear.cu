@@ -176,8 +176,8 @@ __device__ __forceinline__ Rows2 rows_of(const Linear& a, int tile, int g8, int 
     return r;
 }
 template <bool kWords>
-__device__ __forceinline__ void load_piece(const Linear& a, const Rows2& r, int c, int t4, Piece& p) {
-    if (!kWords && c * 4 + t4 >= a.K / kGroup) {   // the last chunk's missing groups: scale 0
+__device__ __forceinline__ void load_piece(const Linear& a, const Rows2& r, int c, int chunk, int t4, Piece& p) {
+    if (!kWords && chunk * 4 + t4 >= a.K / kGroup) {   // groups past the row's end: scale 0
         p.w[0] = p.w[1] = make_uint4(0u, 0u, 0u, 0u);
         p.g[0] = p.g[1] = 0u;
         return;
@@ -283,24 +283,24 @@ __device__ __forceinline__ void finish_tile(const Linear& a, int S, int tile, in
     }
 }
 
-// The same for whole steps of U chunks (kWords, x in one slab). A CTA takes a run of
+// The same with x in one slab, in steps of U chunks (the last one filled up with zeros). A CTA takes a run of
 // tiles, its warps even parts of the run's steps, so that no warp waits for another
 // before the end: a warp that begins inside a tile leaves its sums of it in shared
 // memory, and the one that has the tile's beginning adds them in order. Two sets of
 // registers take turns, one being multiplied while the other's loads are on their way.
-template <int NT, int U>
+template <int NT, int U, bool kWords>
 __global__ void __launch_bounds__(kThreads, 1)
 linear_steps_kernel(const __grid_constant__ Linear a, int) {
     extern __shared__ __align__(128) unsigned char smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g8 = lane >> 2, t4 = lane & 3;
     const int r0 = (blockIdx.x % a.row_tiles) * 8 * NT;
     const int cta = blockIdx.x / a.row_tiles, ctas = gridDim.x / a.row_tiles;
-    const int tiles = (a.N + 15) / 16, chunks = a.K / kChunk, steps = chunks / U, rowb = row_bytes(chunks);
+    const int tiles = (a.N + 15) / 16, chunks = a.slab, steps = chunks / U, rowb = row_bytes(chunks);
     const int tile0 = int(int64_t(tiles) * cta / ctas), run = (int(int64_t(tiles) * (cta + 1) / ctas) - tile0) * steps;
     auto begin = [&](int w) { return int(int64_t(run) * w / kWarps); };
     float4* const sums = reinterpret_cast<float4*>(smem + 8 * NT * rowb);   // [warp][NT][lane]
     const unsigned char* const x0 = smem + g8 * rowb + t4 * 16;
-    const uint32_t sel = uint32_t(t4 | (4 + t4) << 4);
+    const uint32_t sel = kWords ? uint32_t(t4 | (4 + t4) << 4) : 0x40u;   // the lane's scale codes of two outputs
     struct Set {
         Piece p[U];
     };
@@ -316,7 +316,7 @@ linear_steps_kernel(const __grid_constant__ Linear a, int) {
         if (l_left == 0) return;
         --l_left;
 #pragma unroll
-        for (int j = 0; j < U; ++j) load_piece<true>(a, rows, j, t4, set.p[j]);
+        for (int j = 0; j < U; ++j) load_piece<kWords>(a, rows, j, l_at * U + j, t4, set.p[j]);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             rows.w[i] += U * 64;
@@ -341,7 +341,7 @@ linear_steps_kernel(const __grid_constant__ Linear a, int) {
     };
     auto take = [&](const Set& set) {
 #pragma unroll
-        for (int j = 0; j < U; ++j) multiply<NT, true>(set.p[j], x0 + (at * U + j) * 256, rowb, sel, a.nibbles, acc);
+        for (int j = 0; j < U; ++j) multiply<NT, kWords>(set.p[j], x0 + (at * U + j) * 256, rowb, sel, a.nibbles, acc);
         --left;
         if (++at == steps) {
             if (joined)
@@ -387,9 +387,10 @@ linear_steps_kernel(const __grid_constant__ Linear a, int) {
     pdl_trigger();
 }
 
-// Row tiles of 8 NT rows; S warps share an output tile. Every warp goes through its
-// tiles, the slabs of x and its part of a slab's chunks, two chunks at a time, with
-// the next two's loads (those of its next tile among them) in flight.
+// The same for more inputs than shared memory holds of 8 rows, which are staged a slab at
+// a time: row tiles of 8 NT rows, S warps an output tile. Every warp goes through its
+// tiles, the slabs of x and its part of a slab's chunks, two chunks at a time, with the
+// next two's loads (those of its next tile among them) in flight.
 template <int NT, bool kWords>
 __global__ void __launch_bounds__(kThreads, 1)
 linear_rows_kernel(const __grid_constant__ Linear a, int S) {
@@ -430,7 +431,7 @@ linear_rows_kernel(const __grid_constant__ Linear a, int S) {
         const int n = p.tile < tiles ? p.end - p.c : 0;
 #pragma unroll
         for (int j = 0; j < kPair; ++j)
-            if (j < n) load_piece<kWords>(a, rows, p.c + j, t4, piece[j]);
+            if (j < n) load_piece<kWords>(a, rows, p.c + j, p.c + j, t4, piece[j]);
     };
     load(at, now);
     if (one_slab) {
@@ -503,48 +504,54 @@ int launch_one(void (*kernel)(Linear, int), std::atomic<bool> (&ready)[64], cons
 
 template <int NT>
 int launch(Linear a, cudaStream_t stream) {
-    constexpr int U = 2, kSums = kWarps * NT * 512;
-    static std::atomic<bool> ready[4][64] = {};
+    constexpr int kSums = kWarps * NT * 512;
+    static std::atomic<bool> ready[6][64] = {};
     const int chunks = (a.K + kChunk - 1) / kChunk, tiles = (a.N + 15) / 16, sms = sm_count();
     a.row_tiles = (a.R + 8 * NT - 1) / (8 * NT);
     int ctas = sms / a.row_tiles;
     if (ctas < 1) ctas = 1;
     a.nibbles = 0x000F000Fu;
     const bool words = a.K % kChunk == 0 && (reinterpret_cast<uintptr_t>(a.g) & 3u) == 0;
-    const int whole = 8 * NT * row_bytes(chunks);
-    if (words && whole + kSums <= kMaxSmem) {
+    // Steps of two chunks where every warp has several of them: with four in flight, or with more warps and fewer
+    // registers, a lane's weights leave no room to work ahead (128,000 outputs, 1 and 16 rows: 27.7 and 34.9 us; four
+    // chunks 31.6 and 42.7; 24 warps 32.8 and 45.9, one chunk 29.3 and 41.5). An odd number of chunks is filled up
+    // where the scales are read a byte at a time anyway, which knows the row's end.
+    const int tiles_cta = (tiles + ctas - 1) / ctas;
+    const bool two = (!words || chunks % 2 == 0) && tiles_cta * ((chunks + 1) / 2) >= 2 * kWarps;
+    a.slab = two ? (chunks + 1) / 2 * 2 : chunks;
+    const int whole = 8 * NT * row_bytes(a.slab) + kSums;
+    if (whole <= kMaxSmem) {
         if (ctas > tiles) ctas = tiles;
-        a.slab = chunks;
-        // Steps of two chunks where every warp has several of them: with four in flight, or with more warps and
-        // fewer registers, a lane's weights leave no room to work ahead (128,000 outputs, 1 and 16 rows: 27.7 and
-        // 34.9 us; four chunks 31.6 and 42.7; 24 warps 32.8 and 45.9, one chunk 29.3 and 41.5).
-        const int steps = (tiles + ctas - 1) / ctas * (chunks / U);
-        if (chunks % U == 0 && steps >= 2 * kWarps)
-            return launch_one(linear_steps_kernel<NT, U>, ready[0], a, ctas, 1, whole + kSums, stream);
-        return launch_one(linear_steps_kernel<NT, 1>, ready[1], a, ctas, 1, whole + kSums, stream);
+        if (words)
+            return two ? launch_one(linear_steps_kernel<NT, 2, true>, ready[0], a, ctas, 1, whole, stream)
+                       : launch_one(linear_steps_kernel<NT, 1, true>, ready[1], a, ctas, 1, whole, stream);
+        return two ? launch_one(linear_steps_kernel<NT, 2, false>, ready[2], a, ctas, 1, whole, stream)
+                   : launch_one(linear_steps_kernel<NT, 1, false>, ready[3], a, ctas, 1, whole, stream);
     }
     const int S = split_of(tiles, chunks, ctas), need = (tiles + kWarps / S - 1) / (kWarps / S);
     if (ctas > need) ctas = need;
     a.slab = ((kMaxSmem - sum_bytes(NT, S)) / (8 * NT) - 64) / (kChunk * 2);
     if (a.slab > chunks) a.slab = chunks;
     const int smem = 8 * NT * row_bytes(a.slab) + sum_bytes(NT, S);
-    return words ? launch_one(linear_rows_kernel<NT, true>, ready[2], a, ctas, S, smem, stream)
-                 : launch_one(linear_rows_kernel<NT, false>, ready[3], a, ctas, S, smem, stream);
+    return words ? launch_one(linear_rows_kernel<NT, true>, ready[4], a, ctas, S, smem, stream)
+                 : launch_one(linear_rows_kernel<NT, false>, ready[5], a, ctas, S, smem, stream);
 }
 
 // Tiles of 8 rows that a CTA takes: as many as there are, up to four, if their inputs lie
 // in shared memory as a whole; fewer (the weights then come from L2 more than once)
 // before they are staged a slab at a time; and fewer while SMs would stand idle, since
 // most of a small call's time is the staging. 16 rows of 8,192 inputs to 4,992 outputs
-// 15.0 us in two tiles of 8 rows, 44.6 in slabs; 32 rows of 4,096 to 10,000 22.9 and
+// 15.0 us in two tiles of 8 rows, 44.6 in slabs; 32 rows of 4,096 to 10,000 17 and
 // 49.2; 32 rows of 2,048 to 512 outputs 4.1 us in four tiles on 128 SMs, 7.6 on 32.
 int row_tiles_of(int R, int K, int N) {
-    const int chunks = (K + kChunk - 1) / kChunk, most = R < 25 ? (R + 7) / 8 : 4;
+    const int chunks = ((K + kChunk - 1) / kChunk + 1) / 2 * 2, most = R < 25 ? (R + 7) / 8 : 4;   // (filled up)
     int nt = most;
     while (nt > 0 && 8 * nt * row_bytes(chunks) + sum_bytes(nt, 2) > kMaxSmem) --nt;
     if (nt == 0) return most;
-    auto ctas = [&](int tiles) { return int64_t((N + 15) / 16) * ((R + 8 * tiles - 1) / (8 * tiles)); };
-    while (nt > 1 && ctas(nt - 1) <= sm_count()) --nt;
+    const int groups = (R + 7) / 8;
+    auto abreast = [&](int tiles) { return (groups + tiles - 1) / tiles; };   // CTAs that share outputs
+    while (nt > 1 && int64_t((N + 15) / 16) * abreast(nt - 1) <= sm_count()) --nt;
+    nt = (groups + abreast(nt) - 1) / abreast(nt);   // 32 rows as 16 and 16, not 24 and 8
     return nt;
 }
 
