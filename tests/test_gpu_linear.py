@@ -102,6 +102,17 @@ def test_inputs_in_slabs(tf, x8):
         assert torch.equal(call(tf, x, xs, *w), want), R
 
 
+@pytest.mark.parametrize("x8", [False, True])
+def test_odd_inputs_in_slabs(tf, x8):
+    """The same with a last chunk of one group, and scales at an odd address."""
+    w, gs, s = weights(45, 41024, 23, whole=True)
+    gs = torch.cat([gs.new_zeros(1), gs.reshape(-1)])[1:].view(gs.shape)
+    for R in (2, 11, 26):
+        x, xs, v = rows(R, 41024, 24, x8, whole=True)
+        want = (v @ matrix(w, gs).T).float().to(torch.bfloat16)
+        assert torch.equal(call(tf, x, xs, w, gs, s), want), R
+
+
 def test_vocabulary(tf):
     w = weights(128000, 2048, 3)
     x, xs, v = rows(5, 2048, 4, False)
