@@ -76,6 +76,43 @@ def test_many_rows(tf, residual):
     check(2048, *a)
 
 
+@pytest.mark.parametrize("W", [32, 96, 480, 992, 1024, 1056])
+@pytest.mark.parametrize("residual", [False, True])
+def test_many_narrow_rows(tf, W, residual):
+    """Several rows a CTA, the last one's partly missing; rows behind the last stay as they are."""
+    for R in (1024, 1031, 3000):
+        x, r, w, s, codes, scales = inputs(R + 9, W, R, residual, pads=(8, 16, 24))
+        cut = lambda t: None if t is None else t[:R]
+        call(tf, W, x[:R], cut(r), w, cut(s), codes[:R], scales[:R])
+        check(W, x[:R], cut(r), w, cut(s), codes[:R], scales[:R], what=(W, R))
+        assert (codes[R:] == 0xAA).all() and (scales[R:] == 0xAA).all()
+
+
+@pytest.mark.parametrize("R", [3, 1500])
+def test_infinite_products(tf, R):
+    """Infinite weights and products past fp32: NaN codes there, the others' scales as if they were not."""
+    W = 256
+    x, r, w, s, codes, scales = inputs(R, W, 9, False)
+    x[:, 40] = 2.0
+    w[40] = float("inf")
+    w[70] = float("-inf")
+    w[100] = 3e38
+    x[:, 100] = 1e4
+    call(tf, W, x, r, w, s, codes, scales)
+    bad = [40, 70, 100]
+    assert ((codes[:, bad] & 0x7F) == 0x7F).all()
+    keep = torch.ones(W, dtype=torch.bool, device="cuda")
+    keep[bad] = False
+    assert ((codes[:, keep] & 0x7F) != 0x7F).all()
+    from scaled import exponent
+    h = x.double()
+    n = h / torch.sqrt((h * h).mean(1, keepdim=True) + EPS) * torch.where(keep, w.double(), 0.0)
+    top = n.view(R, W // 32, 32).abs().amax(-1)
+    e = exponent(n.view(R, W // 32, 32), -1)[..., 0]
+    near = (top / torch.ldexp(torch.full_like(top, 464), e) - 1).abs() < 2.0 ** -16
+    assert ((scales.int() - 127 == e) | near).all()
+
+
 @pytest.mark.parametrize("std", [0.0, 1e-30, 1e-4, 1e15])
 def test_sizes(tf, std):
     for W in (96, 2048):
