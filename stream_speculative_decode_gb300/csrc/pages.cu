@@ -16,7 +16,8 @@
 // of keys x 128 bytes. Measured: 1,000 whole 64-key pages in 8 pools 152 us (1.05
 // GB, the measured copy rate); 64 forks of 16-key pages in 20 pools 5.2 us. Scaled,
 // 1,000 whole 128-key pages in 8 pools 154 us; 64 forks of 64-key pages, partly
-// filled, in 20 pools 9.6 us.
+// filled, in 20 pools 9.6 us. Few copies of large pages take several CTAs each (3
+// parts of 256-key pages in 8 pools 4.1 us, a CTA a copy 7.6).
 #include <algorithm>
 #include <memory>
 #include <utility>
@@ -29,6 +30,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kUnroll = 8;         // 16-byte loads in flight a thread
+constexpr int kPart = kThreads * kUnroll;   // vectors that a CTA has in flight
 constexpr int kPools = 64;         // pools a launch
 
 struct Copy {
@@ -58,10 +60,10 @@ pages_copy_kernel(const __grid_constant__ Batch<kN> b, int page_keys) {
         uint8_t* scales = b.scales[blockIdx.y];
         const int per_head = page_keys / TF_SCALE_KEYS, used = (c.keys + TF_SCALE_KEYS - 1) / TF_SCALE_KEYS;
         const int i = threadIdx.x, at = i / per_head, block = i % per_head;   // at most 8 x 16 bytes a page
-        if (at < TF_NKV && block < used)
+        if (at < TF_NKV && block < used && blockIdx.z == 0)
             scales[size_t(c.dst) * TF_NKV * per_head + i] = scales[size_t(c.src) * TF_NKV * per_head + i];
     }
-    for (int i0 = threadIdx.x; i0 < n; i0 += kThreads * kUnroll) {
+    for (int i0 = blockIdx.z * kPart + threadIdx.x; i0 < n; i0 += gridDim.z * kPart) {
         uint4 v[kUnroll];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
@@ -92,7 +94,11 @@ int launch_batches(void* const* pools, void* const* scales, int n_pools, int pag
             for (int i = c0; i < std::min(n, c0 + kN); ++i)
                 if (!keys || keys[i] > 0) b->copies[nc++] = {src[i], dst[i], keys ? keys[i] : page_keys};
             if (nc == 0) continue;
-            const int rc = launch_pdl(pages_copy_kernel<kN, kScaled>, dim3(nc, np), dim3(kThreads), 0, stream, *b,
+            // few copies of large pages: several CTAs a copy, as long as SMs would stand idle
+            const int parts = (TF_NKV * page_keys * TF_D * (kScaled ? 1 : 2) / 16 + kPart - 1) / kPart;
+            const int64_t ctas = int64_t(nc) * np, idle = 2 * sm_count() / ctas;
+            const int z = idle < 1 ? 1 : idle < parts ? int(idle) : parts;
+            const int rc = launch_pdl(pages_copy_kernel<kN, kScaled>, dim3(nc, np, z), dim3(kThreads), 0, stream, *b,
                                       page_keys);
             if (rc != TF_OK) return rc;
         }
