@@ -29,8 +29,8 @@
 // 192. (An MMA of 64 keys that reads its 128 query rows from shared memory is bound by
 // that: 4 KB of queries beside 2 KB of keys.)
 //
-// Measured: 64 windows of 16 rows at 16 to 32,768 keys 114 us (3.4 TB/s, 50 % of the
-// measured copy rate); a 2,048-row prompt chunk at 8,179 keys 181 us (662 TFLOP/s).
+// Measured: 64 windows of 16 rows at 16 to 32,768 keys 112 us (3.4 TB/s, 51 % of the
+// measured copy rate); a 2,048-row prompt chunk at 8,179 keys 178 us (675 TFLOP/s).
 // What bounds it is the chain of a tile, no unit by itself: a 64-key tile is 8 KB
 // from HBM, 350 cycles of an SM's share, and the tensor cores take some 270 (M = 128
 // whatever the window's rows), but from weights to weights two tiles on it is P.V's
@@ -374,15 +374,15 @@ __device__ __forceinline__ void st_two(uint32_t taddr, uint32_t a, uint32_t b) {
 // its two e4m3 parts in tensor memory, under the power of two that puts its largest at
 // 2^7..2^8; returns the factor of its scores. Dual: two threads a row, 32 dimensions
 // each. 8 columns hold 32 dimensions (an MMA's K) of a part.
-// (Loops and not straight code, here and where a unit ends: what runs once a unit is
-// fetched anew each time.)
+// (Loops, here and where a unit ends, and not all of it straight code: what runs once a
+// unit is fetched anew each time.)
 template <bool DUAL>
 __device__ __forceinline__ float convert_query(uint32_t sQ, uint32_t trow, int warp, int lane) {
     const int r = 32 * warp + (DUAL ? (lane & 15) : lane);
     constexpr int NP = DUAL ? 4 : 8;   // pieces of 8 dimensions
     const int p0 = DUAL ? (lane >> 4) * 4 : 0;
     uint32_t most = 0;
-#pragma unroll 1
+#pragma unroll 4
     for (int i = 0; i < NP; ++i) {
         const uint4 v = lds128(sQ + r * 128 + (((p0 + i) ^ (r & 7)) << 4));
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -394,7 +394,7 @@ __device__ __forceinline__ float convert_query(uint32_t sQ, uint32_t trow, int w
     if (DUAL) most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 16));
     const int up = min(134 - int(most >> 23), 126);
     const float mul = __uint_as_float(uint32_t(127 + up) << 23);
-#pragma unroll 1
+#pragma unroll 4
     for (int i = 0; i < NP; ++i) {
         const uint4 v = lds128(sQ + r * 128 + (((p0 + i) ^ (r & 7)) << 4));
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};

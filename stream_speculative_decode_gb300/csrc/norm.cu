@@ -10,7 +10,7 @@
 // stream that the next addition reads. A row is read once and stays in registers
 // between its sum of squares and its codes: 8 columns a thread (and pass of the
 // width), 4 neighbouring lanes a scale. HBM bound with a residual, 7 bytes a value:
-// 16,381 rows of 2,048 36.1 us, 6.5 TB/s, 98 % of the measured copy rate. Without
+// 16,381 rows of 2,048 35.7 us, 6.6 TB/s, 98 % of the measured copy rate. Without
 // one, 3 bytes a value, issue bounds it (23.3 us, 65 %), so pairs of numbers go
 // through packed fp32 instructions, and what only an infinity needs is in a branch.
 #include <cuda_bf16.h>

@@ -193,6 +193,16 @@ int32_t scaled_chunk_keys(int32_t rows, int32_t keys, int prompt_windows) {
     return std::min(most, std::max(share, prompt_windows ? 512 : 2048));
 }
 
+// How a window's chunks are finished (tf_internal.cuh). Over scaled pools the chunks of a
+// short prompt (at most 4 windows) go to the merge kernel, which has CTAs for every row,
+// not one for all of a window's: 26 rows at 1,564 keys 15.1 us, by the last CTA 20.9,
+// 100 at 3,000 24.0 and 26.9; 300 at 6,000 53.9 and 43.3.
+int32_t merge_mode_of(int32_t rows, int32_t n_chunks, bool scaled, int prompt_windows) {
+    if (n_chunks == 1) return kMergeDirect;
+    if (scaled && prompt_windows > 0 && prompt_windows <= 4) return kMergeKernel;
+    return 4 * rows * n_chunks <= kMergeLastCtaMaxRecords ? kMergeLastCta : kMergeKernel;
+}
+
 // The plan of a set of windows, each of at most `max_window_rows` rows
 // (TF_MAX_ROWS for the verify tables, kPromptTileRows for a prompt call).
 int plan_windows(const tf_stream* streams, int n_streams, tf_plan* out, int max_window_rows, bool scaled) {
@@ -210,8 +220,8 @@ int plan_windows(const tf_stream* streams, int n_streams, tf_plan* out, int max_
         if (st.rows > max_window_rows || st.kv_capacity > TF_MAX_KEYS) return TF_ERANGE;
         if (st.row_offset != R) return TF_EINVAL;          // packed, in order
         if (st.keys < st.rows || st.keys > st.kv_capacity) return TF_EINVAL;
-        int64_t chunk = scaled ? scaled_chunk_keys(st.rows, st.keys, max_window_rows > TF_MAX_ROWS ? n_streams : 0)
-                               : tf_chunk_keys(st.rows);
+        const int prompt_windows = max_window_rows > TF_MAX_ROWS ? n_streams : 0;
+        int64_t chunk = scaled ? scaled_chunk_keys(st.rows, st.keys, prompt_windows) : tf_chunk_keys(st.rows);
         int64_t nch = (st.keys + chunk - 1) / chunk;
         R += st.rows;
         parts += int64_t(st.rows) * TF_NQ * nch;
@@ -219,7 +229,7 @@ int plan_windows(const tf_stream* streams, int n_streams, tf_plan* out, int max_
         tiles += (st.rows + tf::kConvTileRows - 1) / tf::kConvTileRows;
         max_rows = std::max(max_rows, int(st.rows));
         (tf::attn_path_of(st.rows) == tf::kAttnTc ? any_tc : any_mma) = true;
-        if (nch > 1 && 4 * st.rows * nch > tf::kMergeLastCtaMaxRecords) any_merge = true;
+        if (merge_mode_of(st.rows, int32_t(nch), scaled, prompt_windows) == kMergeKernel) any_merge = true;
     }
     if (R > (1 << 24)) return TF_ERANGE;
     out->n_streams = n_streams;
@@ -640,8 +650,7 @@ int build_verify(const tf_stream* streams, int n_streams, const void* const* con
         d.n_chunks = (st.keys + d.chunk_keys - 1) / d.chunk_keys;
         d.pbase = pbase;
         pbase += int64_t(st.rows) * TF_NQ * d.n_chunks;
-        d.merge_mode = d.n_chunks == 1 ? kMergeDirect
-                     : (4 * st.rows * d.n_chunks <= kMergeLastCtaMaxRecords ? kMergeLastCta : kMergeKernel);
+        d.merge_mode = merge_mode_of(st.rows, d.n_chunks, pg && pg->scaled, 0);
         d.n_qg = 1;
         for (int i = 0; i < st.rows; ++i) row_stream[st.row_offset + i] = s;
         for (int r0 = 0; r0 < st.rows; r0 += kConvTileRows)
@@ -730,8 +739,7 @@ int build_prompt(int32_t rows, int32_t keys, int32_t kv_capacity, const void* co
         d.n_chunks = (st.keys + d.chunk_keys - 1) / d.chunk_keys;
         d.pbase = pbase;
         pbase += int64_t(st.rows) * TF_NQ * d.n_chunks;
-        d.merge_mode = d.n_chunks == 1 ? kMergeDirect
-                     : (4 * st.rows * d.n_chunks <= kMergeLastCtaMaxRecords ? kMergeLastCta : kMergeKernel);
+        d.merge_mode = merge_mode_of(st.rows, d.n_chunks, pg && pg->scaled, T);
         d.n_qg = 1;
         for (int i = 0; i < st.rows; ++i) row_stream[st.row_offset + i] = 1 + t;
         for (int c = 0; c < d.n_chunks; ++c) items.push_back({1 + t, c, 0, 0});
