@@ -67,11 +67,9 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 __device__ __forceinline__ uint64_t unpack2(uint32_t w) {
     return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
-__device__ __forceinline__ uint32_t code2(uint64_t v) {   // finite numbers, or NaN, under the scale
+__device__ __forceinline__ uint32_t code2(uint64_t v) {
     const float2 f = both(v);
-    uint16_t d;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(f.y), "f"(f.x));
-    return d;
+    return e4m3_finite(f.x, f.y);
 }
 
 // kRows rows a CTA, each by blockDim.x / kRows threads in kIter passes over the width.

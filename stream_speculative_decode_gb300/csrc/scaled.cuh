@@ -47,6 +47,12 @@ __device__ __forceinline__ uint16_t e4m3_pair(float a, float b) {
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(b), "f"(a));
     return d;
 }
+// The same where neither is an infinity.
+__device__ __forceinline__ uint32_t e4m3_finite(float a, float b) {
+    uint16_t d;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(b), "f"(a));
+    return d;
+}
 __device__ __forceinline__ uint32_t e4m3_quad(float a, float b, float c, float d) {
     return uint32_t(e4m3_pair(a, b)) | uint32_t(e4m3_pair(c, d)) << 16;
 }
