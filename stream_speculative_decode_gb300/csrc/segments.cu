@@ -193,13 +193,16 @@ int32_t scaled_chunk_keys(int32_t rows, int32_t keys, int prompt_windows) {
     return std::min(most, std::max(share, prompt_windows ? 512 : 2048));
 }
 
-// How a window's chunks are finished (tf_internal.cuh). Over scaled pools the chunks of a
-// short prompt (at most 4 windows) go to the merge kernel, which has CTAs for every row,
-// not one for all of a window's: 26 rows at 1,564 keys 15.1 us, by the last CTA 20.9,
-// 100 at 3,000 24.0 and 26.9; 300 at 6,000 53.9 and 43.3.
+// How a window's chunks are finished (tf_internal.cuh). Over scaled pools the merge kernel,
+// which has CTAs for every row, takes those that one CTA would be long about: the chunks of
+// a short prompt (at most 4 windows; 26 rows at 1,564 keys 15.1 us, by the last CTA 20.9,
+// 100 at 3,000 24.0 and 26.9, but 300 at 6,000 53.9 and 43.3), and many chunks of few rows,
+// whose records 16 threads a query read one after another (4 single rows at 100,000 keys
+// 69.7 and 80.8, one at 30,000 10.3 and 11.7, 8 windows of 4 at 30,000 52.9 and 56.6, but 64
+// of 8 at 16 to 32,768 76.5 and 67.2).
 int32_t merge_mode_of(int32_t rows, int32_t n_chunks, bool scaled, int prompt_windows) {
     if (n_chunks == 1) return kMergeDirect;
-    if (scaled && prompt_windows > 0 && prompt_windows <= 4) return kMergeKernel;
+    if (scaled && (prompt_windows > 0 ? prompt_windows <= 4 : rows <= 4 && n_chunks > 8)) return kMergeKernel;
     return 4 * rows * n_chunks <= kMergeLastCtaMaxRecords ? kMergeLastCta : kMergeKernel;
 }
 
