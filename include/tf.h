@@ -632,7 +632,7 @@ int tf_norm_rows(const void* x, int64_t x_stride, const void* res, int64_t res_s
  *   s         float [N]
  *   y         bf16, row r at y + r*y_stride (any 2-byte address and stride >= N);
  *             overlaps nothing else
- * K is a multiple of TF_SCALE_COLUMNS. The weights are read once for up to 32 rows.
+ * K is a multiple of TF_SCALE_COLUMNS. Up to 32 rows take the weights from HBM once.
  * Values of x below bf16's smallest, 2^-133, are rounded to multiples of it; the
  * other products are exact. Sums run in an order that R, K and N fix. A NaN or an infinity in a row of x reaches that row of
  * y only. Needs no table; R == 0 is a no-op. Errors: TF_EINVAL (null, misaligned,
