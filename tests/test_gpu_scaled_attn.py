@@ -228,6 +228,8 @@ def test_layers_side_by_side(tf):
 
 
 @pytest.mark.parametrize("streams,prompt", [([(16, 2049), (9, 8192), (12, 8193), (16, 33000), (8, 4096)], False),
+                                            ([(1, 20000), (4, 12000), (2, 8193), (6, 30000), (16, 9000)], False),
+                                            ([(1, 9217), (3, 9216)], False),
                                             ([(20, 4100)], True), ([(65, 2600)], True), ([(300, 5001)], True)])
 def test_chunks_and_their_scratch(tf, streams, prompt):
     """Windows of as many chunks as their table gives them, and nothing behind the table's scratch is written."""
