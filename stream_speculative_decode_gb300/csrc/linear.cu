@@ -580,7 +580,8 @@ extern "C" int tf_linear_rows(const void* x, int64_t x_stride, const void* x_sca
         overlap(w_scales, size_t(N) * (K / kGroup), y, yb) || overlap(s, size_t(N) * 4, y, yb) ||
         (x_scales && overlap(x_scales, size_t(R) * (K / kGroup), y, yb)))
         return TF_EINVAL;
-    if (!on_this_device(x) || !on_this_device(w) || !on_this_device(y)) return TF_EINVAL;
+    for (const void* p : {x, x_scales, w, w_scales, static_cast<const void*>(s), static_cast<const void*>(y)})
+        if (p && !on_this_device(p)) return TF_EINVAL;
     Linear a = {};
     a.x = static_cast<const uint8_t*>(x);
     a.xs = static_cast<const uint8_t*>(x_scales);

@@ -222,7 +222,9 @@ extern "C" int tf_norm_rows(const void* x, int64_t x_stride, const void* res, in
     for (const Span& in : {sx, sr, sw, ss})
         if (!apart(in, sc) || !apart(in, sb)) return TF_EINVAL;
     if (!apart(ss, sw) || !apart(sc, sb)) return TF_EINVAL;
-    if (!on_this_device(x) || !on_this_device(codes)) return TF_EINVAL;
+    for (const void* p : {x, res, w, static_cast<const void*>(sum), static_cast<const void*>(codes),
+                          static_cast<const void*>(scales)})
+        if (p && !on_this_device(p)) return TF_EINVAL;
     const NormRows a = {static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(res),
                         static_cast<const uint16_t*>(w), static_cast<uint16_t*>(sum), static_cast<uint8_t*>(codes),
                         static_cast<uint8_t*>(scales), x_stride, res_stride, sum_stride, eps, width, R};
