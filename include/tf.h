@@ -634,11 +634,13 @@ int tf_norm_rows(const void* x, int64_t x_stride, const void* res, int64_t res_s
  *             overlaps nothing else
  * K is a multiple of TF_SCALE_COLUMNS. Up to 32 rows take the weights from HBM once.
  * Values of x below bf16's smallest, 2^-133, are rounded to multiples of it; the
- * other products are exact. Sums run in an order that R, K and N fix. A NaN or an infinity in a row of x reaches that row of
- * y only. Needs no table; R == 0 is a no-op. Errors: TF_EINVAL (null, misaligned,
- * overlaps, a bad K or stride, N < 1, another device's memory), TF_ERANGE
- * (R > TF_LINEAR_MAX_ROWS, K > TF_LINEAR_MAX_INPUTS, N > TF_LINEAR_MAX_OUTPUTS, a
- * stride beyond 2^32). */
+ * other products are exact. Sums run in an order that R, K, N and the device's
+ * number of SMs fix: a row's bits may differ between calls of different R, not with
+ * its place among the rows or with an address. A NaN or an infinity in a row of x
+ * reaches that row of y only. Needs no table; R == 0 is a no-op. Errors: TF_EINVAL
+ * (null, misaligned, overlaps, a bad K or stride, N < 1, another device's memory),
+ * TF_ERANGE (R > TF_LINEAR_MAX_ROWS, K > TF_LINEAR_MAX_INPUTS,
+ * N > TF_LINEAR_MAX_OUTPUTS, a stride beyond 2^32). */
 #define TF_LINEAR_MAX_ROWS (1 << 20)
 #define TF_LINEAR_MAX_INPUTS (1 << 20)
 #define TF_LINEAR_MAX_OUTPUTS (1 << 24)

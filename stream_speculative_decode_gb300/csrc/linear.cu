@@ -511,13 +511,15 @@ int launch(Linear a, cudaStream_t stream) {
     int ctas = sms / a.row_tiles;
     if (ctas < 1) ctas = 1;
     a.nibbles = 0x000F000Fu;
-    const bool words = a.K % kChunk == 0 && (reinterpret_cast<uintptr_t>(a.g) & 3u) == 0;
+    const bool whole_chunks = a.K % kChunk == 0;
+    const bool words = whole_chunks && (reinterpret_cast<uintptr_t>(a.g) & 3u) == 0;
     // Steps of two chunks where every warp has several of them: with four in flight, or with more warps and fewer
     // registers, a lane's weights leave no room to work ahead (128,000 outputs, 1 and 16 rows: 27.7 and 34.9 us; four
     // chunks 31.6 and 42.7; 24 warps 32.8 and 45.9, one chunk 29.3 and 41.5). An odd number of chunks is filled up
-    // where the scales are read a byte at a time anyway, which knows the row's end.
+    // where the last one ends inside a chunk: its scales are read a byte at a time, which knows the row's end. (The
+    // step decides where warps divide a sum, so it goes by K and N and not by the scales' address.)
     const int tiles_cta = (tiles + ctas - 1) / ctas;
-    const bool two = (!words || chunks % 2 == 0) && tiles_cta * ((chunks + 1) / 2) >= 2 * kWarps;
+    const bool two = (!whole_chunks || chunks % 2 == 0) && tiles_cta * ((chunks + 1) / 2) >= 2 * kWarps;
     a.slab = two ? (chunks + 1) / 2 * 2 : chunks;
     const int whole = 8 * NT * row_bytes(a.slab) + kSums;
     if (whole <= kMaxSmem) {

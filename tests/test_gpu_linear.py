@@ -184,6 +184,21 @@ def test_strides_and_odd_addresses(tf, x8):
     assert (buf[:1] == 7).all() and (buf[1:].view(R, 51)[:, N:] == 7).all()
 
 
+@pytest.mark.parametrize("N,K", [(20000, 2176), (12000, 896), (9500, 384), (300, 640), (70, 41088)])
+@pytest.mark.parametrize("x8", [False, True])
+def test_bits_do_not_depend_on_an_address(tf, N, K, x8):
+    """An odd number of whole 128-input chunks, as runs of tiles and in slabs: the scales at a multiple of 4 and
+    behind it give the same bits, for each tile of rows."""
+    w, gs, s = weights(N, K, 25)
+    for R in (1, 12, 20, 40):
+        x, xs, v = rows(R, K, 26, x8)
+        want = call(tf, x, xs, w, gs, s)
+        for off in (1, 2):
+            at = torch.cat([gs.new_zeros(off), gs.reshape(-1)])[off:].view(gs.shape)
+            got = call(tf, x, xs, w, at, s)
+            assert torch.equal(got.view(torch.int16), want.view(torch.int16)), (R, off)
+
+
 @pytest.mark.parametrize("x8", [False, True])
 def test_nonfinite_rows(tf, x8):
     w = weights(300, 512, 11)
