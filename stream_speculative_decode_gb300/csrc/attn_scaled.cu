@@ -193,7 +193,7 @@ attn_scaled_kernel(SegTable t, int layer, const uint16_t* __restrict__ q, float*
         uint32_t m = 0;
         for (int i = tid; i < nblocks; i += kThreads) {
             const uint32_t b = blocks[i], e = vs[b];
-            scales[i] = make_float2(__uint_as_float(uint32_t(ks[b]) << 23), float(e));
+            scales[i] = make_float2(scale_value(ks[b]), float(e));
             m = max(m, e);
         }
         if (tid == 0 && (nblocks & 1)) scales[nblocks] = make_float2(1.f, 0.f);   // a last pair's missing block, masked

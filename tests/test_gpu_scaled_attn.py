@@ -122,6 +122,18 @@ def test_blocks_of_very_different_size(tf):
     a.check()
 
 
+@pytest.mark.parametrize("path", ["mma", "tc"])
+def test_the_smallest_scale_of_k(tf, path, monkeypatch):
+    """Scale byte 0 is 2^-127, which queries near 2^120 can tell from 0."""
+    from scaled import ScaledAttn
+    monkeypatch.setenv("TF_ATTN_PATH", path)
+    a = ScaledAttn(tf, [(16, 700), (4, 90), (1, 2100), (10, 3000)], 32, seed=23)
+    a.ks[0].zero_()
+    a.q[0] = (a.q[0].float() * 2.0 ** 120).to(torch.bfloat16)
+    a.run()
+    a.check(what=path)
+
+
 @pytest.mark.parametrize("factor", [0.0, 2.0 ** -120, 2.0 ** 100])
 def test_queries_of_any_size(tf, factor):
     from scaled import ScaledAttn
