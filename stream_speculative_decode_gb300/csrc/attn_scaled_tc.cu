@@ -6,21 +6,22 @@
 // With c the codes, ek and ev a block's exponents, E the chunk's largest ev and x the
 // scores in log2 units:
 //   x_t = (q . ck_t) * 2^ek * log2(e) / 8
-//   o = 2^E * sum 2^(x_t - m) (2^(ev - E) cv_t) / sum 2^(x_t - m)
+//   o = 2^E * sum 2^(x_t - m + ev - E) cv_t / sum 2^(x_t - m)
 // K's codes go into the MMA as they are (kind::f8f6f4): a query, under a power of two
 // of its own that puts its largest at 2^7..2^8, is split into two e4m3 parts, its
 // rounding and the rounding of the remainder. A bf16 value has 8 significant bits and
 // the two parts 4 each, so together they are exact down to 2^-9 of the largest, and
 // off by at most 2^-10 (2^-17 of the largest) below. K's scale is a factor of the
-// softmax's 16 scores of a block, which costs it nothing but the factor.
-// V's codes become fp16 tiles in shared memory (exact) times 2^(ev - E + 7), at most
-// 448 * 2^7; that is exact too for blocks down to 2^-22 of the chunk's largest, and off
-// by at most 2^-25 (2^-32 of the largest block's scale) below.
+// softmax's 16 scores of a block, which costs it nothing but the factor. V's enters
+// the weights that go into P.V, w = 2^(x - m + ev - E), as in attn_scaled.cu, and V's
+// codes become fp16 tiles in shared memory as they are (exact): a key is rounded by what
+// it adds to the output, and the sum l takes w * 2^(E - ev). (With the scales on V's
+// tiles instead, a key of a small weight and a large scale would vanish from P.V.)
 //
 // Persistent, two CTAs an SM, 8 warps:
 //   warp 7      TMA loads of the codes (64 keys: 4 KB of K, 64-byte swizzle, and 4 KB
-//               of V) into a ring of 6 stages, each with its blocks' K scales and V
-//               factors beside it; at a unit's start its V scales, for E;
+//               of V) into a ring of 6 stages, each with its blocks' scales beside it;
+//               at a unit's start its V scales, for E;
 //   warps 5, 6  the conversion of the V tiles, half a tile each, ring of 3;
 //   warp 4      both products' MMAs, and the queries' TMA loads;
 //   warps 0-3   softmax and records; at a unit's start the queries' two parts, each
@@ -30,7 +31,8 @@
 // that: 4 KB of queries beside 2 KB of keys.)
 //
 // Measured: 64 windows of 16 rows at 16 to 32,768 keys 112 us (3.4 TB/s, 51 % of the
-// measured copy rate); a 2,048-row prompt chunk at 8,179 keys 178 us (675 TFLOP/s).
+// measured copy rate); a 2,048-row prompt chunk at 8,179 keys 181 us (664 TFLOP/s). With
+// V's scales on its tiles, which leaves out the keys named above, 110.5 and 176 us.
 // What bounds it is the chain of a tile, no unit by itself: a 64-key tile is 8 KB
 // from HBM, 350 cycles of an SM's share, and the tensor cores take some 270 (M = 128
 // whatever the window's rows), but from weights to weights two tiles on it is P.V's
@@ -47,9 +49,10 @@
 // 211); a quarter of the exponentials as polynomials (125 and 213); the second half
 // of a tile's scores loaded ahead (111 and 189 against 111 and 184).
 //
-// A weight is at most 2^15 (fp16), the largest of a row at 2^6 when its reference
-// moves: weights below 2^-31 of it vanish. A block of V whose scale is 2^31 below the
-// chunk's largest counts as zero.
+// A weight w is at most 2^15 (fp16), the largest of a row at 2^6 when its reference
+// moves: it is off by 2^-11 of itself, or by 2^-31 of the row's largest where that is
+// more (those below vanish). A block of V whose scale is more than 2^64 below the
+// chunk's largest counts as if it were 2^64 below.
 //
 // A NaN code of V must not reach the rows that do not see its key (0 * NaN): in tiles
 // that reach past the first row's keys the converters write 0 for it and note, for
@@ -78,7 +81,7 @@ constexpr uint32_t kColQ = 192;             // 32 columns: dimensions 0-31 (8 co
 constexpr float kLog2e8 = 0.18033688011112042f;
 constexpr float kSumMax = 32768.f;          // a thread's weights of a tile adding up to more move the row's reference
 constexpr float kHeadroom = 6.f;            // log2 of the largest weight after that
-constexpr int kVShift = 7;
+constexpr int kMaxShift = 64;
 constexpr int kBlocks = 512 * TF_MAX_ROWS / TF_SCALE_KEYS;   // blocks of the longest chunk
 constexpr int kScaleRing = 16;              // tiles whose scales are kept
 constexpr int kUnits = 8;                   // units whose notes are kept (no role is that far ahead of another)
@@ -106,8 +109,7 @@ struct Bars {
     int32_t top[kUnits];                     // a unit's E, as a scale byte
     int32_t any_nan[kUnits];
     int32_t nan_key[kUnits][TF_D];           // first key (of the chunk) with a NaN code taken out, by dimension
-    alignas(16) float k_scale[kScaleRing][4];    // by running tile, a block each
-    alignas(16) uint32_t v_scale[kScaleRing][4]; // 2^(ev - E + 7) as fp16 pairs
+    float4 scale[kScaleRing][4];             // by running tile, a block each: K's scale, ev - E, 2^(E - ev)
     alignas(16) uint32_t block[kBlocks];     // warp 7: where the unit's blocks lie in the pools, and their scale bytes
     alignas(16) uint8_t k_byte[kBlocks];
     alignas(16) uint8_t v_byte[kBlocks];
@@ -184,40 +186,44 @@ __device__ __forceinline__ uint32_t pack_h2(float a, float b) {
     __half2 h = __floats2half2_rn(a, b);
     return *reinterpret_cast<uint32_t*>(&h);
 }
-__device__ __forceinline__ uint32_t mul_h2(uint32_t a, uint32_t b) {
-    __half2 r = __hmul2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
-    return *reinterpret_cast<uint32_t*>(&r);
-}
-// 2^(7 - d) as an fp16 pair, d >= 0: subnormal from d = 22 on, 0 from 32 on.
-__device__ __forceinline__ uint32_t v_factor(int d) {
-    const uint32_t h = d <= 21 ? uint32_t(22 - d) << 10 : d <= 31 ? 0x400u >> (d - 21) : 0u;
-    return h | h << 16;
+// What a block's scales make of a row's scores and weights: x = score * f + d, 2^-d = u.
+struct BlockScale {
+    float f, d, u;
+};
+__device__ __forceinline__ BlockScale block_scale(uint32_t scale, float cq) {
+    const uint4 s = lds128(scale);   // f is never 0: masked scores are -inf
+    return {fmaf(cq, __uint_as_float(s.x), 0x1p-149f), __uint_as_float(s.y), __uint_as_float(s.z)};
 }
 
-// Weights 2^(v * f - mu) of a thread's scores, f one factor for 16 of them, packed to
-// fp16 pairs; returns their sum. mu = 0 stands for a reference of -inf.
+// Weights 2^(v * f + d - mu) of a thread's scores, 16 of a block, packed to fp16 pairs.
+// Returns their sum, and adds theirs without V's scales to l. mu = 0 stands for a
+// reference of -inf.
 template <int NV>
-__device__ __forceinline__ float weigh(const float (&v)[NV], const float (&f)[NV / 16], float mref,
-                                       uint32_t (&own)[NV / 2]) {
+__device__ __forceinline__ float weigh(const float (&v)[NV], uint32_t scale, float cq, float mref,
+                                       uint32_t (&own)[NV / 2], float& l) {
     const float mu = (mref == -INFINITY) ? 0.f : mref;
-    const uint64_t nmu2 = f2pack(-mu, -mu);
-    uint64_t sum2[2] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f)};
+    float all = 0.f;
 #pragma unroll
     for (int b = 0; b < NV / 16; ++b) {
-        const uint64_t f2 = f2pack(f[b], f[b]);
+        const BlockScale s = block_scale(scale + 16 * b, cq);
+        const float at = s.d - mu;
+        const uint64_t f2 = f2pack(s.f, s.f), at2 = f2pack(at, at);
+        uint64_t sum2[2];
 #pragma unroll
-        for (int c = 8 * b; c < 8 * b + 8; ++c) {
+        for (int i = 0; i < 8; ++i) {
+            const int c = 8 * b + i;
             float x0, x1;
-            f2unpack(ffma2(f2pack(v[2 * c], v[2 * c + 1]), f2, nmu2), x0, x1);
+            f2unpack(ffma2(f2pack(v[2 * c], v[2 * c + 1]), f2, at2), x0, x1);
             const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-            sum2[c & 1] = fadd2(sum2[c & 1], f2pack(p0, p1));
+            sum2[i & 1] = i < 2 ? f2pack(p0, p1) : fadd2(sum2[i & 1], f2pack(p0, p1));
             own[c] = pack_h2(p0, p1);
         }
+        float s0, s1;
+        f2unpack(fadd2(sum2[0], sum2[1]), s0, s1);
+        all += s0 + s1;
+        l = fmaf(s0 + s1, s.u, l);
     }
-    float s4[4];
-    f2unpack(sum2[0], s4[0], s4[1]);
-    f2unpack(sum2[1], s4[2], s4[3]);
-    return (s4[0] + s4[1]) + (s4[2] + s4[3]);
+    return all;
 }
 
 // State of one softmax thread for one unit; rows and lanes as in attn_tc.cu (windows
@@ -249,12 +255,7 @@ __device__ __forceinline__ void softmax_tiles(SoftState& st) {
         if (threadIdx.x == 0) mbar_arrive(su32(&bars->k_free[gj % kStages]));
         tc_fence_after();
         if (st.wact) {
-            float f[NB];
-            {
-                const float* ks = bars->k_scale[gj % kScaleRing] + half * NB;
-#pragma unroll
-                for (int i = 0; i < NB; ++i) f[i] = fmaf(st.cq, ks[i], 0x1p-149f);   // never 0 (masked scores are -inf)
-            }
+            const uint32_t scale = su32(&bars->scale[gj % kScaleRing][half * NB]);
             const bool edge = j * kKT + kKT > st.lim_all;
             // 32 of the thread's scores, -inf past the row's last key
             auto load_scores = [&](int h, float (&v)[32]) {
@@ -275,18 +276,19 @@ __device__ __forceinline__ void softmax_tiles(SoftState& st) {
             };
             // the tile's weights, kept in registers until all are there (P lies over S)
             uint32_t own[NH][16];
+            float l;   // this tile's part of st.l
             auto weigh_tile = [&]() {
                 float sum = 0.f;
+                l = 0.f;
 #pragma unroll
                 for (int h = 0; h < NH; ++h) {
                     float v[32];
                     load_scores(h, v);
-                    const float f2[2] = {f[2 * h], f[2 * h + 1]};
-                    sum += weigh<32>(v, f2, st.mref, own[h]);
+                    sum += weigh<32>(v, scale + 32 * h, st.cq, st.mref, own[h], l);
                 }
                 return sum;
             };
-            float psum = weigh_tile();
+            const float psum = weigh_tile();
             // a weight is at most its tile's sum; a row that has no reference yet, or too
             // large a sum (or a NaN), takes the warp through the maxima, and moves its own
             // reference (which other rows have no say in)
@@ -307,7 +309,8 @@ __device__ __forceinline__ void softmax_tiles(SoftState& st) {
                         }
                         m2[0] = fmaxf(m2[0], v[16 * i + 14]);
                         m2[1] = fmaxf(m2[1], v[16 * i + 15]);
-                        mx = fmaxf(mx, fmaxf(m2[0], m2[1]) * f[2 * h + i]);
+                        const BlockScale s = block_scale(scale + 32 * h + 16 * i, st.cq);
+                        mx = fmaxf(mx, fmaf(fmaxf(m2[0], m2[1]), s.f, s.d));
                     }
                 }
                 bool row_slow = slow;
@@ -345,7 +348,7 @@ __device__ __forceinline__ void softmax_tiles(SoftState& st) {
                         tc_wait_st();
                     }
                 }
-                psum = weigh_tile();
+                weigh_tile();
             }
             if constexpr (DUAL) {
                 tc_st16x2_16<kKT / 4>(st.trow + colS, own[0]);
@@ -353,7 +356,7 @@ __device__ __forceinline__ void softmax_tiles(SoftState& st) {
                 tc_st_n<16>(st.trow + colS, own[0]);
                 tc_st_n<16>(st.trow + colS + 16, own[NH - 1]);
             }
-            st.l += psum;
+            st.l += l;
             tc_wait_st();
         }
         tc_fence_before();
@@ -601,8 +604,10 @@ attn_scaled_tc_kernel(SegTable t, int layer, float* __restrict__ part_o, float2*
                 }
                 r.next();
                 if (lane < 4) {
-                    bars->k_scale[gt % kScaleRing][lane] = scale_value(bars->k_byte[4 * j + lane]);
-                    bars->v_scale[gt % kScaleRing][lane] = v_factor(int(top) - int(bars->v_byte[4 * j + lane]));
+                    const int down = min(int(top) - int(bars->v_byte[4 * j + lane]), kMaxShift);
+                    bars->scale[gt % kScaleRing][lane] =
+                        make_float4(scale_value(bars->k_byte[4 * j + lane]), float(-down),
+                                    __uint_as_float(uint32_t(127 + down) << 23), 0.f);
                 }
                 __syncwarp();
                 if (lane == 0) {
@@ -658,7 +663,6 @@ attn_scaled_tc_kernel(SegTable t, int layer, float* __restrict__ part_o, float2*
                 }
                 r.next();
                 const uint32_t src = sRaw + s * kStageB + kRawB + r0 * TF_D + uint32_t(lane) * 16u;
-                const uint2 f = *reinterpret_cast<const uint2*>(bars->v_scale[gt % kScaleRing] + (r0 >> 4));
                 uint4 v[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) v[i] = lds128(src + i * 512);
@@ -690,13 +694,13 @@ attn_scaled_tc_kernel(SegTable t, int layer, float* __restrict__ part_o, float2*
                 }
                 vr.next();
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {   // rows 8 i .. 8 i + 7 of the half are of its block i / 2
+                for (int i = 0; i < 4; ++i) {
                     const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
                     uint32_t o[8];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        o[2 * k] = mul_h2(e4m3_low(w[k]), i < 2 ? f.x : f.y);
-                        o[2 * k + 1] = mul_h2(e4m3_high(w[k]), i < 2 ? f.x : f.y);
+                        o[2 * k] = e4m3_low(w[k]);
+                        o[2 * k + 1] = e4m3_high(w[k]);
                     }
                     store_codes(sV + b * kTileB, r0 + 8 * i + (lane >> 2), lane & 3, o);
                 }
@@ -749,8 +753,8 @@ attn_scaled_tc_kernel(SegTable t, int layer, float* __restrict__ part_o, float2*
             const volatile int32_t* const nan_key = bars->nan_key[m % kUnits];
             const bool any_nan = reinterpret_cast<volatile int32_t*>(bars->any_nan)[m % kUnits] != 0;
             if (wact) {
-                // (m, l, O) relative to the row's reference -> the chunk's record, O in units of 2^(E - 7)
-                const int e = reinterpret_cast<volatile int32_t*>(bars->top)[m % kUnits] - kScaleBias - kVShift;
+                // (m, l, O) relative to the row's reference -> the chunk's record, O in units of 2^E
+                const int e = reinterpret_cast<volatile int32_t*>(bars->top)[m % kUnits] - kScaleBias;
                 const float up0 = __uint_as_float(uint32_t(127 + e / 2) << 23);
                 const float up1 = __uint_as_float(uint32_t(127 + e - e / 2) << 23);
                 float lsum = ss.l;

@@ -123,6 +123,45 @@ def test_blocks_of_very_different_size(tf):
 
 
 @pytest.mark.parametrize("path", ["mma", "tc"])
+def test_weights_count_with_their_scales(tf, path, monkeypatch):
+    """V blocks 2^45 to 2^60 below others under weights 2^34 to 2^38 above theirs. With A = sum p |v|, an output is off
+    by (as in scaled.check_attention) the error of the scores, e, and of the sums, 2^-11 of a weight in fp16, and
+    2^-31 of the row's largest p times its scale, where that is more, times a code of up to 448: no key may
+    vanish beside a weight that its own scale makes small. The weights' exponents are sums of up to 128 in size."""
+    from scaled import ScaledAttn, BLOCK, NKV
+    monkeypatch.setenv("TF_ATTN_PATH", path)
+    a = ScaledAttn(tf, [(16, 9000), (1, 900), (12, 70), (6, 40), (4, 3001)], 64, seed=21)
+    g = torch.Generator(device="cuda").manual_seed(22)
+    used = (a.K[0] & 0x7F) != 0x7F
+    low = torch.rand(a.ks[0].shape, generator=g, device="cuda") < 0.5      # blocks of small weights, large V
+    pick = lambda *v: torch.tensor(v, device="cuda")[torch.randint(0, len(v), a.K[0].shape[:3], generator=g, device="cuda")]
+    k = torch.where(low.repeat_interleave(BLOCK, 2), pick(0.0, 0.25), pick(3.0, 3.25))    # q.k / 8 = 8 k of queries of ones
+    a.K[0] = torch.where(used, k.to(torch.float8_e4m3fn).view(torch.uint8)[..., None], a.K[0])
+    a.ks[0] = torch.full_like(a.ks[0], 127)
+    down = torch.randint(0, 11, a.vs[0].shape, generator=g, device="cuda", dtype=torch.int32)
+    a.vs[0] = (127 - torch.where(low, down, 45 + (down * 3) // 2)).to(torch.uint8)
+    a.q[0] = torch.ones_like(a.q[0]) * (1 - 0.5 * (torch.rand(a.q[0].shape[:2] + (1,), generator=g, device="cuda") < 0.3)).to(torch.bfloat16)
+    a.build()
+    a.run()
+    for (rows, o, keys), ids in zip(a.streams, a.lists):
+        kv, _ = a.cache(a.K[0], a.ks[0], ids, keys)
+        v, vs = a.cache(a.V[0], a.vs[0], ids, keys)
+        sees = torch.arange(keys, device="cuda")[None] < keys - rows + 1 + torch.arange(rows, device="cuda")[:, None]
+        q = a.q[0][o:o + rows].double().view(rows, NKV, -1, 64)
+        for h in range(NKV):
+            s = torch.einsum("rhd,kd->rhk", q[:, h], kv[h]) / 8
+            p = torch.softmax(torch.where(sees[:, None], s, -torch.inf), -1)
+            ref, A = p @ v[h], p @ v[h].abs()
+            e = 70 * 2.0 ** -23 * s.abs().amax(-1) + 2.0 ** -21 + 2.0 ** -22 * 128
+            top = (p * torch.exp2(vs[h].double() - 127)).amax(-1)
+            bound = (2 * e + 2.0 ** -11 + 2 * (keys / 64 + 64) * 2.0 ** -23)[..., None] * A \
+                + (keys * 2.0 ** -31 * 448 * top)[..., None]
+            bound = bound + 2.0 ** -8 * (ref.abs() + bound)
+            err = (a.out[0][o:o + rows].view(rows, NKV, -1, 64)[:, h].double() - ref).abs()
+            assert (err <= bound).all(), (rows, keys, h, float((err / bound).max()), float((err / ref.abs()).max()))
+
+
+@pytest.mark.parametrize("path", ["mma", "tc"])
 def test_the_smallest_scale_of_k(tf, path, monkeypatch):
     """Scale byte 0 is 2^-127, which queries near 2^120 can tell from 0."""
     from scaled import ScaledAttn
