@@ -567,15 +567,16 @@ int tf_pages_copy(void* const* pools, int n_pools, int32_t page_keys, int32_t n_
  *                 alone. Windows of 9 rows or more take a quarter of the keys a
  *                 chunk (2,048 at least, tf_chunk_keys at most), prompts of few
  *                 windows less than tf_chunk_keys too (tf_partials_bytes and
- *                 tf_segments_query tell the table's own sizes). P.V runs with fp16 weights (off by 2^-12 of each) and
- *                 exact codes, summed in fp32. A weight there is taken times its
- *                 block's V scale, relative to its chunk's largest: keys whose
- *                 product is below 2^-31 of a row's largest do not count in P.V, and
- *                 a block of V whose scale is more than 2^64 below its chunk's
- *                 largest counts as if 2^64 below. The tensor-core kernel (windows
- *                 of 9 rows or more, prompts; TF_ATTN_PATH as for tf_attn) takes a
- *                 query as the sum of two e4m3 parts: exact for elements down to
- *                 2^-9 of a head's largest, smaller ones off by at most 2^-17 of it.
+ *                 tf_segments_query tell the table's own sizes). P.V runs with fp16
+ *                 weights and exact codes, summed in fp32. A weight there is taken
+ *                 times its block's V scale, relative to its chunk's largest, and is
+ *                 off by at most 2^-11 of itself, or 2^-31 of the row's largest
+ *                 product where that is more (keys below do not count in P.V); a
+ *                 block of V whose scale is more than 2^64 below its chunk's largest
+ *                 counts as if 2^64 below. The tensor-core kernel (windows of 9 rows
+ *                 or more, prompts; TF_ATTN_PATH as for tf_attn) takes a query as
+ *                 the sum of two e4m3 parts: exact for elements down to 2^-9 of a
+ *                 head's largest, smaller ones off by at most 2^-17 of it.
  *                 A NaN reaches the rows that see its key, no other. q, partials
  *                 and out lie apart. */
 int tf_paged_scaled_build(const tf_stream* streams, int n_streams, const void* const* conv_state,
