@@ -166,6 +166,33 @@ def test_many_rows(tf, x8):
     assert torch.equal(call(tf, x, xs, *w), (v @ matrix(*w[:2]).T).float().to(torch.bfloat16))
 
 
+@pytest.mark.parametrize("R,N,K", [(1024, 2048, 2048), (2049, 1000, 2080), (64, 20000, 2048)])
+@pytest.mark.parametrize("x8", [False, True])
+def test_a_layer_of_many_rows(tf, R, N, K, x8):
+    """A prompt's or a drafted round's rows through a projection, exactly."""
+    w = weights(N, K, 27, whole=True)
+    x, xs, v = rows(R, K, 28, x8, whole=True)
+    assert torch.equal(call(tf, x, xs, *w), (v @ matrix(*w[:2]).T).float().to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("R,N,K", [(40, 20000, 2176), (70, 300, 4224), (33, 70, 40960)])
+def test_bits_do_not_depend_on_a_rows_place(tf, R, N, K):
+    w = weights(N, K, 29)
+    x, xs, v = rows(R, K, 30, False)
+    want = call(tf, x, xs, *w)
+    move = torch.randperm(R, generator=torch.Generator().manual_seed(31)).cuda()
+    got = call(tf, x[move].contiguous(), None, *w)
+    assert torch.equal(got.view(torch.int16), want[move].view(torch.int16))
+
+
+def test_no_rows_write_nothing(tf):
+    w = weights(40, 64, 32)
+    x, xs, v = rows(2, 64, 33, False)
+    y = torch.full((2, 40), 7.0, dtype=torch.bfloat16, device="cuda")
+    tf.tf_linear_rows(x, 64, None, 0, 64, *w, 40, y, 40)
+    assert (y == 7).all()
+
+
 @pytest.mark.parametrize("x8", [False, True])
 def test_strides_and_odd_addresses(tf, x8):
     """Padded rows of x (NaN between them) and y (left alone between them), y and the scales at odd addresses."""

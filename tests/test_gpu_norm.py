@@ -174,3 +174,13 @@ def test_captured_on_another_stream(tf):
 
 def test_empty_and_host_memory(tf):
     call(tf, 64, *inputs(0, 64, 9, True))
+
+
+def test_no_rows_write_nothing(tf):
+    W = 64
+    x, r, w, s, codes, scales = inputs(2, W, 10, True)
+    before = [t.clone() for t in (s, codes, scales)]
+    tf.tf_norm_rows(x, W, r, W, w, EPS, 0, W, s, W, codes, scales)
+    tf.tf_norm_rows(x, W, None, W, w, EPS, 0, W, None, W, codes, scales)
+    for a, b in zip((s, codes, scales), before):
+        assert torch.equal(a, b)
