@@ -564,9 +564,10 @@ int tf_pages_copy(void* const* pools, int n_pools, int32_t page_keys, int32_t n_
  *                 format above.
  *   tf_attn_paged reads codes and scales (q and out bf16; the window's own rows
  *                 are read back as coded); a stream's bits depend on that stream
- *                 alone. Windows of 9 rows or more take a quarter of the keys a
- *                 chunk (2,048 at least, tf_chunk_keys at most), prompts of few
- *                 windows less than tf_chunk_keys too (tf_partials_bytes and
+ *                 alone (a row's in tf_norm_rows and tf_linear_rows also on how many
+ *                 rows the call has). Windows of 9 rows or more take a quarter of
+ *                 the keys a chunk (2,048 at least, tf_chunk_keys at most), prompts
+ *                 of few windows less than tf_chunk_keys too (tf_partials_bytes and
  *                 tf_segments_query tell the table's own sizes). P.V runs with fp16
  *                 weights and exact codes, summed in fp32. A weight there is taken
  *                 times its block's V scale, relative to its chunk's largest, and is
@@ -591,7 +592,8 @@ int tf_paged_scaled_prompt_build(int32_t rows, int32_t keys, int32_t kv_capacity
                                  int n_conv, int n_attn, tf_cuda_stream stream, tf_segments** out);
 
 /* tf_pages_copy for scaled pools: the codes of keys [0, keys[i]) and the scales of
- * the blocks that hold them.
+ * the blocks that hold them. Where keys[i] ends inside a block, the destination's
+ * codes behind it stay and come under the copied scale.
  *   pools, scales  host arrays [n_pools] of device pointers
  * The other arguments, rules and errors are tf_pages_copy's. */
 int tf_pages_copy_scaled(void* const* pools, void* const* scales, int n_pools, int32_t page_keys, int32_t n_pages,
@@ -612,8 +614,10 @@ int tf_pages_copy_scaled(void* const* pools, void* const* scales, int n_pools, i
  *   scales  uint8 [R][width / TF_SCALE_COLUMNS], at any address
  * width is a multiple of TF_SCALE_COLUMNS, strides are multiples of 8; other
  * overlaps of an output with anything are refused. A NaN or an infinity in a row
- * makes that row's codes NaN (or, where the root is infinite, 0). Needs no table;
- * R == 0 is a no-op. Errors: TF_EINVAL (null, one of res and sum alone, misaligned,
+ * makes that row's codes NaN (or, where the root is infinite, 0); finite rows whose
+ * mean of squares passes fp32 (h beyond some 2^64) become 0 too. Sums run in an
+ * order that R and width fix. Needs no table; R == 0 is a no-op. Errors: TF_EINVAL
+ * (null, one of res and sum alone, misaligned,
  * overlaps, a bad width or stride, eps not positive and finite, another device's
  * memory), TF_ERANGE (R > 2^24, width > TF_NORM_MAX_WIDTH, a stride beyond 2^32). */
 #define TF_NORM_MAX_WIDTH (1 << 14)
@@ -633,7 +637,9 @@ int tf_norm_rows(const void* x, int64_t x_stride, const void* res, int64_t res_s
  *   s         float [N]
  *   y         bf16, row r at y + r*y_stride (any 2-byte address and stride >= N);
  *             overlaps nothing else
- * K is a multiple of TF_SCALE_COLUMNS. Up to 32 rows take the weights from HBM once.
+ * K is a multiple of TF_SCALE_COLUMNS. Up to 32 rows take the weights from HBM once;
+ * every 32 rows decode them anew, so hundreds of rows run far below the rate of a
+ * bf16 matrix product (some 300 of 1,900 TFLOP/s on a GB300).
  * Values of x below bf16's smallest, 2^-133, are rounded to multiples of it; the
  * other products are exact. Sums run in an order that R, K, N and the device's
  * number of SMs fix: a row's bits may differ between calls of different R, not with

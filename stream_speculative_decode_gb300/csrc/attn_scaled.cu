@@ -34,10 +34,11 @@
 //
 // Measured: 4 windows of 6 rows at 65,536 to 130,816 keys 90.8 us (4.6 TB/s; a
 // block at a time 97.1), of 2 rows 72.8 us (5.7 TB/s, 85 % of the measured copy
-// rate); 16 single rows at 256 to 4,096 keys 9.4 us. What bounds it is issue: some
-// 245 instructions a block of 24 queries, half of the issue slots used. The queries
-// of 3 or 4 tiles lie in shared memory, which leaves three CTAs an SM their
-// registers; four CTAs a block at a time with 24 queries 97.7 us.
+// rate); 16 single rows at 256 to 4,096 keys 9.4 us. What bounds it is latency: three
+// warps a scheduler in chains of dependent instructions, some 245 a block of 24
+// queries, which wait mostly for one another; half of the issue slots are used, and no
+// pipe above 40 %. The queries of 3 or 4 tiles lie in shared memory, which leaves three
+// CTAs an SM their registers; four CTAs a block at a time with 24 queries 97.7 us.
 //
 // What no row of the item may see is kept out: scores are masked, and in blocks
 // that reach past the first row's keys a NaN code of V is taken out of the

@@ -21,9 +21,12 @@
 // SM with a run of 16-output tiles, whose inputs the warps share out evenly.
 //
 // Measured, 128,000 outputs by 2,048 inputs (139 MB): 1 row 27.3 us, 16 rows 34.1
-// us (5.1 and 4.2 TB/s; the same loads alone 21.5 us). What bounds it is issue:
-// of a chunk's 144 instructions 56 take its codes apart at half rate, and 16 warps
-// wait for one another's turn, not for memory. Warps that share tiles and meet at
+// us (5.1 and 4.2 TB/s; the same loads alone 21.5 us). What bounds it is the pipe that
+// takes the codes apart, at half rate 56 of a chunk's 144 instructions: the warps wait
+// for it and for one another's turn (54 % of the issue slots used), not for memory. That
+// is paid again for every 32 rows: 32 rows 52 us, 64 96, 1,024 1,700 (316 TFLOP/s; the
+// products alone would take 283 at the cuBLAS rate), and 16,381 rows of 2,048 to 2,048
+// outputs 461 (72): this is a kernel for few rows. Warps that share tiles and meet at
 // each one's end (37.1 and 45.8), loads a chunk at a time into a ring in shared
 // memory (47 and 80), into the registers just used (48.5 and 56) or with the scales'
 // codes picked apart as they arrive (44 and 51) were slower.

@@ -199,7 +199,8 @@ int32_t scaled_chunk_keys(int32_t rows, int32_t keys, int prompt_windows) {
 // 100 at 3,000 24.0 and 26.9, but 300 at 6,000 53.9 and 43.3), and many chunks of few rows,
 // whose records 16 threads a query read one after another (4 single rows at 100,000 keys
 // 69.7 and 80.8, one at 30,000 10.3 and 11.7, 8 windows of 4 at 30,000 52.9 and 56.6, but 64
-// of 8 at 16 to 32,768 76.5 and 67.2).
+// of 8 at 16 to 32,768 76.5 and 67.2). Where the SMs are full anyway it costs a little (64
+// windows of 4 rows 50.7 and 48.6): how a window ends may not depend on the others.
 int32_t merge_mode_of(int32_t rows, int32_t n_chunks, bool scaled, int prompt_windows) {
     if (n_chunks == 1) return kMergeDirect;
     if (scaled && (prompt_windows > 0 ? prompt_windows <= 4 : rows <= 4 && n_chunks > 8)) return kMergeKernel;
