@@ -185,6 +185,18 @@ def test_bits_do_not_depend_on_a_rows_place(tf, R, N, K):
     assert torch.equal(got.view(torch.int16), want[move].view(torch.int16))
 
 
+@pytest.mark.parametrize("R,K,N", [(1 << 20, 32, 40), (1, 32, 1 << 24), (9, 1 << 20, 20)])
+def test_the_largest_sizes(tf, R, K, N):
+    """The documented limits, one at a time. (Products are multiples of 1/4 of either sign, some 10 in size: the sums of
+    2^20 of them stay near 2^14, far below the 2^22 up to which fp32 holds them exactly.)"""
+    w = weights(N, K, 34, whole=True)
+    x, xs, v = rows(R, K, 35, True, whole=True)
+    got = call(tf, x, xs, *w)
+    for n in range(0, N, 1 << 21):
+        m = matrix(w[0][n:n + (1 << 21)], w[1][n:n + (1 << 21)])
+        assert torch.equal(got[:, n:n + (1 << 21)], (v @ m.T).float().to(torch.bfloat16)), n
+
+
 def test_no_rows_write_nothing(tf):
     w = weights(40, 64, 32)
     x, xs, v = rows(2, 64, 33, False)

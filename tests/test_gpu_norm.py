@@ -176,6 +176,15 @@ def test_empty_and_host_memory(tf):
     call(tf, 64, *inputs(0, 64, 9, True))
 
 
+@pytest.mark.parametrize("R,W", [(1 << 24, 32), (3, 1 << 14)])
+def test_the_largest_sizes(tf, R, W):
+    x, r, w, s, codes, scales = inputs(R, W, 11, True)
+    call(tf, W, x, r, w, s, codes, scales)
+    for i in (0, R // 2, R - min(R, 1 << 20)):
+        at = slice(i, i + (1 << 20))
+        check(W, x[at], r[at], w, s[at], codes[at], scales[at], what=i)
+
+
 def test_no_rows_write_nothing(tf):
     W = 64
     x, r, w, s, codes, scales = inputs(2, W, 10, True)
